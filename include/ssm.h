@@ -11,7 +11,13 @@
  *   - ssm_selective_scan_bwd: the gradients of the scan (training);
  *   - ssm_block_fwd: a whole Mamba block around the scan (with a plan);
  *   - ssm_ssd_fwd: the SSD (Mamba-2) layer, chunked on the matrix cores;
- *   - ssm_ssd_step: one decode step of that layer on a resident state.
+ *   - ssm_ssd_step: one decode step of that layer on a resident state;
+ *   - ssm_gated_scan_fwd, _bwd, _step: a gated linear recurrence, whose decay
+ *     is itself an input, with its gradients and its decode step;
+ *   - ssm_add_rmsnorm_fwd, _bwd: the residual sum and the RMSNorm between two
+ *     blocks in one pass, with its gradients;
+ *   - ssm_gated_rmsnorm_fwd, _bwd: the RMSNorm of a gated layer output over
+ *     groups of channels, with its gradients.
  *
  * The operations are defined on these pages (cited by title and section):
  *   [P1] "Mamba: Linear-Time Sequence Modeling with Selective State Spaces"
@@ -63,7 +69,7 @@
 extern "C" {
 #endif
 
-#define SSM_ABI_VERSION 10
+#define SSM_ABI_VERSION 11
 #define SSM_MAX_DSTATE 16 /* largest N the kernels hold in registers */
 #define SSM_MAX_CONV_K 4  /* largest conv1d kernel width */
 
@@ -491,6 +497,232 @@ typedef struct ssm_ssd_step_args {
 } ssm_ssd_step_args_t;
 
 ssm_status_t ssm_ssd_step(const ssm_ssd_step_args_t *args, void *stream);
+
+/*
+ * The gated linear recurrence: one state per channel, whose decay a_t is an
+ * input of every step rather than exp(dt A).  Per batch row b and channel d,
+ *   h_t = a_t h_{t-1} + b_t, from h0 (or 0);   y_t = h_t;   h_final = h_{L-1}
+ * with a_t and b_t formed from the inputs by `mode` (sig the logistic
+ * function; a bias that is not given is 0):
+ *   SSM_GATE_DECAY    a = gate,            b = x
+ *   SSM_GATE_SIGMOID  s = sig(gate + gate_bias),  a = 1 - s,  b = s x
+ *                     ([P1] Theorem 1, the gated RNN the scan reduces to)
+ *   SSM_GATE_RATE     r = sig(gate + gate_bias),  a = exp(A r),
+ *                     b = sqrt(1 - a^2) sig(in_gate + in_bias) x
+ *                     (without in_gate: b = sqrt(1 - a^2) x).  A <= 0: the
+ *                     input weight keeps a unit-variance input's state at unit
+ *                     variance; where A > 0 it is 0.
+ * Where reset[b,t] != 0 the state is dropped before step t (h_t = b_t,
+ * whatever h_{t-1} was, an infinity or a NaN included): sequences packed one
+ * behind the other in a row come out as in calls of their own, and a row
+ * padded on the left resets at its first token.
+ *
+ * In SSM_GATE_DECAY the decays are meant to lie in [-1, 1].  Others are
+ * computed too, but the products of up to SSM_GATED_TILE decays formed inside
+ * must stay below 2^127: growth beyond it gives an infinity or a NaN also
+ * where the states themselves stay finite.
+ *
+ * Arithmetic is fp32 (the hardware's exponential, reciprocal and square root,
+ * 1 ulp); y is rounded once.  Results do not change from run to run.
+ */
+typedef enum ssm_gate_mode {
+    SSM_GATE_DECAY = 0,
+    SSM_GATE_SIGMOID = 1,
+    SSM_GATE_RATE = 2
+} ssm_gate_mode_t;
+
+#define SSM_GATED_BLOCK 128 /* steps between two checkpoints of the gated scan */
+#define SSM_GATED_TILE 256  /* most steps whose decays are multiplied together */
+
+typedef struct ssm_gated_scan_args {
+    int64_t batch, seqlen;  /* B >= 0, L >= 0                                  */
+    int64_t dim;            /* D, 1 <= D <= 2^20                               */
+    int32_t io_dtype;       /* ssm_dtype_t of x, gate, in_gate and y           */
+    int32_t mode;           /* ssm_gate_mode_t                                 */
+    const void *x;          /* (B,L,D) io_dtype, required                      */
+    const void *gate;       /* (B,L,D) io_dtype, required                      */
+    const void *in_gate;    /* (B,L,D) io_dtype, or NULL; SSM_GATE_RATE only   */
+    const float *A;         /* (D) fp32; required with SSM_GATE_RATE, else NULL */
+    const float *gate_bias; /* (D) fp32, or NULL; not with SSM_GATE_DECAY      */
+    const float *in_bias;   /* (D) fp32, or NULL; only with in_gate            */
+    const uint8_t *reset;   /* (B,L) bytes, or NULL (no resets)                */
+    const float *h0;        /* (B,D) fp32 initial state, or NULL (= 0)         */
+    void *y;                /* (B,L,D) io_dtype output, required               */
+    float *h_final;         /* (B,D) fp32 output, or NULL                      */
+    float *checkpoints;     /* (ceil(L/SSM_GATED_BLOCK), B, D) fp32 output, or NULL:
+                               the state entering step SSM_GATED_BLOCK * j, before
+                               a reset there (h0 or 0 for j = 0)               */
+    void *workspace;        /* device scratch of workspace_bytes, 256-aligned  */
+    size_t workspace_bytes; /* >= ssm_gated_scan_workspace_size(args)          */
+} ssm_gated_scan_args_t;
+
+/* Bytes of device workspace ssm_gated_scan_fwd needs (only the size fields and
+ * io_dtype are read); its contents on entry do not matter.  (size_t)-1 for
+ * invalid sizes. */
+size_t ssm_gated_scan_workspace_size(const ssm_gated_scan_args_t *args);
+
+/* Enqueue the recurrence.  Outputs must not overlap any input, each other or
+ * the workspace.  L == 0 copies h0 (or zeros) to h_final. */
+ssm_status_t ssm_gated_scan_fwd(const ssm_gated_scan_args_t *args, void *stream);
+
+/*
+ * Gradients of the recurrence for dL/dy = dy and dL/dh_final = dh_final:
+ *   lambda_t = dy_t + a_{t+1} lambda_{t+1}  (0 through a reset at t + 1;
+ *              lambda_{L-1} adds dh_final)
+ *   da_t = lambda_t h_{t-1} (0 at a reset), db_t = lambda_t, and the chain rule
+ *   through a and b above;  dA, dgate_bias, din_bias summed over batch and
+ *   time;  dh0 = a_0 lambda_0 (0 with a reset at 0).
+ * The states are recomputed in fp32 from the forward's checkpoints (which the
+ * backward computes itself when none are given).  Where sqrt(1 - a^2) is 0 its
+ * derivative is taken as 0.
+ */
+typedef struct ssm_gated_scan_bwd_args {
+    int64_t batch, seqlen, dim; /* as in ssm_gated_scan_args_t                 */
+    int32_t io_dtype;       /* of x, gate, in_gate, dy, dx, dgate, din_gate    */
+    int32_t mode;           /* as in ssm_gated_scan_args_t                     */
+    const void *x, *gate, *in_gate;                       /* forward inputs    */
+    const float *A, *gate_bias, *in_bias;
+    const uint8_t *reset;
+    const float *h0;
+    const void *dy;         /* (B,L,D) io_dtype, required                      */
+    const float *dh_final;  /* (B,D) fp32, or NULL (= 0)                       */
+    const float *checkpoints; /* of an ssm_gated_scan_fwd call on the same inputs, or NULL */
+    void *dx, *dgate;       /* (B,L,D) io_dtype outputs, required              */
+    void *din_gate;         /* (B,L,D) io_dtype output; required iff in_gate   */
+    float *dA;              /* (D) fp32 output; required iff SSM_GATE_RATE     */
+    float *dgate_bias;      /* (D) fp32 output, or NULL; not with SSM_GATE_DECAY */
+    float *din_bias;        /* (D) fp32 output, or NULL; only with in_gate     */
+    float *dh0;             /* (B,D) fp32 output, or NULL                      */
+    void *workspace;        /* device scratch, 256-aligned                     */
+    size_t workspace_bytes; /* >= ssm_gated_scan_bwd_workspace_size(args)      */
+} ssm_gated_scan_bwd_args_t;
+
+/* Workspace bytes ssm_gated_scan_bwd needs: the size fields, io_dtype, mode and
+ * whether checkpoints are given are read.  (size_t)-1 for invalid sizes. */
+size_t ssm_gated_scan_bwd_workspace_size(const ssm_gated_scan_bwd_args_t *args);
+
+/* Enqueue the backward pass.  Outputs must not overlap any input, each other
+ * or the workspace; every output given is overwritten. */
+ssm_status_t ssm_gated_scan_bwd(const ssm_gated_scan_bwd_args_t *args, void *stream);
+
+/*
+ * One decode step of the recurrence on a state kept between calls:
+ *   state[b,d] <- a state[b,d] + b (state taken as 0 where reset[b] != 0);
+ *   y[b,d] = state[b,d]
+ * The state is read and written IN PLACE; it is h_final of a prefill.
+ */
+typedef struct ssm_gated_step_args {
+    int64_t batch, dim;     /* B >= 0, 1 <= D <= 2^20                          */
+    int32_t io_dtype, mode; /* as in ssm_gated_scan_args_t                     */
+    float *state;           /* (B,D) fp32, updated in place; required          */
+    const void *x, *gate;   /* (B,D) io_dtype, required                        */
+    const void *in_gate;    /* (B,D) io_dtype, or NULL; SSM_GATE_RATE only     */
+    const float *A, *gate_bias, *in_bias; /* as in ssm_gated_scan_args_t       */
+    const uint8_t *reset;   /* (B) bytes, or NULL                              */
+    void *y;                /* (B,D) io_dtype output, required                 */
+} ssm_gated_step_args_t;
+
+/* y must not overlap any input or the state, nor the state an input. */
+ssm_status_t ssm_gated_scan_step(const ssm_gated_step_args_t *args, void *stream);
+
+/*
+ * The boundary between two pre-norm residual blocks in one pass over the rows
+ * ([P1] sec. 4a: the block's output is added to its input, the next block
+ * begins with the norm).  Per row, with RMS(v) = v / sqrt(mean(v^2) + eps):
+ *   u       = x, or RMS(x) * post_w when post_w is given (a norm behind the
+ *             block as well)
+ *   res_out = residual + scale * u   (residual NULL: 0; scale NULL: 1)
+ *   y       = RMS(res_out) * w       (of the sum before its rounding)
+ */
+typedef struct ssm_add_norm_args {
+    int64_t rows;           /* >= 0                                            */
+    int64_t dim;            /* D, 1 <= D <= 2^20                               */
+    int32_t io_dtype;       /* ssm_dtype_t of x and y                          */
+    int32_t res_dtype;      /* ssm_dtype_t of residual and res_out             */
+    const void *x;          /* (rows,D) io_dtype, required                     */
+    const void *residual;   /* (rows,D) res_dtype, or NULL                     */
+    const float *scale;     /* (D) fp32, or NULL                               */
+    const float *post_w;    /* (D) fp32, or NULL                               */
+    const float *w;         /* (D) fp32, required                              */
+    void *res_out;          /* (rows,D) res_dtype output, or NULL; may be exactly residual */
+    void *y;                /* (rows,D) io_dtype output, required              */
+    float eps;              /* > 0                                             */
+} ssm_add_norm_args_t;
+
+/* Outputs must not overlap an input (but res_out may be residual) or each other. */
+ssm_status_t ssm_add_rmsnorm_fwd(const ssm_add_norm_args_t *args, void *stream);
+
+/*
+ * Its gradients for dL/dy = dy and dL/dres_out = dres_out.  The forward's
+ * inputs are read again and every intermediate is recomputed in fp32 from
+ * them, so the sums dw, dscale and dpost_w do not see a rounded stream.
+ */
+typedef struct ssm_add_norm_bwd_args {
+    int64_t rows, dim;
+    int32_t io_dtype;       /* of x, dy, dx                                    */
+    int32_t res_dtype;      /* of residual, dres_out, dresidual                */
+    const void *x, *residual;               /* forward inputs (before an in-place update) */
+    const float *scale, *post_w, *w;
+    const void *dy;         /* (rows,D) io_dtype, required                     */
+    const void *dres_out;   /* (rows,D) res_dtype, or NULL (= 0)               */
+    void *dx;               /* (rows,D) io_dtype output, required              */
+    void *dresidual;        /* (rows,D) res_dtype output, or NULL; only with residual */
+    float *dw;              /* (D) fp32 output, required                       */
+    float *dscale;          /* (D) fp32 output, or NULL; only with scale       */
+    float *dpost_w;         /* (D) fp32 output, or NULL; only with post_w      */
+    void *workspace;        /* device scratch, 256-aligned                     */
+    size_t workspace_bytes; /* >= ssm_add_rmsnorm_bwd_workspace_size(args)     */
+    float eps;              /* > 0                                             */
+} ssm_add_norm_bwd_args_t;
+
+/* Workspace bytes (the size fields and types and whether scale and post_w are given
+ * are read); (size_t)-1 for invalid sizes. */
+size_t ssm_add_rmsnorm_bwd_workspace_size(const ssm_add_norm_bwd_args_t *args);
+
+/* Outputs must not overlap an input, each other or the workspace, except that
+ * dresidual may be exactly dres_out. */
+ssm_status_t ssm_add_rmsnorm_bwd(const ssm_add_norm_bwd_args_t *args, void *stream);
+
+/*
+ * RMSNorm of a gated layer output (the output of ssm_ssd_fwd or
+ * ssm_gated_scan_fwd ahead of the output projection), over `groups` groups of
+ * D / groups consecutive channels each.  With g = SiLU(z):
+ *   gate_first = 1:  v = x g,  y = v / sqrt(mean_group(v^2) + eps) * w
+ *   gate_first = 0:  y = x / sqrt(mean_group(x^2) + eps) * w * g
+ */
+typedef struct ssm_gated_norm_args {
+    int64_t rows;           /* >= 0                                            */
+    int64_t dim;            /* D, 1 <= D <= 2^20                               */
+    int64_t groups;         /* G >= 1, divides D                               */
+    int32_t io_dtype;       /* ssm_dtype_t of x, z and y                       */
+    int32_t gate_first;     /* 0 or 1                                          */
+    const void *x, *z;      /* (rows,D) io_dtype, required                     */
+    const float *w;         /* (D) fp32, required                              */
+    void *y;                /* (rows,D) io_dtype output, required              */
+    float eps;              /* > 0                                             */
+} ssm_gated_norm_args_t;
+
+/* y must not overlap an input, except that it may be exactly x or z. */
+ssm_status_t ssm_gated_rmsnorm_fwd(const ssm_gated_norm_args_t *args, void *stream);
+
+typedef struct ssm_gated_norm_bwd_args {
+    int64_t rows, dim, groups;
+    int32_t io_dtype, gate_first;
+    const void *x, *z;      /* forward inputs                                  */
+    const float *w;
+    const void *dy;         /* (rows,D) io_dtype, required                     */
+    void *dx, *dz;          /* (rows,D) io_dtype outputs, required             */
+    float *dw;              /* (D) fp32 output, required                       */
+    void *workspace;        /* device scratch, 256-aligned                     */
+    size_t workspace_bytes; /* >= ssm_gated_rmsnorm_bwd_workspace_size(args)   */
+    float eps;              /* > 0                                             */
+} ssm_gated_norm_bwd_args_t;
+
+/* Workspace bytes (the size fields and io_dtype are read); (size_t)-1 for invalid sizes. */
+size_t ssm_gated_rmsnorm_bwd_workspace_size(const ssm_gated_norm_bwd_args_t *args);
+
+/* Outputs must not overlap an input, each other or the workspace. */
+ssm_status_t ssm_gated_rmsnorm_bwd(const ssm_gated_norm_bwd_args_t *args, void *stream);
 
 /* Static description of a status code (never NULL). */
 const char *ssm_status_string(ssm_status_t status);

@@ -9,8 +9,20 @@ from .ssm import (  # noqa: F401
     BlockPlan,
     SSMError,
     abi_version,
+    add_rmsnorm,
+    add_rmsnorm_bwd,
+    add_rmsnorm_fwd,
     causal_conv1d_silu,
     checkpoint_shape,
+    gated_checkpoint_shape,
+    gated_rmsnorm,
+    gated_rmsnorm_bwd,
+    gated_rmsnorm_fwd,
+    gated_scan,
+    gated_scan_bwd,
+    gated_scan_fwd,
+    gated_scan_step,
+    gated_scan_step_args,
     lib,
     mamba_block_fwd,
     selective_scan,
@@ -27,7 +39,10 @@ from .ssm import (  # noqa: F401
     status_string,
 )
 
-__all__ = ["NOALLOC_SCRATCH_BYTES", "BlockPlan", "SSMError", "abi_version", "causal_conv1d_silu", "checkpoint_shape", "lib", "mamba_block_fwd",
+__all__ = ["NOALLOC_SCRATCH_BYTES", "BlockPlan", "SSMError", "abi_version", "add_rmsnorm",
+           "add_rmsnorm_bwd", "add_rmsnorm_fwd", "causal_conv1d_silu", "checkpoint_shape",
+           "gated_checkpoint_shape", "gated_rmsnorm", "gated_rmsnorm_bwd", "gated_rmsnorm_fwd", "gated_scan",
+           "gated_scan_bwd", "gated_scan_fwd", "gated_scan_step", "gated_scan_step_args", "lib", "mamba_block_fwd",
            "selective_scan", "selective_scan_args", "selective_scan_bwd", "selective_scan_fwd",
            "selective_scan_fwd_noalloc", "selective_scan_workspace_size", "ssd_fwd",
            "ssd_step", "ssd_step_args", "state_update", "state_update_args", "status_string"]

@@ -642,3 +642,369 @@ ssm_status_t ssm_ssd_step(const ssm_ssd_step_args_t *a, void *stream) {
 }
 
 }  // extern "C"
+
+// ------------------------------------------------- gated recurrence and fused norms
+namespace {
+
+// Grids and lane offsets of the gated scan and the norms stay in 32 bits up to this width.
+constexpr int64_t kMaxWidth = (int64_t)1 << 20;
+
+bool io_ok(int32_t dt) { return dt == SSM_F32 || dt == SSM_BF16; }
+
+// Every output against every input, the other outputs and the workspace.  `same_ok`: pairs
+// (output, input) that may be the very same tensor.
+struct SameOk {
+    const void *out, *in;
+};
+
+ssm_status_t check_overlaps(const Range *in, int nin, const Range *out, int nout, const Range &ws,
+                            SameOk s0 = SameOk{nullptr, nullptr}, SameOk s1 = SameOk{nullptr, nullptr}) {
+    for (int i = 0; i < nout; ++i) {
+        for (int k = 0; k < nin; ++k) {
+            const bool same = out[i].lo == in[k].lo && out[i].hi == in[k].hi;
+            const uintptr_t o = out[i].lo, n = in[k].lo;
+            if (same && ((o == (uintptr_t)s0.out && n == (uintptr_t)s0.in) ||
+                         (o == (uintptr_t)s1.out && n == (uintptr_t)s1.in)))
+                continue;
+            if (overlaps(out[i], in[k])) return fail(SSM_ERR_ALIAS, "%s overlaps %s", out[i].name, in[k].name);
+        }
+        for (int k = i + 1; k < nout; ++k)
+            if (overlaps(out[i], out[k])) return fail(SSM_ERR_ALIAS, "%s overlaps %s", out[i].name, out[k].name);
+        if (overlaps(ws, out[i])) return fail(SSM_ERR_ALIAS, "workspace overlaps %s", out[i].name);
+    }
+    for (int k = 0; k < nin; ++k)
+        if (overlaps(ws, in[k])) return fail(SSM_ERR_ALIAS, "workspace overlaps %s", in[k].name);
+    return SSM_OK;
+}
+
+ssm_status_t check_workspace(const void *ws, size_t have, size_t need) {
+    if (need == 0) return SSM_OK;
+    if (!ws) return fail(SSM_ERR_WORKSPACE, "workspace of %zu bytes required", need);
+    if (have < need) return fail(SSM_ERR_WORKSPACE, "workspace has %zu bytes, %zu required", have, need);
+    if (!aligned(ws, 256)) return fail(SSM_ERR_WORKSPACE, "workspace is not 256-byte aligned");
+    return SSM_OK;
+}
+
+ssm_status_t check_align(const void *const *io, int nio, int64_t es, const void *const *f, int nf) {
+    for (int i = 0; i < nio; ++i)
+        if (!aligned(io[i], es))
+            return fail(SSM_ERR_ALIGN, "an io_dtype pointer is not %lld-byte aligned", (long long)es);
+    for (int i = 0; i < nf; ++i)
+        if (!aligned(f[i], 4)) return fail(SSM_ERR_ALIGN, "an fp32 pointer is not 4-byte aligned");
+    return SSM_OK;
+}
+
+#define COUNT(a) ((int)(sizeof(a) / sizeof((a)[0])))
+
+// Sizes, types and the pairing of options shared by the gated scan, its backward and its step.
+ssm_status_t check_gated(int64_t B, int64_t L, int64_t D, int32_t io, int32_t mode, const void *in_gate,
+                         const float *A, const float *gate_bias, const float *in_bias) {
+    if (!io_ok(io)) return fail(SSM_ERR_BAD_DTYPE, "io_dtype %d is not SSM_F32 or SSM_BF16", io);
+    if (B < 0 || L < 0)
+        return fail(SSM_ERR_BAD_SHAPE, "negative batch (%lld) or seqlen (%lld)", (long long)B, (long long)L);
+    if (D < 1) return fail(SSM_ERR_BAD_SHAPE, "dim must be >= 1 (got %lld)", (long long)D);
+    if (D > kMaxWidth) return fail(SSM_ERR_UNSUPPORTED, "dim %lld exceeds 2^20", (long long)D);
+    if (mode != SSM_GATE_DECAY && mode != SSM_GATE_SIGMOID && mode != SSM_GATE_RATE)
+        return fail(SSM_ERR_UNSUPPORTED, "mode %d is not one of ssm_gate_mode_t", mode);
+    if (!mul_ok(B, L, 4 * D)) return fail(SSM_ERR_BAD_SHAPE, "sizes overflow");
+    // one workgroup per 128 steps of 32 channels, in a one-dimensional grid
+    if (!mul_ok(B, L / SSM_GATED_BLOCK + 1, D / 32 + 1) ||
+        B * (L / SSM_GATED_BLOCK + 1) * (D / 32 + 1) > ((int64_t)1 << 23))
+        return fail(SSM_ERR_UNSUPPORTED, "batch * ceil(seqlen / 128) * ceil(dim / 32) exceeds 2^23");
+    if (mode != SSM_GATE_RATE && (in_gate || A))
+        return fail(SSM_ERR_BAD_SHAPE, "in_gate and A are for SSM_GATE_RATE only");
+    if (mode == SSM_GATE_DECAY && gate_bias) return fail(SSM_ERR_BAD_SHAPE, "SSM_GATE_DECAY takes no gate_bias");
+    // (an empty in_gate has no address)
+    if (B > 0 && L > 0 && in_bias && !in_gate) return fail(SSM_ERR_BAD_SHAPE, "in_bias given without in_gate");
+    return SSM_OK;
+}
+
+int64_t gated_blocks(int64_t L) { return (L + SSM_GATED_BLOCK - 1) / SSM_GATED_BLOCK; }
+
+}  // namespace
+
+extern "C" {
+
+size_t ssm_gated_scan_workspace_size(const ssm_gated_scan_args_t *a) {
+    if (!a || check_gated(a->batch, a->seqlen, a->dim, a->io_dtype, SSM_GATE_DECAY, nullptr, nullptr, nullptr,
+                          nullptr) != SSM_OK)
+        return (size_t)-1;
+    return a->batch > 0 && a->seqlen > 0 ? ssm::gated_scan_workspace_bytes(*a) : 0;
+}
+
+ssm_status_t ssm_gated_scan_fwd(const ssm_gated_scan_args_t *a, void *stream) {
+    if (!a) return fail(SSM_ERR_NULL_ARG, "args is NULL");
+    ssm_status_t s = check_gated(a->batch, a->seqlen, a->dim, a->io_dtype, a->mode, a->in_gate, a->A, a->gate_bias,
+                                 a->in_bias);
+    if (s != SSM_OK) return s;
+    const int64_t B = a->batch, L = a->seqlen, D = a->dim, es = io_bytes(a->io_dtype), n = B * L * D;
+    const bool work = B > 0 && L > 0;
+    if (work) {
+        if (!a->x) return fail(SSM_ERR_NULL_ARG, "x is NULL");
+        if (!a->gate) return fail(SSM_ERR_NULL_ARG, "gate is NULL");
+        if (!a->y) return fail(SSM_ERR_NULL_ARG, "y is NULL");
+        if (a->mode == SSM_GATE_RATE && !a->A) return fail(SSM_ERR_NULL_ARG, "A is NULL");
+    }
+    const void *io[] = {a->x, a->gate, a->in_gate, a->y};
+    const void *f[] = {a->A, a->gate_bias, a->in_bias, a->h0, a->h_final, a->checkpoints};
+    if ((s = check_align(io, COUNT(io), es, f, COUNT(f))) != SSM_OK) return s;
+    const size_t need = work ? ssm::gated_scan_workspace_bytes(*a) : 0;
+    if ((s = check_workspace(a->workspace, a->workspace_bytes, need)) != SSM_OK) return s;
+    const Range in[] = {range(a->x, n, es, "x"), range(a->gate, n, es, "gate"), range(a->in_gate, n, es, "in_gate"),
+                        range(a->A, D, 4, "A"), range(a->gate_bias, D, 4, "gate_bias"),
+                        range(a->in_bias, D, 4, "in_bias"), range(a->reset, B * L, 1, "reset"),
+                        range(a->h0, B * D, 4, "h0")};
+    const Range out[] = {range(a->y, n, es, "y"), range(a->h_final, B * D, 4, "h_final"),
+                         range(a->checkpoints, gated_blocks(L) * B * D, 4, "checkpoints")};
+    const Range ws = range(need ? a->workspace : nullptr, (int64_t)need, 1, "workspace");
+    if ((s = check_overlaps(in, COUNT(in), out, COUNT(out), ws)) != SSM_OK) return s;
+    if (B == 0) return ok();
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    hipError_t e = hipSuccess;
+    if (L > 0)
+        e = ssm::launch_gated_scan_fwd(*a, st);
+    else if (a->h_final)
+        e = ssm::launch_copy_or_zero(a->h_final, a->h0, B * D, st);
+    if (e != hipSuccess) return fail(SSM_ERR_HIP, "HIP error: %s", hipGetErrorString(e));
+    return ok();
+}
+
+size_t ssm_gated_scan_bwd_workspace_size(const ssm_gated_scan_bwd_args_t *a) {
+    if (!a || check_gated(a->batch, a->seqlen, a->dim, a->io_dtype, a->mode, nullptr, nullptr, nullptr, nullptr) !=
+                  SSM_OK)
+        return (size_t)-1;
+    return a->batch > 0 && a->seqlen > 0 ? ssm::gated_scan_bwd_workspace_bytes(*a) : 0;
+}
+
+ssm_status_t ssm_gated_scan_bwd(const ssm_gated_scan_bwd_args_t *a, void *stream) {
+    if (!a) return fail(SSM_ERR_NULL_ARG, "args is NULL");
+    ssm_status_t s = check_gated(a->batch, a->seqlen, a->dim, a->io_dtype, a->mode, a->in_gate, a->A, a->gate_bias,
+                                 a->in_bias);
+    if (s != SSM_OK) return s;
+    const int64_t B = a->batch, L = a->seqlen, D = a->dim, es = io_bytes(a->io_dtype), n = B * L * D;
+    const bool work = B > 0 && L > 0;
+    if (work) {
+        const struct { const void *p; const char *name; } req[] = {
+            {a->x, "x"}, {a->gate, "gate"}, {a->dy, "dy"}, {a->dx, "dx"}, {a->dgate, "dgate"}};
+        for (const auto &r : req)
+            if (!r.p) return fail(SSM_ERR_NULL_ARG, "%s is NULL", r.name);
+        if (a->mode == SSM_GATE_RATE && !a->A) return fail(SSM_ERR_NULL_ARG, "A is NULL");
+        if (a->in_gate && !a->din_gate) return fail(SSM_ERR_NULL_ARG, "din_gate is NULL but in_gate is given");
+    }
+    if (a->mode == SSM_GATE_RATE && !a->dA) return fail(SSM_ERR_NULL_ARG, "dA is NULL");
+    if (a->mode != SSM_GATE_RATE && a->dA) return fail(SSM_ERR_BAD_SHAPE, "dA is for SSM_GATE_RATE only");
+    if (a->mode == SSM_GATE_DECAY && a->dgate_bias) return fail(SSM_ERR_BAD_SHAPE, "SSM_GATE_DECAY has no gate_bias");
+    // (with B == 0 or L == 0 the (B,L,D) inputs may be absent)
+    if (work && !a->in_gate && (a->din_gate || a->din_bias))
+        return fail(SSM_ERR_BAD_SHAPE, "din_gate or din_bias given without in_gate");
+    if (a->mode != SSM_GATE_RATE && (a->din_gate || a->din_bias))
+        return fail(SSM_ERR_BAD_SHAPE, "din_gate and din_bias are for SSM_GATE_RATE only");
+    const void *io[] = {a->x, a->gate, a->in_gate, a->dy, a->dx, a->dgate, a->din_gate};
+    const void *f[] = {a->A, a->gate_bias, a->in_bias, a->h0, a->dh_final, a->checkpoints, a->dA, a->dgate_bias,
+                       a->din_bias, a->dh0};
+    if ((s = check_align(io, COUNT(io), es, f, COUNT(f))) != SSM_OK) return s;
+    const size_t need = work ? ssm::gated_scan_bwd_workspace_bytes(*a) : 0;
+    if ((s = check_workspace(a->workspace, a->workspace_bytes, need)) != SSM_OK) return s;
+    const Range in[] = {range(a->x, n, es, "x"), range(a->gate, n, es, "gate"), range(a->in_gate, n, es, "in_gate"),
+                        range(a->A, D, 4, "A"), range(a->gate_bias, D, 4, "gate_bias"),
+                        range(a->in_bias, D, 4, "in_bias"), range(a->reset, B * L, 1, "reset"),
+                        range(a->h0, B * D, 4, "h0"), range(a->dy, n, es, "dy"),
+                        range(a->dh_final, B * D, 4, "dh_final"),
+                        range(a->checkpoints, gated_blocks(L) * B * D, 4, "checkpoints")};
+    const Range out[] = {range(a->dx, n, es, "dx"), range(a->dgate, n, es, "dgate"),
+                         range(a->din_gate, n, es, "din_gate"), range(a->dA, D, 4, "dA"),
+                         range(a->dgate_bias, D, 4, "dgate_bias"), range(a->din_bias, D, 4, "din_bias"),
+                         range(a->dh0, B * D, 4, "dh0")};
+    const Range ws = range(need ? a->workspace : nullptr, (int64_t)need, 1, "workspace");
+    if ((s = check_overlaps(in, COUNT(in), out, COUNT(out), ws)) != SSM_OK) return s;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    hipError_t e = hipSuccess;
+    if (work) {
+        e = ssm::launch_gated_scan_bwd(*a, st);
+    } else {
+        float *sums[] = {a->dA, a->dgate_bias, a->din_bias};
+        for (float *p : sums)
+            if (e == hipSuccess && p) e = ssm::launch_copy_or_zero(p, nullptr, D, st);
+        if (e == hipSuccess && a->dh0 && B > 0) e = ssm::launch_copy_or_zero(a->dh0, a->dh_final, B * D, st);
+    }
+    if (e != hipSuccess) return fail(SSM_ERR_HIP, "HIP error: %s", hipGetErrorString(e));
+    return ok();
+}
+
+ssm_status_t ssm_gated_scan_step(const ssm_gated_step_args_t *a, void *stream) {
+    if (!a) return fail(SSM_ERR_NULL_ARG, "args is NULL");
+    ssm_status_t s = check_gated(a->batch, 1, a->dim, a->io_dtype, a->mode, a->in_gate, a->A, a->gate_bias,
+                                 a->in_bias);
+    if (s != SSM_OK) return s;
+    const int64_t B = a->batch, D = a->dim, es = io_bytes(a->io_dtype), n = B * D;
+    if (B == 0) return ok();
+    const struct { const void *p; const char *name; } req[] = {
+        {a->state, "state"}, {a->x, "x"}, {a->gate, "gate"}, {a->y, "y"}};
+    for (const auto &r : req)
+        if (!r.p) return fail(SSM_ERR_NULL_ARG, "%s is NULL", r.name);
+    if (a->mode == SSM_GATE_RATE && !a->A) return fail(SSM_ERR_NULL_ARG, "A is NULL");
+    const void *io[] = {a->x, a->gate, a->in_gate, a->y};
+    const void *f[] = {a->A, a->gate_bias, a->in_bias, a->state};
+    if ((s = check_align(io, COUNT(io), es, f, COUNT(f))) != SSM_OK) return s;
+    const Range in[] = {range(a->x, n, es, "x"), range(a->gate, n, es, "gate"), range(a->in_gate, n, es, "in_gate"),
+                        range(a->A, D, 4, "A"), range(a->gate_bias, D, 4, "gate_bias"),
+                        range(a->in_bias, D, 4, "in_bias"), range(a->reset, B, 1, "reset")};
+    const Range out[] = {range(a->state, n, 4, "state"), range(a->y, n, es, "y")};
+    if ((s = check_overlaps(in, COUNT(in), out, COUNT(out), range(nullptr, 0, 1, ""))) != SSM_OK) return s;
+    const hipError_t e = ssm::launch_gated_step(*a, static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return fail(SSM_ERR_HIP, "HIP error: %s", hipGetErrorString(e));
+    return ok();
+}
+
+static ssm_status_t check_norm(int64_t rows, int64_t D, float eps) {
+    if (rows < 0) return fail(SSM_ERR_BAD_SHAPE, "negative rows (%lld)", (long long)rows);
+    if (D < 1) return fail(SSM_ERR_BAD_SHAPE, "dim must be >= 1 (got %lld)", (long long)D);
+    if (D > kMaxWidth) return fail(SSM_ERR_UNSUPPORTED, "dim %lld exceeds 2^20", (long long)D);
+    if (!mul_ok(rows, 4 * D)) return fail(SSM_ERR_BAD_SHAPE, "sizes overflow");
+    if (!(eps > 0.0f) || !(eps < 1e30f)) return fail(SSM_ERR_BAD_SHAPE, "eps must be > 0");
+    return SSM_OK;
+}
+
+ssm_status_t ssm_add_rmsnorm_fwd(const ssm_add_norm_args_t *a, void *stream) {
+    if (!a) return fail(SSM_ERR_NULL_ARG, "args is NULL");
+    if (!io_ok(a->io_dtype) || !io_ok(a->res_dtype))
+        return fail(SSM_ERR_BAD_DTYPE, "io_dtype (%d) and res_dtype (%d) must be SSM_F32 or SSM_BF16", a->io_dtype,
+                    a->res_dtype);
+    ssm_status_t s = check_norm(a->rows, a->dim, a->eps);
+    if (s != SSM_OK) return s;
+    if (a->rows == 0) return ok();
+    if (!a->x) return fail(SSM_ERR_NULL_ARG, "x is NULL");
+    if (!a->w) return fail(SSM_ERR_NULL_ARG, "w is NULL");
+    if (!a->y) return fail(SSM_ERR_NULL_ARG, "y is NULL");
+    const int64_t D = a->dim, n = a->rows * D, es = io_bytes(a->io_dtype), rs = io_bytes(a->res_dtype);
+    const void *io[] = {a->x, a->y}, *res[] = {a->residual, a->res_out}, *f[] = {a->scale, a->post_w, a->w};
+    if ((s = check_align(io, COUNT(io), es, f, COUNT(f))) != SSM_OK) return s;
+    if ((s = check_align(res, COUNT(res), rs, nullptr, 0)) != SSM_OK) return s;
+    const Range in[] = {range(a->x, n, es, "x"), range(a->residual, n, rs, "residual"),
+                        range(a->scale, D, 4, "scale"), range(a->post_w, D, 4, "post_w"), range(a->w, D, 4, "w")};
+    const Range out[] = {range(a->res_out, n, rs, "res_out"), range(a->y, n, es, "y")};
+    s = check_overlaps(in, COUNT(in), out, COUNT(out), range(nullptr, 0, 1, ""), SameOk{a->res_out, a->residual});
+    if (s != SSM_OK) return s;
+    const hipError_t e = ssm::launch_add_norm_fwd(*a, static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return fail(SSM_ERR_HIP, "HIP error: %s", hipGetErrorString(e));
+    return ok();
+}
+
+size_t ssm_add_rmsnorm_bwd_workspace_size(const ssm_add_norm_bwd_args_t *a) {
+    if (!a || !io_ok(a->io_dtype) || !io_ok(a->res_dtype) || check_norm(a->rows, a->dim, 1.0f) != SSM_OK)
+        return (size_t)-1;
+    return a->rows > 0 ? ssm::add_norm_bwd_workspace_bytes(*a) : 0;
+}
+
+ssm_status_t ssm_add_rmsnorm_bwd(const ssm_add_norm_bwd_args_t *a, void *stream) {
+    if (!a) return fail(SSM_ERR_NULL_ARG, "args is NULL");
+    if (!io_ok(a->io_dtype) || !io_ok(a->res_dtype))
+        return fail(SSM_ERR_BAD_DTYPE, "io_dtype (%d) and res_dtype (%d) must be SSM_F32 or SSM_BF16", a->io_dtype,
+                    a->res_dtype);
+    ssm_status_t s = check_norm(a->rows, a->dim, a->eps);
+    if (s != SSM_OK) return s;
+    const bool work = a->rows > 0;
+    if (work) {
+        const struct { const void *p; const char *name; } req[] = {
+            {a->x, "x"}, {a->w, "w"}, {a->dy, "dy"}, {a->dx, "dx"}};
+        for (const auto &r : req)
+            if (!r.p) return fail(SSM_ERR_NULL_ARG, "%s is NULL", r.name);
+        if (a->dresidual && !a->residual) return fail(SSM_ERR_BAD_SHAPE, "dresidual given without residual");
+    }
+    if (!a->dw) return fail(SSM_ERR_NULL_ARG, "dw is NULL");
+    if (a->dscale && !a->scale) return fail(SSM_ERR_BAD_SHAPE, "dscale given without scale");
+    if (a->dpost_w && !a->post_w) return fail(SSM_ERR_BAD_SHAPE, "dpost_w given without post_w");
+    const int64_t D = a->dim, n = a->rows * D, es = io_bytes(a->io_dtype), rs = io_bytes(a->res_dtype);
+    const void *io[] = {a->x, a->dy, a->dx}, *res[] = {a->residual, a->dres_out, a->dresidual};
+    const void *f[] = {a->scale, a->post_w, a->w, a->dw, a->dscale, a->dpost_w};
+    if ((s = check_align(io, COUNT(io), es, f, COUNT(f))) != SSM_OK) return s;
+    if ((s = check_align(res, COUNT(res), rs, nullptr, 0)) != SSM_OK) return s;
+    const size_t need = work ? ssm::add_norm_bwd_workspace_bytes(*a) : 0;
+    if ((s = check_workspace(a->workspace, a->workspace_bytes, need)) != SSM_OK) return s;
+    const Range in[] = {range(a->x, n, es, "x"), range(a->residual, n, rs, "residual"),
+                        range(a->scale, D, 4, "scale"), range(a->post_w, D, 4, "post_w"), range(a->w, D, 4, "w"),
+                        range(a->dy, n, es, "dy"), range(a->dres_out, n, rs, "dres_out")};
+    const Range out[] = {range(a->dx, n, es, "dx"), range(a->dresidual, n, rs, "dresidual"),
+                         range(a->dw, D, 4, "dw"), range(a->dscale, D, 4, "dscale"),
+                         range(a->dpost_w, D, 4, "dpost_w")};
+    const Range ws = range(need ? a->workspace : nullptr, (int64_t)need, 1, "workspace");
+    s = check_overlaps(in, COUNT(in), out, COUNT(out), ws, SameOk{a->dresidual, a->dres_out});
+    if (s != SSM_OK) return s;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    hipError_t e = hipSuccess;
+    if (work) {
+        e = ssm::launch_add_norm_bwd(*a, st);
+    } else {
+        float *sums[] = {a->dw, a->dscale, a->dpost_w};
+        for (float *p : sums)
+            if (e == hipSuccess && p) e = ssm::launch_copy_or_zero(p, nullptr, D, st);
+    }
+    if (e != hipSuccess) return fail(SSM_ERR_HIP, "HIP error: %s", hipGetErrorString(e));
+    return ok();
+}
+
+static ssm_status_t check_gated_norm(int64_t rows, int64_t D, int64_t G, int32_t io, int32_t gate_first, float eps) {
+    if (!io_ok(io)) return fail(SSM_ERR_BAD_DTYPE, "io_dtype %d is not SSM_F32 or SSM_BF16", io);
+    const ssm_status_t s = check_norm(rows, D, eps);
+    if (s != SSM_OK) return s;
+    if (G < 1 || D % G != 0)
+        return fail(SSM_ERR_BAD_SHAPE, "groups (%lld) must divide dim (%lld)", (long long)G, (long long)D);
+    if (gate_first != 0 && gate_first != 1) return fail(SSM_ERR_UNSUPPORTED, "gate_first must be 0 or 1");
+    return SSM_OK;
+}
+
+ssm_status_t ssm_gated_rmsnorm_fwd(const ssm_gated_norm_args_t *a, void *stream) {
+    if (!a) return fail(SSM_ERR_NULL_ARG, "args is NULL");
+    ssm_status_t s = check_gated_norm(a->rows, a->dim, a->groups, a->io_dtype, a->gate_first, a->eps);
+    if (s != SSM_OK) return s;
+    if (a->rows == 0) return ok();
+    if (!a->x) return fail(SSM_ERR_NULL_ARG, "x is NULL");
+    if (!a->z) return fail(SSM_ERR_NULL_ARG, "z is NULL");
+    if (!a->w) return fail(SSM_ERR_NULL_ARG, "w is NULL");
+    if (!a->y) return fail(SSM_ERR_NULL_ARG, "y is NULL");
+    const int64_t D = a->dim, n = a->rows * D, es = io_bytes(a->io_dtype);
+    const void *io[] = {a->x, a->z, a->y}, *f[] = {a->w};
+    if ((s = check_align(io, COUNT(io), es, f, COUNT(f))) != SSM_OK) return s;
+    const Range in[] = {range(a->x, n, es, "x"), range(a->z, n, es, "z"), range(a->w, D, 4, "w")};
+    const Range out[] = {range(a->y, n, es, "y")};
+    s = check_overlaps(in, COUNT(in), out, COUNT(out), range(nullptr, 0, 1, ""), SameOk{a->y, a->x}, SameOk{a->y, a->z});
+    if (s != SSM_OK) return s;
+    const hipError_t e = ssm::launch_gated_norm_fwd(*a, static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return fail(SSM_ERR_HIP, "HIP error: %s", hipGetErrorString(e));
+    return ok();
+}
+
+size_t ssm_gated_rmsnorm_bwd_workspace_size(const ssm_gated_norm_bwd_args_t *a) {
+    if (!a || check_gated_norm(a->rows, a->dim, a->groups, a->io_dtype, 0, 1.0f) != SSM_OK) return (size_t)-1;
+    return a->rows > 0 ? ssm::gated_norm_bwd_workspace_bytes(*a) : 0;
+}
+
+ssm_status_t ssm_gated_rmsnorm_bwd(const ssm_gated_norm_bwd_args_t *a, void *stream) {
+    if (!a) return fail(SSM_ERR_NULL_ARG, "args is NULL");
+    ssm_status_t s = check_gated_norm(a->rows, a->dim, a->groups, a->io_dtype, a->gate_first, a->eps);
+    if (s != SSM_OK) return s;
+    const bool work = a->rows > 0;
+    if (work) {
+        const struct { const void *p; const char *name; } req[] = {
+            {a->x, "x"}, {a->z, "z"}, {a->w, "w"}, {a->dy, "dy"}, {a->dx, "dx"}, {a->dz, "dz"}};
+        for (const auto &r : req)
+            if (!r.p) return fail(SSM_ERR_NULL_ARG, "%s is NULL", r.name);
+    }
+    if (!a->dw) return fail(SSM_ERR_NULL_ARG, "dw is NULL");
+    const int64_t D = a->dim, n = a->rows * D, es = io_bytes(a->io_dtype);
+    const void *io[] = {a->x, a->z, a->dy, a->dx, a->dz}, *f[] = {a->w, a->dw};
+    if ((s = check_align(io, COUNT(io), es, f, COUNT(f))) != SSM_OK) return s;
+    const size_t need = work ? ssm::gated_norm_bwd_workspace_bytes(*a) : 0;
+    if ((s = check_workspace(a->workspace, a->workspace_bytes, need)) != SSM_OK) return s;
+    const Range in[] = {range(a->x, n, es, "x"), range(a->z, n, es, "z"), range(a->w, D, 4, "w"),
+                        range(a->dy, n, es, "dy")};
+    const Range out[] = {range(a->dx, n, es, "dx"), range(a->dz, n, es, "dz"), range(a->dw, D, 4, "dw")};
+    const Range ws = range(need ? a->workspace : nullptr, (int64_t)need, 1, "workspace");
+    if ((s = check_overlaps(in, COUNT(in), out, COUNT(out), ws)) != SSM_OK) return s;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    const hipError_t e = work ? ssm::launch_gated_norm_bwd(*a, st) : ssm::launch_copy_or_zero(a->dw, nullptr, D, st);
+    if (e != hipSuccess) return fail(SSM_ERR_HIP, "HIP error: %s", hipGetErrorString(e));
+    return ok();
+}
+
+}  // extern "C"

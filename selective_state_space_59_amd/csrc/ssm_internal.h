@@ -53,6 +53,24 @@ bool ssd_step_supported(int64_t dstate);
 hipError_t launch_ssd_step(const ssm_ssd_step_args_t &a, hipStream_t stream);
 hipError_t launch_ssd_fwd(const ssm_ssd_args_t &a, hipStream_t stream);
 
+// Gated recurrence (gated_scan.hip, gated_scan_bwd.hip).  Forward and backward take
+// batch, seqlen > 0; the step batch > 0.
+size_t gated_scan_workspace_bytes(const ssm_gated_scan_args_t &a);
+hipError_t launch_gated_scan_fwd(const ssm_gated_scan_args_t &a, hipStream_t stream);
+hipError_t launch_gated_step(const ssm_gated_step_args_t &a, hipStream_t stream);
+size_t gated_scan_bwd_workspace_bytes(const ssm_gated_scan_bwd_args_t &a);
+hipError_t launch_gated_scan_bwd(const ssm_gated_scan_bwd_args_t &a, hipStream_t stream);
+// out[i] = in ? in[i] : 0 for i < n (the state of an empty recurrence, the gradients of none).
+hipError_t launch_copy_or_zero(float *out, const float *in, int64_t n, hipStream_t stream);
+
+// Fused norms (norms.hip).  rows > 0 in the forward; the backward takes rows >= 0.
+hipError_t launch_add_norm_fwd(const ssm_add_norm_args_t &a, hipStream_t stream);
+size_t add_norm_bwd_workspace_bytes(const ssm_add_norm_bwd_args_t &a);
+hipError_t launch_add_norm_bwd(const ssm_add_norm_bwd_args_t &a, hipStream_t stream);
+hipError_t launch_gated_norm_fwd(const ssm_gated_norm_args_t &a, hipStream_t stream);
+size_t gated_norm_bwd_workspace_bytes(const ssm_gated_norm_bwd_args_t &a);
+hipError_t launch_gated_norm_bwd(const ssm_gated_norm_bwd_args_t &a, hipStream_t stream);
+
 // Copy or zero-fill the final state for an empty (L == 0) scan.
 hipError_t launch_empty_scan_state(const ssm_scan_args_t &a, hipStream_t stream);
 

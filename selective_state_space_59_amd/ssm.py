@@ -39,7 +39,12 @@ EXPORTED_SYMBOLS = ("ssm_selective_scan_workspace_size", "ssm_selective_scan_fwd
                     "ssm_selective_scan_bwd_workspace_size", "ssm_selective_scan_bwd",
                     "ssm_block_plan_create", "ssm_block_workspace_size", "ssm_block_fwd",
                     "ssm_block_plan_destroy", "ssm_ssd_fwd", "ssm_ssd_workspace_size",
-                    "ssm_ssd_step", "ssm_selective_scan_fwd_noalloc")
+                    "ssm_ssd_step", "ssm_selective_scan_fwd_noalloc",
+                    "ssm_gated_scan_workspace_size", "ssm_gated_scan_fwd",
+                    "ssm_gated_scan_bwd_workspace_size", "ssm_gated_scan_bwd", "ssm_gated_scan_step",
+                    "ssm_add_rmsnorm_fwd", "ssm_add_rmsnorm_bwd_workspace_size", "ssm_add_rmsnorm_bwd",
+                    "ssm_gated_rmsnorm_fwd", "ssm_gated_rmsnorm_bwd_workspace_size",
+                    "ssm_gated_rmsnorm_bwd")
 NOALLOC_SCRATCH_BYTES = 32 << 20
 
 _P = ctypes.c_void_p
@@ -110,6 +115,58 @@ class SsdStepArgs(ctypes.Structure):
                 ("z", _P), ("delta_bias", _P), ("y", _P)]
 
 
+class GatedScanArgs(ctypes.Structure):
+    """Mirror of ssm_gated_scan_args_t."""
+    _fields_ = [("batch", _I64), ("seqlen", _I64), ("dim", _I64), ("io_dtype", _I32), ("mode", _I32),
+                ("x", _P), ("gate", _P), ("in_gate", _P), ("A", _P), ("gate_bias", _P), ("in_bias", _P),
+                ("reset", _P), ("h0", _P), ("y", _P), ("h_final", _P), ("checkpoints", _P),
+                ("workspace", _P), ("workspace_bytes", ctypes.c_size_t)]
+
+
+class GatedScanBwdArgs(ctypes.Structure):
+    """Mirror of ssm_gated_scan_bwd_args_t."""
+    _fields_ = [("batch", _I64), ("seqlen", _I64), ("dim", _I64), ("io_dtype", _I32), ("mode", _I32),
+                ("x", _P), ("gate", _P), ("in_gate", _P), ("A", _P), ("gate_bias", _P), ("in_bias", _P),
+                ("reset", _P), ("h0", _P), ("dy", _P), ("dh_final", _P), ("checkpoints", _P),
+                ("dx", _P), ("dgate", _P), ("din_gate", _P), ("dA", _P), ("dgate_bias", _P),
+                ("din_bias", _P), ("dh0", _P), ("workspace", _P), ("workspace_bytes", ctypes.c_size_t)]
+
+
+class GatedStepArgs(ctypes.Structure):
+    """Mirror of ssm_gated_step_args_t."""
+    _fields_ = [("batch", _I64), ("dim", _I64), ("io_dtype", _I32), ("mode", _I32), ("state", _P),
+                ("x", _P), ("gate", _P), ("in_gate", _P), ("A", _P), ("gate_bias", _P), ("in_bias", _P),
+                ("reset", _P), ("y", _P)]
+
+
+class AddNormArgs(ctypes.Structure):
+    """Mirror of ssm_add_norm_args_t."""
+    _fields_ = [("rows", _I64), ("dim", _I64), ("io_dtype", _I32), ("res_dtype", _I32), ("x", _P),
+                ("residual", _P), ("scale", _P), ("post_w", _P), ("w", _P), ("res_out", _P), ("y", _P),
+                ("eps", ctypes.c_float)]
+
+
+class AddNormBwdArgs(ctypes.Structure):
+    """Mirror of ssm_add_norm_bwd_args_t."""
+    _fields_ = [("rows", _I64), ("dim", _I64), ("io_dtype", _I32), ("res_dtype", _I32), ("x", _P),
+                ("residual", _P), ("scale", _P), ("post_w", _P), ("w", _P), ("dy", _P), ("dres_out", _P),
+                ("dx", _P), ("dresidual", _P), ("dw", _P), ("dscale", _P), ("dpost_w", _P),
+                ("workspace", _P), ("workspace_bytes", ctypes.c_size_t), ("eps", ctypes.c_float)]
+
+
+class GatedNormArgs(ctypes.Structure):
+    """Mirror of ssm_gated_norm_args_t."""
+    _fields_ = [("rows", _I64), ("dim", _I64), ("groups", _I64), ("io_dtype", _I32), ("gate_first", _I32),
+                ("x", _P), ("z", _P), ("w", _P), ("y", _P), ("eps", ctypes.c_float)]
+
+
+class GatedNormBwdArgs(ctypes.Structure):
+    """Mirror of ssm_gated_norm_bwd_args_t."""
+    _fields_ = [("rows", _I64), ("dim", _I64), ("groups", _I64), ("io_dtype", _I32), ("gate_first", _I32),
+                ("x", _P), ("z", _P), ("w", _P), ("dy", _P), ("dx", _P), ("dz", _P), ("dw", _P),
+                ("workspace", _P), ("workspace_bytes", ctypes.c_size_t), ("eps", ctypes.c_float)]
+
+
 class SSMError(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__(message)
@@ -161,6 +218,16 @@ def lib() -> ctypes.CDLL:
         L.ssm_ssd_step.argtypes = [ctypes.POINTER(SsdStepArgs), _P]
         L.ssm_ssd_step.restype = ctypes.c_int
         L.ssm_ssd_workspace_size.restype = ctypes.c_size_t
+        for name, args in (("gated_scan_fwd", GatedScanArgs), ("gated_scan_bwd", GatedScanBwdArgs),
+                           ("gated_scan_step", GatedStepArgs), ("add_rmsnorm_fwd", AddNormArgs),
+                           ("add_rmsnorm_bwd", AddNormBwdArgs), ("gated_rmsnorm_fwd", GatedNormArgs),
+                           ("gated_rmsnorm_bwd", GatedNormBwdArgs)):
+            f = getattr(L, "ssm_" + name)
+            f.argtypes, f.restype = [ctypes.POINTER(args), _P], ctypes.c_int
+        for name, args in (("gated_scan", GatedScanArgs), ("gated_scan_bwd", GatedScanBwdArgs),
+                           ("add_rmsnorm_bwd", AddNormBwdArgs), ("gated_rmsnorm_bwd", GatedNormBwdArgs)):
+            f = getattr(L, "ssm_%s_workspace_size" % name)
+            f.argtypes, f.restype = [ctypes.POINTER(args)], ctypes.c_size_t
         _lib = L
     return _lib
 
@@ -759,3 +826,395 @@ def ssd_step_args(state, x, delta, A, Bm, Cm, Dskip=None, z=None, delta_bias=Non
                     delta=_ptr(delta), A=_ptr(A), Bm=_ptr(Bm), Cm=_ptr(Cm), Dskip=_ptr(Dskip),
                     z=_ptr(z), delta_bias=_ptr(delta_bias), y=_ptr(y))
     return a, y
+
+
+# ------------------------------------------------------------------ gated linear recurrence
+GATE_MODES = {"decay": 0, "sigmoid": 1, "rate": 2}  # ssm_gate_mode_t
+GATED_BLOCK = 128  # SSM_GATED_BLOCK
+_NO_SIZE = ctypes.c_size_t(-1).value
+
+
+def gated_checkpoint_shape(batch: int, seqlen: int, dim: int) -> tuple:
+    """Shape of the fp32 checkpoint tensor of gated_scan_fwd: the state entering every
+    GATED_BLOCK-step block, (ceil(L / GATED_BLOCK), B, D)."""
+    return ((seqlen + GATED_BLOCK - 1) // GATED_BLOCK, batch, dim)
+
+
+def _call(fn, args, dev: torch.device):
+    """One library call on torch's current stream of `dev`, with that device current."""
+    if dev.index == torch.cuda.current_device():
+        return fn(ctypes.byref(args), _stream(dev))
+    with torch.cuda.device(dev):
+        return fn(ctypes.byref(args), _stream(dev))
+
+
+def _run(name: str, args, dev: torch.device, size_fn=None, workspace: Optional[torch.Tensor] = None):
+    """ssm_<name>(args), with a workspace where size_fn(args) asks for one.  Invalid sizes are
+    reported by the call itself, which checks its arguments before anything is launched."""
+    L = lib()
+    fn = getattr(L, name)
+    if size_fn is not None:
+        need = getattr(L, size_fn)(ctypes.byref(args))
+        if need != _NO_SIZE and need > 0:
+            ws = workspace if workspace is not None else _workspace(dev, need)
+            if ws.device != dev or not ws.is_contiguous() or ws.numel() * ws.element_size() < need:
+                raise ValueError("workspace must be a contiguous tensor on %s of >= %d bytes" % (dev, need))
+            args.workspace = ws.data_ptr()
+            args.workspace_bytes = ws.numel() * ws.element_size()
+    status = _call(fn, args, dev)
+    if status != SSM_OK:
+        _check(status, name)
+
+
+def _gpu(t, name: str, dims: int, shape: str) -> torch.device:
+    if not isinstance(t, torch.Tensor) or t.dim() != dims or t.device.type != "cuda":
+        raise ValueError("%s must be a %s GPU tensor" % (name, shape))
+    return t.device
+
+
+def _gates(a, x, gate, mode, A, in_gate, gate_bias, in_bias, dev):
+    """Check the gate inputs against x's shape and put them into `a`."""
+    if mode not in GATE_MODES:
+        raise ValueError("mode must be one of %s, got %r" % (", ".join(GATE_MODES), mode))
+    f32, D = torch.float32, x.shape[-1]
+    a.io_dtype, a.mode = _io_code(x.dtype), GATE_MODES[mode]
+    a.x = _ptr(_req(x, "x", x.shape, x.dtype, dev))
+    a.gate = _ptr(_req(gate, "gate", x.shape, x.dtype, dev))
+    a.in_gate = _ptr(_opt(in_gate, "in_gate", x.shape, x.dtype, dev))
+    a.A = _ptr(_opt(A, "A", (D,), f32, dev))
+    a.gate_bias = _ptr(_opt(gate_bias, "gate_bias", (D,), f32, dev))
+    a.in_bias = _ptr(_opt(in_bias, "in_bias", (D,), f32, dev))
+
+
+def _resets(reset, shape, dev):
+    """A reset mask as the library's bytes: uint8, or bool (the same bytes, 0 or 1)."""
+    if reset is None:
+        return None
+    if isinstance(reset, torch.Tensor) and reset.dtype == torch.bool:
+        reset = reset.view(torch.uint8)
+    return _ptr(_opt(reset, "reset", shape, torch.uint8, dev))
+
+
+def gated_scan_fwd(x: torch.Tensor, gate: torch.Tensor, mode: str = "rate",
+                   A: Optional[torch.Tensor] = None, in_gate: Optional[torch.Tensor] = None,
+                   gate_bias: Optional[torch.Tensor] = None, in_bias: Optional[torch.Tensor] = None,
+                   reset: Optional[torch.Tensor] = None, h0: Optional[torch.Tensor] = None,
+                   return_final_state: bool = False, y: Optional[torch.Tensor] = None,
+                   h_final: Optional[torch.Tensor] = None, checkpoints: Optional[torch.Tensor] = None,
+                   workspace: Optional[torch.Tensor] = None):
+    """ssm_gated_scan_fwd: h_t = a_t h_{t-1} + b_t per channel.  x, gate, in_gate: (B, L, D) bf16
+    or fp32; A, gate_bias, in_bias: (D,) fp32; reset: (B, L) uint8 or bool; h0: (B, D) fp32.
+
+    mode "decay": a = gate, b = x.  "sigmoid": s = sigmoid(gate + gate_bias), a = 1 - s, b = s x.
+    "rate": a = exp(A sigmoid(gate + gate_bias)), b = sqrt(1 - a^2) sigmoid(in_gate + in_bias) x.
+
+    Returns (y, h_final or None).  A float32 tensor `checkpoints` of gated_checkpoint_shape(B, L, D)
+    also receives the state entering every GATED_BLOCK-step block, for gated_scan_bwd."""
+    dev = _gpu(x, "x", 3, "(B, L, D)")
+    B, L, D = x.shape
+    f32 = torch.float32
+    a = GatedScanArgs(batch=B, seqlen=L, dim=D)
+    _gates(a, x, gate, mode, A, in_gate, gate_bias, in_bias, dev)
+    a.reset = _resets(reset, (B, L), dev)
+    a.h0 = _ptr(_opt(h0, "h0", (B, D), f32, dev))
+    if y is None:
+        y = torch.empty_like(x)
+    a.y = _ptr(_req(y, "y", (B, L, D), x.dtype, dev))
+    if h_final is None and return_final_state:
+        h_final = torch.empty((B, D), device=dev, dtype=f32)
+    a.h_final = _ptr(_opt(h_final, "h_final", (B, D), f32, dev))
+    a.checkpoints = _ptr(_opt(checkpoints, "checkpoints", gated_checkpoint_shape(B, L, D), f32, dev))
+    _run("ssm_gated_scan_fwd", a, dev, "ssm_gated_scan_workspace_size", workspace)
+    return y, h_final
+
+
+def gated_scan_bwd(x: torch.Tensor, gate: torch.Tensor, dy: torch.Tensor, mode: str = "rate",
+                   A: Optional[torch.Tensor] = None, in_gate: Optional[torch.Tensor] = None,
+                   gate_bias: Optional[torch.Tensor] = None, in_bias: Optional[torch.Tensor] = None,
+                   reset: Optional[torch.Tensor] = None, h0: Optional[torch.Tensor] = None,
+                   dh_final: Optional[torch.Tensor] = None, checkpoints: Optional[torch.Tensor] = None,
+                   workspace: Optional[torch.Tensor] = None) -> dict:
+    """ssm_gated_scan_bwd: the gradients of gated_scan_fwd for dL/dy = dy, dL/dh_final = dh_final.
+    `checkpoints` are the ones a gated_scan_fwd call with the same inputs wrote (else the backward
+    recomputes them).
+
+    Returns a dict with dx, dgate (x's dtype) and, for the inputs given, din_gate (x's dtype), dA,
+    dgate_bias, din_bias, dh0 (float32)."""
+    dev = _gpu(x, "x", 3, "(B, L, D)")
+    B, L, D = x.shape
+    f32 = dict(device=dev, dtype=torch.float32)
+    a = GatedScanBwdArgs(batch=B, seqlen=L, dim=D)
+    _gates(a, x, gate, mode, A, in_gate, gate_bias, in_bias, dev)
+    a.reset = _resets(reset, (B, L), dev)
+    a.h0 = _ptr(_opt(h0, "h0", (B, D), torch.float32, dev))
+    a.dy = _ptr(_req(dy, "dy", (B, L, D), x.dtype, dev))
+    a.dh_final = _ptr(_opt(dh_final, "dh_final", (B, D), torch.float32, dev))
+    a.checkpoints = _ptr(_opt(checkpoints, "checkpoints", gated_checkpoint_shape(B, L, D), torch.float32, dev))
+    out = dict(dx=torch.empty_like(x), dgate=torch.empty_like(x))
+    if in_gate is not None:
+        out["din_gate"] = torch.empty_like(x)
+    for name, given in (("dA", mode == "rate"), ("dgate_bias", gate_bias is not None),
+                        ("din_bias", in_bias is not None)):
+        if given:
+            out[name] = torch.empty(D, **f32)
+    if h0 is not None:
+        out["dh0"] = torch.empty(B, D, **f32)
+    for name, t in out.items():
+        setattr(a, name, t.data_ptr())
+    _run("ssm_gated_scan_bwd", a, dev, "ssm_gated_scan_bwd_workspace_size", workspace)
+    return out
+
+
+def gated_scan_step(state: torch.Tensor, x: torch.Tensor, gate: torch.Tensor, mode: str = "rate",
+                    A: Optional[torch.Tensor] = None, in_gate: Optional[torch.Tensor] = None,
+                    gate_bias: Optional[torch.Tensor] = None, in_bias: Optional[torch.Tensor] = None,
+                    reset: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """ssm_gated_scan_step: one decode token; advances `state` (B, D) fp32 in place and returns
+    y (B, D).  x, gate, in_gate: (B, D) bf16 or fp32; reset: (B,) uint8 or bool, rows whose state
+    is taken as 0 (a new sequence); the rest as in gated_scan_fwd."""
+    a, y = gated_scan_step_args(state, x, gate, mode, A, in_gate, gate_bias, in_bias, reset, y)
+    status = _call(lib().ssm_gated_scan_step, a, state.device)
+    if status != SSM_OK:
+        _check(status, "ssm_gated_scan_step")
+    return y
+
+
+def gated_scan_step_args(state, x, gate, mode="rate", A=None, in_gate=None, gate_bias=None, in_bias=None,
+                         reset=None, y=None):
+    """The checked ssm_gated_step_args_t of a gated_scan_step call, and its y (allocated when not
+    given), for callers that launch the same step repeatedly through lib().ssm_gated_scan_step.
+    The tensors must outlive the struct."""
+    dev = _gpu(state, "state", 2, "(B, D) float32")
+    B, D = state.shape
+    if not isinstance(x, torch.Tensor) or x.shape != state.shape:
+        raise ValueError("x must be a %s tensor like the state" % (tuple(state.shape),))
+    a = GatedStepArgs(batch=B, dim=D)
+    a.state = _ptr(_req(state, "state", (B, D), torch.float32, dev))
+    _gates(a, x, gate, mode, A, in_gate, gate_bias, in_bias, dev)
+    a.reset = _resets(reset, (B,), dev)
+    if y is None:
+        y = torch.empty_like(x)
+    a.y = _ptr(_req(y, "y", (B, D), x.dtype, dev))
+    return a, y
+
+
+class _GatedScanFn(torch.autograd.Function):
+    """gated_scan as a torch autograd function: the forward writes the checkpoints, the
+    backward reads them (ssm_gated_scan_fwd / _bwd)."""
+
+    @staticmethod
+    def forward(ctx, x, gate, A, in_gate, gate_bias, in_bias, h0, mode, reset):
+        _gpu(x, "x", 3, "(B, L, D)")
+        ck = None
+        if any(ctx.needs_input_grad):
+            ck = torch.empty(gated_checkpoint_shape(*x.shape), device=x.device, dtype=torch.float32)
+        y, hf = gated_scan_fwd(x, gate, mode, A=A, in_gate=in_gate, gate_bias=gate_bias, in_bias=in_bias,
+                               reset=reset, h0=h0, return_final_state=True, checkpoints=ck)
+        ctx.save_for_backward(x, gate, A, in_gate, gate_bias, in_bias, h0, reset, ck)
+        ctx.mode = mode
+        return y, hf
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy, dh_final):
+        x, gate, A, in_gate, gate_bias, in_bias, h0, reset, ck = ctx.saved_tensors
+        g = gated_scan_bwd(x, gate, dy.contiguous(), ctx.mode, A=A, in_gate=in_gate, gate_bias=gate_bias,
+                           in_bias=in_bias, reset=reset, h0=h0, dh_final=dh_final.contiguous(), checkpoints=ck)
+        return (g["dx"], g["dgate"], g.get("dA"), g.get("din_gate"), g.get("dgate_bias"), g.get("din_bias"),
+                g.get("dh0"), None, None)
+
+
+def gated_scan(x: torch.Tensor, gate: torch.Tensor, mode: str = "rate", A: Optional[torch.Tensor] = None,
+               in_gate: Optional[torch.Tensor] = None, gate_bias: Optional[torch.Tensor] = None,
+               in_bias: Optional[torch.Tensor] = None, reset: Optional[torch.Tensor] = None,
+               h0: Optional[torch.Tensor] = None):
+    """The gated recurrence as a differentiable torch op (arguments as in gated_scan_fwd): returns
+    (y, h_final), and backward() runs ssm_gated_scan_bwd from the checkpoints the forward kept.
+
+    To capture a backward() into a graph, capture it on leaves that no earlier, still living
+    autograd graph has used (torch's own rule for gradient accumulation under capture)."""
+    return _GatedScanFn.apply(x, gate, A, in_gate, gate_bias, in_bias, h0, mode, reset)
+
+
+# ----------------------------------------------------------------------------- fused norms
+def _add_norm(a, x, w, residual, scale, post_w, eps, dev):
+    R, D = x.shape
+    f32 = torch.float32
+    a.rows, a.dim, a.eps = R, D, float(eps)
+    a.io_dtype = _io_code(x.dtype)
+    res_dtype = x.dtype
+    if residual is not None:
+        if not isinstance(residual, torch.Tensor):
+            raise TypeError("residual must be a torch.Tensor")
+        res_dtype = residual.dtype
+    a.res_dtype = _io_code(res_dtype)
+    a.x = _ptr(_req(x, "x", (R, D), x.dtype, dev))
+    a.w = _ptr(_req(w, "w", (D,), f32, dev))
+    a.residual = _ptr(_opt(residual, "residual", (R, D), res_dtype, dev))
+    a.scale = _ptr(_opt(scale, "scale", (D,), f32, dev))
+    a.post_w = _ptr(_opt(post_w, "post_w", (D,), f32, dev))
+    return res_dtype
+
+
+def _rows_of(t, shape, name):
+    """A (..., D) tensor as (rows, D): a view, so it has to be contiguous."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return t if t.dim() == 2 else t.view(-1, shape[-1]) if t.numel() else t.new_empty((0, shape[-1]))
+
+
+def _shape_of(x):
+    if not isinstance(x, torch.Tensor) or x.dim() < 1 or x.device.type != "cuda" or x.shape[-1] < 1:
+        raise ValueError("x must be a (..., D) GPU tensor")
+    return x.shape
+
+
+def add_rmsnorm_fwd(x: torch.Tensor, w: torch.Tensor, residual: Optional[torch.Tensor] = None,
+                    scale: Optional[torch.Tensor] = None, post_w: Optional[torch.Tensor] = None,
+                    eps: float = 1e-5, y: Optional[torch.Tensor] = None,
+                    res_out: Optional[torch.Tensor] = None):
+    """ssm_add_rmsnorm_fwd: u = x, or RMSNorm(x) * post_w; res_out = residual + scale * u;
+    y = RMSNorm(res_out) * w.  x: (..., D) bf16 or fp32; residual: x's shape, bf16 or fp32 (the
+    residual stream keeps its dtype; without one res_out has x's); w, scale, post_w: (D,) fp32.
+    `res_out` may be `residual` (updated in place).  Returns (y, res_out)."""
+    shape = _shape_of(x)
+    dev = x.device
+    a = AddNormArgs()
+    res_dtype = _add_norm(a, _rows_of(x, shape, "x"), w, _rows_of(residual, shape, "residual"), scale, post_w,
+                          eps, dev)
+    if y is None:
+        y = torch.empty_like(x)
+    if res_out is None:
+        res_out = torch.empty(shape, device=dev, dtype=res_dtype)
+    a.y = _ptr(_req(y, "y", shape, x.dtype, dev))
+    a.res_out = _ptr(_req(res_out, "res_out", shape, res_dtype, dev))
+    _run("ssm_add_rmsnorm_fwd", a, dev)
+    return y, res_out
+
+
+def add_rmsnorm_bwd(x: torch.Tensor, w: torch.Tensor, residual: Optional[torch.Tensor], dy: torch.Tensor,
+                    dres_out: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None,
+                    post_w: Optional[torch.Tensor] = None, eps: float = 1e-5,
+                    workspace: Optional[torch.Tensor] = None) -> dict:
+    """ssm_add_rmsnorm_bwd: the gradients of add_rmsnorm_fwd on the same x and residual (the
+    residual before an in-place update) for dL/dy = dy and dL/dres_out = dres_out.
+
+    Returns a dict with dx (x's dtype), dw and, for the inputs given, dresidual (residual's dtype),
+    dscale, dpost_w (float32)."""
+    shape = _shape_of(x)
+    dev = x.device
+    a = AddNormBwdArgs()
+    res_dtype = _add_norm(a, _rows_of(x, shape, "x"), w, _rows_of(residual, shape, "residual"), scale, post_w,
+                          eps, dev)
+    a.dy = _ptr(_req(dy, "dy", shape, x.dtype, dev))
+    a.dres_out = _ptr(_opt(dres_out, "dres_out", shape, res_dtype, dev))
+    out = dict(dx=torch.empty_like(x), dw=torch.empty_like(w))
+    if residual is not None:
+        out["dresidual"] = torch.empty_like(residual)
+    if scale is not None:
+        out["dscale"] = torch.empty_like(w)
+    if post_w is not None:
+        out["dpost_w"] = torch.empty_like(w)
+    for name, t in out.items():
+        setattr(a, name, t.data_ptr())
+    _run("ssm_add_rmsnorm_bwd", a, dev, "ssm_add_rmsnorm_bwd_workspace_size", workspace)
+    return out
+
+
+class _AddNormFn(torch.autograd.Function):
+    """add_rmsnorm as a torch autograd function (ssm_add_rmsnorm_fwd / _bwd)."""
+
+    @staticmethod
+    def forward(ctx, x, w, residual, scale, post_w, eps):
+        y, r = add_rmsnorm_fwd(x, w, residual, scale=scale, post_w=post_w, eps=eps)
+        ctx.save_for_backward(x, w, residual, scale, post_w)
+        ctx.eps = eps
+        return y, r
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy, dres_out):
+        x, w, residual, scale, post_w = ctx.saved_tensors
+        g = add_rmsnorm_bwd(x, w, residual, dy.contiguous(), dres_out.contiguous(), scale=scale, post_w=post_w,
+                            eps=ctx.eps)
+        return g["dx"], g["dw"], g.get("dresidual"), g.get("dscale"), g.get("dpost_w"), None
+
+
+def add_rmsnorm(x: torch.Tensor, w: torch.Tensor, residual: Optional[torch.Tensor] = None,
+                scale: Optional[torch.Tensor] = None, post_w: Optional[torch.Tensor] = None,
+                eps: float = 1e-5):
+    """The fused residual sum and norm as a differentiable torch op (arguments as in
+    add_rmsnorm_fwd): returns (y, res_out)."""
+    return _AddNormFn.apply(x, w, residual, scale, post_w, eps)
+
+
+def _gated_norm(a, x, z, w, groups, gate_first, eps, shape, dev):
+    D = shape[-1]
+    a.rows, a.dim, a.groups, a.eps = x.numel() // D, D, int(groups), float(eps)
+    a.io_dtype, a.gate_first = _io_code(x.dtype), int(bool(gate_first))
+    a.x = _ptr(_req(x, "x", shape, x.dtype, dev))
+    a.z = _ptr(_req(z, "z", shape, x.dtype, dev))
+    a.w = _ptr(_req(w, "w", (D,), torch.float32, dev))
+
+
+def gated_rmsnorm_fwd(x: torch.Tensor, z: torch.Tensor, w: torch.Tensor, groups: int = 1,
+                      gate_first: bool = True, eps: float = 1e-5,
+                      y: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """ssm_gated_rmsnorm_fwd: with gate_first RMSNorm(x * silu(z)) * w, else RMSNorm(x) * w * silu(z),
+    the mean square over each of `groups` groups of D / groups consecutive channels.  x, z: (..., D)
+    bf16 or fp32; w: (D,) fp32.  `y` may be x or z."""
+    shape = _shape_of(x)
+    dev = x.device
+    a = GatedNormArgs()
+    _gated_norm(a, x, z, w, groups, gate_first, eps, shape, dev)
+    if y is None:
+        y = torch.empty_like(x)
+    a.y = _ptr(_req(y, "y", shape, x.dtype, dev))
+    _run("ssm_gated_rmsnorm_fwd", a, dev)
+    return y
+
+
+def gated_rmsnorm_bwd(x: torch.Tensor, z: torch.Tensor, w: torch.Tensor, dy: torch.Tensor, groups: int = 1,
+                      gate_first: bool = True, eps: float = 1e-5,
+                      workspace: Optional[torch.Tensor] = None) -> dict:
+    """ssm_gated_rmsnorm_bwd: the gradients of gated_rmsnorm_fwd for dL/dy = dy.  Returns a dict
+    with dx, dz (x's dtype) and dw (float32)."""
+    shape = _shape_of(x)
+    dev = x.device
+    a = GatedNormBwdArgs()
+    _gated_norm(a, x, z, w, groups, gate_first, eps, shape, dev)
+    a.dy = _ptr(_req(dy, "dy", shape, x.dtype, dev))
+    out = dict(dx=torch.empty_like(x), dz=torch.empty_like(z), dw=torch.empty_like(w))
+    for name, t in out.items():
+        setattr(a, name, t.data_ptr())
+    _run("ssm_gated_rmsnorm_bwd", a, dev, "ssm_gated_rmsnorm_bwd_workspace_size", workspace)
+    return out
+
+
+class _GatedNormFn(torch.autograd.Function):
+    """gated_rmsnorm as a torch autograd function (ssm_gated_rmsnorm_fwd / _bwd)."""
+
+    @staticmethod
+    def forward(ctx, x, z, w, groups, gate_first, eps):
+        ctx.save_for_backward(x, z, w)
+        ctx.opts = dict(groups=groups, gate_first=gate_first, eps=eps)
+        return gated_rmsnorm_fwd(x, z, w, **ctx.opts)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        x, z, w = ctx.saved_tensors
+        g = gated_rmsnorm_bwd(x, z, w, dy.contiguous(), **ctx.opts)
+        return g["dx"], g["dz"], g["dw"], None, None, None
+
+
+def gated_rmsnorm(x: torch.Tensor, z: torch.Tensor, w: torch.Tensor, groups: int = 1, gate_first: bool = True,
+                  eps: float = 1e-5) -> torch.Tensor:
+    """The gated norm as a differentiable torch op (arguments as in gated_rmsnorm_fwd)."""
+    return _GatedNormFn.apply(x, z, w, groups, gate_first, eps)

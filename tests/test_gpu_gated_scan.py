@@ -1,0 +1,382 @@
+"""The gated recurrence on the GPU against its fp64 definition (needs an MI355X): forward,
+backward, decode step; every gate mode, both I/O types, one token to long rows, odd widths,
+resets, states handed over, special values, empty calls."""
+import numpy as np
+import pytest
+import torch
+
+import selective_state_space_59_amd as ssm
+from oracle import recurrent as R
+from tests.recurrent_helpers import check, f64, scan_case, scan_case64
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+BF, F32 = torch.bfloat16, torch.float32
+MODES = ("decay", "sigmoid", "rate")
+SHAPES = [(1, 1, 1), (2, 3, 5), (1, 17, 64), (3, 127, 33), (2, 128, 72), (1, 129, 65), (2, 255, 40),
+          (1, 256, 8), (2, 257, 96), (1, 700, 130), (2, 1025, 24), (1, 5000, 40), (70, 5, 7)]
+
+
+def _fwd(k, **kw):
+    return ssm.gated_scan_fwd(return_final_state=True, **k, **kw)
+
+
+def _check_fwd(k, what):
+    B, L, D = k["x"].shape
+    ck = torch.full(ssm.gated_checkpoint_shape(B, L, D), float("nan"), device=DEV)
+    y, hf = _fwd(k, checkpoints=ck)
+    torch.cuda.synchronize()
+    H, _, E = R.gated_scan(**scan_case64(k))
+    check(y, H, E, what + " y")
+    check(hf, H[:, -1], E[:, -1], what + " h_final")
+    first = np.zeros((B, D)) if "h0" not in k else f64(k["h0"])
+    for j in range(ck.shape[0]):
+        t = j * ssm.ssm.GATED_BLOCK
+        check(ck[j], first if j == 0 else H[:, t - 1], np.zeros((B, D)) if j == 0 else E[:, t - 1],
+              "%s checkpoint %d" % (what, j))
+    return ck
+
+
+def _check_bwd(k, what, ck=None, dhf=True, seed=5):
+    g = torch.Generator().manual_seed(seed)
+    dy = torch.randn(k["x"].shape, generator=g).to(k["x"].dtype).to(DEV)
+    dh = torch.randn(k["x"].shape[0], k["x"].shape[2], generator=g).to(DEV) if dhf else None
+    got = ssm.gated_scan_bwd(dy=dy, dh_final=dh, checkpoints=ck, **k)
+    torch.cuda.synchronize()
+    ref = R.gated_scan_bwd(dy=f64(dy), dh_final=f64(dh), **scan_case64(k))
+    assert set(got) == set(ref), (set(got), set(ref))
+    for name, (v, e) in ref.items():
+        check(got[name], v, e, "%s %s" % (what, name))
+    return got
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("mode", MODES)
+@pytest.mark.parametrize("B,L,D", SHAPES)
+def test_forward_and_backward(mode, B, L, D, dtype):
+    k = scan_case(mode, B, L, D, dtype, seed=B + 3 * L + 7 * D, doc=50 if L > 100 else 3, h0=D % 2 == 0,
+                  bias=D % 3 != 0, in_gate=D % 5 != 0)
+    what = "%s B=%d L=%d D=%d" % (mode, B, L, D)
+    print(what, flush=True)
+    ck = _check_fwd(k, what)
+    got = _check_bwd(k, what, ck)
+    own = _check_bwd(k, what + " without checkpoints")
+    for name in got:
+        assert torch.equal(got[name], own[name]), name  # the same states, recomputed
+
+
+@pytest.mark.parametrize("mode", MODES)
+def test_without_resets_state_or_final_gradient(mode):
+    k = scan_case(mode, 2, 600, 40, F32, seed=3, h0=False, bias=False, in_gate=False)
+    _check_bwd(k, mode, _check_fwd(k, mode), dhf=False)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+def test_pointers_at_any_element_offset(dtype):
+    """Tensors that begin one element into an allocation (no wide alignment), odd width."""
+    k = scan_case("rate", 2, 300, 67, dtype, seed=11, doc=40)
+
+    def shifted(t):
+        if not isinstance(t, torch.Tensor):
+            return t
+        buf = torch.empty(t.numel() + 1, dtype=t.dtype, device=DEV)
+        buf[1:] = t.reshape(-1)
+        return buf[1:].view(t.shape)
+
+    s = {m: shifted(v) for m, v in k.items()}
+    _check_bwd(s, "shifted", _check_fwd(s, "shifted"))
+    assert torch.equal(_fwd(s)[0], _fwd(k)[0])
+
+
+def test_every_step_a_reset_and_none():
+    for value in (0, 1, 255):
+        k = scan_case("sigmoid", 2, 400, 64, F32, seed=13)
+        k["reset"] = torch.full((2, 400), value, dtype=torch.uint8, device=DEV)
+        _check_bwd(k, "reset %d" % value, _check_fwd(k, "reset %d" % value))
+    kb = dict(k, reset=k["reset"] != 0)
+    assert torch.equal(_fwd(kb)[0], _fwd(k)[0])
+
+
+@pytest.mark.parametrize("mode", MODES)
+def test_a_reset_keeps_infinities_and_nans_out(mode):
+    """Values before a reset, and the state ahead of a first-step reset, leave no trace behind
+    it: the rows come out as without them, bit for bit.  The NaNs include the one whose bits are
+    all set."""
+    L, cut = 1300, 777
+    k = scan_case(mode, 1, L, 40, F32, seed=17, doc=0)
+    k["reset"] = torch.zeros(1, L, dtype=torch.uint8, device=DEV)
+    k["reset"][0, cut] = 1
+    want, hf = _fwd(k)
+    bad = dict(k, x=k["x"].clone(), gate=k["gate"].clone(), h0=k["h0"].clone())
+    ones = torch.tensor([-1], dtype=torch.int32, device=DEV).view(torch.float32)
+    bad["x"][0, 5, :10] = float("inf")
+    bad["x"][0, 600, 10:20] = float("nan")
+    bad["x"][0, 300, 20:25] = ones
+    bad["gate"][0, 100, 25:30] = ones
+    bad["h0"][0, 30:33] = float("-inf")
+    bad["h0"][0, 33:36] = ones
+    got, hg = _fwd(bad)
+    torch.cuda.synchronize()
+    assert torch.equal(got[:, cut:], want[:, cut:]) and torch.equal(hg, hf)
+    assert not torch.isfinite(got[0, 600:cut, :36]).any()
+    assert torch.equal(got[:, :cut, 36:], want[:, :cut, 36:])
+    # and the gradients behind the reset do not see what lies before it
+    dy = torch.randn_like(k["x"])
+    a, b = ssm.gated_scan_bwd(dy=dy, **k), ssm.gated_scan_bwd(dy=dy, **bad)
+    for n in ("dx", "dgate"):
+        assert torch.equal(a[n][:, cut:], b[n][:, cut:]), n
+
+
+def test_nan_gradients_do_not_cross_a_reset():
+    k = scan_case("decay", 1, 900, 40, F32, seed=19, h0=True)
+    k["reset"] = torch.zeros(1, 900, dtype=torch.uint8, device=DEV)
+    k["reset"][0, 500] = 1
+    dy = torch.randn_like(k["x"])
+    want = ssm.gated_scan_bwd(dy=dy, **k)
+    dy[0, 600:, :7] = torch.tensor([-1], dtype=torch.int32, device=DEV).view(torch.float32)
+    got = ssm.gated_scan_bwd(dy=dy, **k)
+    torch.cuda.synchronize()
+    assert torch.equal(got["dx"][:, :500], want["dx"][:, :500])
+    assert torch.equal(got["dh0"], want["dh0"])
+    assert got["dx"][0, 500:, :7].isnan().all()
+
+
+@pytest.mark.parametrize("mode", ["sigmoid", "rate"])
+def test_saturated_gates(mode):
+    """Gates at the far ends, infinities included: decays of exactly 0 and 1."""
+    k = scan_case(mode, 1, 300, 40, F32, seed=23, bias=False)
+    k["gate"][:, :, 0] = float("inf")
+    k["gate"][:, :, 1] = float("-inf")
+    k["gate"][:, :, 2] = 200.0
+    k["gate"][:, :, 3] = -200.0
+    k["gate"][:, :, 4] = torch.finfo(torch.float32).min
+    if mode == "rate":
+        k["A"][5] = 0.0
+        k["A"][6] = -200.0
+        k["A"][0] = -float("inf")  # decay 0 at r = 1
+    y, hf = _fwd(k)
+    g = ssm.gated_scan_bwd(dy=torch.ones_like(k["x"]), **k)
+    torch.cuda.synchronize()
+    sel = [i for i in range(40) if not (mode == "rate" and i == 0)]
+    k64 = scan_case64(k)
+    for n in ("x", "gate", "in_gate"):
+        if n in k64:
+            k64[n] = np.clip(k64[n][:, :, sel], -1e4, 1e4)  # (the bound counts |v|)
+    for n in ("h0", "A"):
+        if n in k64:
+            k64[n] = k64[n][..., sel]
+    H, _, E = R.gated_scan(**k64)
+    check(y[:, :, sel], H, E, "y")
+    assert torch.isfinite(y).all() and torch.isfinite(hf).all()
+    for n, t in g.items():
+        if mode == "rate":
+            t = t[..., 1:]
+        assert torch.isfinite(t).all(), n
+
+
+def test_positive_rates_take_no_input():
+    k = scan_case("rate", 1, 20, 24, F32, seed=29, in_gate=False, bias=False)
+    k["A"] = k["A"].abs() * 0.01
+    y, _ = _fwd(k)
+    r = torch.sigmoid(k["gate"].double())
+    want = k["h0"].double().unsqueeze(1) * torch.exp(torch.cumsum(k["A"].double() * r, 1))
+    check(y, f64(want), 400 * 2.0 ** -24 * np.abs(f64(want)), "y")
+
+
+@pytest.mark.parametrize("mode", MODES)
+@pytest.mark.parametrize("cut", [1, 128, 256, 512, 300])
+def test_resuming_from_the_final_state_equals_one_pass(mode, cut):
+    k = scan_case(mode, 2, 900, 72, F32, seed=31, doc=100)
+    y, hf = _fwd(k)
+    part = lambda lo, hi: {m: v[:, lo:hi].contiguous() if m in ("x", "gate", "in_gate", "reset") else v  # noqa: E731
+                           for m, v in k.items()}
+    y1, h1 = _fwd(part(0, cut))
+    y2, h2 = _fwd(dict(part(cut, 900), h0=h1))
+    torch.cuda.synchronize()
+    H, _, E = R.gated_scan(**scan_case64(k))
+    check(torch.cat([y1, y2], 1), H, E, "resumed")
+    if cut % 256 == 0:  # the same tiles: the same bits
+        assert torch.equal(torch.cat([y1, y2], 1), y) and torch.equal(h2, hf)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("mode", MODES)
+@pytest.mark.parametrize("B,D", [(1, 1), (3, 67), (1, 1536), (200, 130), (33, 512)])
+def test_step(mode, B, D, dtype):
+    k = scan_case(mode, B, 4, D, dtype, seed=B + D, doc=4, bias=D != 67, in_gate=D != 130)
+    state = k.pop("h0").clone()
+    k64 = dict(scan_case64(k), h0=f64(state))
+    H, _, E = R.gated_scan(**k64)
+    for t in range(4):
+        kt = {m: v[:, t].contiguous() if m in ("x", "gate", "in_gate", "reset") else v for m, v in k.items()}
+        y = ssm.gated_scan_step(state, **kt)
+        torch.cuda.synchronize()
+        check(y, H[:, t], E[:, t], "step %d y" % t)
+        check(state, H[:, t], E[:, t], "step %d state" % t)
+
+
+def test_step_after_prefill_equals_one_longer_prefill():
+    k = scan_case("rate", 3, 261, 200, BF, seed=37, doc=60)
+    want, hw = _fwd(k)
+    head = {m: v[:, :260].contiguous() if m in ("x", "gate", "in_gate", "reset") else v for m, v in k.items()}
+    _, state = _fwd(head)
+    last = {m: v[:, 260].contiguous() if m in ("x", "gate", "in_gate", "reset") else v for m, v in k.items()
+            if m != "h0"}
+    y = ssm.gated_scan_step(state, **last)
+    torch.cuda.synchronize()
+    H, _, E = R.gated_scan(**scan_case64(k))
+    check(y, H[:, 260], E[:, 260], "y")
+    check(state, H[:, 260], E[:, 260], "state")
+    check(want[:, 260].contiguous(), H[:, 260], E[:, 260], "prefill")
+
+
+def test_left_padded_batch_equals_rows_of_their_own():
+    lens, L, D = [5, 300, 513], 513, 48
+    k = scan_case("rate", 3, L, D, F32, seed=41, h0=False)
+    k["reset"] = torch.zeros(3, L, dtype=torch.uint8, device=DEV)
+    for b, n in enumerate(lens):
+        k["reset"][b, L - n] = 1
+        k["x"][b, :L - n] = float("nan")  # whatever the padding holds
+    y, hf = _fwd(k)
+    for b, n in enumerate(lens):
+        row = {m: v[b:b + 1, L - n:].contiguous() if m in ("x", "gate", "in_gate") else v for m, v in k.items()
+               if m != "reset"}
+        H, _, E = R.gated_scan(**scan_case64(row))
+        check(y[b:b + 1, L - n:], H, E, "row %d" % b)
+        check(hf[b:b + 1], H[:, -1], E[:, -1], "state %d" % b)
+
+
+def test_empty_calls():
+    k = scan_case("rate", 2, 0, 24, F32, seed=43)
+    y, hf = _fwd(k)
+    assert y.shape == (2, 0, 24) and torch.equal(hf, k["h0"])
+    dh = torch.randn(2, 24, device=DEV)
+    g = ssm.gated_scan_bwd(dy=torch.empty(2, 0, 24, device=DEV), dh_final=dh, **k)
+    assert torch.equal(g["dh0"], dh) and not g["dA"].any() and not g["dgate_bias"].any() and not g["din_bias"].any()
+    k.pop("h0")
+    assert not _fwd(k)[1].any()
+    z = scan_case("rate", 0, 5, 24, F32, seed=44)
+    y, hf = _fwd(z)
+    assert y.shape == (0, 5, 24) and hf.shape == (0, 24)
+    g = ssm.gated_scan_bwd(dy=torch.empty(0, 5, 24, device=DEV), **z)
+    assert not g["dA"].any()
+    st = torch.empty(0, 24, device=DEV)
+    assert ssm.gated_scan_step(st, torch.empty(0, 24, device=DEV), torch.empty(0, 24, device=DEV), "decay").shape == (0, 24)
+
+
+def test_neighbouring_memory_is_left_alone():
+    """Outputs inside a larger buffer: what lies around them keeps its bytes."""
+    k = scan_case("rate", 2, 300, 67, BF, seed=47, doc=50)
+    B, L, D = k["x"].shape
+
+    def framed(shape, dtype):
+        n = int(np.prod(shape))
+        buf = torch.full((n + 64,), 7.0, dtype=dtype, device=DEV)
+        return buf, buf[33:33 + n].view(shape)
+
+    by, y = framed((B, L, D), BF)
+    bh, hf = framed((B, D), F32)
+    bc, ck = framed(ssm.gated_checkpoint_shape(B, L, D), F32)
+    ssm.gated_scan_fwd(y=y, h_final=hf, checkpoints=ck, **k)
+    torch.cuda.synchronize()
+    for buf in (by, bh, bc):
+        assert (buf[:33] == 7).all() and (buf[-31:] == 7).all()
+    _check_bwd(k, "framed", ck)
+
+
+def test_two_runs_give_the_same_bits():
+    k = scan_case("rate", 2, 4100, 200, BF, seed=53, doc=300)
+    dy = torch.randn(k["x"].shape, device=DEV).to(BF)
+    a, b = _fwd(k), _fwd(k)
+    ga, gb = ssm.gated_scan_bwd(dy=dy, **k), ssm.gated_scan_bwd(dy=dy, **k)
+    torch.cuda.synchronize()
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    for n in ga:
+        assert torch.equal(ga[n], gb[n]), n
+
+
+def test_two_streams_at_once():
+    k1 = scan_case("rate", 1, 6000, 128, BF, seed=59)
+    k2 = scan_case("sigmoid", 1, 7000, 96, F32, seed=61, doc=500)
+    w1, w2 = _fwd(k1), _fwd(k2)
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(3):
+        with torch.cuda.stream(s1):
+            g1 = _fwd(k1)
+        with torch.cuda.stream(s2):
+            g2 = _fwd(k2)
+    torch.cuda.synchronize()
+    assert torch.equal(g1[0], w1[0]) and torch.equal(g2[0], w2[0]) and torch.equal(g1[1], w1[1])
+
+
+def test_rows_past_32_bit_offsets():
+    """2.2e9 elements a tensor: the last steps of a row equal a call of their own from the
+    checkpoint that the long call wrote."""
+    L, D = 2200 * 1024, 1000
+    g = torch.Generator(DEV).manual_seed(67)
+    x = torch.randn(1, L, D, generator=g, device=DEV, dtype=BF)
+    gate = torch.rand(1, L, D, generator=g, device=DEV, dtype=BF)
+    ck = torch.empty(ssm.gated_checkpoint_shape(1, L, D), device=DEV)
+    y, hf = ssm.gated_scan_fwd(x, gate, "decay", checkpoints=ck, return_final_state=True)
+    t = L - 512
+    yt, ht = ssm.gated_scan_fwd(x[:, t:].contiguous(), gate[:, t:].contiguous(), "decay",
+                                h0=ck[t // 128].contiguous(), return_final_state=True)
+    torch.cuda.synchronize()
+    assert torch.equal(y[:, t:], yt) and torch.equal(hf, ht)
+    y0, _ = ssm.gated_scan_fwd(x[:, :512].contiguous(), gate[:, :512].contiguous(), "decay")
+    assert torch.equal(y[:, :512], y0)
+    del y
+    dy = torch.ones_like(x)
+    got = ssm.gated_scan_bwd(x, gate, dy, "decay", checkpoints=ck)
+    tail = ssm.gated_scan_bwd(x[:, t:].contiguous(), gate[:, t:].contiguous(), dy[:, t:].contiguous(), "decay",
+                              h0=ck[t // 128].contiguous())
+    torch.cuda.synchronize()
+    assert torch.equal(got["dx"][:, t:], tail["dx"]) and torch.equal(got["dgate"][:, t:], tail["dgate"])
+
+
+@pytest.mark.parametrize("mode", MODES)
+def test_autograd(mode):
+    """backward() through the differentiable op gives the direct backward's gradients."""
+    k = scan_case(mode, 2, 200, 40, BF, seed=71, doc=30)
+    leaves = {m: v.clone().requires_grad_() for m, v in k.items()
+              if isinstance(v, torch.Tensor) and m != "reset"}
+    y, hf = ssm.gated_scan(mode=mode, reset=k["reset"], **leaves)
+    dy, dh = torch.randn_like(y), torch.randn_like(hf)
+    torch.autograd.backward([y, hf], [dy, dh])
+    want = ssm.gated_scan_bwd(dy=dy, dh_final=dh, **k)
+    torch.cuda.synchronize()
+    names = dict(x="dx", gate="dgate", in_gate="din_gate", A="dA", gate_bias="dgate_bias", in_bias="din_bias",
+                 h0="dh0")
+    for m, v in leaves.items():
+        assert torch.equal(v.grad, want[names[m]]), m
+    only = k["x"].clone().requires_grad_()
+    kk = {m: v for m, v in k.items() if m not in ("x", "mode", "reset")}
+    y, _ = ssm.gated_scan(only, mode=mode, reset=k["reset"], **kk)
+    y.backward(dy)
+    assert torch.equal(only.grad, ssm.gated_scan_bwd(dy=dy, **k)["dx"])
+
+
+def test_refusals():
+    k = scan_case("rate", 2, 8, 24, F32, seed=73)
+    x, gate = k["x"], k["gate"]
+    for kw, err in ((dict(mode="gru"), ValueError), (dict(A=None), ssm.SSMError),
+                    (dict(mode="decay", A=None, in_gate=None, in_bias=None), ssm.SSMError),  # gate_bias
+                    (dict(mode="sigmoid", gate_bias=None), ssm.SSMError),                    # A, in_gate
+                    (dict(in_gate=None), ssm.SSMError),                                       # in_bias alone
+                    (dict(gate=gate[:, :, :12]), ValueError), (dict(gate=gate.to(BF)), TypeError),
+                    (dict(x=x.transpose(0, 1)), ValueError), (dict(x=x.half(), gate=gate.half()), TypeError),
+                    (dict(reset=torch.zeros(2, 8, device=DEV)), TypeError),
+                    (dict(h0=torch.zeros(2, 24)), ValueError), (dict(y=x), ssm.SSMError),
+                    (dict(checkpoints=torch.empty(2, 2, 24, device=DEV)), ValueError),
+                    (dict(h_final=k["h0"]), ssm.SSMError)):
+        with pytest.raises(err):
+            ssm.gated_scan_fwd(**{**k, **kw})
+    with pytest.raises(ValueError):
+        ssm.gated_scan_bwd(dy=x[:, :4], **k)
+    with pytest.raises(ValueError):
+        ssm.gated_scan_step(k["h0"], x[:, 0, :5], gate[:, 0, :5], "decay")
+    with pytest.raises(ssm.SSMError):
+        ssm.gated_scan_step(k["h0"], x[:, 0].contiguous(), gate[:, 0].contiguous(), "decay", y=k["h0"])
+    with pytest.raises(ValueError):
+        ssm.gated_scan_fwd(x.cpu(), gate.cpu(), "decay")

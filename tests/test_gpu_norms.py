@@ -1,0 +1,238 @@
+"""The fused norms on the GPU against their fp64 definitions (needs an MI355X)."""
+import numpy as np
+import pytest
+import torch
+
+import selective_state_space_59_amd as ssm
+from oracle import recurrent as R
+from tests.recurrent_helpers import check, f64, gnorm_bound, norm_bound
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+BF, F32 = torch.bfloat16, torch.float32
+SHAPES = [(1, 1), (3, 7), (1, 2560), (5, 768), (300, 64), (7, 520), (2, 1023), (33, 2048), (4, 5121), (9, 8192),
+          (2, 20000), (1025, 24), (3, 70001)]
+TYPES = [(F32, F32), (BF, BF), (BF, F32), (F32, BF)]
+
+
+def _draw(rows, D, io, res, post, scale, residual, seed):
+    g = torch.Generator().manual_seed(seed)
+    n = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+    k = dict(x=n(rows, D).to(io), w=1 + 0.1 * n(D), residual=(2 * n(rows, D)).to(res) if residual else None,
+             scale=0.5 + 0.1 * n(D) if scale else None, post_w=1 + 0.1 * n(D) if post else None)
+    dy, dres = n(rows, D).to(io), n(rows, D).to(res if residual else io)
+    d = lambda t: None if t is None else t.to(DEV)  # noqa: E731
+    return {m: d(v) for m, v in k.items()}, d(dy), d(dres)
+
+
+@pytest.mark.parametrize("io,res", TYPES, ids=["f32_f32", "bf16_bf16", "bf16_f32", "f32_bf16"])
+@pytest.mark.parametrize("rows,D", SHAPES)
+def test_add_rmsnorm(rows, D, io, res):
+    for i, (post, scale, residual, up) in enumerate([(False, False, True, True), (True, True, True, True),
+                                                     (False, True, False, False), (True, False, True, False)]):
+        if D > 10000 and i in (2, 3):
+            continue
+        k, dy, dres = _draw(rows, D, io, res, post, scale, residual, seed=rows + D + i)
+        dres = dres if up else None
+        what = "%dx%d post=%d scale=%d residual=%d" % (rows, D, post, scale, residual)
+        print(what, flush=True)
+        y, r = ssm.add_rmsnorm_fwd(**k)
+        got = ssm.add_rmsnorm_bwd(dy=dy, dres_out=dres, **k)
+        torch.cuda.synchronize()
+        k64 = {m: f64(v) for m, v in k.items()}
+        ry, rr = R.add_rmsnorm(**k64)
+        b = norm_bound(k64["x"], k64["w"], k64["residual"], k64["scale"], k64["post_w"], f64(dy), f64(dres))
+        assert r.dtype == (res if residual else io)
+        check(y, ry, b["y"], what + " y")
+        check(r, rr, b["res_out"], what + " res_out")
+        ref = R.add_rmsnorm_bwd(k64["x"], k64["w"], k64["residual"], f64(dy), f64(dres), k64["scale"], k64["post_w"])
+        assert set(ref) == set(got)
+        for n, v in ref.items():
+            check(got[n], v, b[n], "%s %s" % (what, n))
+
+
+def _gdraw(rows, D, io, seed):
+    g = torch.Generator().manual_seed(seed)
+    n = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+    return [t.to(DEV) for t in (n(rows, D).to(io), n(rows, D).to(io), 1 + 0.1 * n(D), n(rows, D).to(io))]
+
+
+@pytest.mark.parametrize("io", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("gate_first", [True, False], ids=["gate_first", "norm_first"])
+@pytest.mark.parametrize("rows,D,groups", [(1, 1, 1), (3, 6, 3), (1, 1536, 1), (5, 768, 8), (300, 128, 2), (7, 515, 5),
+                                           (2, 5120, 8), (4, 4095, 1), (40, 96, 96), (9, 8192, 64), (3, 70001, 1),
+                                           (2, 66000, 3)])
+def test_gated_rmsnorm(rows, D, groups, gate_first, io):
+    x, z, w, dy = _gdraw(rows, D, io, seed=rows + D)
+    what = "%dx%d groups=%d" % (rows, D, groups)
+    print(what, flush=True)
+    y = ssm.gated_rmsnorm_fwd(x, z, w, groups=groups, gate_first=gate_first)
+    got = ssm.gated_rmsnorm_bwd(x, z, w, dy, groups=groups, gate_first=gate_first)
+    torch.cuda.synchronize()
+    a = [f64(t) for t in (x, z, w)]
+    b = gnorm_bound(*a, groups, gate_first, f64(dy))
+    check(y, R.gated_rmsnorm(*a, groups, gate_first), b["y"], what + " y")
+    ref = R.gated_rmsnorm_bwd(*a, f64(dy), groups, gate_first)
+    for n, v in ref.items():
+        check(got[n], v, b[n], "%s %s" % (what, n))
+
+
+@pytest.mark.parametrize("io", [F32, BF], ids=["f32", "bf16"])
+def test_pointers_at_any_element_offset(io):
+    def shifted(t):
+        buf = torch.empty(t.numel() + 1, dtype=t.dtype, device=DEV)
+        buf[1:] = t.reshape(-1)
+        return buf[1:].view(t.shape)
+
+    k, dy, dres = _draw(5, 333, io, io, True, True, True, seed=3)
+    s = {m: shifted(v) for m, v in k.items()}
+    for a, b in zip(ssm.add_rmsnorm_fwd(**k), ssm.add_rmsnorm_fwd(**s)):
+        assert torch.equal(a, b)
+    a = ssm.add_rmsnorm_bwd(dy=dy, dres_out=dres, **k)
+    b = ssm.add_rmsnorm_bwd(dy=shifted(dy), dres_out=shifted(dres), **s)
+    for n in a:
+        assert torch.equal(a[n], b[n]), n
+    g = _gdraw(5, 333, io, seed=4)
+    a, b = ssm.gated_rmsnorm_bwd(*g, groups=3), ssm.gated_rmsnorm_bwd(*[shifted(t) for t in g], groups=3)
+    for n in a:
+        assert torch.equal(a[n], b[n]), n
+    assert torch.equal(ssm.gated_rmsnorm_fwd(*g[:3]), ssm.gated_rmsnorm_fwd(*[shifted(t) for t in g[:3]]))
+
+
+def test_in_place_forms():
+    k, dy, dres = _draw(70, 776, BF, BF, True, True, True, seed=5)
+    y, r = ssm.add_rmsnorm_fwd(**k)
+    res = k["residual"].clone()
+    y2, r2 = ssm.add_rmsnorm_fwd(**dict(k, residual=res), res_out=res)
+    assert r2 is res and torch.equal(y, y2) and torch.equal(r, r2)
+    x, z, w, _ = _gdraw(70, 776, BF, seed=6)
+    want = ssm.gated_rmsnorm_fwd(x, z, w, groups=2)
+    for into in (0, 1):
+        pair = [x.clone(), z.clone()]
+        got = ssm.gated_rmsnorm_fwd(*pair, w, groups=2, y=pair[into])
+        assert got is pair[into] and torch.equal(got, want)
+
+
+def test_rows_of_zeros_and_of_nans():
+    """A row of zeros gives zeros and finite gradients; a NaN or an infinity stays in its row."""
+    k, dy, dres = _draw(6, 300, F32, F32, False, False, True, seed=7)
+    k["x"][2], k["residual"][2] = 0.0, 0.0
+    k["x"][4, 17] = float("nan")
+    k["x"][5, 3] = float("inf")
+    y, r = ssm.add_rmsnorm_fwd(**k)
+    g = ssm.add_rmsnorm_bwd(dy=dy, dres_out=dres, **k)
+    assert not y[2].any() and torch.isfinite(y[:4]).all() and torch.isfinite(g["dx"][:4]).all()
+    assert y[4].isnan().all() and not torch.isfinite(r[5, 3])
+    x, z, w, dy = _gdraw(6, 300, F32, seed=8)
+    x[2] = 0.0
+    x[4, 17] = float("nan")
+    for first in (True, False):
+        y = ssm.gated_rmsnorm_fwd(x, z, w, groups=3, gate_first=first)
+        g = ssm.gated_rmsnorm_bwd(x, z, w, dy, groups=3, gate_first=first)
+        assert not y[2].any() and torch.isfinite(g["dz"][:4]).all()
+        assert y[4, :100].isnan().all() and torch.isfinite(y[4, 100:]).all() and torch.isfinite(y[5]).all()
+
+
+def test_large_and_small_values():
+    """Rows whose squares are near the ends of the fp32 range, and gates at the far ends."""
+    k, _, _ = _draw(4, 512, F32, F32, False, False, False, seed=9)
+    for row, s in ((0, 1e15), (1, 1e-15), (2, 1e17)):
+        k["x"][row] *= s
+    y, _ = ssm.add_rmsnorm_fwd(**k)
+    k64 = {m: f64(v) for m, v in k.items()}
+    check(y, R.add_rmsnorm(**k64)[0], norm_bound(k64["x"], k64["w"], None, None, None)["y"], "y")
+    x, z, w, dy = _gdraw(3, 256, F32, seed=10)
+    z[0], z[1] = 1e4, -1e4
+    y = ssm.gated_rmsnorm_fwd(x, z, w, gate_first=False)
+    g = ssm.gated_rmsnorm_bwd(x, z, w, dy)
+    assert torch.isfinite(y).all() and not y[1].any()
+    assert all(torch.isfinite(v).all() for v in g.values())
+
+
+def test_empty_and_leading_shapes():
+    w = torch.ones(24, device=DEV)
+    e = torch.empty(0, 3, 24, device=DEV)
+    y, r = ssm.add_rmsnorm_fwd(e, w, e)
+    assert y.shape == r.shape == (0, 3, 24)
+    g = ssm.add_rmsnorm_bwd(e, w, e, e, e)
+    assert not g["dw"].any() and g["dx"].shape == (0, 3, 24)
+    assert ssm.gated_rmsnorm_fwd(e, e, w).shape == (0, 3, 24)
+    assert not ssm.gated_rmsnorm_bwd(e, e, w, e)["dw"].any()
+    k, dy, dres = _draw(30, 40, BF, F32, True, True, True, seed=11)
+    cut = lambda t: t.view(2, 3, 5, 40) if t is not None and t.dim() == 2 else t  # noqa: E731
+    a, b = ssm.add_rmsnorm_fwd(**k), ssm.add_rmsnorm_fwd(**{m: cut(v) for m, v in k.items()})
+    assert b[0].shape == (2, 3, 5, 40) and torch.equal(a[0], b[0].view(30, 40)) and torch.equal(a[1], b[1].view(30, 40))
+    one = ssm.add_rmsnorm_fwd(k["x"][3], k["w"], k["residual"][3])
+    assert torch.equal(one[0], ssm.add_rmsnorm_fwd(k["x"], k["w"], k["residual"])[0][3])
+
+
+def test_more_rows_than_a_launch_has_workgroups():
+    x, z, w, dy = _gdraw(200000, 16, BF, seed=12)
+    y = ssm.gated_rmsnorm_fwd(x, z, w, groups=2)
+    g = ssm.gated_rmsnorm_bwd(x, z, w, dy, groups=2)
+    a = [f64(t) for t in (x, z, w)]
+    b = gnorm_bound(*a, 2, True, f64(dy))
+    check(y, R.gated_rmsnorm(*a, 2), b["y"], "y")
+    for n, v in R.gated_rmsnorm_bwd(*a, f64(dy), 2).items():
+        check(g[n], v, b[n], n)
+
+
+def test_two_runs_give_the_same_bits():
+    k, dy, dres = _draw(5000, 776, BF, F32, True, True, True, seed=13)
+    a, b = (ssm.add_rmsnorm_bwd(dy=dy, dres_out=dres, **k) for _ in range(2))
+    x, z, w, dz = _gdraw(5000, 776, BF, seed=14)
+    c, d = (ssm.gated_rmsnorm_bwd(x, z, w, dz, groups=4) for _ in range(2))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a[n], b[n]) for n in a) and all(torch.equal(c[n], d[n]) for n in c)
+
+
+def test_rows_past_32_bit_offsets():
+    rows, D = 280000, 8192
+    x = torch.ones(rows, D, device=DEV, dtype=BF)
+    z = torch.ones(rows, D, device=DEV, dtype=BF)
+    x[-1] = torch.arange(D, device=DEV).remainder(7).to(BF)
+    w = torch.ones(D, device=DEV)
+    y = ssm.gated_rmsnorm_fwd(x, z, w)
+    assert torch.equal(y[-1], ssm.gated_rmsnorm_fwd(x[-1], z[-1], w)) and torch.equal(y[0], y[rows // 2])
+    y, r = ssm.add_rmsnorm_fwd(x, w, z)
+    one = ssm.add_rmsnorm_fwd(x[-1], w, z[-1])
+    assert torch.equal(y[-1], one[0]) and torch.equal(r[-1], one[1])
+    del y, r
+    g = ssm.gated_rmsnorm_bwd(x, z, w, z)
+    assert torch.equal(g["dx"][-1], ssm.gated_rmsnorm_bwd(x[-1], z[-1], w, z[-1])["dx"])
+
+
+def test_autograd():
+    k, dy, dres = _draw(60, 264, BF, F32, True, True, True, seed=15)
+    leaves = {m: v.clone().requires_grad_() for m, v in k.items()}
+    y, r = ssm.add_rmsnorm(**leaves)
+    torch.autograd.backward([y, r], [dy, dres])
+    want = ssm.add_rmsnorm_bwd(dy=dy, dres_out=dres, **k)
+    for m, v in leaves.items():
+        assert torch.equal(v.grad, want["d" + m]), m
+    x, z, w, dz = _gdraw(60, 264, BF, seed=16)
+    lv = [t.clone().requires_grad_() for t in (x, z, w)]
+    ssm.gated_rmsnorm(*lv, groups=3, gate_first=False).backward(dz)
+    want = ssm.gated_rmsnorm_bwd(x, z, w, dz, groups=3, gate_first=False)
+    for t, n in zip(lv, ("dx", "dz", "dw")):
+        assert torch.equal(t.grad, want[n]), n
+
+
+def test_refusals():
+    k, dy, dres = _draw(4, 24, F32, F32, False, False, True, seed=17)
+    x, w, res = k["x"], k["w"], k["residual"]
+    for kw, err in ((dict(w=w.to(BF)), TypeError), (dict(w=w[:12]), ValueError), (dict(residual=res[:2]), ValueError),
+                    (dict(residual=res.half()), TypeError), (dict(x=x.half()), TypeError),
+                    (dict(x=x.t().contiguous().t()), ValueError), (dict(x=x.cpu()), ValueError),
+                    (dict(eps=0.0), ssm.SSMError), (dict(eps=float("nan")), ssm.SSMError),
+                    (dict(y=x), ssm.SSMError), (dict(res_out=x), ssm.SSMError), (dict(scale=w[:3]), ValueError)):
+        with pytest.raises(err):
+            ssm.add_rmsnorm_fwd(**{**k, **kw})
+    with pytest.raises(ValueError):
+        ssm.add_rmsnorm_bwd(dy=dy[:2], **k)
+    for kw, err in ((dict(groups=5), ssm.SSMError), (dict(groups=0), ssm.SSMError), (dict(eps=-1.0), ssm.SSMError),
+                    (dict(z=x[:2]), ValueError), (dict(z=x.to(BF)), TypeError), (dict(w=w[:2]), ValueError)):
+        with pytest.raises(err):
+            ssm.gated_rmsnorm_fwd(**{**dict(x=x, z=res, w=w), **kw})
+    with pytest.raises(ssm.SSMError):
+        ssm.gated_rmsnorm_fwd(x[1:], x[1:], w, y=x[:3])
