@@ -69,15 +69,33 @@ __global__ __launch_bounds__(256) void gated_sum_kernel(const float *part, int64
 
 size_t r256(size_t v) { return (v + 255) & ~(size_t)255; }
 size_t ckpt_bytes(const ssm_gated_scan_bwd_args_t &a) {
-    if (a.checkpoints) return 0;
     return r256((size_t)((a.seqlen + SSM_GATED_BLOCK - 1) / SSM_GATED_BLOCK * a.batch * a.dim) * 4);
+}
+
+// The forward call that writes the checkpoints alone (y and h_final NULL).
+ssm_gated_scan_args_t forward_of(const ssm_gated_scan_bwd_args_t &a) {
+    ssm_gated_scan_args_t f = {};
+    f.batch = a.batch;
+    f.seqlen = a.seqlen;
+    f.dim = a.dim;
+    f.io_dtype = a.io_dtype;
+    f.mode = a.mode;
+    f.x = a.x;
+    f.gate = a.gate;
+    f.in_gate = a.in_gate;
+    f.A = a.A;
+    f.gate_bias = a.gate_bias;
+    f.in_bias = a.in_bias;
+    f.reset = a.reset;
+    f.h0 = a.h0;
+    return f;
 }
 
 }  // namespace
 
 size_t gated_scan_bwd_workspace_bytes(const ssm_gated_scan_bwd_args_t &a) {
-    return ckpt_bytes(a) + (a.checkpoints ? 0 : (size_t)(a.batch * a.seqlen * a.dim) * 4) +
-           r256((size_t)(3 * a.batch * a.dim) * 4);
+    const size_t sums = r256((size_t)(3 * a.batch * a.dim) * 4);
+    return sums + (a.checkpoints ? 0 : ckpt_bytes(a) + gated_scan_workspace_bytes(forward_of(a)));
 }
 
 hipError_t launch_gated_scan_bwd(const ssm_gated_scan_bwd_args_t &a, hipStream_t stream) {
@@ -86,22 +104,9 @@ hipError_t launch_gated_scan_bwd(const ssm_gated_scan_bwd_args_t &a, hipStream_t
     hipError_t e = hipSuccess;
     if (!ck) {
         char *at = static_cast<char *>(a.workspace) + r256((size_t)(3 * a.batch * a.dim) * 4);
-        ssm_gated_scan_args_t f = {};
-        f.batch = a.batch;
-        f.seqlen = a.seqlen;
-        f.dim = a.dim;
-        f.io_dtype = a.io_dtype;
-        f.mode = a.mode;
-        f.x = a.x;
-        f.gate = a.gate;
-        f.in_gate = a.in_gate;
-        f.A = a.A;
-        f.gate_bias = a.gate_bias;
-        f.in_bias = a.in_bias;
-        f.reset = a.reset;
-        f.h0 = a.h0;
+        ssm_gated_scan_args_t f = forward_of(a);
         f.checkpoints = reinterpret_cast<float *>(at);
-        f.y = at + ckpt_bytes(a);
+        f.workspace = at + ckpt_bytes(a);
         ck = f.checkpoints;
         e = launch_gated_scan_fwd(f, stream);
     }
