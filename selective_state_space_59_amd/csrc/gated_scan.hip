@@ -85,16 +85,12 @@ __global__ __launch_bounds__(kGatedThreads) void gated_scan_kernel(ssm_gated_sca
     __syncthreads();
     if (tid < CB) {
         const int d = cblk * CB + tid;
-        float gp[G], gl[G], tp = 1.0f, tl = 0.0f;
-#pragma unroll
+        float tp = 1.0f, tl = 0.0f;
+#pragma unroll 8
         for (int i = 0; i < G; ++i) {
-            gp[i] = sp[i][tid];
-            gl[i] = sl[i][tid];
-        }
-#pragma unroll
-        for (int i = 0; i < G; ++i) {
-            tl = run_apply(gp[i], gl[i], tl);
-            tp *= gp[i];
+            const float p = sp[i][tid];
+            tl = run_apply(p, sl[i][tid], tl);
+            tp *= p;
         }
         float h = tile == 0 && a.h0 && d < D ? a.h0[b * D + d] : 0.0f;
         u64_t *mine = rec + ((int64_t)chain * tiles + tile) * CB + tid;
@@ -107,12 +103,13 @@ __global__ __launch_bounds__(kGatedThreads) void gated_scan_kernel(ssm_gated_sca
             rec_put(mine, kRecState, after);
         else if (a.h_final && d < D)
             a.h_final[b * D + d] = after;
-#pragma unroll
+#pragma unroll 8
         for (int i = 0; i < G; ++i) {
             if (i * R % SSM_GATED_BLOCK == 0 && a.checkpoints && d < D && i * R < left)
                 a.checkpoints[((t0 + i * R) / SSM_GATED_BLOCK * a.batch + b) * D + d] = h;
+            const float p = sp[i][tid];
             sp[i][tid] = h;
-            h = run_apply(gp[i], gl[i], h);
+            h = run_apply(p, sl[i][tid], h);
         }
     }
     __syncthreads();
@@ -126,7 +123,7 @@ __global__ __launch_bounds__(kGatedThreads) void gated_scan_kernel(ssm_gated_sca
             float f[V];
 #pragma unroll
             for (int v = 0; v < V; ++v) f[v] = run_apply(p[j][v], l[j][v], e[v]);
-            if (g * R + j < left) store_row<IO>(out + off[j], nv, f);
+            if (g * R + j < left) store_words<IO>(out + off[j], nv, lane_pack<IO>(f));
         }
     }
 }

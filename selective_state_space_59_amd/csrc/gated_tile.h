@@ -67,9 +67,8 @@ __device__ __forceinline__ u32x4_t lane_pack(const float (&f)[TileShape<IO>::V])
 }
 
 template <typename IO>
-__device__ __forceinline__ void store_row(char *p, int nv, const float (&f)[TileShape<IO>::V]) {
+__device__ __forceinline__ void store_words(char *p, int nv, const u32x4_t &q) {
     constexpr int V = TileShape<IO>::V;
-    const u32x4_t q = lane_pack<IO>(f);
     if (nv == V) {
         *reinterpret_cast<u32x4_a2 *>(p) = q;
     } else {

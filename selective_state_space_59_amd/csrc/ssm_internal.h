@@ -63,6 +63,12 @@ hipError_t launch_gated_scan_bwd(const ssm_gated_scan_bwd_args_t &a, hipStream_t
 // out[i] = in ? in[i] : 0 for i < n (the state of an empty recurrence, the gradients of none).
 hipError_t launch_copy_or_zero(float *out, const float *in, int64_t n, hipStream_t stream);
 
+// out[k][d] = sum over i < n of part[k][i][d] for k < K <= 3 (out[k] may be NULL: not formed), added in a
+// fixed order; scratch of column_sums_scratch_bytes (colsum.hip).  n >= 1.
+size_t column_sums_scratch_bytes(int64_t n, int64_t D, int K);
+hipError_t launch_column_sums(const float *part, int64_t n, int64_t D, int K, float *const out[], float *scratch,
+                              hipStream_t stream);
+
 // Fused norms (norms.hip).  rows > 0 in the forward; the backward takes rows >= 0.
 hipError_t launch_add_norm_fwd(const ssm_add_norm_args_t &a, hipStream_t stream);
 size_t add_norm_bwd_workspace_bytes(const ssm_add_norm_bwd_args_t &a);
