@@ -56,7 +56,7 @@ hipError_t launch_column_sums(const float *part, int64_t n, int64_t D, int K, fl
     while (n > kLastRows) {
         const int64_t chunks = (n + kStageRows - 1) / kStageRows;
         Outs o = {};
-        for (int k = 0; k < K; ++k) o.p[k] = scratch + (int64_t)k * chunks * D;
+        for (int k = 0; k < K; ++k) o.p[k] = out[k] ? scratch + (int64_t)k * chunks * D : nullptr;
         colsum_kernel<4><<<dim3(cols, (unsigned)chunks, (unsigned)K), 256, 0, stream>>>(part, n, D, kStageRows, o);
         part = scratch;
         scratch += chunks * D * K;

@@ -4,13 +4,9 @@
 #pragma once
 
 #include "gated_device.h"
+#include "wide_io.h"
 
 namespace ssm {
-
-typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
-// 16 bytes at the alignment of an element: one global_load_dwordx4 / store (the hardware takes
-// unaligned addresses), so odd widths and shifted tensors run on the same path.
-typedef u32x4_t u32x4_a2 __attribute__((aligned(2)));
 
 constexpr int kLanesPerRow = 8;  // 8 lanes x 16 bytes: a 128-byte piece of a row
 constexpr int kGatedThreads = 256;

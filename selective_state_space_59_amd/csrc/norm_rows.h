@@ -1,0 +1,146 @@
+// norm_rows.h -- how the fused norms walk over rows (gfx950): teams, sums over a team, launch
+// shapes.  A "row" here is what one mean square is taken over: a row of the tensor, or a group
+// of its channels.
+//
+// A team of lanes owns a row, 8 elements a lane and group, read once into registers:
+//   rows of up to 256      8 or 32 lanes, several rows a wave (adjacent groups side by side)
+//   up to 512 * NR         one wave, NR groups a lane: sums without a barrier
+//   up to kBlockRow        one workgroup of as many waves as the row needs, one group a lane
+//   longer                 one workgroup of 1024, reading the row again for each of its passes
+// A team keeps its columns over all its rows, so the weights stay in registers and the
+// gradients of the weights add up there.
+#pragma once
+
+#include <algorithm>
+
+#include "ssm_internal.h"
+#include "wide_io.h"
+
+namespace ssm {
+
+constexpr int kBlockRow = 8192;   // longest row held in a workgroup's registers
+constexpr int kTeamThreads = 256; // workgroup of the teams of up to a wave
+
+// TEAM lanes (1 << n up to 64, or 0: the workgroup) with NR groups of 8 each.
+template <int TEAM_, int NR_>
+struct Shape {
+    static constexpr int TEAM = TEAM_, NR = NR_;
+};
+
+template <int TEAM>
+__device__ __forceinline__ float lanes_sum(float v) {
+#pragma unroll
+    for (int s = TEAM / 2; s >= 1; s /= 2) v += __shfl_xor(v, s, 64);
+    return v;
+}
+
+// Sums over the team, of one or two values.  For a workgroup: through LDS with one barrier; the
+// slots alternate, so that a wave still reading one sum meets no write of the next.
+struct SumSlots {
+    float v[2][2][16];
+};
+
+template <int TEAM>
+__device__ __forceinline__ void team_sum(float &a, float &b, SumSlots &s, int &turn) {
+    a = lanes_sum<TEAM == 0 ? 64 : TEAM>(a);
+    b = lanes_sum<TEAM == 0 ? 64 : TEAM>(b);
+    if constexpr (TEAM == 0) {
+        const int wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+        if ((threadIdx.x & 63) == 0) {
+            s.v[turn][0][wave] = a;
+            s.v[turn][1][wave] = b;
+        }
+        __syncthreads();
+        a = b = 0.0f;
+        for (int i = 0; i < waves; ++i) {
+            a += s.v[turn][0][i];
+            b += s.v[turn][1][i];
+        }
+        turn ^= 1;
+    }
+}
+
+template <int TEAM>
+__device__ __forceinline__ float team_sum(float a, SumSlots &s, int &turn) {
+    float b = 0.0f;
+    team_sum<TEAM>(a, b, s, turn);
+    return a;
+}
+
+__device__ __forceinline__ float inv_rms(float sum, float inv_n, float eps) {
+    return 1.0f / sqrtf(__builtin_fmaf(sum, inv_n, eps));
+}
+
+// Eight weights (the first n of them) as floats.
+__device__ __forceinline__ void load_vec(const float *p, int64_t i, int n, float (&w)[8]) {
+    const Raw8<io_f32> r = load8<io_f32>(p, i, n);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e] = r[e];
+}
+
+// Column sums of the waves of a workgroup that hold the same columns: into wave 0's registers.
+template <int NR>
+__device__ __forceinline__ void waves_sum(float (&v)[NR][8], float *lds, int lane) {
+    constexpr int W = kTeamThreads / 64;
+    const int wave = threadIdx.x / 64;
+#pragma unroll
+    for (int c = 0; c < NR; ++c) {
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < 8; ++e) lds[(wave * 8 + e) * 64 + lane] = v[c][e];
+        __syncthreads();
+        if (wave == 0)
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                for (int i = 1; i < W; ++i) v[c][e] += lds[(i * 8 + e) * 64 + lane];
+    }
+}
+
+// The rows of a team: group `g` of every row from `row` on, `step` apart.
+struct TeamRows {
+    int64_t g, row, step;
+};
+
+// How many workgroups, and over how many rows of the tensor they run at once (`slots`, the rows
+// of partial sums too).
+struct RowGrid {
+    unsigned blocks, threads;
+    int64_t slots;
+};
+
+// Team sizes of up to half a wave put the groups of a tensor row side by side; a wave or a
+// workgroup takes one group (blockIdx % groups).
+template <int TEAM>
+__device__ __forceinline__ TeamRows team_rows(int64_t groups, int64_t slots) {
+    if constexpr (TEAM == 0) return {blockIdx.x % groups, blockIdx.x / groups, slots};
+    if constexpr (TEAM == 64) {
+        const int64_t slot = blockIdx.x / groups * (kTeamThreads / 64) + threadIdx.x / 64;
+        return {blockIdx.x % groups, slot, slots};
+    }
+    const int64_t t = (int64_t)blockIdx.x * (kTeamThreads / TEAM) + threadIdx.x / TEAM;
+    const int64_t slot = t / groups;
+    return {t % groups, slot < slots ? slot : (int64_t)1 << 62, slots};  // spare teams: no rows
+}
+
+// `blocks_wanted`: workgroups that keep the chip busy.
+inline RowGrid row_grid(int team, int64_t len, int64_t rows, int64_t groups, int64_t blocks_wanted) {
+    RowGrid g;
+    if (team == 0 || team == 64) {
+        const int64_t per = team == 0 ? 1 : kTeamThreads / 64;
+        const int64_t most = (rows + per - 1) / per, want = std::max<int64_t>(1, blocks_wanted / groups);
+        const int64_t n = std::min(most, want);
+        g.blocks = (unsigned)(n * groups);
+        g.slots = n * per;
+        g.threads = team == 0 ? (unsigned)std::min<int64_t>(1024, (len + 511) / 512 * 64) : kTeamThreads;
+    } else {
+        const int64_t per = kTeamThreads / team;  // teams of a workgroup
+        const int64_t most = (rows * groups + per - 1) / per, least = (groups + per - 1) / per;
+        const int64_t n = std::max(least, std::min(most, blocks_wanted));
+        g.blocks = (unsigned)n;
+        g.slots = n * per / groups;
+        g.threads = kTeamThreads;
+    }
+    return g;
+}
+
+}  // namespace ssm
