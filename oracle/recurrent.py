@@ -23,9 +23,9 @@ def gates(mode, x, gate, A=None, in_gate=None, gate_bias=None, in_bias=None):
     g = gate if gate_bias is None else gate + gate_bias
     if mode == "decay":
         return dict(a=gate, w=np.ones_like(x), ca=np.zeros_like(x), cw=np.zeros_like(x), x=x)
-    # exp2(-|v| log2 e): bias sum (1), log2 e itself (1) and the product (1) move the argument by
-    # 3 |v| u; the exponential 2, the sum 1, the reciprocal 2 and one product 1 follow
-    cs = 3 * np.abs(g) + 6
+    # exp2 of -(gate + bias) log2 e: log2 e itself, the products and the sum move the argument by
+    # 3 u of |gate| + |bias|; the exponential 2, the sum 1, the reciprocal 2 and one product 1 follow
+    cs = 3 * (np.abs(gate) + (0 if gate_bias is None else np.abs(gate_bias))) + 6
     if mode == "sigmoid":
         return dict(a=sig(-g), w=sig(g), ca=cs, cw=cs, x=x, s=sig(g), c=sig(-g))
     r = sig(g)
@@ -35,15 +35,15 @@ def gates(mode, x, gate, A=None, in_gate=None, gate_bias=None, in_bias=None):
     with np.errstate(invalid="ignore"):
         q = np.maximum(-np.expm1(2 * la), 0.0)
     # q = 1 - a^2: relative error of its argument (cs + 2) at worst as it is (|dq/q| <= |dw/w|);
-    # the series adds 6 operations, the difference 1 - a^2 at most 4 / q with q > 0.39
-    cq = cs + 2 + 14
+    # the series adds 6 operations, the difference 1 - a^2 at most 3 / q with q > 0.11
+    cq = cs + 2 + 28
     w = np.sqrt(q)
     cw = 0.5 * cq + 4
     i = np.ones_like(x)
     if in_gate is not None:
         gi = in_gate if in_bias is None else in_gate + in_bias
         i = sig(gi)
-        cw = cw + 3 * np.abs(gi) + 7
+        cw = cw + 3 * (np.abs(in_gate) + (0 if in_bias is None else np.abs(in_bias))) + 7
     return dict(a=np.exp(la), w=w * i, ca=ca, cw=cw, x=x, r=r, beta=w, i=i, cs=cs, cq=cq)
 
 

@@ -41,31 +41,39 @@ struct Sig {
     float s, c;  // sig(v) and 1 - sig(v)
 };
 
-__device__ __forceinline__ Sig sigmoid_pair(float v) {
-    const float t = hw_exp2(-fabsf(v) * kLog2e);  // in (0, 1]; NaN stays NaN
+// Logistics of v = v2 / log2(e).
+__device__ __forceinline__ Sig sigmoid_pair(float v2) {
+    const float t = hw_exp2(-fabsf(v2));  // in (0, 1]; NaN stays NaN
     const float hi = hw_rcp(1.0f + t), lo = t * hi;
     Sig r;
-    r.s = v < 0.0f ? lo : hi;
-    r.c = v < 0.0f ? hi : lo;
+    r.s = v2 < 0.0f ? lo : hi;
+    r.c = v2 < 0.0f ? hi : lo;
     return r;
 }
+// sig(v) alone: 1 / (1 + e^-v) does not cancel either.
+__device__ __forceinline__ float sigmoid(float v2) { return hw_rcp(1.0f + hw_exp2(-v2)); }
 
-// 1 - a^2 for a = e^{la}, w = 2 la <= 0 (0 where la > 0).
-__device__ __forceinline__ float one_minus_sq(float w, float a) {
-    float p = __builtin_fmaf(w, 1.0f / 720.0f, 1.0f / 120.0f);
-    p = __builtin_fmaf(w, p, 1.0f / 24.0f);
-    p = __builtin_fmaf(w, p, 1.0f / 6.0f);
-    p = __builtin_fmaf(w, p, 0.5f);
-    p = __builtin_fmaf(w, p, 1.0f);
-    // |w| < 1/4: the series' next term is below 2^-24 of it
-    const float q = w > -0.25f ? -w * p : __builtin_fmaf(-a, a, 1.0f);
+// 1 - a^2 for a = 2^{y}, y <= 0 (0 where y > 0).
+__device__ __forceinline__ float one_minus_sq(float y, float a) {
+    // -(e^w - 1) with w = 2 ln2 y, as w (1 + w/2 + w^2/6 + ...) in powers of y
+    constexpr float k = 1.38629436111989062f;
+    float p = __builtin_fmaf(y, k * k * k * k * k / 120.0f, k * k * k * k / 24.0f);
+    p = __builtin_fmaf(y, p, k * k * k / 6.0f);
+    p = __builtin_fmaf(y, p, k * k / 2.0f);
+    p = __builtin_fmaf(y, p, k);
+    // |w| < 1/8: the series' next term is below 2^-24 of it; beyond, 1 - a^2 > 0.117 loses at
+    // most 3 bits to the subtraction
+    const float series = -y * p, direct = __builtin_fmaf(-a, a, 1.0f);
+    const float q = y > -0.09f ? series : direct;
     return q < 0.0f ? 0.0f : q;
 }
 
-// Per-channel constants of a lane.
+// Per-channel constants of a lane: A and the biases, these in units of the exponential's argument.
 struct GateChannel {
-    float A, gb, ib;
+    float A, gb2, ib2;
 };
+
+__device__ __forceinline__ float gate_arg(float g, float b2) { return __builtin_fmaf(g, kLog2e, b2); }
 
 // a and b of one step.  `g`, `ig` without their biases; IG: an input gate is given.
 template <int MODE, bool IG>
@@ -74,15 +82,62 @@ __device__ __forceinline__ void gate_step(float x, float g, float ig, const Gate
         a = g;
         b = x;
     } else if constexpr (MODE == SSM_GATE_SIGMOID) {
-        const Sig s = sigmoid_pair(g + c.gb);
+        const Sig s = sigmoid_pair(gate_arg(g, c.gb2));
         a = s.c;
         b = s.s * x;
     } else {
-        const float la = c.A * sigmoid_pair(g + c.gb).s;
-        a = hw_exp2(la * kLog2e);
-        b = __builtin_amdgcn_sqrtf(one_minus_sq(2.0f * la, a)) * x;
-        if constexpr (IG) b *= sigmoid_pair(ig + c.ib).s;
+        const float y = c.A * kLog2e * sigmoid(gate_arg(g, c.gb2));
+        a = hw_exp2(y);
+        b = __builtin_amdgcn_sqrtf(one_minus_sq(y, a)) * x;
+        if constexpr (IG) b *= sigmoid(gate_arg(ig, c.ib2));
     }
+}
+
+// One step with all that its gradients need.
+template <int MODE, bool IG>
+struct Gate {
+    float a, w;  // h_t = a h_{t-1} + w x
+    float s, sc; // the gate's logistic and its derivative
+    float i, ic; // the input gate's
+    float beta, inv_beta;
+};
+
+struct Logistic {
+    float s, sc;  // sig(v), sig(v) (1 - sig(v))
+};
+__device__ __forceinline__ Logistic logistic(float v2) {
+    const float t = hw_exp2(-fabsf(v2)), hi = hw_rcp(1.0f + t), lo = t * hi;
+    return {v2 < 0.0f ? lo : hi, lo * hi};
+}
+
+template <int MODE, bool IG>
+__device__ __forceinline__ Gate<MODE, IG> gate_of(float g, float ig, const GateChannel &c) {
+    Gate<MODE, IG> o = {};
+    if constexpr (MODE == SSM_GATE_DECAY) {
+        o.a = g;
+        o.w = 1.0f;
+    } else if constexpr (MODE == SSM_GATE_SIGMOID) {
+        const Sig s = sigmoid_pair(gate_arg(g, c.gb2));
+        o.a = s.c;
+        o.w = o.s = s.s;
+        o.sc = s.s * s.c;
+    } else {
+        const Logistic r = logistic(gate_arg(g, c.gb2));
+        o.s = r.s;
+        o.sc = r.sc;
+        const float y = c.A * kLog2e * r.s;
+        o.a = hw_exp2(y);
+        const float q = one_minus_sq(y, o.a);
+        o.inv_beta = q > 0.0f ? __builtin_amdgcn_rsqf(q) : 0.0f;  // 0 where sqrt(1 - a^2) is 0
+        o.w = o.beta = q * o.inv_beta;
+        if constexpr (IG) {
+            const Logistic i = logistic(gate_arg(ig, c.ib2));
+            o.i = i.s;
+            o.ic = i.sc;
+            o.w *= i.s;
+        }
+    }
+    return o;
 }
 
 // Gradients of one step: da = dL/da (lambda h_{t-1}, 0 at a reset), db = dL/db (lambda).
@@ -92,28 +147,23 @@ struct GateGrad {
 };
 
 template <int MODE, bool IG>
-__device__ __forceinline__ GateGrad gate_grad(float x, float g, float ig, const GateChannel &c, float da, float db) {
+__device__ __forceinline__ GateGrad gate_grad(const Gate<MODE, IG> &t, float x, float A, float da, float db) {
     GateGrad o = {};
     if constexpr (MODE == SSM_GATE_DECAY) {
         o.dx = db;
         o.dg = da;
     } else if constexpr (MODE == SSM_GATE_SIGMOID) {
-        const Sig s = sigmoid_pair(g + c.gb);
-        o.dx = db * s.s;
-        o.dg = __builtin_fmaf(db, x, -da) * (s.s * s.c);
+        o.dx = db * t.s;
+        o.dg = __builtin_fmaf(db, x, -da) * t.sc;
     } else {
-        const Sig r = sigmoid_pair(g + c.gb);
-        const float la = c.A * r.s, a = hw_exp2(la * kLog2e), q = one_minus_sq(2.0f * la, a);
-        const float rs = q > 0.0f ? __builtin_amdgcn_rsqf(q) : 0.0f;  // 1 / sqrt(1 - a^2), 0 where that is 0
-        Sig i = {1.0f, 0.0f};
-        if constexpr (IG) i = sigmoid_pair(ig + c.ib);
-        const float dbb = db * (q * rs);  // dL/d(i x)
-        o.dx = dbb * i.s;
-        if constexpr (IG) o.di = dbb * x * (i.s * i.c);
+        const float di = db * x;
+        if constexpr (IG) o.di = di * t.beta * t.ic;
+        o.dx = db * t.w;
         // dL/d(log a): da a from the state, and d sqrt(1 - a^2) / d(log a) = -a^2 / sqrt(1 - a^2)
-        const float dla = a * __builtin_fmaf(-(db * i.s * x) * a, rs, da);
-        o.dA = dla * r.s;
-        o.dg = dla * c.A * (r.s * r.c);
+        const float dbeta = IG ? di * t.i : di;
+        const float dla = t.a * __builtin_fmaf(-dbeta * t.a, t.inv_beta, da);
+        o.dA = dla * t.s;
+        o.dg = dla * A * t.sc;
     }
     return o;
 }

@@ -17,83 +17,97 @@
 namespace ssm {
 namespace {
 
-constexpr int kFwdRows = 4;  // R
+template <typename IO>
+using FwdTile = Tile<IO, 4, 4, 512>;
+static_assert(FwdTile<io_bf16>::T == FwdTile<io_f32>::T && FwdTile<io_bf16>::T <= SSM_GATED_TILE, "tile size");
+static_assert(SSM_GATED_BLOCK % FwdTile<io_bf16>::R == 0, "checkpoints lie between lane groups");
 
-template <typename IO, int MODE, bool IG, int R>
-__global__ __launch_bounds__(kGatedThreads) void gated_scan_kernel(ssm_gated_scan_args_t a, int chains, int tiles,
-                                                                   u64_t *rec, unsigned *tickets) {
-    constexpr int V = TileShape<IO>::V, CB = TileShape<IO>::CB, G = kRowGroups, T = G * R;
-    __shared__ __attribute__((aligned(16))) float sp[G][CB], sl[G][CB];
+template <typename IO, int MODE, bool IG>
+__global__ __launch_bounds__(FwdTile<IO>::THREADS) void gated_scan_kernel(ssm_gated_scan_args_t a, int chains,
+                                                                         int tiles, u64_t *rec, unsigned *tickets) {
+    using TL = FwdTile<IO>;
+    constexpr int V = TL::V, CB = TL::CB, G = TL::G, T = TL::T, R = TL::R, W = TL::W;
+    constexpr int NP = TL::THREADS / CB, GP = G / NP;  // runs of GP lane groups
+    __shared__ __attribute__((aligned(16))) float sp[G][CB], sl[G][CB], pp[NP][CB], pl[NP][CB], sc[3][CB];
     __shared__ int s_tile;
     const int tid = threadIdx.x;
-    // consecutive workgroups take different chains, so that a chain stays on one XCD where the
-    // number of chains is a multiple of 8
-    const int chain = blockIdx.x % chains;
-    int tile = 0;
-    if (tiles > 1) {
-        if (tid == 0) s_tile = (int)atomicAdd(&tickets[chain], 1u);
-        __syncthreads();
-        tile = s_tile;
-    }
+    const int chain = chain_of(blockIdx.x, chains, tiles);
     const int nblk = (int)((a.dim + CB - 1) / CB);
     const int cblk = chain % nblk;
+    if (tid == 0) s_tile = tiles > 1 ? (int)atomicAdd(&tickets[chain], 1u) : 0;
+    if (tid < CB) {
+        const int d = min(cblk * CB + tid, (int)a.dim - 1);
+        sc[0][tid] = MODE == SSM_GATE_RATE ? a.A[d] : 0.0f;
+        sc[1][tid] = MODE != SSM_GATE_DECAY && a.gate_bias ? a.gate_bias[d] * kLog2e : 0.0f;
+        sc[2][tid] = IG && a.in_bias ? a.in_bias[d] * kLog2e : 0.0f;
+    }
+    __syncthreads();
+    const int tile = s_tile;
     const int64_t b = chain / nblk, L = a.seqlen, t0 = (int64_t)tile * T;
-    const int D = (int)a.dim, d0 = cblk * CB + (tid % kLanesPerRow) * V, nv = min(V, D - d0), g = tid / kLanesPerRow;
+    const int D = (int)a.dim, lc = tid % TL::LANES * V, d0 = cblk * CB + lc, nv = min(V, D - d0), g = tid / TL::LANES;
     const int left = (int)min(L - t0, (int64_t)T);  // valid steps of this tile
 
-    GateChannel c[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const int d = min(d0 + v, D - 1);
-        c[v].A = MODE == SSM_GATE_RATE ? a.A[d] : 0.0f;
-        c[v].gb = MODE != SSM_GATE_DECAY && a.gate_bias ? a.gate_bias[d] : 0.0f;
-        c[v].ib = IG && a.in_bias ? a.in_bias[d] : 0.0f;
-    }
     const int64_t row0 = (b * L + t0) * D * IO::bytes;
     uint32_t off[R];
 #pragma unroll
     for (int j = 0; j < R; ++j)  // steps past the end read the last one and are made the identity below
         off[j] = ((uint32_t)min(g * R + j, left - 1) * (uint32_t)D + (uint32_t)d0) * IO::bytes;
-    u32x4_t qx[R], qg[R], qi[R];
-    load_rows<IO, R>(static_cast<const char *>(a.x) + row0, off, nv, qx);
-    load_rows<IO, R>(static_cast<const char *>(a.gate) + row0, off, nv, qg);
-    if constexpr (IG) load_rows<IO, R>(static_cast<const char *>(a.in_gate) + row0, off, nv, qi);
-    bool cut[R];
-#pragma unroll
-    for (int j = 0; j < R; ++j) cut[j] = a.reset && a.reset[b * L + t0 + min(g * R + j, left - 1)] != 0;
-
+    Words<W> qx[R], qg[R], qi[R];
+    load_rows<IO, W, R>(static_cast<const char *>(a.x) + row0, off, nv, qx);
+    load_rows<IO, W, R>(static_cast<const char *>(a.gate) + row0, off, nv, qg);
+    if constexpr (IG) load_rows<IO, W, R>(static_cast<const char *>(a.in_gate) + row0, off, nv, qi);
     float p[R][V], l[R][V];
+    auto step = [&](int j, int v, float &at, float &bt) {
+        gate_step<MODE, IG>(lane_elem<IO>(qx[j], v), lane_elem<IO>(qg[j], v), IG ? lane_elem<IO>(qi[j], v) : 0.0f, GateChannel{sc[0][lc + v], sc[1][lc + v], sc[2][lc + v]},
+                            at, bt);
+    };
+    const bool special = left < T || a.reset;  // the same for the whole workgroup
 #pragma unroll
     for (int j = 0; j < R; ++j) {
-        const bool in = g * R + j < left;
+        float at[V], bt[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            float at, bt;
-            gate_step<MODE, IG>(lane_elem<IO>(qx[j], v), lane_elem<IO>(qg[j], v), IG ? lane_elem<IO>(qi[j], v) : 0.0f,
-                                c[v], at, bt);
-            const float pp = j ? p[j - 1][v] : 1.0f, pl = j ? l[j - 1][v] : 0.0f;
-            p[j][v] = !in ? pp : cut[j] ? __builtin_nanf("") : at * pp;
-            l[j][v] = !in ? pl : cut[j] ? bt : __builtin_fmaf(at, pl, bt);
+            step(j, v, at[v], bt[v]);
+            p[j][v] = j ? at[v] * p[j - 1][v] : at[v];
+            l[j][v] = __builtin_fmaf(at[v], j ? l[j - 1][v] : 0.0f, bt[v]);  // (a NaN decay shows from the first step)
         }
-    }
+        if (special) {
+            const bool in = g * R + j < left;
+            const bool cut = a.reset && a.reset[b * L + t0 + min(g * R + j, left - 1)] != 0;
 #pragma unroll
-    for (int v = 0; v < V; v += 4) {
-        const int ch = (tid % kLanesPerRow) * V + v;
-        *reinterpret_cast<float4 *>(&sp[g][ch]) = make_float4(p[R - 1][v], p[R - 1][v + 1], p[R - 1][v + 2], p[R - 1][v + 3]);
-        *reinterpret_cast<float4 *>(&sl[g][ch]) = make_float4(l[R - 1][v], l[R - 1][v + 1], l[R - 1][v + 2], l[R - 1][v + 3]);
+            for (int v = 0; v < V; ++v) {
+                p[j][v] = !in ? (j ? p[j - 1][v] : 1.0f) : cut ? __builtin_nanf("") : p[j][v];
+                l[j][v] = !in ? (j ? l[j - 1][v] : 0.0f) : cut ? bt[v] : l[j][v];
+            }
+        }
+        __builtin_amdgcn_sched_barrier(0);  // a row at a time: fewer live registers
     }
+    lds_put<V>(&sp[g][lc], p[R - 1]);
+    lds_put<V>(&sl[g][lc], l[R - 1]);
     __syncthreads();
-    if (tid < CB) {
-        const int d = cblk * CB + tid;
-        float tp = 1.0f, tl = 0.0f;
-#pragma unroll 8
-        for (int i = 0; i < G; ++i) {
-            const float p = sp[i][tid];
-            tl = run_apply(p, sl[i][tid], tl);
-            tp *= p;
+    // a thread per channel and run of GP groups: the runs first, then one thread per channel over
+    // the runs and back through the groups
+    const int ch = tid % CB, part = tid / CB, d = cblk * CB + ch;
+    float tp = 1.0f, tl = 0.0f;
+#pragma unroll
+    for (int i = 0; i < GP; ++i) {
+        const float gp = sp[part * GP + i][ch];
+        tl = run_apply(gp, sl[part * GP + i][ch], tl);
+        tp *= gp;
+    }
+    pp[part][ch] = tp;
+    pl[part][ch] = tl;
+    __syncthreads();
+    if (part == 0) {
+        tp = 1.0f;
+        tl = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            tl = run_apply(pp[i][ch], pl[i][ch], tl);
+            tp *= pp[i][ch];
         }
         float h = tile == 0 && a.h0 && d < D ? a.h0[b * D + d] : 0.0f;
-        u64_t *mine = rec + ((int64_t)chain * tiles + tile) * CB + tid;
+        u64_t *mine = rec + ((int64_t)chain * tiles + tile) * CB + ch;
         if (tile > 0) {
             if (tile + 1 < tiles) rec_put(mine, rec_hi(tp), tl);
             h = chain_enter(mine, CB, tile);
@@ -103,27 +117,37 @@ __global__ __launch_bounds__(kGatedThreads) void gated_scan_kernel(ssm_gated_sca
             rec_put(mine, kRecState, after);
         else if (a.h_final && d < D)
             a.h_final[b * D + d] = after;
-#pragma unroll 8
-        for (int i = 0; i < G; ++i) {
-            if (i * R % SSM_GATED_BLOCK == 0 && a.checkpoints && d < D && i * R < left)
-                a.checkpoints[((t0 + i * R) / SSM_GATED_BLOCK * a.batch + b) * D + d] = h;
-            const float p = sp[i][tid];
-            sp[i][tid] = h;
-            h = run_apply(p, sl[i][tid], h);
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            const float q = pp[i][ch];
+            pp[i][ch] = h;
+            h = run_apply(q, pl[i][ch], h);
         }
+    }
+    __syncthreads();
+    float h = pp[part][ch];
+#pragma unroll
+    for (int i = 0; i < GP; ++i) {
+        const int step = (part * GP + i) * R;
+        if ((t0 + step) % SSM_GATED_BLOCK == 0 && a.checkpoints && d < D && step < left)
+            a.checkpoints[((t0 + step) / SSM_GATED_BLOCK * a.batch + b) * D + d] = h;
+        const float gp = sp[part * GP + i][ch];
+        sp[part * GP + i][ch] = h;
+        h = run_apply(gp, sl[part * GP + i][ch], h);
     }
     __syncthreads();
     if (a.y) {
         float e[V];
 #pragma unroll
-        for (int v = 0; v < V; ++v) e[v] = sp[g][(tid % kLanesPerRow) * V + v];
+        for (int v = 0; v < V; ++v) e[v] = sp[g][lc + v];
         char *out = static_cast<char *>(a.y) + row0;
 #pragma unroll
         for (int j = 0; j < R; ++j) {
             float f[V];
 #pragma unroll
-            for (int v = 0; v < V; ++v) f[v] = run_apply(p[j][v], l[j][v], e[v]);
-            if (g * R + j < left) store_words<IO>(out + off[j], nv, lane_pack<IO>(f));
+            for (int v = 0; v < V; ++v)
+                f[v] = a.reset ? run_apply(p[j][v], l[j][v], e[v]) : __builtin_fmaf(p[j][v], e[v], l[j][v]);
+            if (g * R + j < left) store_row<IO>(out + off[j], nv, lane_pack<IO, W>(f));
         }
     }
 }
@@ -132,7 +156,8 @@ template <typename IO, int MODE, bool IG>
 __global__ __launch_bounds__(64) void gated_step_kernel(ssm_gated_step_args_t a) {
     const int64_t d = (int64_t)blockIdx.x * 64 + threadIdx.x, b = blockIdx.y;
     if (d >= a.dim) return;
-    GateChannel c = {a.A ? a.A[d] : 0.0f, a.gate_bias ? a.gate_bias[d] : 0.0f, a.in_bias ? a.in_bias[d] : 0.0f};
+    GateChannel c = {a.A ? a.A[d] : 0.0f, a.gate_bias ? a.gate_bias[d] * kLog2e : 0.0f,
+                           a.in_bias ? a.in_bias[d] * kLog2e : 0.0f};
     const int64_t i = b * a.dim + d;
     float at, bt;
     gate_step<MODE, IG>(load_io<IO>(a.x, i), load_io<IO>(a.gate, i), IG ? load_io<IO>(a.in_gate, i) : 0.0f, c, at, bt);
@@ -155,15 +180,12 @@ __global__ __launch_bounds__(256) void chain_init_kernel(uint4 *rec, int64_t n16
 }
 
 ChainPlan fwd_plan(const ssm_gated_scan_args_t &a) {
-    const int64_t cb = a.io_dtype == SSM_BF16 ? TileShape<io_bf16>::CB : TileShape<io_f32>::CB;
-    const int64_t t = kRowGroups * kFwdRows;
+    const int64_t cb = a.io_dtype == SSM_BF16 ? FwdTile<io_bf16>::CB : FwdTile<io_f32>::CB;
+    const int64_t t = FwdTile<io_bf16>::T;
     return ChainPlan{a.batch * ((a.dim + cb - 1) / cb), (a.seqlen + t - 1) / t, cb};
 }
 
 }  // namespace
-
-static_assert(SSM_GATED_BLOCK % kFwdRows == 0 && kRowGroups * kFwdRows <= SSM_GATED_TILE, "tile and checkpoint sizes");
-static_assert((kRowGroups * kFwdRows) % SSM_GATED_BLOCK == 0, "a tile begins at a checkpoint");
 
 hipError_t launch_chain_init(const ChainPlan &p, void *workspace, hipStream_t stream) {
     const int64_t n16 = (int64_t)(p.rec_bytes() / 16);
@@ -186,8 +208,8 @@ hipError_t launch_gated_scan_fwd(const ssm_gated_scan_args_t &a, hipStream_t str
     }
     const unsigned grid = (unsigned)(p.chains * p.tiles);
     gate_dispatch(a.io_dtype, a.mode, a.in_gate != nullptr, [&](auto io, auto mode, auto ig) {
-        gated_scan_kernel<decltype(io), decltype(mode)::value, decltype(ig)::value, kFwdRows>
-            <<<grid, kGatedThreads, 0, stream>>>(a, (int)p.chains, (int)p.tiles, rec, tickets);
+        gated_scan_kernel<decltype(io), decltype(mode)::value, decltype(ig)::value>
+            <<<grid, FwdTile<decltype(io)>::THREADS, 0, stream>>>(a, (int)p.chains, (int)p.tiles, rec, tickets);
     });
     return hipGetLastError();
 }

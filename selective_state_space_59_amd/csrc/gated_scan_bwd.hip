@@ -18,146 +18,216 @@
 namespace ssm {
 namespace {
 
-constexpr int R = 4, G = kRowGroups, T = G * R;
-static_assert(T == SSM_GATED_BLOCK, "a tile begins at its checkpoint");
+template <typename IO>
+using BwdTile = Tile<IO, 4, 4, 256>;
+constexpr int T = BwdTile<io_bf16>::T;
+static_assert(T % SSM_GATED_BLOCK == 0 && BwdTile<io_f32>::T == T, "a tile begins at a checkpoint");
 
-template <typename IO, int MODE, bool IG>
-__global__ __launch_bounds__(kGatedThreads) void gated_bwd_kernel(ssm_gated_scan_bwd_args_t a, const float *ck,
+template <bool IG>
+__device__ __forceinline__ void pin_row(uint32_t &x, uint32_t &g, uint32_t &i, uint32_t &d) {
+    asm volatile("" : "+v"(x), "+v"(g), "+v"(d));
+    if constexpr (IG) asm volatile("" : "+v"(i));
+}
+
+template <typename IO, int MODE, bool IG, bool SPECIAL>
+__global__ __launch_bounds__(BwdTile<IO>::THREADS) void gated_bwd_kernel(ssm_gated_scan_bwd_args_t a, const float *ck,
                                                                   float *part, int chains, int tiles, u64_t *rec,
                                                                   unsigned *tickets) {
-    constexpr int V = TileShape<IO>::V, CB = TileShape<IO>::CB, PER = V / 4;  // channels of a register
+    using TL = BwdTile<IO>;
+    constexpr int V = TL::V, CB = TL::CB, G = TL::G, R = TL::R, W = TL::W;
+    constexpr int PER = V / W;  // channels of a word
     // the groups' decay products, forward runs and backward runs; later their entering states
     // and the partial sums
-    __shared__ __attribute__((aligned(16))) float sp[G][CB], sl[G][CB], sm[G][CB];
+    constexpr int NP = TL::THREADS / CB, GP = G / NP;  // runs of GP lane groups
+    __shared__ __attribute__((aligned(16))) float sp[G][CB], sl[G][CB], sm[G][CB], pp[NP][CB], pl[NP][CB], pm[NP][CB],
+        sc[3][CB];
     __shared__ int s_ticket;
-    const int tid = threadIdx.x, chain = blockIdx.x % chains;
-    int k = 0;
-    if (tiles > 1) {
-        if (tid == 0) s_ticket = (int)atomicAdd(&tickets[chain], 1u);
-        __syncthreads();
-        k = s_ticket;
-    }
-    const int tile = tiles - 1 - k;
+    const int tid = threadIdx.x, chain = chain_of(blockIdx.x, chains, tiles);
     const int nblk = (int)((a.dim + CB - 1) / CB), cblk = chain % nblk;
+    if (tid == 0) s_ticket = tiles > 1 ? (int)atomicAdd(&tickets[chain], 1u) : 0;
+    if (tid < CB) {
+        const int d = min(cblk * CB + tid, (int)a.dim - 1);
+        sc[0][tid] = MODE == SSM_GATE_RATE ? a.A[d] : 0.0f;
+        sc[1][tid] = MODE != SSM_GATE_DECAY && a.gate_bias ? a.gate_bias[d] * kLog2e : 0.0f;
+        sc[2][tid] = IG && a.in_bias ? a.in_bias[d] * kLog2e : 0.0f;
+    }
+    __syncthreads();
+    const int k = s_ticket;
+    const int tile = tiles - 1 - k;
     const int64_t b = chain / nblk, L = a.seqlen, t0 = (int64_t)tile * T;
-    const int D = (int)a.dim, lc = (tid % kLanesPerRow) * V, d0 = cblk * CB + lc, nv = min(V, D - d0);
-    const int g = tid / kLanesPerRow, left = (int)min(L - t0, (int64_t)T);
+    const int D = (int)a.dim, lc = tid % TL::LANES * V, d0 = cblk * CB + lc, nv = min(V, D - d0);
+    const int g = tid / TL::LANES, left = (int)min(L - t0, (int64_t)T);
     const int64_t row0 = (b * L + t0) * D * IO::bytes;
     uint32_t off[R];
 #pragma unroll
     for (int j = 0; j < R; ++j)
         off[j] = ((uint32_t)min(g * R + j, left - 1) * (uint32_t)D + (uint32_t)d0) * IO::bytes;
-    u32x4_t qx[R], qg[R], qi[R], qd[R];
-    load_rows<IO, R>(static_cast<const char *>(a.x) + row0, off, nv, qx);
-    load_rows<IO, R>(static_cast<const char *>(a.gate) + row0, off, nv, qg);
-    if constexpr (IG) load_rows<IO, R>(static_cast<const char *>(a.in_gate) + row0, off, nv, qi);
-    load_rows<IO, R>(static_cast<const char *>(a.dy) + row0, off, nv, qd);
+    Words<W> qx[R], qg[R], qi[R], qd[R];
+    load_rows<IO, W, R>(static_cast<const char *>(a.x) + row0, off, nv, qx);
+    load_rows<IO, W, R>(static_cast<const char *>(a.gate) + row0, off, nv, qg);
+    if constexpr (IG) load_rows<IO, W, R>(static_cast<const char *>(a.in_gate) + row0, off, nv, qi);
+    load_rows<IO, W, R>(static_cast<const char *>(a.dy) + row0, off, nv, qd);
     bool cut[R], in[R];
 #pragma unroll
     for (int j = 0; j < R; ++j) {
         cut[j] = a.reset && a.reset[b * L + t0 + min(g * R + j, left - 1)] != 0;
         in[j] = g * R + j < left;
     }
-    auto channel = [&](int v) {
-        const int d = min(d0 + v, D - 1);
-        GateChannel c;
-        c.A = MODE == SSM_GATE_RATE ? a.A[d] : 0.0f;
-        c.gb = MODE != SSM_GATE_DECAY && a.gate_bias ? a.gate_bias[d] : 0.0f;
-        c.ib = IG && a.in_bias ? a.in_bias[d] : 0.0f;
-        return c;
-    };
+    auto channel = [&](int v) { return GateChannel{sc[0][lc + v], sc[1][lc + v], sc[2][lc + v]}; };
 
+    {
+        float p[V], l[V], m[V];
 #pragma unroll
-    for (int v0 = 0; v0 < V; v0 += 4) {
-        float p[4], l[4], m[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int v = v0 + u;
+        for (int v = 0; v < V; ++v) {
             const GateChannel c = channel(v);
-            float at[R];
-            p[u] = 1.0f;
-            l[u] = m[u] = 0.0f;
+            float at[R], bt[R];
 #pragma unroll
-            for (int j = 0; j < R; ++j) {
-                float bt;
+            for (int j = 0; j < R; ++j)
                 gate_step<MODE, IG>(lane_elem<IO>(qx[j], v), lane_elem<IO>(qg[j], v),
-                                    IG ? lane_elem<IO>(qi[j], v) : 0.0f, c, at[j], bt);
-                l[u] = !in[j] ? l[u] : cut[j] ? bt : __builtin_fmaf(at[j], l[u], bt);
-                p[u] = !in[j] ? p[u] : cut[j] ? __builtin_nanf("") : at[j] * p[u];
+                                    IG ? lane_elem<IO>(qi[j], v) : 0.0f, c, at[j], bt[j]);
+            p[v] = 1.0f;
+            l[v] = m[v] = 0.0f;
+            if constexpr (!SPECIAL) {
+#pragma unroll
+                for (int j = 0; j < R; ++j) {
+                    l[v] = __builtin_fmaf(at[j], l[v], bt[j]);
+                    p[v] *= at[j];
+                    m[v] = at[R - 1 - j] * (lane_elem<IO>(qd[R - 1 - j], v) + m[v]);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < R; ++j) {
+                    l[v] = !in[j] ? l[v] : cut[j] ? bt[j] : __builtin_fmaf(at[j], l[v], bt[j]);
+                    p[v] = !in[j] ? p[v] : cut[j] ? __builtin_nanf("") : at[j] * p[v];
+                }
+#pragma unroll
+                for (int j = R - 1; j >= 0; --j)
+                    m[v] = !in[j] ? m[v] : cut[j] ? 0.0f : at[j] * (lane_elem<IO>(qd[j], v) + m[v]);
+            }
+            __builtin_amdgcn_sched_barrier(0);  // a channel at a time: fewer live registers
+        }
+        lds_put<V>(&sp[g][lc], p);
+        lds_put<V>(&sl[g][lc], l);
+        lds_put<V>(&sm[g][lc], m);
+    }
+    __syncthreads();
+    // a thread per channel and run of GP groups: the runs first, then one thread per channel over
+    // the runs, and out to the groups again
+    {
+        const int ch = tid % CB, pt = tid / CB, d = cblk * CB + ch;
+        float tp = 1.0f, tl = 0.0f, tm = 0.0f;
+#pragma unroll
+        for (int i = 0; i < GP; ++i) {
+            const int f = pt * GP + i, r = pt * GP + GP - 1 - i;
+            tl = run_apply(sp[f][ch], sl[f][ch], tl);
+            tm = run_apply(sp[r][ch], sm[r][ch], tm);
+            tp *= sp[f][ch];
+        }
+        pp[pt][ch] = tp;
+        pl[pt][ch] = tl;
+        pm[pt][ch] = tm;
+        __syncthreads();
+        if (pt == 0) {
+            tp = 1.0f;
+            tm = 0.0f;
+#pragma unroll
+            for (int i = NP - 1; i >= 0; --i) {
+                tm = run_apply(pp[i][ch], pm[i][ch], tm);
+                tp *= pp[i][ch];
+            }
+            u64_t *mine = rec + ((int64_t)chain * tiles + k) * CB + ch;
+            if (k > 0 && k + 1 < tiles) rec_put(mine, rec_hi(tp), tm);
+            float h = d < D ? ck[(t0 / SSM_GATED_BLOCK * a.batch + b) * D + d] : 0.0f;
+            float mu = k == 0 && a.dh_final && d < D ? a.dh_final[b * D + d] : 0.0f;
+            if (k > 0) mu = chain_enter(mine, CB, k);
+            const float after = run_apply(tp, tm, mu);
+            if (k + 1 < tiles)
+                rec_put(mine, kRecState, after);
+            else if (a.dh0 && d < D)
+                a.dh0[b * D + d] = after;
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+                const float l = pl[i][ch];
+                pl[i][ch] = h;
+                h = run_apply(pp[i][ch], l, h);
             }
 #pragma unroll
-            for (int j = R - 1; j >= 0; --j)
-                m[u] = !in[j] ? m[u] : cut[j] ? 0.0f : at[j] * (lane_elem<IO>(qd[j], v) + m[u]);
+            for (int i = NP - 1; i >= 0; --i) {
+                const float m = pm[i][ch];
+                pm[i][ch] = mu;
+                mu = run_apply(pp[i][ch], m, mu);
+            }
         }
-        *reinterpret_cast<float4 *>(&sp[g][lc + v0]) = make_float4(p[0], p[1], p[2], p[3]);
-        *reinterpret_cast<float4 *>(&sl[g][lc + v0]) = make_float4(l[0], l[1], l[2], l[3]);
-        *reinterpret_cast<float4 *>(&sm[g][lc + v0]) = make_float4(m[0], m[1], m[2], m[3]);
-    }
-    __syncthreads();
-    if (tid < CB) {
-        const int d = cblk * CB + tid;
-        // the tile's own run, from its last group to its first
-        float tp = 1.0f, tm = 0.0f;
-#pragma unroll 8
-        for (int i = G - 1; i >= 0; --i) {
-            const float p = sp[i][tid];
-            tm = run_apply(p, sm[i][tid], tm);
-            tp *= p;
-        }
-        u64_t *mine = rec + ((int64_t)chain * tiles + k) * CB + tid;
-        if (k > 0 && k + 1 < tiles) rec_put(mine, rec_hi(tp), tm);
-        // the states entering the groups, while the records before this one appear
-        float h = d < D ? ck[((int64_t)tile * a.batch + b) * D + d] : 0.0f;
-#pragma unroll 8
-        for (int i = 0; i < G; ++i) {
-            const float l = sl[i][tid];
-            sl[i][tid] = h;
-            h = run_apply(sp[i][tid], l, h);
-        }
-        float mu = k == 0 && a.dh_final && d < D ? a.dh_final[b * D + d] : 0.0f;
-        if (k > 0) mu = chain_enter(mine, CB, k);
-        const float after = run_apply(tp, tm, mu);
-        if (k + 1 < tiles)
-            rec_put(mine, kRecState, after);
-        else if (a.dh0 && d < D)
-            a.dh0[b * D + d] = after;
-#pragma unroll 8
-        for (int i = G - 1; i >= 0; --i) {
-            const float m = sm[i][tid];
-            sm[i][tid] = mu;
-            mu = run_apply(sp[i][tid], m, mu);
-        }
-    }
-    __syncthreads();
+        __syncthreads();
+        float h = pl[pt][ch], mu = pm[pt][ch];
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
+        for (int i = 0; i < GP; ++i) {
+            const float l = sl[pt * GP + i][ch];
+            sl[pt * GP + i][ch] = h;
+            h = run_apply(sp[pt * GP + i][ch], l, h);
+        }
+#pragma unroll
+        for (int i = GP - 1; i >= 0; --i) {
+            const float m = sm[pt * GP + i][ch];
+            sm[pt * GP + i][ch] = mu;
+            mu = run_apply(sp[pt * GP + i][ch], m, mu);
+        }
+    }
+    __syncthreads();
+    // What follows forms the gates again from the rows.  The empty asm statements keep the
+    // compiler from carrying gates over from above, and from putting a word's gradients off until
+    // the stores: either would double the registers.
+#pragma unroll
+    for (int j = 0; j < R; ++j)
+#pragma unroll
+        for (int w = 0; w < W; ++w) pin_row<IG>(qx[j].w[w], qg[j].w[w], qi[j].w[w], qd[j].w[w]);
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
         float ox[R][PER], og[R][PER], oi[R][PER];
 #pragma unroll
         for (int u = 0; u < PER; ++u) {
             const int v = w * PER + u;
             const GateChannel c = channel(v);
-            float h = sl[g][lc + v], mu = sm[g][lc + v], at[R], hp[R], sA = 0.0f, sg = 0.0f, si = 0.0f;
+            float h = sl[g][lc + v], mu = sm[g][lc + v], da[R], lam[R], sA = 0.0f, sg = 0.0f, si = 0.0f;
+            Gate<MODE, IG> t[R];
 #pragma unroll
-            for (int j = 0; j < R; ++j) {
-                float bt;
-                gate_step<MODE, IG>(lane_elem<IO>(qx[j], v), lane_elem<IO>(qg[j], v),
-                                    IG ? lane_elem<IO>(qi[j], v) : 0.0f, c, at[j], bt);
-                hp[j] = h;
-                h = cut[j] ? bt : __builtin_fmaf(at[j], h, bt);
+            for (int j = 0; j < R; ++j)
+                t[j] = gate_of<MODE, IG>(lane_elem<IO>(qg[j], v), IG ? lane_elem<IO>(qi[j], v) : 0.0f, c);
+            if constexpr (!SPECIAL) {
+#pragma unroll
+                for (int j = 0; j < R; ++j) {
+                    da[j] = h;
+                    h = __builtin_fmaf(t[j].a, h, t[j].w * lane_elem<IO>(qx[j], v));
+                }
+#pragma unroll
+                for (int j = R - 1; j >= 0; --j) {
+                    lam[j] = lane_elem<IO>(qd[j], v) + mu;
+                    da[j] *= lam[j];
+                    mu = t[j].a * lam[j];
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < R; ++j) {
+                    da[j] = h;
+                    const float b = t[j].w * lane_elem<IO>(qx[j], v);
+                    h = cut[j] ? b : __builtin_fmaf(t[j].a, h, b);
+                }
+#pragma unroll
+                for (int j = R - 1; j >= 0; --j) {  // steps past the end: no gradient
+                    lam[j] = in[j] ? lane_elem<IO>(qd[j], v) + mu : 0.0f;
+                    da[j] = cut[j] || !in[j] ? 0.0f : da[j] * lam[j];
+                    mu = !in[j] ? mu : cut[j] ? 0.0f : t[j].a * lam[j];
+                }
             }
 #pragma unroll
-            for (int j = R - 1; j >= 0; --j) {
-                const float lam = lane_elem<IO>(qd[j], v) + mu;
-                const GateGrad o = gate_grad<MODE, IG>(lane_elem<IO>(qx[j], v), lane_elem<IO>(qg[j], v),
-                                                       IG ? lane_elem<IO>(qi[j], v) : 0.0f, c,
-                                                       cut[j] ? 0.0f : lam * hp[j], lam);
-                mu = !in[j] ? mu : cut[j] ? 0.0f : at[j] * lam;
+            for (int j = 0; j < R; ++j) {
+                const GateGrad o = gate_grad<MODE, IG>(t[j], lane_elem<IO>(qx[j], v), c.A, da[j], lam[j]);
                 ox[j][u] = o.dx;
                 og[j][u] = o.dg;
                 oi[j][u] = o.di;
-                sA += in[j] ? o.dA : 0.0f;
-                sg += in[j] ? o.dg : 0.0f;
-                si += in[j] ? o.di : 0.0f;
+                sA += o.dA;
+                sg += o.dg;
+                si += o.di;
             }
             if constexpr (MODE != SSM_GATE_DECAY) {
                 // this lane's own words: read above, by no other lane
@@ -165,32 +235,36 @@ __global__ __launch_bounds__(kGatedThreads) void gated_bwd_kernel(ssm_gated_scan
                 if constexpr (MODE == SSM_GATE_RATE) sl[g][lc + v] = sA;
                 if constexpr (IG) sm[g][lc + v] = si;
             }
+            __builtin_amdgcn_sched_barrier(0);
         }
 #pragma unroll
         for (int j = 0; j < R; ++j) {
             if constexpr (IO::bytes == 2) {
-                qx[j][w] = pack_bf16x2(ox[j][0], ox[j][PER - 1]);
-                qg[j][w] = pack_bf16x2(og[j][0], og[j][PER - 1]);
-                if constexpr (IG) qi[j][w] = pack_bf16x2(oi[j][0], oi[j][PER - 1]);
+                qx[j].w[w] = pack_bf16x2(ox[j][0], ox[j][PER - 1]);
+                qg[j].w[w] = pack_bf16x2(og[j][0], og[j][PER - 1]);
+                if constexpr (IG) qi[j].w[w] = pack_bf16x2(oi[j][0], oi[j][PER - 1]);
             } else {
-                qx[j][w] = __float_as_uint(ox[j][0]);
-                qg[j][w] = __float_as_uint(og[j][0]);
-                if constexpr (IG) qi[j][w] = __float_as_uint(oi[j][0]);
+                qx[j].w[w] = __float_as_uint(ox[j][0]);
+                qg[j].w[w] = __float_as_uint(og[j][0]);
+                if constexpr (IG) qi[j].w[w] = __float_as_uint(oi[j][0]);
             }
+            pin_row<IG>(qx[j].w[w], qg[j].w[w], qi[j].w[w], qd[j].w[w]);
         }
+        __builtin_amdgcn_sched_barrier(0);
     }
 #pragma unroll
     for (int j = 0; j < R; ++j)
-        if (in[j]) {
-            store_words<IO>(static_cast<char *>(a.dx) + row0 + off[j], nv, qx[j]);
-            store_words<IO>(static_cast<char *>(a.dgate) + row0 + off[j], nv, qg[j]);
-            if constexpr (IG) store_words<IO>(static_cast<char *>(a.din_gate) + row0 + off[j], nv, qi[j]);
+        if (!SPECIAL || in[j]) {
+            store_row<IO>(static_cast<char *>(a.dx) + row0 + off[j], nv, qx[j]);
+            store_row<IO>(static_cast<char *>(a.dgate) + row0 + off[j], nv, qg[j]);
+            if constexpr (IG) store_row<IO>(static_cast<char *>(a.din_gate) + row0 + off[j], nv, qi[j]);
         }
     if constexpr (MODE != SSM_GATE_DECAY) {
         // this tile's row of the partial sums: gate_bias, then A, then in_bias
         __syncthreads();
         const int which = tid / CB, ch = tid % CB, d = cblk * CB + ch;
         constexpr int K = MODE == SSM_GATE_SIGMOID ? 1 : IG ? 3 : 2;
+        static_assert(K * CB <= TL::THREADS, "a thread per sum");
         if (which < K && d < D) {
             const float(*s)[CB] = which == 0 ? sp : which == 1 ? sl : sm;
             float v = 0.0f;
@@ -229,7 +303,7 @@ ssm_gated_scan_args_t forward_of(const ssm_gated_scan_bwd_args_t &a) {
 
 // The workspace is sized without looking at which gradients are asked for.
 BwdPlan plan_of(const ssm_gated_scan_bwd_args_t &a) {
-    const int64_t cb = a.io_dtype == SSM_BF16 ? TileShape<io_bf16>::CB : TileShape<io_f32>::CB;
+    const int64_t cb = a.io_dtype == SSM_BF16 ? BwdTile<io_bf16>::CB : BwdTile<io_f32>::CB;
     const int64_t tiles = (a.seqlen + T - 1) / T;
     BwdPlan p;
     p.chain = ChainPlan{a.batch * ((a.dim + cb - 1) / cb), tiles, cb};
@@ -245,7 +319,7 @@ BwdPlan plan_of(const ssm_gated_scan_bwd_args_t &a) {
     p.o_scratch = take(column_sums_scratch_bytes(p.rows, a.dim, p.sums));
     p.o_ck = p.o_fwd = o;
     if (!a.checkpoints) {
-        p.o_ck = take((size_t)(tiles * a.batch * a.dim) * 4);
+        p.o_ck = take((size_t)((a.seqlen + SSM_GATED_BLOCK - 1) / SSM_GATED_BLOCK * a.batch * a.dim) * 4);
         p.o_fwd = take(gated_scan_workspace_bytes(forward_of(a)));
     }
     p.total = o;
@@ -274,9 +348,16 @@ hipError_t launch_gated_scan_bwd(const ssm_gated_scan_bwd_args_t &a, hipStream_t
     unsigned *tickets = reinterpret_cast<unsigned *>(ws + p.chain.rec_bytes());
     const unsigned grid = (unsigned)(p.chain.chains * p.chain.tiles);
     gate_dispatch(a.io_dtype, a.mode, a.in_gate != nullptr, [&](auto io, auto mode, auto ig) {
-        gated_bwd_kernel<decltype(io), decltype(mode)::value, decltype(ig)::value>
-            <<<grid, kGatedThreads, 0, stream>>>(a, ck, part, (int)p.chain.chains, (int)p.chain.tiles,
-                                                 reinterpret_cast<u64_t *>(ws), tickets);
+        auto go = [&](auto special) {
+            gated_bwd_kernel<decltype(io), decltype(mode)::value, decltype(ig)::value, decltype(special)::value>
+                <<<grid, BwdTile<decltype(io)>::THREADS, 0, stream>>>(a, ck, part, (int)p.chain.chains,
+                                                                      (int)p.chain.tiles, reinterpret_cast<u64_t *>(ws),
+                                                                      tickets);
+        };
+        if (a.reset || a.seqlen % T != 0)
+            go(std::true_type{});
+        else
+            go(std::false_type{});
     });
     e = hipGetLastError();
     float *out[3] = {a.dgate_bias, a.dA, a.din_bias};

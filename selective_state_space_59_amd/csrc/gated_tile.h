@@ -8,74 +8,130 @@
 
 namespace ssm {
 
-constexpr int kLanesPerRow = 8;  // 8 lanes x 16 bytes: a 128-byte piece of a row
-constexpr int kGatedThreads = 256;
-constexpr int kRowGroups = kGatedThreads / kLanesPerRow;  // lane groups stacked in time
+// A lane holds W words (4 bytes) of each of its rows.
+template <int W>
+struct Words {
+    uint32_t w[W];
+};
 
-template <typename IO>
-struct TileShape {
-    static constexpr int V = 16 / IO::bytes;        // channels of a lane
-    static constexpr int CB = V * kLanesPerRow;     // channels of a workgroup: 64 (bf16), 32 (fp32)
+template <int W>
+__device__ __forceinline__ Words<W> load_words(const char *p) {
+    Words<W> r;
+    typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+    typedef u32x2_t u32x2_a2 __attribute__((aligned(2)));
+    typedef uint32_t u32_a2 __attribute__((aligned(2)));
+    if constexpr (W == 4) {
+        const u32x4_t v = *reinterpret_cast<const u32x4_a2 *>(p);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r.w[i] = v[i];
+    } else if constexpr (W == 2) {
+        const u32x2_t v = *reinterpret_cast<const u32x2_a2 *>(p);
+        r.w[0] = v[0];
+        r.w[1] = v[1];
+    } else {
+        r.w[0] = *reinterpret_cast<const u32_a2 *>(p);
+    }
+    return r;
+}
+
+template <int W>
+__device__ __forceinline__ void store_words(char *p, const Words<W> &q) {
+    typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+    typedef u32x2_t u32x2_a2 __attribute__((aligned(2)));
+    typedef uint32_t u32_a2 __attribute__((aligned(2)));
+    if constexpr (W == 4)
+        *reinterpret_cast<u32x4_a2 *>(p) = u32x4_t{q.w[0], q.w[1], q.w[2], q.w[3]};
+    else if constexpr (W == 2)
+        *reinterpret_cast<u32x2_a2 *>(p) = u32x2_t{q.w[0], q.w[1]};
+    else
+        *reinterpret_cast<u32_a2 *>(p) = q.w[0];
+}
+
+// How a tile lies over a workgroup: THREADS lanes, W words of R consecutive rows each; the lanes
+// of a row cover kRowBytes.
+constexpr int kRowBytes = 128;
+
+template <typename IO, int W_, int R_, int THREADS_>
+struct Tile {
+    static constexpr int W = W_, R = R_, THREADS = THREADS_;
+    static constexpr int V = 4 * W / IO::bytes;           // channels of a lane
+    static constexpr int LANES = kRowBytes / (4 * W);     // lanes of a row
+    static constexpr int CB = kRowBytes / IO::bytes;      // channels of a workgroup
+    static constexpr int G = THREADS / LANES;             // lane groups, one behind the other in time
+    static constexpr int T = G * R;                       // steps
 };
 
 // R rows of a lane: `off[j]` bytes behind the wave-uniform `base`, `nv` valid channels (the last
 // channel block of an odd width takes its elements one by one).
-template <typename IO, int R>
-__device__ __forceinline__ void load_rows(const char *base, const uint32_t (&off)[R], int nv, u32x4_t (&q)[R]) {
-    constexpr int V = TileShape<IO>::V;
-    if (nv == V) {
+template <typename IO, int W, int R>
+__device__ __forceinline__ void load_rows(const char *base, const uint32_t (&off)[R], int nv, Words<W> (&q)[R]) {
+    constexpr int V = 4 * W / IO::bytes;
+    if (nv >= V) {
 #pragma unroll
-        for (int j = 0; j < R; ++j) q[j] = *reinterpret_cast<const u32x4_a2 *>(base + off[j]);
+        for (int j = 0; j < R; ++j) q[j] = load_words<W>(base + off[j]);
     } else {
 #pragma unroll
         for (int j = 0; j < R; ++j) {
-            u32x4_t v = {0, 0, 0, 0};
+            q[j] = Words<W>{};
 #pragma unroll
             for (int e = 0; e < V; ++e)
                 if (e < nv) {
                     if constexpr (IO::bytes == 2)
-                        v[e / 2] |= (uint32_t)reinterpret_cast<const uint16_t *>(base + off[j])[e] << (16 * (e & 1));
+                        q[j].w[e / 2] |= (uint32_t)reinterpret_cast<const uint16_t *>(base + off[j])[e] << (16 * (e & 1));
                     else
-                        v[e] = reinterpret_cast<const uint32_t *>(base + off[j])[e];
+                        q[j].w[e] = reinterpret_cast<const uint32_t *>(base + off[j])[e];
                 }
-            q[j] = v;
         }
     }
 }
 
-template <typename IO>
-__device__ __forceinline__ float lane_elem(const u32x4_t &q, int v) {
-    if constexpr (IO::bytes == 2) return __uint_as_float(v & 1 ? q[v / 2] & 0xffff0000u : q[v / 2] << 16);
-    return __uint_as_float(q[v]);
-}
-
-template <typename IO>
-__device__ __forceinline__ u32x4_t lane_pack(const float (&f)[TileShape<IO>::V]) {
-    u32x4_t q;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if constexpr (IO::bytes == 2)
-            q[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
-        else
-            q[i] = __float_as_uint(f[i]);
-    }
-    return q;
-}
-
-template <typename IO>
-__device__ __forceinline__ void store_words(char *p, int nv, const u32x4_t &q) {
-    constexpr int V = TileShape<IO>::V;
-    if (nv == V) {
-        *reinterpret_cast<u32x4_a2 *>(p) = q;
+template <typename IO, int W>
+__device__ __forceinline__ void store_row(char *p, int nv, const Words<W> &q) {
+    constexpr int V = 4 * W / IO::bytes;
+    if (nv >= V) {
+        store_words(p, q);
     } else {
 #pragma unroll
         for (int e = 0; e < V; ++e)
             if (e < nv) {
                 if constexpr (IO::bytes == 2)
-                    reinterpret_cast<uint16_t *>(p)[e] = (uint16_t)(q[e / 2] >> (16 * (e & 1)));
+                    reinterpret_cast<uint16_t *>(p)[e] = (uint16_t)(q.w[e / 2] >> (16 * (e & 1)));
                 else
-                    reinterpret_cast<uint32_t *>(p)[e] = q[e];
+                    reinterpret_cast<uint32_t *>(p)[e] = q.w[e];
             }
+    }
+}
+
+template <typename IO, int W>
+__device__ __forceinline__ float lane_elem(const Words<W> &q, int v) {
+    if constexpr (IO::bytes == 2) return __uint_as_float(v & 1 ? q.w[v / 2] & 0xffff0000u : q.w[v / 2] << 16);
+    return __uint_as_float(q.w[v]);
+}
+
+template <typename IO, int W>
+__device__ __forceinline__ Words<W> lane_pack(const float (&f)[4 * W / IO::bytes]) {
+    Words<W> q;
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+        if constexpr (IO::bytes == 2)
+            q.w[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
+        else
+            q.w[i] = __float_as_uint(f[i]);
+    }
+    return q;
+}
+
+// V floats of a lane to and from LDS.
+template <int V>
+__device__ __forceinline__ void lds_put(float *p, const float (&f)[V]) {
+    if constexpr (V % 4 == 0) {
+#pragma unroll
+        for (int v = 0; v < V; v += 4) *reinterpret_cast<float4 *>(p + v) = make_float4(f[v], f[v + 1], f[v + 2], f[v + 3]);
+    } else if constexpr (V == 2) {
+        *reinterpret_cast<float2 *>(p) = make_float2(f[0], f[1]);
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) p[v] = f[v];
     }
 }
 
@@ -94,7 +150,7 @@ __device__ __forceinline__ float run_apply(float p, float l, float h) {
 // meets a state.  A record is one atomic word, so it needs no flag and no fence: the high word
 // tells what it holds, with two NaN patterns that p is never stored as.
 constexpr uint32_t kRecEmpty = 0xffffffffu, kRecState = 0xfffffffeu;
-constexpr int kLook = 8;  // records read at once
+constexpr int kLook = 8;  // records looked at together
 
 typedef unsigned long long u64_t;
 
@@ -111,42 +167,43 @@ __device__ __forceinline__ void rec_put(u64_t *r, uint32_t hi, float lo) {
 // runs, so the tiles before it belong to workgroups that run or have ended, the first never
 // waits, and a tile leaves its state without waiting for a later one.
 __device__ __forceinline__ float chain_enter(const u64_t *rec, int64_t stride, int k) {
-    float h = 0.0f;
-    bool found = false;
-    while (!found) {
+    for (;;) {
         u64_t v[kLook];
 #pragma unroll
         for (int j = 0; j < kLook; ++j)
             v[j] = j < k ? __hip_atomic_load(rec - (int64_t)(j + 1) * stride, __ATOMIC_RELAXED,
                                              __HIP_MEMORY_SCOPE_AGENT)
                          : ~(u64_t)0;
-        int at = -1;
-        bool open = true;
+        float h = 0.0f;
+        bool known = false;  // h is the state after the record at hand
 #pragma unroll
-        for (int j = 0; j < kLook; ++j) {
+        for (int j = kLook - 1; j >= 0; --j) {
             const uint32_t hi = (uint32_t)(v[j] >> 32);
-            if (open && hi == kRecState) at = j;
-            open = open && hi != kRecState && hi != kRecEmpty;
+            const float lo = __uint_as_float((uint32_t)v[j]);
+            known = hi == kRecState || (known && hi != kRecEmpty);
+            h = hi == kRecState ? lo : run_apply(__uint_as_float(hi), lo, h);
         }
-        if (at >= 0) {
-#pragma unroll
-            for (int j = kLook - 1; j >= 0; --j) {
-                const float lo = __uint_as_float((uint32_t)v[j]), p = __uint_as_float((uint32_t)(v[j] >> 32));
-                if (j == at)
-                    h = lo;
-                else if (j < at)
-                    h = run_apply(p, lo, h);
-            }
-            found = true;
-        } else {
-            __builtin_amdgcn_s_sleep(1);
-        }
+        if (__all(known)) return h;
+        __builtin_amdgcn_s_sleep(1);
     }
-    return h;
 }
 
 // p as a record's high word: one NaN pattern for every NaN.
 __device__ __forceinline__ uint32_t rec_hi(float p) { return p != p ? 0x7fc00000u : __float_as_uint(p); }
+
+// The chain of workgroup i of chains * tiles (the tile within it is the ticket it draws).
+// Workgroups go to the XCDs in turn.  A short chain's tiles are dealt out one chain after the
+// other; a long chain's run over all XCDs, eight at a time, so that no chain waits for one XCD that
+// is behind (1M tokens x 1024 channels: 1750 us, against 2013 us dealt out; the 130M-like layer,
+// 8 tiles a chain, 52.4 us dealt out against 53.1).  Either way every chain gets `tiles`.
+constexpr int kLongChain = 64;
+
+__device__ __forceinline__ int chain_of(unsigned i, int chains, int tiles) {
+    constexpr int kXcds = 8;
+    const unsigned whole = (unsigned)(tiles / kXcds * kXcds) * chains;
+    if (tiles < kLongChain || i >= whole) return i % chains;
+    return i / kXcds % chains;
+}
 
 // Workspace of a chained launch: the records, then one ticket counter per chain.
 struct ChainPlan {
