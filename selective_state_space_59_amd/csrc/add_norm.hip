@@ -33,7 +33,7 @@ __device__ __forceinline__ void stream8(const Raw8<IO> &x, const Raw8<RES> &res,
 }
 
 template <typename IO, typename RES, bool EXTRA, typename SH>
-__global__ __launch_bounds__(SH::TEAM == 0 ? 1024 : kTeamThreads) void add_norm_kernel(ssm_add_norm_args_t a,
+__global__ __launch_bounds__(SH::THREADS) void add_norm_kernel(ssm_add_norm_args_t a,
                                                                                        int64_t slots) {
     constexpr int TEAM = SH::TEAM, NR = SH::NR;
     __shared__ SumSlots sums;
@@ -92,7 +92,7 @@ __global__ __launch_bounds__(SH::TEAM == 0 ? 1024 : kTeamThreads) void add_norm_
 }
 
 template <typename IO, typename RES, bool EXTRA, typename SH>
-__global__ __launch_bounds__(SH::TEAM == 0 ? 1024 : kTeamThreads) void add_norm_bwd_kernel(ssm_add_norm_bwd_args_t a,
+__global__ __launch_bounds__(SH::THREADS) void add_norm_bwd_kernel(ssm_add_norm_bwd_args_t a,
                                                                                            int64_t slots, float *part,
                                                                                            int64_t prows) {
     constexpr int TEAM = SH::TEAM, NR = SH::NR;
@@ -306,9 +306,10 @@ void with_types(int32_t io, int32_t res, F &&f) {
     }
 }
 
-constexpr int64_t kFwdBlocks = 2048, kBwdBlocks = 512, kLongBlocks = 256;
+constexpr int64_t kFwdBlocks = 1024, kBwdBlocks = 512, kLongBlocks = 256;
 
-// The launch shape of the backward for rows of D (the forward adds NR = 4: it holds less per row).
+// The launch shape of the backward for rows of D (the forward adds half a wave with NR = 3 and a
+// wave with NR = 4: it holds less per row, and leaves no partial sums).
 RowGrid bwd_grid(int64_t rows, int64_t D) {
     if (D > kBlockRow) return RowGrid{(unsigned)std::min(rows, kLongBlocks), 1024, std::min(rows, kLongBlocks)};
     return row_grid(D <= 64 ? 8 : D <= 256 ? 32 : D <= 1024 ? 64 : 0, D, rows, 1, kBwdBlocks);
@@ -338,9 +339,11 @@ hipError_t launch_add_norm_fwd(const ssm_add_norm_args_t &a, hipStream_t stream)
         if (D <= 64) go(Shape<8, 1>{});
         else if (D <= 256) go(Shape<32, 1>{});
         else if (D <= 512) go(Shape<64, 1>{});
+        else if (D <= 768) go(Shape<32, 3>{});
         else if (D <= 1024) go(Shape<64, 2>{});
         else if (D <= 2048) go(Shape<64, 4>{});
-        else if (D <= kBlockRow) go(Shape<0, 1>{});
+        else if (D <= 4096) go(Shape<0, 1, 512>{});
+        else if (D <= kBlockRow) go(Shape<0, 1, 1024>{});
         else
             add_norm_long_kernel<IO, RES><<<(unsigned)std::min<int64_t>(a.rows, 2048), 1024, 0, stream>>>(a);
     });
@@ -370,7 +373,8 @@ hipError_t launch_add_norm_bwd(const ssm_add_norm_bwd_args_t &a, hipStream_t str
         else if (D <= 256) go(Shape<32, 1>{});
         else if (D <= 512) go(Shape<64, 1>{});
         else if (D <= 1024) go(Shape<64, 2>{});
-        else if (D <= kBlockRow) go(Shape<0, 1>{});
+        else if (D <= 4096) go(Shape<0, 1, 512>{});
+        else if (D <= kBlockRow) go(Shape<0, 1, 1024>{});
         else
             add_norm_bwd_long_kernel<IO, RES><<<g.blocks, 1024, 0, stream>>>(a, part, n);
     });

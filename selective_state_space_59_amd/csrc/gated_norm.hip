@@ -16,7 +16,7 @@ namespace {
 __device__ __forceinline__ float logistic(float z) { return hw_rcp(1.0f + hw_exp2(-z * kLog2e)); }
 
 template <typename IO, bool FIRST, typename SH>
-__global__ __launch_bounds__(SH::TEAM == 0 ? 1024 : kTeamThreads) void gated_norm_kernel(ssm_gated_norm_args_t a,
+__global__ __launch_bounds__(SH::THREADS) void gated_norm_kernel(ssm_gated_norm_args_t a,
                                                                                          int64_t slots) {
     constexpr int TEAM = SH::TEAM, NR = SH::NR;
     __shared__ SumSlots sums;
@@ -63,7 +63,7 @@ __global__ __launch_bounds__(SH::TEAM == 0 ? 1024 : kTeamThreads) void gated_nor
 }
 
 template <typename IO, bool FIRST, typename SH>
-__global__ __launch_bounds__(SH::TEAM == 0 ? 1024 : kTeamThreads) void gated_norm_bwd_kernel(
+__global__ __launch_bounds__(SH::THREADS) void gated_norm_bwd_kernel(
     ssm_gated_norm_bwd_args_t a, int64_t slots, float *part) {
     constexpr int TEAM = SH::TEAM, NR = SH::NR;
     __shared__ SumSlots sums;
@@ -81,15 +81,31 @@ __global__ __launch_bounds__(SH::TEAM == 0 ? 1024 : kTeamThreads) void gated_nor
         n[c] = max(0, min(8, S - i));
         load_vec(a.w, col + i, n[c], w[c]);
     }
-    for (int64_t row = t.row; row < a.rows; row += t.step) {
+    Raw8<IO> x[NR], z[NR], dy[NR], x1[NR], z1[NR], dy1[NR];
+    auto load_row = [&](int64_t row, Raw8<IO>(&x)[NR], Raw8<IO>(&z)[NR], Raw8<IO>(&dy)[NR]) {
         const int64_t base = row * a.dim + col;
-        Raw8<IO> x[NR], z[NR], dy[NR];
 #pragma unroll
         for (int c = 0; c < NR; ++c) {
             const int i = 8 * (lane + c * width);
             x[c] = load8<IO>(a.x, base + i, n[c]);
             z[c] = load8<IO>(a.z, base + i, n[c]);
             dy[c] = load8<IO>(a.dy, base + i, n[c]);
+        }
+    };
+    constexpr bool AHEAD = NR <= 2;  // the next row is on its way while this one's sums are formed
+    if (AHEAD && t.row < a.rows) load_row(t.row, x1, z1, dy1);
+    for (int64_t row = t.row; row < a.rows; row += t.step) {
+        const int64_t base = row * a.dim + col;
+        if constexpr (AHEAD) {
+#pragma unroll
+            for (int c = 0; c < NR; ++c) {
+                x[c] = x1[c];
+                z[c] = z1[c];
+                dy[c] = dy1[c];
+            }
+            if (row + t.step < a.rows) load_row(row + t.step, x1, z1, dy1);
+        } else {
+            load_row(row, x, z, dy);
         }
         float sg[NR][8], s = 0.0f, dot = 0.0f;
 #pragma unroll
@@ -198,15 +214,25 @@ __global__ __launch_bounds__(1024) void gated_norm_bwd_long_kernel(ssm_gated_nor
 
 constexpr int64_t kFwdBlocks = 2048, kBwdBlocks = 512, kLongBlocks = 256;
 
-int team_of(int64_t S, int64_t wave_most) { return S <= 64 ? 8 : S <= 256 ? 32 : S <= wave_most ? 64 : 0; }
+// Groups of 513 to 768 channels: half a wave with three groups of 8 a lane leaves fewer lanes idle
+// than a wave with two (16384 x 5120 in 8 groups of 640: forward and backward 262 us against
+// 283), but each of its teams leaves a row of partial sums, so in the backward only where several
+// groups share a row (16384 x 768 in one group: 79 against 75).
+bool half_wave(int64_t S) { return S > 512 && S <= 768; }
+
+int bwd_team(int64_t S, int64_t groups) {
+    if (half_wave(S) && groups >= 4) return 32;
+    return S <= 64 ? 8 : S <= 256 ? 32 : S <= 1024 ? 64 : 0;
+}
 
 RowGrid bwd_grid(int64_t rows, int64_t S, int64_t groups) {
-    return row_grid(team_of(S, 1024), std::min<int64_t>(S, kBlockRow), rows, groups, S > kBlockRow ? kLongBlocks : kBwdBlocks);
+    return row_grid(bwd_team(S, groups), std::min<int64_t>(S, kBlockRow), rows, groups,
+                    S > kBlockRow ? kLongBlocks : kBwdBlocks);
 }
 
 int64_t partial_rows(int64_t rows, int64_t S, int64_t groups) {
     const RowGrid g = bwd_grid(rows, S, groups);
-    return team_of(S, 1024) == 64 ? g.blocks / groups : g.slots;
+    return bwd_team(S, groups) == 64 ? g.blocks / groups : g.slots;
 }
 
 }  // namespace
@@ -224,9 +250,11 @@ hipError_t launch_gated_norm_fwd(const ssm_gated_norm_args_t &a, hipStream_t str
         if (S <= 64) go(Shape<8, 1>{});
         else if (S <= 256) go(Shape<32, 1>{});
         else if (S <= 512) go(Shape<64, 1>{});
+        else if (half_wave(S)) go(Shape<32, 3>{});
         else if (S <= 1024) go(Shape<64, 2>{});
         else if (S <= 2048) go(Shape<64, 4>{});
-        else if (S <= kBlockRow) go(Shape<0, 1>{});
+        else if (S <= 4096) go(Shape<0, 1, 512>{});
+        else if (S <= kBlockRow) go(Shape<0, 1, 1024>{});
         else {
             const RowGrid g = row_grid(0, kBlockRow, a.rows, a.groups, kFwdBlocks);
             gated_norm_long_kernel<IO, FIRST><<<g.blocks, 1024, 0, stream>>>(a, g.slots);
@@ -263,8 +291,10 @@ hipError_t launch_gated_norm_bwd(const ssm_gated_norm_bwd_args_t &a, hipStream_t
         if (S <= 64) go(Shape<8, 1>{});
         else if (S <= 256) go(Shape<32, 1>{});
         else if (S <= 512) go(Shape<64, 1>{});
+        else if (bwd_team(S, a.groups) == 32) go(Shape<32, 3>{});
         else if (S <= 1024) go(Shape<64, 2>{});
-        else if (S <= kBlockRow) go(Shape<0, 1>{});
+        else if (S <= 4096) go(Shape<0, 1, 512>{});
+        else if (S <= kBlockRow) go(Shape<0, 1, 1024>{});
         else gated_norm_bwd_long_kernel<IO, FIRST><<<g.blocks, 1024, 0, stream>>>(a, g.slots, part);
     };
     auto with_io = [&](auto io) {

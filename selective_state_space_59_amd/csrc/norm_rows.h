@@ -21,10 +21,10 @@ namespace ssm {
 constexpr int kBlockRow = 8192;   // longest row held in a workgroup's registers
 constexpr int kTeamThreads = 256; // workgroup of the teams of up to a wave
 
-// TEAM lanes (1 << n up to 64, or 0: the workgroup) with NR groups of 8 each.
-template <int TEAM_, int NR_>
+// TEAM lanes (1 << n up to 64, or 0: the workgroup, of at most THREADS) with NR groups of 8 each.
+template <int TEAM_, int NR_, int THREADS_ = kTeamThreads>
 struct Shape {
-    static constexpr int TEAM = TEAM_, NR = NR_;
+    static constexpr int TEAM = TEAM_, NR = NR_, THREADS = THREADS_;
 };
 
 template <int TEAM>

@@ -840,28 +840,52 @@ def gated_checkpoint_shape(batch: int, seqlen: int, dim: int) -> tuple:
     return ((seqlen + GATED_BLOCK - 1) // GATED_BLOCK, batch, dim)
 
 
-def _call(fn, args, dev: torch.device):
-    """One library call on torch's current stream of `dev`, with that device current."""
-    if dev.index == torch.cuda.current_device():
-        return fn(ctypes.byref(args), _stream(dev))
-    with torch.cuda.device(dev):
-        return fn(ctypes.byref(args), _stream(dev))
+# The calls below serve single decode tokens, where the marshalling itself is what a step costs:
+# an argument that is as expected passes one expression, and only one that is not goes to the
+# checks that name what is wrong.
+_raw_stream = torch._C._cuda_getCurrentRawStream  # torch.cuda.current_stream(i).cuda_stream
+
+
+def _arg(t, name, shape, dtype, device):
+    """Address of an optional tensor argument (None: not given)."""
+    if t is None:
+        return None
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device
+            and t.is_contiguous()):
+        return t.data_ptr()
+    return _opt(t, name, shape, dtype, device).data_ptr()
+
+
+def _need(t, name, shape, dtype, device):
+    if t is None:
+        raise ValueError("%s is required" % name)
+    return _arg(t, name, shape, dtype, device)
 
 
 def _run(name: str, args, dev: torch.device, size_fn=None, workspace: Optional[torch.Tensor] = None):
-    """ssm_<name>(args), with a workspace where size_fn(args) asks for one.  Invalid sizes are
-    reported by the call itself, which checks its arguments before anything is launched."""
+    """ssm_<name>(args) on torch's current stream of `dev`, with that device current and with a
+    workspace where size_fn(args) asks for one.  Invalid sizes are reported by the call itself,
+    which checks its arguments before anything is launched."""
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _run(name, args, dev, size_fn, workspace)
     L = lib()
-    fn = getattr(L, name)
+    ref = ctypes.byref(args)
+    stream = _raw_stream(dev.index)
     if size_fn is not None:
-        need = getattr(L, size_fn)(ctypes.byref(args))
+        need = getattr(L, size_fn)(ref)
         if need != _NO_SIZE and need > 0:
-            ws = workspace if workspace is not None else _workspace(dev, need)
-            if ws.device != dev or not ws.is_contiguous() or ws.numel() * ws.element_size() < need:
+            if workspace is None:
+                # the cached buffer of this stream (see _workspace), where it is large enough
+                workspace = _ws_cache.get((dev.type, dev.index, stream))
+                if workspace is None or workspace.numel() < need or torch.cuda.is_current_stream_capturing():
+                    workspace = _workspace(dev, need)
+            have = workspace.numel() * workspace.element_size()
+            if workspace.device != dev or not workspace.is_contiguous() or have < need:
                 raise ValueError("workspace must be a contiguous tensor on %s of >= %d bytes" % (dev, need))
-            args.workspace = ws.data_ptr()
-            args.workspace_bytes = ws.numel() * ws.element_size()
-    status = _call(fn, args, dev)
+            args.workspace = workspace.data_ptr()
+            args.workspace_bytes = have
+    status = getattr(L, name)(ref, stream)
     if status != SSM_OK:
         _check(status, name)
 
@@ -878,12 +902,12 @@ def _gates(a, x, gate, mode, A, in_gate, gate_bias, in_bias, dev):
         raise ValueError("mode must be one of %s, got %r" % (", ".join(GATE_MODES), mode))
     f32, D = torch.float32, x.shape[-1]
     a.io_dtype, a.mode = _io_code(x.dtype), GATE_MODES[mode]
-    a.x = _ptr(_req(x, "x", x.shape, x.dtype, dev))
-    a.gate = _ptr(_req(gate, "gate", x.shape, x.dtype, dev))
-    a.in_gate = _ptr(_opt(in_gate, "in_gate", x.shape, x.dtype, dev))
-    a.A = _ptr(_opt(A, "A", (D,), f32, dev))
-    a.gate_bias = _ptr(_opt(gate_bias, "gate_bias", (D,), f32, dev))
-    a.in_bias = _ptr(_opt(in_bias, "in_bias", (D,), f32, dev))
+    a.x = _need(x, "x", x.shape, x.dtype, dev)
+    a.gate = _need(gate, "gate", x.shape, x.dtype, dev)
+    a.in_gate = _arg(in_gate, "in_gate", x.shape, x.dtype, dev)
+    a.A = _arg(A, "A", (D,), f32, dev)
+    a.gate_bias = _arg(gate_bias, "gate_bias", (D,), f32, dev)
+    a.in_bias = _arg(in_bias, "in_bias", (D,), f32, dev)
 
 
 def _resets(reset, shape, dev):
@@ -892,7 +916,7 @@ def _resets(reset, shape, dev):
         return None
     if isinstance(reset, torch.Tensor) and reset.dtype == torch.bool:
         reset = reset.view(torch.uint8)
-    return _ptr(_opt(reset, "reset", shape, torch.uint8, dev))
+    return _arg(reset, "reset", shape, torch.uint8, dev)
 
 
 def gated_scan_fwd(x: torch.Tensor, gate: torch.Tensor, mode: str = "rate",
@@ -916,14 +940,14 @@ def gated_scan_fwd(x: torch.Tensor, gate: torch.Tensor, mode: str = "rate",
     a = GatedScanArgs(batch=B, seqlen=L, dim=D)
     _gates(a, x, gate, mode, A, in_gate, gate_bias, in_bias, dev)
     a.reset = _resets(reset, (B, L), dev)
-    a.h0 = _ptr(_opt(h0, "h0", (B, D), f32, dev))
+    a.h0 = _arg(h0, "h0", (B, D), f32, dev)
     if y is None:
         y = torch.empty_like(x)
-    a.y = _ptr(_req(y, "y", (B, L, D), x.dtype, dev))
+    a.y = _need(y, "y", (B, L, D), x.dtype, dev)
     if h_final is None and return_final_state:
         h_final = torch.empty((B, D), device=dev, dtype=f32)
-    a.h_final = _ptr(_opt(h_final, "h_final", (B, D), f32, dev))
-    a.checkpoints = _ptr(_opt(checkpoints, "checkpoints", gated_checkpoint_shape(B, L, D), f32, dev))
+    a.h_final = _arg(h_final, "h_final", (B, D), f32, dev)
+    a.checkpoints = _arg(checkpoints, "checkpoints", gated_checkpoint_shape(B, L, D), f32, dev)
     _run("ssm_gated_scan_fwd", a, dev, "ssm_gated_scan_workspace_size", workspace)
     return y, h_final
 
@@ -946,10 +970,10 @@ def gated_scan_bwd(x: torch.Tensor, gate: torch.Tensor, dy: torch.Tensor, mode: 
     a = GatedScanBwdArgs(batch=B, seqlen=L, dim=D)
     _gates(a, x, gate, mode, A, in_gate, gate_bias, in_bias, dev)
     a.reset = _resets(reset, (B, L), dev)
-    a.h0 = _ptr(_opt(h0, "h0", (B, D), torch.float32, dev))
-    a.dy = _ptr(_req(dy, "dy", (B, L, D), x.dtype, dev))
-    a.dh_final = _ptr(_opt(dh_final, "dh_final", (B, D), torch.float32, dev))
-    a.checkpoints = _ptr(_opt(checkpoints, "checkpoints", gated_checkpoint_shape(B, L, D), torch.float32, dev))
+    a.h0 = _arg(h0, "h0", (B, D), torch.float32, dev)
+    a.dy = _need(dy, "dy", (B, L, D), x.dtype, dev)
+    a.dh_final = _arg(dh_final, "dh_final", (B, D), torch.float32, dev)
+    a.checkpoints = _arg(checkpoints, "checkpoints", gated_checkpoint_shape(B, L, D), torch.float32, dev)
     out = dict(dx=torch.empty_like(x), dgate=torch.empty_like(x))
     if in_gate is not None:
         out["din_gate"] = torch.empty_like(x)
@@ -973,9 +997,7 @@ def gated_scan_step(state: torch.Tensor, x: torch.Tensor, gate: torch.Tensor, mo
     y (B, D).  x, gate, in_gate: (B, D) bf16 or fp32; reset: (B,) uint8 or bool, rows whose state
     is taken as 0 (a new sequence); the rest as in gated_scan_fwd."""
     a, y = gated_scan_step_args(state, x, gate, mode, A, in_gate, gate_bias, in_bias, reset, y)
-    status = _call(lib().ssm_gated_scan_step, a, state.device)
-    if status != SSM_OK:
-        _check(status, "ssm_gated_scan_step")
+    _run("ssm_gated_scan_step", a, state.device)
     return y
 
 
@@ -989,12 +1011,12 @@ def gated_scan_step_args(state, x, gate, mode="rate", A=None, in_gate=None, gate
     if not isinstance(x, torch.Tensor) or x.shape != state.shape:
         raise ValueError("x must be a %s tensor like the state" % (tuple(state.shape),))
     a = GatedStepArgs(batch=B, dim=D)
-    a.state = _ptr(_req(state, "state", (B, D), torch.float32, dev))
+    a.state = _need(state, "state", (B, D), torch.float32, dev)
     _gates(a, x, gate, mode, A, in_gate, gate_bias, in_bias, dev)
     a.reset = _resets(reset, (B,), dev)
     if y is None:
         y = torch.empty_like(x)
-    a.y = _ptr(_req(y, "y", (B, D), x.dtype, dev))
+    a.y = _need(y, "y", (B, D), x.dtype, dev)
     return a, y
 
 
@@ -1048,11 +1070,11 @@ def _add_norm(a, x, w, residual, scale, post_w, eps, dev):
             raise TypeError("residual must be a torch.Tensor")
         res_dtype = residual.dtype
     a.res_dtype = _io_code(res_dtype)
-    a.x = _ptr(_req(x, "x", (R, D), x.dtype, dev))
-    a.w = _ptr(_req(w, "w", (D,), f32, dev))
-    a.residual = _ptr(_opt(residual, "residual", (R, D), res_dtype, dev))
-    a.scale = _ptr(_opt(scale, "scale", (D,), f32, dev))
-    a.post_w = _ptr(_opt(post_w, "post_w", (D,), f32, dev))
+    a.x = _need(x, "x", (R, D), x.dtype, dev)
+    a.w = _need(w, "w", (D,), f32, dev)
+    a.residual = _arg(residual, "residual", (R, D), res_dtype, dev)
+    a.scale = _arg(scale, "scale", (D,), f32, dev)
+    a.post_w = _arg(post_w, "post_w", (D,), f32, dev)
     return res_dtype
 
 
@@ -1092,8 +1114,8 @@ def add_rmsnorm_fwd(x: torch.Tensor, w: torch.Tensor, residual: Optional[torch.T
         y = torch.empty_like(x)
     if res_out is None:
         res_out = torch.empty(shape, device=dev, dtype=res_dtype)
-    a.y = _ptr(_req(y, "y", shape, x.dtype, dev))
-    a.res_out = _ptr(_req(res_out, "res_out", shape, res_dtype, dev))
+    a.y = _need(y, "y", shape, x.dtype, dev)
+    a.res_out = _need(res_out, "res_out", shape, res_dtype, dev)
     _run("ssm_add_rmsnorm_fwd", a, dev)
     return y, res_out
 
@@ -1112,8 +1134,8 @@ def add_rmsnorm_bwd(x: torch.Tensor, w: torch.Tensor, residual: Optional[torch.T
     a = AddNormBwdArgs()
     res_dtype = _add_norm(a, _rows_of(x, shape, "x"), w, _rows_of(residual, shape, "residual"), scale, post_w,
                           eps, dev)
-    a.dy = _ptr(_req(dy, "dy", shape, x.dtype, dev))
-    a.dres_out = _ptr(_opt(dres_out, "dres_out", shape, res_dtype, dev))
+    a.dy = _need(dy, "dy", shape, x.dtype, dev)
+    a.dres_out = _arg(dres_out, "dres_out", shape, res_dtype, dev)
     out = dict(dx=torch.empty_like(x), dw=torch.empty_like(w))
     if residual is not None:
         out["dresidual"] = torch.empty_like(residual)
@@ -1158,9 +1180,9 @@ def _gated_norm(a, x, z, w, groups, gate_first, eps, shape, dev):
     D = shape[-1]
     a.rows, a.dim, a.groups, a.eps = x.numel() // D, D, int(groups), float(eps)
     a.io_dtype, a.gate_first = _io_code(x.dtype), int(bool(gate_first))
-    a.x = _ptr(_req(x, "x", shape, x.dtype, dev))
-    a.z = _ptr(_req(z, "z", shape, x.dtype, dev))
-    a.w = _ptr(_req(w, "w", (D,), torch.float32, dev))
+    a.x = _need(x, "x", shape, x.dtype, dev)
+    a.z = _need(z, "z", shape, x.dtype, dev)
+    a.w = _need(w, "w", (D,), torch.float32, dev)
 
 
 def gated_rmsnorm_fwd(x: torch.Tensor, z: torch.Tensor, w: torch.Tensor, groups: int = 1,
@@ -1175,7 +1197,7 @@ def gated_rmsnorm_fwd(x: torch.Tensor, z: torch.Tensor, w: torch.Tensor, groups:
     _gated_norm(a, x, z, w, groups, gate_first, eps, shape, dev)
     if y is None:
         y = torch.empty_like(x)
-    a.y = _ptr(_req(y, "y", shape, x.dtype, dev))
+    a.y = _need(y, "y", shape, x.dtype, dev)
     _run("ssm_gated_rmsnorm_fwd", a, dev)
     return y
 
@@ -1189,7 +1211,7 @@ def gated_rmsnorm_bwd(x: torch.Tensor, z: torch.Tensor, w: torch.Tensor, dy: tor
     dev = x.device
     a = GatedNormBwdArgs()
     _gated_norm(a, x, z, w, groups, gate_first, eps, shape, dev)
-    a.dy = _ptr(_req(dy, "dy", shape, x.dtype, dev))
+    a.dy = _need(dy, "dy", shape, x.dtype, dev)
     out = dict(dx=torch.empty_like(x), dz=torch.empty_like(z), dw=torch.empty_like(w))
     for name, t in out.items():
         setattr(a, name, t.data_ptr())
