@@ -152,18 +152,44 @@ __global__ __launch_bounds__(FwdTile<IO>::THREADS) void gated_scan_kernel(ssm_ga
     }
 }
 
+// One token: a thread per four channels of a row (16 bytes of state), bound by the launch for a few
+// rows and by HBM for many (256 x 5120 bf16: see the step's row of the table).
+constexpr int kStepV = 4;
+
 template <typename IO, int MODE, bool IG>
-__global__ __launch_bounds__(64) void gated_step_kernel(ssm_gated_step_args_t a) {
-    const int64_t d = (int64_t)blockIdx.x * 64 + threadIdx.x, b = blockIdx.y;
-    if (d >= a.dim) return;
-    GateChannel c = {a.A ? a.A[d] : 0.0f, a.gate_bias ? a.gate_bias[d] * kLog2e : 0.0f,
-                           a.in_bias ? a.in_bias[d] * kLog2e : 0.0f};
-    const int64_t i = b * a.dim + d;
-    float at, bt;
-    gate_step<MODE, IG>(load_io<IO>(a.x, i), load_io<IO>(a.gate, i), IG ? load_io<IO>(a.in_gate, i) : 0.0f, c, at, bt);
-    const float h = a.reset && a.reset[b] ? bt : __builtin_fmaf(at, a.state[i], bt);
-    a.state[i] = h;
-    store_io<IO>(a.y, i, h);
+__global__ __launch_bounds__(256) void gated_step_kernel(ssm_gated_step_args_t a, unsigned per_row, unsigned total) {
+    constexpr int V = kStepV, W = V * IO::bytes / 4;
+    const unsigned id = blockIdx.x * 256u + threadIdx.x;
+    if (id >= total) return;
+    const unsigned b = id / per_row, d0 = id % per_row * V;
+    const int nv = (int)min((unsigned)V, (unsigned)a.dim - d0);
+    const int64_t i = (int64_t)b * a.dim + d0;
+    const uint32_t off[1] = {0};
+    Words<W> qx[1], qg[1], qi[1] = {};
+    Words<V> st[1];
+    load_rows<IO, W, 1>(static_cast<const char *>(a.x) + i * IO::bytes, off, nv, qx);
+    load_rows<IO, W, 1>(static_cast<const char *>(a.gate) + i * IO::bytes, off, nv, qg);
+    if constexpr (IG) load_rows<IO, W, 1>(static_cast<const char *>(a.in_gate) + i * IO::bytes, off, nv, qi);
+    load_rows<io_f32, V, 1>(reinterpret_cast<const char *>(a.state + i), off, nv, st);
+    // the channels' constants the same way (absent ones stay 0)
+    Words<V> cA[1] = {}, cg[1] = {}, ci[1] = {};
+    if constexpr (MODE == SSM_GATE_RATE) load_rows<io_f32, V, 1>(reinterpret_cast<const char *>(a.A + d0), off, nv, cA);
+    if (MODE != SSM_GATE_DECAY && a.gate_bias)
+        load_rows<io_f32, V, 1>(reinterpret_cast<const char *>(a.gate_bias + d0), off, nv, cg);
+    if (IG && a.in_bias) load_rows<io_f32, V, 1>(reinterpret_cast<const char *>(a.in_bias + d0), off, nv, ci);
+    const bool cut = a.reset && a.reset[b] != 0;
+    float h[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const GateChannel c = {__uint_as_float(cA[0].w[v]), __uint_as_float(cg[0].w[v]) * kLog2e,
+                               __uint_as_float(ci[0].w[v]) * kLog2e};
+        float at, bt;
+        gate_step<MODE, IG>(lane_elem<IO>(qx[0], v), lane_elem<IO>(qg[0], v), IG ? lane_elem<IO>(qi[0], v) : 0.0f, c, at,
+                            bt);
+        h[v] = cut ? bt : __builtin_fmaf(at, __uint_as_float(st[0].w[v]), bt);
+    }
+    store_row<io_f32>(reinterpret_cast<char *>(a.state + i), nv, lane_pack<io_f32, V>(h));
+    store_row<IO>(static_cast<char *>(a.y) + i * IO::bytes, nv, lane_pack<IO, W>(h));
 }
 
 __global__ __launch_bounds__(256) void copy_or_zero_kernel(float *out, const float *in, int64_t n) {
@@ -215,9 +241,10 @@ hipError_t launch_gated_scan_fwd(const ssm_gated_scan_args_t &a, hipStream_t str
 }
 
 hipError_t launch_gated_step(const ssm_gated_step_args_t &a, hipStream_t stream) {
-    const dim3 grid((unsigned)((a.dim + 63) / 64), (unsigned)a.batch);
+    const unsigned per_row = (unsigned)((a.dim + kStepV - 1) / kStepV), total = per_row * (unsigned)a.batch;
     gate_dispatch(a.io_dtype, a.mode, a.in_gate != nullptr, [&](auto io, auto mode, auto ig) {
-        gated_step_kernel<decltype(io), decltype(mode)::value, decltype(ig)::value><<<grid, 64, 0, stream>>>(a);
+        gated_step_kernel<decltype(io), decltype(mode)::value, decltype(ig)::value>
+            <<<(total + 255) / 256, 256, 0, stream>>>(a, per_row, total);
     });
     return hipGetLastError();
 }

@@ -850,16 +850,22 @@ def _arg(t, name, shape, dtype, device):
     """Address of an optional tensor argument (None: not given)."""
     if t is None:
         return None
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device
-            and t.is_contiguous()):
-        return t.data_ptr()
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == device.index and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass  # not a tensor: named by the check below
     return _opt(t, name, shape, dtype, device).data_ptr()
 
 
 def _need(t, name, shape, dtype, device):
-    if t is None:
-        raise ValueError("%s is required" % name)
-    return _arg(t, name, shape, dtype, device)
+    """Address of a required tensor argument."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == device.index and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    return _req(t, name, shape, dtype, device).data_ptr()
 
 
 def _run(name: str, args, dev: torch.device, size_fn=None, workspace: Optional[torch.Tensor] = None):
@@ -898,16 +904,22 @@ def _gpu(t, name: str, dims: int, shape: str) -> torch.device:
 
 def _gates(a, x, gate, mode, A, in_gate, gate_bias, in_bias, dev):
     """Check the gate inputs against x's shape and put them into `a`."""
-    if mode not in GATE_MODES:
+    code = GATE_MODES.get(mode)
+    if code is None:
         raise ValueError("mode must be one of %s, got %r" % (", ".join(GATE_MODES), mode))
-    f32, D = torch.float32, x.shape[-1]
-    a.io_dtype, a.mode = _io_code(x.dtype), GATE_MODES[mode]
-    a.x = _need(x, "x", x.shape, x.dtype, dev)
-    a.gate = _need(gate, "gate", x.shape, x.dtype, dev)
-    a.in_gate = _arg(in_gate, "in_gate", x.shape, x.dtype, dev)
-    a.A = _arg(A, "A", (D,), f32, dev)
-    a.gate_bias = _arg(gate_bias, "gate_bias", (D,), f32, dev)
-    a.in_bias = _arg(in_bias, "in_bias", (D,), f32, dev)
+    shape, io = x.shape, x.dtype
+    a.io_dtype, a.mode = _io_code(io), code
+    a.x = _need(x, "x", shape, io, dev)
+    a.gate = _need(gate, "gate", shape, io, dev)
+    if in_gate is not None:
+        a.in_gate = _arg(in_gate, "in_gate", shape, io, dev)
+    per_channel, f32 = (shape[-1],), torch.float32
+    if A is not None:
+        a.A = _arg(A, "A", per_channel, f32, dev)
+    if gate_bias is not None:
+        a.gate_bias = _arg(gate_bias, "gate_bias", per_channel, f32, dev)
+    if in_bias is not None:
+        a.in_bias = _arg(in_bias, "in_bias", per_channel, f32, dev)
 
 
 def _resets(reset, shape, dev):
@@ -1007,16 +1019,20 @@ def gated_scan_step_args(state, x, gate, mode="rate", A=None, in_gate=None, gate
     given), for callers that launch the same step repeatedly through lib().ssm_gated_scan_step.
     The tensors must outlive the struct."""
     dev = _gpu(state, "state", 2, "(B, D) float32")
-    B, D = state.shape
-    if not isinstance(x, torch.Tensor) or x.shape != state.shape:
-        raise ValueError("x must be a %s tensor like the state" % (tuple(state.shape),))
-    a = GatedStepArgs(batch=B, dim=D)
-    a.state = _need(state, "state", (B, D), torch.float32, dev)
+    shape = state.shape
+    if not isinstance(x, torch.Tensor) or x.shape != shape:
+        raise ValueError("x must be a %s tensor like the state" % (tuple(shape),))
+    a = GatedStepArgs()
+    a.batch, a.dim = shape
+    a.state = _need(state, "state", shape, torch.float32, dev)
     _gates(a, x, gate, mode, A, in_gate, gate_bias, in_bias, dev)
-    a.reset = _resets(reset, (B,), dev)
+    if reset is not None:
+        a.reset = _resets(reset, (shape[0],), dev)
     if y is None:
         y = torch.empty_like(x)
-    a.y = _need(y, "y", (B, D), x.dtype, dev)
+        a.y = y.data_ptr()
+    else:
+        a.y = _need(y, "y", shape, x.dtype, dev)
     return a, y
 
 
