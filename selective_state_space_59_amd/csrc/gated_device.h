@@ -53,7 +53,7 @@ __device__ __forceinline__ Sig sigmoid_pair(float v2) {
 // sig(v) alone: 1 / (1 + e^-v) does not cancel either.
 __device__ __forceinline__ float sigmoid(float v2) { return hw_rcp(1.0f + hw_exp2(-v2)); }
 
-// 1 - a^2 for a = 2^{y}, y <= 0 (0 where y > 0).
+// 1 - a^2 for a = 2^{y}, y <= 0 (not above 0 where y > 0).
 __device__ __forceinline__ float one_minus_sq(float y, float a) {
     // -(e^w - 1) with w = 2 ln2 y, as w (1 + w/2 + w^2/6 + ...) in powers of y
     constexpr float k = 1.38629436111989062f;
@@ -64,13 +64,13 @@ __device__ __forceinline__ float one_minus_sq(float y, float a) {
     // |w| < 1/8: the series' next term is below 2^-24 of it; beyond, 1 - a^2 > 0.117 loses at
     // most 3 bits to the subtraction
     const float series = -y * p, direct = __builtin_fmaf(-a, a, 1.0f);
-    const float q = y > -0.09f ? series : direct;
-    return q < 0.0f ? 0.0f : q;
+    return y > -0.09f ? series : direct;
 }
 
-// Per-channel constants of a lane: A and the biases, these in units of the exponential's argument.
+// Per-channel constants of a lane, A and the biases in units of the exponential's argument
+// (times log2(e)).
 struct GateChannel {
-    float A, gb2, ib2;
+    float A2, gb2, ib2;
 };
 
 __device__ __forceinline__ float gate_arg(float g, float b2) { return __builtin_fmaf(g, kLog2e, b2); }
@@ -86,9 +86,10 @@ __device__ __forceinline__ void gate_step(float x, float g, float ig, const Gate
         a = s.c;
         b = s.s * x;
     } else {
-        const float y = c.A * kLog2e * sigmoid(gate_arg(g, c.gb2));
+        const float y = c.A2 * sigmoid(gate_arg(g, c.gb2));
         a = hw_exp2(y);
-        b = __builtin_amdgcn_sqrtf(one_minus_sq(y, a)) * x;
+        const float q = one_minus_sq(y, a);
+        b = __builtin_amdgcn_sqrtf(q < 0.0f ? 0.0f : q) * x;
         if constexpr (IG) b *= sigmoid(gate_arg(ig, c.ib2));
     }
 }
@@ -125,7 +126,7 @@ __device__ __forceinline__ Gate<MODE, IG> gate_of(float g, float ig, const GateC
         const Logistic r = logistic(gate_arg(g, c.gb2));
         o.s = r.s;
         o.sc = r.sc;
-        const float y = c.A * kLog2e * r.s;
+        const float y = c.A2 * r.s;
         o.a = hw_exp2(y);
         const float q = one_minus_sq(y, o.a);
         o.inv_beta = q > 0.0f ? __builtin_amdgcn_rsqf(q) : 0.0f;  // 0 where sqrt(1 - a^2) is 0

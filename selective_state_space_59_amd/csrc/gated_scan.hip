@@ -37,7 +37,7 @@ __global__ __launch_bounds__(FwdTile<IO>::THREADS) void gated_scan_kernel(ssm_ga
     if (tid == 0) s_tile = tiles > 1 ? (int)atomicAdd(&tickets[chain], 1u) : 0;
     if (tid < CB) {
         const int d = min(cblk * CB + tid, (int)a.dim - 1);
-        sc[0][tid] = MODE == SSM_GATE_RATE ? a.A[d] : 0.0f;
+        sc[0][tid] = MODE == SSM_GATE_RATE ? a.A[d] * kLog2e : 0.0f;
         sc[1][tid] = MODE != SSM_GATE_DECAY && a.gate_bias ? a.gate_bias[d] * kLog2e : 0.0f;
         sc[2][tid] = IG && a.in_bias ? a.in_bias[d] * kLog2e : 0.0f;
     }
@@ -181,7 +181,7 @@ __global__ __launch_bounds__(256) void gated_step_kernel(ssm_gated_step_args_t a
     float h[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        const GateChannel c = {__uint_as_float(cA[0].w[v]), __uint_as_float(cg[0].w[v]) * kLog2e,
+        const GateChannel c = {__uint_as_float(cA[0].w[v]) * kLog2e, __uint_as_float(cg[0].w[v]) * kLog2e,
                                __uint_as_float(ci[0].w[v]) * kLog2e};
         float at, bt;
         gate_step<MODE, IG>(lane_elem<IO>(qx[0], v), lane_elem<IO>(qg[0], v), IG ? lane_elem<IO>(qi[0], v) : 0.0f, c, at,

@@ -30,7 +30,7 @@ __device__ __forceinline__ void pin_row(uint32_t &x, uint32_t &g, uint32_t &i, u
 }
 
 template <typename IO, int MODE, bool IG, bool SPECIAL>
-__global__ __launch_bounds__(BwdTile<IO>::THREADS) void gated_bwd_kernel(ssm_gated_scan_bwd_args_t a, const float *ck,
+__global__ __launch_bounds__(BwdTile<IO>::THREADS, 4) void gated_bwd_kernel(ssm_gated_scan_bwd_args_t a, const float *ck,
                                                                   float *part, int chains, int tiles, u64_t *rec,
                                                                   unsigned *tickets) {
     using TL = BwdTile<IO>;
@@ -47,7 +47,7 @@ __global__ __launch_bounds__(BwdTile<IO>::THREADS) void gated_bwd_kernel(ssm_gat
     if (tid == 0) s_ticket = tiles > 1 ? (int)atomicAdd(&tickets[chain], 1u) : 0;
     if (tid < CB) {
         const int d = min(cblk * CB + tid, (int)a.dim - 1);
-        sc[0][tid] = MODE == SSM_GATE_RATE ? a.A[d] : 0.0f;
+        sc[0][tid] = MODE == SSM_GATE_RATE ? a.A[d] * kLog2e : 0.0f;
         sc[1][tid] = MODE != SSM_GATE_DECAY && a.gate_bias ? a.gate_bias[d] * kLog2e : 0.0f;
         sc[2][tid] = IG && a.in_bias ? a.in_bias[d] * kLog2e : 0.0f;
     }
@@ -189,6 +189,7 @@ __global__ __launch_bounds__(BwdTile<IO>::THREADS) void gated_bwd_kernel(ssm_gat
             const int v = w * PER + u;
             const GateChannel c = channel(v);
             float h = sl[g][lc + v], mu = sm[g][lc + v], da[R], lam[R], sA = 0.0f, sg = 0.0f, si = 0.0f;
+            const float A = c.A2 * 0.69314718055994531f;
             Gate<MODE, IG> t[R];
 #pragma unroll
             for (int j = 0; j < R; ++j)
@@ -221,7 +222,7 @@ __global__ __launch_bounds__(BwdTile<IO>::THREADS) void gated_bwd_kernel(ssm_gat
             }
 #pragma unroll
             for (int j = 0; j < R; ++j) {
-                const GateGrad o = gate_grad<MODE, IG>(t[j], lane_elem<IO>(qx[j], v), c.A, da[j], lam[j]);
+                const GateGrad o = gate_grad<MODE, IG>(t[j], lane_elem<IO>(qx[j], v), A, da[j], lam[j]);
                 ox[j][u] = o.dx;
                 og[j][u] = o.dg;
                 oi[j][u] = o.di;
