@@ -17,15 +17,25 @@
 namespace ssm {
 namespace {
 
-template <typename IO>
-using FwdTile = Tile<IO, 4, 4, 512>;
-static_assert(FwdTile<io_bf16>::T == FwdTile<io_f32>::T && FwdTile<io_bf16>::T <= SSM_GATED_TILE, "tile size");
-static_assert(SSM_GATED_BLOCK % FwdTile<io_bf16>::R == 0, "checkpoints lie between lane groups");
+// 256 steps by 128 bytes of channels.  With the costly gates (RATE) every step's p and l stay in
+// registers until the entering state is known, 4 rows a lane; with the cheap ones the rows do, which
+// take half as many, and are run through again, 8 rows a lane and half the waves (4 x 4096 x 5120
+// bf16 SIGMOID with resets: 128 us, against 142 with p and l kept and 135 with 4 rows).
+template <int MODE>
+constexpr bool kKeep = MODE == SSM_GATE_RATE;
+template <typename IO, int MODE>
+using FwdTile = Tile<IO, 4, kKeep<MODE> ? 4 : 8, kKeep<MODE> ? 512 : 256>;
+constexpr int kFwdSteps = 256;
+template <int MODE>
+constexpr bool kTileOk = FwdTile<io_bf16, MODE>::T == kFwdSteps && FwdTile<io_f32, MODE>::T == kFwdSteps &&
+                         SSM_GATED_BLOCK % FwdTile<io_bf16, MODE>::R == 0;
+static_assert(kTileOk<SSM_GATE_DECAY> && kTileOk<SSM_GATE_SIGMOID> && kTileOk<SSM_GATE_RATE>, "tile sizes");
+static_assert(kFwdSteps <= SSM_GATED_TILE, "the longest product of decays");
 
-template <typename IO, int MODE, bool IG>
-__global__ __launch_bounds__(FwdTile<IO>::THREADS) void gated_scan_kernel(ssm_gated_scan_args_t a, int chains,
+template <typename IO, int MODE, bool IG, int EDGE>
+__global__ __launch_bounds__((FwdTile<IO, MODE>::THREADS)) void gated_scan_kernel(ssm_gated_scan_args_t a, int chains,
                                                                          int tiles, u64_t *rec, unsigned *tickets) {
-    using TL = FwdTile<IO>;
+    using TL = FwdTile<IO, MODE>;
     constexpr int V = TL::V, CB = TL::CB, G = TL::G, T = TL::T, R = TL::R, W = TL::W;
     constexpr int NP = TL::THREADS / CB, GP = G / NP;  // runs of GP lane groups
     __shared__ __attribute__((aligned(16))) float sp[G][CB], sl[G][CB], pp[NP][CB], pl[NP][CB], sc[3][CB];
@@ -44,46 +54,61 @@ __global__ __launch_bounds__(FwdTile<IO>::THREADS) void gated_scan_kernel(ssm_ga
     __syncthreads();
     const int tile = s_tile;
     const int64_t b = chain / nblk, L = a.seqlen, t0 = (int64_t)tile * T;
-    const int D = (int)a.dim, lc = tid % TL::LANES * V, d0 = cblk * CB + lc, nv = min(V, D - d0), g = tid / TL::LANES;
+    const int D = (int)a.dim, lc = tid % TL::LANES * V, g = tid / TL::LANES;
+    const Cols col = cols_of<EDGE>(cblk * CB + lc, D, V);
     const int left = (int)min(L - t0, (int64_t)T);  // valid steps of this tile
 
     const int64_t row0 = (b * L + t0) * D * IO::bytes;
     uint32_t off[R];
 #pragma unroll
     for (int j = 0; j < R; ++j)  // steps past the end read the last one and are made the identity below
-        off[j] = ((uint32_t)min(g * R + j, left - 1) * (uint32_t)D + (uint32_t)d0) * IO::bytes;
+        off[j] = ((uint32_t)min(g * R + j, left - 1) * (uint32_t)D + (uint32_t)col.load) * IO::bytes;
+    uint32_t mark[R] = {};  // ahead of the rows: loads come back in order
+    if (a.reset)
+#pragma unroll
+        for (int j = 0; j < R; ++j) mark[j] = a.reset[b * L + t0 + min(g * R + j, left - 1)];
     Words<W> qx[R], qg[R], qi[R];
-    load_rows<IO, W, R>(static_cast<const char *>(a.x) + row0, off, nv, qx);
-    load_rows<IO, W, R>(static_cast<const char *>(a.gate) + row0, off, nv, qg);
-    if constexpr (IG) load_rows<IO, W, R>(static_cast<const char *>(a.in_gate) + row0, off, nv, qi);
-    float p[R][V], l[R][V];
+    load_rows<IO, EDGE>(static_cast<const char *>(a.x) + row0, off, col.nv, qx);
+    load_rows<IO, EDGE>(static_cast<const char *>(a.gate) + row0, off, col.nv, qg);
+    if constexpr (IG) load_rows<IO, EDGE>(static_cast<const char *>(a.in_gate) + row0, off, col.nv, qi);
+    if constexpr (EDGE == kRagged) {
+        shift_rows<IO>(qx, col.shift);
+        shift_rows<IO>(qg, col.shift);
+        if constexpr (IG) shift_rows<IO>(qi, col.shift);
+    }
     auto step = [&](int j, int v, float &at, float &bt) {
-        gate_step<MODE, IG>(lane_elem<IO>(qx[j], v), lane_elem<IO>(qg[j], v), IG ? lane_elem<IO>(qi[j], v) : 0.0f, GateChannel{sc[0][lc + v], sc[1][lc + v], sc[2][lc + v]},
-                            at, bt);
+        gate_step<MODE, IG>(lane_elem<IO>(qx[j], v), lane_elem<IO>(qg[j], v), IG ? lane_elem<IO>(qi[j], v) : 0.0f,
+                            GateChannel{sc[0][lc + v], sc[1][lc + v], sc[2][lc + v]}, at, bt);
     };
     const bool special = left < T || a.reset;  // the same for the whole workgroup
+    constexpr bool KEEP = kKeep<MODE>;
+    constexpr int K = KEEP ? R : 1;
+    float p[K][V], l[K][V];
 #pragma unroll
     for (int j = 0; j < R; ++j) {
-        float at[V], bt[V];
+        const int to = KEEP ? j : 0, from = KEEP && j ? j - 1 : 0;
+        float at[V], bt[V], was_p[V], was_l[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
+            const float p0 = j ? p[from][v] : 1.0f, l0 = j ? l[from][v] : 0.0f;
             step(j, v, at[v], bt[v]);
-            p[j][v] = j ? at[v] * p[j - 1][v] : at[v];
-            l[j][v] = __builtin_fmaf(at[v], j ? l[j - 1][v] : 0.0f, bt[v]);  // (a NaN decay shows from the first step)
+            was_p[v] = p0;
+            was_l[v] = l0;
+            p[to][v] = at[v] * p0;
+            l[to][v] = __builtin_fmaf(at[v], l0, bt[v]);  // (a NaN decay shows from the first step)
         }
         if (special) {
-            const bool in = g * R + j < left;
-            const bool cut = a.reset && a.reset[b * L + t0 + min(g * R + j, left - 1)] != 0;
+            const bool in = g * R + j < left, cut = mark[j] != 0;
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                p[j][v] = !in ? (j ? p[j - 1][v] : 1.0f) : cut ? __builtin_nanf("") : p[j][v];
-                l[j][v] = !in ? (j ? l[j - 1][v] : 0.0f) : cut ? bt[v] : l[j][v];
+                p[to][v] = !in ? was_p[v] : cut ? __builtin_nanf("") : p[to][v];
+                l[to][v] = !in ? was_l[v] : cut ? bt[v] : l[to][v];
             }
         }
         __builtin_amdgcn_sched_barrier(0);  // a row at a time: fewer live registers
     }
-    lds_put<V>(&sp[g][lc], p[R - 1]);
-    lds_put<V>(&sl[g][lc], l[R - 1]);
+    lds_put<V>(&sp[g][lc], p[K - 1]);
+    lds_put<V>(&sl[g][lc], l[K - 1]);
     __syncthreads();
     // a thread per channel and run of GP groups: the runs first, then one thread per channel over
     // the runs and back through the groups
@@ -136,19 +161,30 @@ __global__ __launch_bounds__(FwdTile<IO>::THREADS) void gated_scan_kernel(ssm_ga
         h = run_apply(gp, sl[part * GP + i][ch], h);
     }
     __syncthreads();
-    if (a.y) {
-        float e[V];
+    if (!a.y) return;
+    float e[V];
 #pragma unroll
-        for (int v = 0; v < V; ++v) e[v] = sp[g][lc + v];
-        char *out = static_cast<char *>(a.y) + row0;
+    for (int v = 0; v < V; ++v) e[v] = sp[g][lc + v];
+    char *out = static_cast<char *>(a.y) + row0 + col.shift * IO::bytes;
+    if constexpr (!KEEP)  // (or the gates of above would be kept after all)
 #pragma unroll
-        for (int j = 0; j < R; ++j) {
-            float f[V];
+        for (int j = 0; j < R; ++j)
 #pragma unroll
-            for (int v = 0; v < V; ++v)
+            for (int w = 0; w < W; ++w) asm volatile("" : "+v"(qx[j].w[w]), "+v"(qg[j].w[w]));
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+        float f[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            if constexpr (KEEP) {
                 f[v] = a.reset ? run_apply(p[j][v], l[j][v], e[v]) : __builtin_fmaf(p[j][v], e[v], l[j][v]);
-            if (g * R + j < left) store_row<IO>(out + off[j], nv, lane_pack<IO, W>(f));
+            } else {
+                float at, bt;
+                step(j, v, at, bt);
+                f[v] = e[v] = mark[j] ? bt : __builtin_fmaf(at, e[v], bt);
+            }
         }
+        if (g * R + j < left) store_row<IO>(out + off[j], col.nv, lane_pack<IO, W>(f));
     }
 }
 
@@ -164,29 +200,27 @@ __global__ __launch_bounds__(256) void gated_step_kernel(ssm_gated_step_args_t a
     const unsigned b = id / per_row, d0 = id % per_row * V;
     const int nv = (int)min((unsigned)V, (unsigned)a.dim - d0);
     const int64_t i = (int64_t)b * a.dim + d0;
-    const uint32_t off[1] = {0};
-    Words<W> qx[1], qg[1], qi[1] = {};
-    Words<V> st[1];
-    load_rows<IO, W, 1>(static_cast<const char *>(a.x) + i * IO::bytes, off, nv, qx);
-    load_rows<IO, W, 1>(static_cast<const char *>(a.gate) + i * IO::bytes, off, nv, qg);
-    if constexpr (IG) load_rows<IO, W, 1>(static_cast<const char *>(a.in_gate) + i * IO::bytes, off, nv, qi);
-    load_rows<io_f32, V, 1>(reinterpret_cast<const char *>(a.state + i), off, nv, st);
+    const Words<W> qx = load_some<IO, W>(static_cast<const char *>(a.x) + i * IO::bytes, nv);
+    const Words<W> qg = load_some<IO, W>(static_cast<const char *>(a.gate) + i * IO::bytes, nv);
+    Words<W> qi = {};
+    if constexpr (IG) qi = load_some<IO, W>(static_cast<const char *>(a.in_gate) + i * IO::bytes, nv);
+    auto floats = [nv](const float *p) { return load_some<io_f32, V>(reinterpret_cast<const char *>(p), nv); };
+    const Words<V> st = floats(a.state + i);
     // the channels' constants the same way (absent ones stay 0)
-    Words<V> cA[1] = {}, cg[1] = {}, ci[1] = {};
-    if constexpr (MODE == SSM_GATE_RATE) load_rows<io_f32, V, 1>(reinterpret_cast<const char *>(a.A + d0), off, nv, cA);
-    if (MODE != SSM_GATE_DECAY && a.gate_bias)
-        load_rows<io_f32, V, 1>(reinterpret_cast<const char *>(a.gate_bias + d0), off, nv, cg);
-    if (IG && a.in_bias) load_rows<io_f32, V, 1>(reinterpret_cast<const char *>(a.in_bias + d0), off, nv, ci);
+    Words<V> cA = {}, cg = {}, ci = {};
+    if constexpr (MODE == SSM_GATE_RATE) cA = floats(a.A + d0);
+    if (MODE != SSM_GATE_DECAY && a.gate_bias) cg = floats(a.gate_bias + d0);
+    if (IG && a.in_bias) ci = floats(a.in_bias + d0);
     const bool cut = a.reset && a.reset[b] != 0;
     float h[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        const GateChannel c = {__uint_as_float(cA[0].w[v]) * kLog2e, __uint_as_float(cg[0].w[v]) * kLog2e,
-                               __uint_as_float(ci[0].w[v]) * kLog2e};
+        const GateChannel c = {__uint_as_float(cA.w[v]) * kLog2e, __uint_as_float(cg.w[v]) * kLog2e,
+                               __uint_as_float(ci.w[v]) * kLog2e};
         float at, bt;
-        gate_step<MODE, IG>(lane_elem<IO>(qx[0], v), lane_elem<IO>(qg[0], v), IG ? lane_elem<IO>(qi[0], v) : 0.0f, c, at,
+        gate_step<MODE, IG>(lane_elem<IO>(qx, v), lane_elem<IO>(qg, v), IG ? lane_elem<IO>(qi, v) : 0.0f, c, at,
                             bt);
-        h[v] = cut ? bt : __builtin_fmaf(at, __uint_as_float(st[0].w[v]), bt);
+        h[v] = cut ? bt : __builtin_fmaf(at, __uint_as_float(st.w[v]), bt);
     }
     store_row<io_f32>(reinterpret_cast<char *>(a.state + i), nv, lane_pack<io_f32, V>(h));
     store_row<IO>(static_cast<char *>(a.y) + i * IO::bytes, nv, lane_pack<IO, W>(h));
@@ -206,9 +240,8 @@ __global__ __launch_bounds__(256) void chain_init_kernel(uint4 *rec, int64_t n16
 }
 
 ChainPlan fwd_plan(const ssm_gated_scan_args_t &a) {
-    const int64_t cb = a.io_dtype == SSM_BF16 ? FwdTile<io_bf16>::CB : FwdTile<io_f32>::CB;
-    const int64_t t = FwdTile<io_bf16>::T;
-    return ChainPlan{a.batch * ((a.dim + cb - 1) / cb), (a.seqlen + t - 1) / t, cb};
+    const int64_t cb = a.io_dtype == SSM_BF16 ? FwdTile<io_bf16, 0>::CB : FwdTile<io_f32, 0>::CB;
+    return ChainPlan{a.batch * ((a.dim + cb - 1) / cb), (a.seqlen + kFwdSteps - 1) / kFwdSteps, cb};
 }
 
 }  // namespace
@@ -234,8 +267,12 @@ hipError_t launch_gated_scan_fwd(const ssm_gated_scan_args_t &a, hipStream_t str
     }
     const unsigned grid = (unsigned)(p.chains * p.tiles);
     gate_dispatch(a.io_dtype, a.mode, a.in_gate != nullptr, [&](auto io, auto mode, auto ig) {
-        gated_scan_kernel<decltype(io), decltype(mode)::value, decltype(ig)::value>
-            <<<grid, FwdTile<decltype(io)>::THREADS, 0, stream>>>(a, (int)p.chains, (int)p.tiles, rec, tickets);
+        using TL = FwdTile<decltype(io), decltype(mode)::value>;
+        auto go = [&](auto edge) {
+            gated_scan_kernel<decltype(io), decltype(mode)::value, decltype(ig)::value, decltype(edge)::value>
+                <<<grid, TL::THREADS, 0, stream>>>(a, (int)p.chains, (int)p.tiles, rec, tickets);
+        };
+        with_edge(edge_of(a.dim, TL::V), go);
     });
     return hipGetLastError();
 }

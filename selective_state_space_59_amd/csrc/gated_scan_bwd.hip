@@ -29,7 +29,7 @@ __device__ __forceinline__ void pin_row(uint32_t &x, uint32_t &g, uint32_t &i, u
     if constexpr (IG) asm volatile("" : "+v"(i));
 }
 
-template <typename IO, int MODE, bool IG, bool SPECIAL>
+template <typename IO, int MODE, bool IG, bool SPECIAL, int EDGE>
 __global__ __launch_bounds__(BwdTile<IO>::THREADS, 4) void gated_bwd_kernel(ssm_gated_scan_bwd_args_t a, const float *ck,
                                                                   float *part, int chains, int tiles, u64_t *rec,
                                                                   unsigned *tickets) {
@@ -55,22 +55,33 @@ __global__ __launch_bounds__(BwdTile<IO>::THREADS, 4) void gated_bwd_kernel(ssm_
     const int k = s_ticket;
     const int tile = tiles - 1 - k;
     const int64_t b = chain / nblk, L = a.seqlen, t0 = (int64_t)tile * T;
-    const int D = (int)a.dim, lc = tid % TL::LANES * V, d0 = cblk * CB + lc, nv = min(V, D - d0);
-    const int g = tid / TL::LANES, left = (int)min(L - t0, (int64_t)T);
+    const int D = (int)a.dim, lc = tid % TL::LANES * V, g = tid / TL::LANES;
+    const Cols col = cols_of<EDGE>(cblk * CB + lc, D, V);
+    const int left = (int)min(L - t0, (int64_t)T);
     const int64_t row0 = (b * L + t0) * D * IO::bytes;
     uint32_t off[R];
 #pragma unroll
     for (int j = 0; j < R; ++j)
-        off[j] = ((uint32_t)min(g * R + j, left - 1) * (uint32_t)D + (uint32_t)d0) * IO::bytes;
+        off[j] = ((uint32_t)min(g * R + j, left - 1) * (uint32_t)D + (uint32_t)col.load) * IO::bytes;
+    uint32_t mark[R] = {};  // ahead of the rows: loads come back in order
+    if (SPECIAL && a.reset)
+#pragma unroll
+        for (int j = 0; j < R; ++j) mark[j] = a.reset[b * L + t0 + min(g * R + j, left - 1)];
     Words<W> qx[R], qg[R], qi[R], qd[R];
-    load_rows<IO, W, R>(static_cast<const char *>(a.x) + row0, off, nv, qx);
-    load_rows<IO, W, R>(static_cast<const char *>(a.gate) + row0, off, nv, qg);
-    if constexpr (IG) load_rows<IO, W, R>(static_cast<const char *>(a.in_gate) + row0, off, nv, qi);
-    load_rows<IO, W, R>(static_cast<const char *>(a.dy) + row0, off, nv, qd);
+    load_rows<IO, EDGE>(static_cast<const char *>(a.x) + row0, off, col.nv, qx);
+    load_rows<IO, EDGE>(static_cast<const char *>(a.gate) + row0, off, col.nv, qg);
+    if constexpr (IG) load_rows<IO, EDGE>(static_cast<const char *>(a.in_gate) + row0, off, col.nv, qi);
+    load_rows<IO, EDGE>(static_cast<const char *>(a.dy) + row0, off, col.nv, qd);
+    if constexpr (EDGE == kRagged) {
+        shift_rows<IO>(qx, col.shift);
+        shift_rows<IO>(qg, col.shift);
+        if constexpr (IG) shift_rows<IO>(qi, col.shift);
+        shift_rows<IO>(qd, col.shift);
+    }
     bool cut[R], in[R];
 #pragma unroll
     for (int j = 0; j < R; ++j) {
-        cut[j] = a.reset && a.reset[b * L + t0 + min(g * R + j, left - 1)] != 0;
+        cut[j] = mark[j] != 0;
         in[j] = g * R + j < left;
     }
     auto channel = [&](int v) { return GateChannel{sc[0][lc + v], sc[1][lc + v], sc[2][lc + v]}; };
@@ -256,9 +267,10 @@ __global__ __launch_bounds__(BwdTile<IO>::THREADS, 4) void gated_bwd_kernel(ssm_
 #pragma unroll
     for (int j = 0; j < R; ++j)
         if (!SPECIAL || in[j]) {
-            store_row<IO>(static_cast<char *>(a.dx) + row0 + off[j], nv, qx[j]);
-            store_row<IO>(static_cast<char *>(a.dgate) + row0 + off[j], nv, qg[j]);
-            if constexpr (IG) store_row<IO>(static_cast<char *>(a.din_gate) + row0 + off[j], nv, qi[j]);
+            const uint32_t at = off[j] + col.shift * IO::bytes;
+            store_row<IO>(static_cast<char *>(a.dx) + row0 + at, col.nv, qx[j]);
+            store_row<IO>(static_cast<char *>(a.dgate) + row0 + at, col.nv, qg[j]);
+            if constexpr (IG) store_row<IO>(static_cast<char *>(a.din_gate) + row0 + at, col.nv, qi[j]);
         }
     if constexpr (MODE != SSM_GATE_DECAY) {
         // this tile's row of the partial sums: gate_bias, then A, then in_bias
@@ -349,16 +361,20 @@ hipError_t launch_gated_scan_bwd(const ssm_gated_scan_bwd_args_t &a, hipStream_t
     unsigned *tickets = reinterpret_cast<unsigned *>(ws + p.chain.rec_bytes());
     const unsigned grid = (unsigned)(p.chain.chains * p.chain.tiles);
     gate_dispatch(a.io_dtype, a.mode, a.in_gate != nullptr, [&](auto io, auto mode, auto ig) {
-        auto go = [&](auto special) {
-            gated_bwd_kernel<decltype(io), decltype(mode)::value, decltype(ig)::value, decltype(special)::value>
-                <<<grid, BwdTile<decltype(io)>::THREADS, 0, stream>>>(a, ck, part, (int)p.chain.chains,
-                                                                      (int)p.chain.tiles, reinterpret_cast<u64_t *>(ws),
-                                                                      tickets);
+        using TL = BwdTile<decltype(io)>;
+        auto go = [&](auto special, auto edge) {
+            gated_bwd_kernel<decltype(io), decltype(mode)::value, decltype(ig)::value, decltype(special)::value,
+                             decltype(edge)::value>
+                <<<grid, TL::THREADS, 0, stream>>>(a, ck, part, (int)p.chain.chains, (int)p.chain.tiles,
+                                                   reinterpret_cast<u64_t *>(ws), tickets);
         };
-        if (a.reset || a.seqlen % T != 0)
-            go(std::true_type{});
+        // the selects for resets and for a cut-off last tile: left out where neither is there and
+        // the width is whole
+        const Edge edge = edge_of(a.dim, TL::V);
+        if (edge == kWhole && !a.reset && a.seqlen % T == 0)
+            go(std::false_type{}, std::integral_constant<int, kWhole>{});
         else
-            go(std::false_type{});
+            with_edge(edge, [&](auto e) { go(std::true_type{}, e); });
     });
     e = hipGetLastError();
     float *out[3] = {a.dgate_bias, a.dA, a.din_bias};

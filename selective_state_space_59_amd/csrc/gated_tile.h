@@ -61,28 +61,93 @@ struct Tile {
     static constexpr int T = G * R;                       // steps
 };
 
-// R rows of a lane: `off[j]` bytes behind the wave-uniform `base`, `nv` valid channels (the last
-// channel block of an odd width takes its elements one by one).
-template <typename IO, int W, int R>
-__device__ __forceinline__ void load_rows(const char *base, const uint32_t (&off)[R], int nv, Words<W> (&q)[R]) {
-    constexpr int V = 4 * W / IO::bytes;
-    if (nv >= V) {
+// What the channel count asks of a lane's loads; a variant of its own for each, because a branch
+// per tensor makes the compiler wait for one tensor before it loads the next (3 x 1237 x 331 fp32,
+// backward: 26 us with such a branch, 17 us without).
+enum Edge {
+    kWhole,   // a multiple of a lane's channels: lanes are full or past the end
+    kRagged,  // at least one lane's channels: the last lane of a row loads the row's last V channels
+              // and shifts them into place
+    kTiny     // fewer: element by element
+};
+
+template <typename IO, int W>
+constexpr int lane_channels = 4 * W / IO::bytes;
+
+inline Edge edge_of(int64_t dim, int V) { return dim % V == 0 ? kWhole : dim > V ? kRagged : kTiny; }
+
+template <typename F>
+void with_edge(Edge e, F &&f) {
+    if (e == kWhole)
+        f(std::integral_constant<int, kWhole>{});
+    else if (e == kRagged)
+        f(std::integral_constant<int, kRagged>{});
+    else
+        f(std::integral_constant<int, kTiny>{});
+}
+
+// A lane's channels d0 .. d0 + V - 1, of which nv are there; it loads from `load` on, `shift`
+// channels earlier (lanes past the end load what is there and use none of it).
+struct Cols {
+    int d0, nv, load, shift;
+};
+template <int EDGE>
+__device__ __forceinline__ Cols cols_of(int d0, int D, int V) {
+    Cols c = {d0, min(V, D - d0), d0, 0};
+    if constexpr (EDGE != kTiny) c.load = min(d0, D - V);
+    if constexpr (EDGE == kRagged) c.shift = c.nv > 0 ? d0 - c.load : 0;
+    return c;
+}
+
+// One word group by elements (nv of them, the others 0).
+template <typename IO, int W>
+__device__ __forceinline__ Words<W> load_elements(const char *p, int nv) {
+    Words<W> q = {};
 #pragma unroll
-        for (int j = 0; j < R; ++j) q[j] = load_words<W>(base + off[j]);
-    } else {
-#pragma unroll
-        for (int j = 0; j < R; ++j) {
-            q[j] = Words<W>{};
-#pragma unroll
-            for (int e = 0; e < V; ++e)
-                if (e < nv) {
-                    if constexpr (IO::bytes == 2)
-                        q[j].w[e / 2] |= (uint32_t)reinterpret_cast<const uint16_t *>(base + off[j])[e] << (16 * (e & 1));
-                    else
-                        q[j].w[e] = reinterpret_cast<const uint32_t *>(base + off[j])[e];
-                }
+    for (int e = 0; e < lane_channels<IO, W>; ++e)
+        if (e < nv) {
+            if constexpr (IO::bytes == 2)
+                q.w[e / 2] |= (uint32_t)reinterpret_cast<const uint16_t *>(p)[e] << (16 * (e & 1));
+            else
+                q.w[e] = reinterpret_cast<const uint32_t *>(p)[e];
         }
+    return q;
+}
+
+// R rows of a lane, `off[j]` bytes behind the wave-uniform `base`.
+template <typename IO, int EDGE, int W, int R>
+__device__ __forceinline__ void load_rows(const char *base, const uint32_t (&off)[R], int nv, Words<W> (&q)[R]) {
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+        if constexpr (EDGE == kTiny)
+            q[j] = load_elements<IO, W>(base + off[j], nv);
+        else
+            q[j] = load_words<W>(base + off[j]);
     }
+}
+
+// Drops the first `shift` (< V) channels of a ragged lane's rows.
+template <typename IO, int W, int R>
+__device__ __forceinline__ void shift_rows(Words<W> (&q)[R], int shift) {
+    if (shift == 0) return;
+    constexpr int PER = 4 / IO::bytes;  // channels of a word
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+        if (PER == 2 && (shift & 1))
+#pragma unroll
+            for (int i = 0; i < W; ++i) q[j].w[i] = q[j].w[i] >> 16 | (i + 1 < W ? q[j].w[i + 1] << 16 : 0);
+#pragma unroll
+        for (int by = 1; by < W; by *= 2)
+            if (shift / PER & by)
+#pragma unroll
+                for (int i = 0; i < W; ++i) q[j].w[i] = i + by < W ? q[j].w[i + by] : 0;
+    }
+}
+
+// V channels of one row where they may be fewer (a single row: nothing to wait for in between).
+template <typename IO, int W>
+__device__ __forceinline__ Words<W> load_some(const char *p, int nv) {
+    return nv >= lane_channels<IO, W> ? load_words<W>(p) : load_elements<IO, W>(p, nv);
 }
 
 template <typename IO, int W>
