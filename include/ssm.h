@@ -573,8 +573,10 @@ ssm_status_t ssm_gated_scan_fwd(const ssm_gated_scan_args_t *args, void *stream)
  *   through a and b above;  dA, dgate_bias, din_bias summed over batch and
  *   time;  dh0 = a_0 lambda_0 (0 with a reset at 0).
  * The states are recomputed in fp32 from the forward's checkpoints (which the
- * backward computes itself when none are given).  Where sqrt(1 - a^2) is 0 its
- * derivative is taken as 0.
+ * backward computes itself when none are given).  Where 1 - a^2 is 0 or below
+ * 2^-126, the derivative of its root is taken as 0.  Steps ahead of a reset take
+ * part in the sums dA, dgate_bias and din_bias also where their dy is 0, so the
+ * inputs in a row's left padding have to be finite.
  */
 typedef struct ssm_gated_scan_bwd_args {
     int64_t batch, seqlen, dim; /* as in ssm_gated_scan_args_t                 */

@@ -129,7 +129,9 @@ __device__ __forceinline__ Gate<MODE, IG> gate_of(float g, float ig, const GateC
         const float y = c.A2 * r.s;
         o.a = hw_exp2(y);
         const float q = one_minus_sq(y, o.a);
-        o.inv_beta = q > 0.0f ? __builtin_amdgcn_rsqf(q) : 0.0f;  // 0 where sqrt(1 - a^2) is 0
+        // 0 where sqrt(1 - a^2) is 0, and below the normal range, whose inverse root the hardware
+        // makes an infinity
+        o.inv_beta = q >= 0x1p-126f ? __builtin_amdgcn_rsqf(q) : 0.0f;
         o.w = o.beta = q * o.inv_beta;
         if constexpr (IG) {
             const Logistic i = logistic(gate_arg(ig, c.ib2));

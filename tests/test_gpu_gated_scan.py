@@ -174,6 +174,24 @@ def test_saturated_gates(mode):
         assert torch.isfinite(t).all(), n
 
 
+def test_rates_at_the_end_of_the_number_range():
+    """Gates from -60 to -110: sig(gate), A sig(gate) and 1 - a^2 pass through the smallest fp32
+    numbers to 0.  What a flush to 0 may lose: sqrt(1 - a^2) below 2^-63 in a step's input, and
+    in dA's term x lambda a^2 sig / sqrt(1 - a^2) at most |x lambda| sqrt(2^-126 / (2 |A|)), with
+    |A| >= 1e-4 and |x lambda| below 5 * 330 under 2e-14 a step, 64 steps under 1.2e-12."""
+    k = scan_case("rate", 1, 64, 101, F32, seed=24, bias=False)
+    k["gate"][:] = -60.0 - 0.5 * torch.arange(101.0, device=DEV)
+    k["A"] = -torch.logspace(-4, 0, 101, device=DEV)[torch.randperm(101, generator=torch.Generator().manual_seed(1)).to(DEV)]
+    dy = torch.randn(k["x"].shape, generator=torch.Generator().manual_seed(2)).to(DEV)
+    y, _ = _fwd(k)
+    got = ssm.gated_scan_bwd(dy=dy, **k)
+    torch.cuda.synchronize()
+    H, _, E = R.gated_scan(**scan_case64(k))
+    check(y, H, E + 1e-17, "y")
+    for n, (v, e) in R.gated_scan_bwd(dy=f64(dy), **scan_case64(k)).items():
+        check(got[n], v, e + 1.2e-12, n)
+
+
 def test_positive_rates_take_no_input():
     k = scan_case("rate", 1, 20, 24, F32, seed=29, in_gate=False, bias=False)
     k["A"] = k["A"].abs() * 0.01
