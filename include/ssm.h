@@ -536,7 +536,7 @@ typedef enum ssm_gate_mode {
 
 typedef struct ssm_gated_scan_args {
     int64_t batch, seqlen;  /* B >= 0, L >= 0                                  */
-    int64_t dim;            /* D, 1 <= D <= 2^20                               */
+    int64_t dim;            /* D, 1 <= D <= 2^20; B ceil(L/128) ceil(D/32) < 2^23 */
     int32_t io_dtype;       /* ssm_dtype_t of x, gate, in_gate and y           */
     int32_t mode;           /* ssm_gate_mode_t                                 */
     const void *x;          /* (B,L,D) io_dtype, required                      */
@@ -614,7 +614,7 @@ ssm_status_t ssm_gated_scan_bwd(const ssm_gated_scan_bwd_args_t *args, void *str
  * The state is read and written IN PLACE; it is h_final of a prefill.
  */
 typedef struct ssm_gated_step_args {
-    int64_t batch, dim;     /* B >= 0, 1 <= D <= 2^20                          */
+    int64_t batch, dim;     /* B >= 0, 1 <= D <= 2^20; B ceil(D/32) < 2^23     */
     int32_t io_dtype, mode; /* as in ssm_gated_scan_args_t                     */
     float *state;           /* (B,D) fp32, updated in place; required          */
     const void *x, *gate;   /* (B,D) io_dtype, required                        */

@@ -4,6 +4,7 @@
 // of the last error and the block plans the caller creates and destroys).
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cstdarg>
 #include <cstdio>
 #include <cstdint>
@@ -707,10 +708,10 @@ ssm_status_t check_gated(int64_t B, int64_t L, int64_t D, int32_t io, int32_t mo
     if (mode != SSM_GATE_DECAY && mode != SSM_GATE_SIGMOID && mode != SSM_GATE_RATE)
         return fail(SSM_ERR_UNSUPPORTED, "mode %d is not one of ssm_gate_mode_t", mode);
     if (!mul_ok(B, L, 4 * D)) return fail(SSM_ERR_BAD_SHAPE, "sizes overflow");
-    // one workgroup per 128 steps of 32 channels, in a one-dimensional grid
-    if (!mul_ok(B, L / SSM_GATED_BLOCK + 1, D / 32 + 1) ||
-        B * (L / SSM_GATED_BLOCK + 1) * (D / 32 + 1) > ((int64_t)1 << 23))
-        return fail(SSM_ERR_UNSUPPORTED, "batch * ceil(seqlen / 128) * ceil(dim / 32) exceeds 2^23");
+    // a workgroup of up to 512 threads per 128 steps of 32 channels, fewer than 2^32 threads a launch
+    const int64_t blocks = (std::max<int64_t>(L, 1) + SSM_GATED_BLOCK - 1) / SSM_GATED_BLOCK, strips = (D + 31) / 32;
+    if (!mul_ok(B, blocks, strips) || B * blocks * strips >= (int64_t)1 << 23)
+        return fail(SSM_ERR_UNSUPPORTED, "batch * ceil(seqlen / 128) * ceil(dim / 32) is not below 2^23");
     if (mode != SSM_GATE_RATE && (in_gate || A))
         return fail(SSM_ERR_BAD_SHAPE, "in_gate and A are for SSM_GATE_RATE only");
     if (mode == SSM_GATE_DECAY && gate_bias) return fail(SSM_ERR_BAD_SHAPE, "SSM_GATE_DECAY takes no gate_bias");

@@ -130,6 +130,20 @@ def test_workspace_sizes():
     assert _run("ssm_gated_scan_bwd", _make(ssm.GatedScanBwdArgs, BWD, dict(workspace_bytes=with_ck))) == HIP
 
 
+def test_grid_limit():
+    """B ceil(L / 128) ceil(D / 32) < 2^23: one more would be 2^32 threads in a launch."""
+    size = lambda **kw: ssm.lib().ssm_gated_scan_workspace_size(  # noqa: E731
+        ctypes.byref(_make(ssm.GatedScanArgs, dict(io_dtype=1, mode=2), kw)))
+    none = ctypes.c_size_t(-1).value
+    for B, L, D in ((1 << 23, 1, 1), (1 << 23, 128, 32), (1 << 22, 129, 24), (1 << 21, 200, 33), (1, 1 << 30, 1)):
+        assert size(batch=B, seqlen=L, dim=D) == none, (B, L, D)
+        if L == 1:
+            assert _run("ssm_gated_scan_step", _make(ssm.GatedStepArgs, STEP, dict(batch=B, dim=D))) == UNSUP
+    for B, L, D in (((1 << 23) - 1, 1, 1), ((1 << 23) - 1, 128, 32), ((1 << 22) - 1, 129, 24), (1, (1 << 30) - 128, 1),
+                    (127, 1, 1 << 20), ((1 << 23) - 1, 0, 32)):
+        assert size(batch=B, seqlen=L, dim=D) != none, (B, L, D)
+
+
 STEP = dict(batch=2, dim=64, io_dtype=ssm.SSM_BF16, mode=2, state=addr(0), x=addr(1), gate=addr(2), in_gate=addr(3),
             A=addr(4), gate_bias=addr(5), in_bias=addr(6), reset=addr(7), y=addr(8))
 

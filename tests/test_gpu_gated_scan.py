@@ -353,6 +353,27 @@ def test_rows_past_32_bit_offsets():
     assert torch.equal(got["dx"][:, t:], tail["dx"]) and torch.equal(got["dgate"][:, t:], tail["dgate"])
 
 
+def test_as_many_rows_as_a_launch_takes():
+    k = scan_case("rate", (1 << 23) - 1, 1, 1, BF, seed=67, h0=False)
+    _check_bwd(k, "rows", _check_fwd(k, "rows"), dhf=False)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+def test_the_widest_rows(dtype):
+    """2^20 channels, more than a tile of steps: the last 300 channels as by themselves."""
+    D, few = 1 << 20, 300
+    k = scan_case("sigmoid", 1, 260, D, dtype, seed=69, doc=60)
+    dy = torch.randn(k["x"].shape, generator=torch.Generator().manual_seed(1)).to(dtype).to(DEV)
+    part = {m: v[..., -few:].contiguous() if isinstance(v, torch.Tensor) and v.shape[-1] == D else v
+            for m, v in k.items()}
+    for got, want in zip(_fwd(k), _fwd(part)):
+        assert torch.equal(got[..., -few:], want)
+    got = ssm.gated_scan_bwd(dy=dy, **k)
+    want = ssm.gated_scan_bwd(dy=dy[..., -few:].contiguous(), **part)
+    for n in got:
+        assert torch.equal(got[n][..., -few:], want[n]), n
+
+
 @pytest.mark.parametrize("mode", MODES)
 def test_autograd(mode):
     """backward() through the differentiable op gives the direct backward's gradients."""
