@@ -524,6 +524,11 @@ ssm_status_t ssm_ssd_step(const ssm_ssd_step_args_t *args, void *stream);
  *
  * Arithmetic is fp32 (the hardware's exponential, reciprocal and square root,
  * 1 ulp); y is rounded once.  Results do not change from run to run.
+ *
+ * A call is several launches on its stream, and its workspace carries data from
+ * one to the next: calls enqueued one after the other on a stream may use the
+ * same workspace, calls from several host threads at once, also on one stream,
+ * may not.
  */
 typedef enum ssm_gate_mode {
     SSM_GATE_DECAY = 0,

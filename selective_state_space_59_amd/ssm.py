@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import threading
 from typing import Optional, Tuple
 
 import torch
@@ -868,10 +869,23 @@ def _need(t, name, shape, dtype, device):
     return _req(t, name, shape, dtype, device).data_ptr()
 
 
+class _Scratch(threading.local):
+    """Cached workspaces of the calling thread.  Two threads may use the same stream at once, and
+    the launches of their calls then alternate on it: a workspace they shared would be emptied by
+    one call between the other's launches."""
+
+    def __init__(self):
+        self.of = {}
+
+
+_scratch = _Scratch()
+
+
 def _run(name: str, args, dev: torch.device, size_fn=None, workspace: Optional[torch.Tensor] = None):
     """ssm_<name>(args) on torch's current stream of `dev`, with that device current and with a
-    workspace where size_fn(args) asks for one.  Invalid sizes are reported by the call itself,
-    which checks its arguments before anything is launched."""
+    workspace where size_fn(args) asks for one: a cached one of this thread and stream, or in a
+    graph capture one of the graph's own.  Invalid sizes are reported by the call itself, which
+    checks its arguments before anything is launched."""
     if dev.index != torch.cuda.current_device():
         with torch.cuda.device(dev):
             return _run(name, args, dev, size_fn, workspace)
@@ -882,10 +896,12 @@ def _run(name: str, args, dev: torch.device, size_fn=None, workspace: Optional[t
         need = getattr(L, size_fn)(ref)
         if need != _NO_SIZE and need > 0:
             if workspace is None:
-                # the cached buffer of this stream (see _workspace), where it is large enough
-                workspace = _ws_cache.get((dev.type, dev.index, stream))
-                if workspace is None or workspace.numel() < need or torch.cuda.is_current_stream_capturing():
-                    workspace = _workspace(dev, need)
+                key = (dev.index, stream)
+                workspace = _scratch.of.get(key)
+                if torch.cuda.is_current_stream_capturing():
+                    workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+                elif workspace is None or workspace.numel() < need:
+                    workspace = _scratch.of[key] = torch.empty(max(need, 1 << 20), dtype=torch.uint8, device=dev)
             have = workspace.numel() * workspace.element_size()
             if workspace.device != dev or not workspace.is_contiguous() or have < need:
                 raise ValueError("workspace must be a contiguous tensor on %s of >= %d bytes" % (dev, need))

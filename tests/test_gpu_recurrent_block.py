@@ -1,6 +1,8 @@
 """The gated recurrence and the fused norms as a model uses them together (needs an MI355X): a
 residual block trained and decoded with them, the norm behind the SSD layer, and all of them
 under HIP graph capture."""
+import threading
+
 import pytest
 import torch
 
@@ -231,3 +233,40 @@ def test_a_captured_training_step():
         torch.cuda.synchronize()
         for a, b in zip(out, want):
             assert torch.equal(a, b)
+
+
+def test_two_threads_on_one_stream():
+    """Calls of two host threads alternate launch by launch on the stream they share; each gets
+    the results it gets alone."""
+    ks = [scan_case("rate", 1, 3000 + 500 * i, 96, F32, seed=91 + i, doc=400) for i in range(2)]
+    gen = torch.Generator().manual_seed(9)
+    rows = [torch.randn(4000 + i, 768, generator=gen).to(DEV) for i in range(2)]
+    w = torch.randn(768, generator=gen).to(DEV)
+
+    def calls(i):
+        y, hf = ssm.gated_scan_fwd(return_final_state=True, **ks[i])
+        g = ssm.gated_scan_bwd(dy=y, **ks[i])
+        n = ssm.add_rmsnorm_bwd(rows[i], w, None, rows[i])
+        return [y, hf, *g.values(), *n.values()]
+
+    want = [calls(0), calls(1)]
+    torch.cuda.synchronize()
+    got, failed = [[], []], []
+
+    def work(i):
+        try:
+            for _ in range(20):
+                got[i].append(calls(i))
+        except Exception as e:  # reported below, by the test's own thread
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed, failed
+    for i in range(2):
+        for run in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(run, want[i]))
