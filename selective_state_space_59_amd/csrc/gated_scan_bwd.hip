@@ -5,13 +5,17 @@
 //   lambda_t = dy_t + mu_{t+1},  mu_t = a_t (dy_t + mu_{t+1}),  mu_L = dh_final,  dh0 = mu_0
 //   da_t = lambda_t h_{t-1},  db_t = lambda_t,  and the chain rule of gated_device.h.
 //
-// Bound by HBM: x, gate, in_gate and dy are read once, dx, dgate and din_gate written once.  The
+// One pass over HBM: x, gate, in_gate and dy are read once, dx, dgate and din_gate written once.  The
 // tiles are the forward's (gated_tile.h), one checkpoint long, and chained from the last to the
 // first.  A tile recomputes its states from its checkpoint in fp32, so neither y nor any state is
 // read, and both directions share the product p of a lane's decays.  The rows stay in registers
 // as they were read; a channel at a time is widened, its gates formed (once for the lane's run,
 // once for its gradients: arithmetic is cheaper here than registers), and its gradients packed
 // into the place of its inputs.
+//
+// Measured in bf16: 8 x 2048 x 1536 RATE with in_gate 91 us, 3.9 TB/s, bound by the issue of its 94
+// vector instructions an element (13 of them exponentials, reciprocals and roots); 4 x 4096 x 5120
+// SIGMOID with resets 180 us, 4.7 TB/s, where the waves wait for the tile's phases.
 #include "gated_tile.h"
 #include "ssm_internal.h"
 

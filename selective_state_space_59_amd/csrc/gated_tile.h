@@ -8,47 +8,43 @@
 
 namespace ssm {
 
-// A lane holds W words (4 bytes) of each of its rows.
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+typedef u32x2_t u32x2_a2 __attribute__((aligned(2)));
+
+// A lane holds W words (4 bytes) of each of its rows: 4, or 2 for the decode step's bf16.
 template <int W>
 struct Words {
+    static_assert(W == 4 || W == 2, "16 or 8 bytes a lane");
     uint32_t w[W];
 };
 
 template <int W>
 __device__ __forceinline__ Words<W> load_words(const char *p) {
     Words<W> r;
-    typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
-    typedef u32x2_t u32x2_a2 __attribute__((aligned(2)));
-    typedef uint32_t u32_a2 __attribute__((aligned(2)));
     if constexpr (W == 4) {
         const u32x4_t v = *reinterpret_cast<const u32x4_a2 *>(p);
 #pragma unroll
         for (int i = 0; i < 4; ++i) r.w[i] = v[i];
-    } else if constexpr (W == 2) {
+    } else {
         const u32x2_t v = *reinterpret_cast<const u32x2_a2 *>(p);
         r.w[0] = v[0];
         r.w[1] = v[1];
-    } else {
-        r.w[0] = *reinterpret_cast<const u32_a2 *>(p);
     }
     return r;
 }
 
 template <int W>
 __device__ __forceinline__ void store_words(char *p, const Words<W> &q) {
-    typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
-    typedef u32x2_t u32x2_a2 __attribute__((aligned(2)));
-    typedef uint32_t u32_a2 __attribute__((aligned(2)));
     if constexpr (W == 4)
         *reinterpret_cast<u32x4_a2 *>(p) = u32x4_t{q.w[0], q.w[1], q.w[2], q.w[3]};
-    else if constexpr (W == 2)
-        *reinterpret_cast<u32x2_a2 *>(p) = u32x2_t{q.w[0], q.w[1]};
     else
-        *reinterpret_cast<u32_a2 *>(p) = q.w[0];
+        *reinterpret_cast<u32x2_a2 *>(p) = u32x2_t{q.w[0], q.w[1]};
 }
 
 // How a tile lies over a workgroup: THREADS lanes, W words of R consecutive rows each; the lanes
-// of a row cover kRowBytes.
+// of a row cover kRowBytes.  128 bytes give a layer of 1536 channels 24 blocks a row, and the lanes
+// of a row one whole line; pieces of 256 or 512 bytes, with as many times fewer and larger
+// workgroups, ran the 8 x 2048 x 1536 bf16 forward in 82 and 99 us where 128 took 71.
 constexpr int kRowBytes = 128;
 
 template <typename IO, int W_, int R_, int THREADS_>
@@ -63,7 +59,7 @@ struct Tile {
 
 // What the channel count asks of a lane's loads; a variant of its own for each, because a branch
 // per tensor makes the compiler wait for one tensor before it loads the next (3 x 1237 x 331 fp32,
-// backward: 26 us with such a branch, 17 us without).
+// backward: 26 us with such a branch, 12 us without).
 enum Edge {
     kWhole,   // a multiple of a lane's channels: lanes are full or past the end
     kRagged,  // at least one lane's channels: the last lane of a row loads the row's last V channels
@@ -186,18 +182,12 @@ __device__ __forceinline__ Words<W> lane_pack(const float (&f)[4 * W / IO::bytes
     return q;
 }
 
-// V floats of a lane to and from LDS.
+// V floats of a lane to LDS.
 template <int V>
 __device__ __forceinline__ void lds_put(float *p, const float (&f)[V]) {
-    if constexpr (V % 4 == 0) {
+    static_assert(V % 4 == 0, "16 bytes at a time");
 #pragma unroll
-        for (int v = 0; v < V; v += 4) *reinterpret_cast<float4 *>(p + v) = make_float4(f[v], f[v + 1], f[v + 2], f[v + 3]);
-    } else if constexpr (V == 2) {
-        *reinterpret_cast<float2 *>(p) = make_float2(f[0], f[1]);
-    } else {
-#pragma unroll
-        for (int v = 0; v < V; ++v) p[v] = f[v];
-    }
+    for (int v = 0; v < V; v += 4) *reinterpret_cast<float4 *>(p + v) = make_float4(f[v], f[v + 1], f[v + 2], f[v + 3]);
 }
 
 // A run of steps maps the state h entering it to p h + l (p the product of its decays, l its
@@ -215,7 +205,7 @@ __device__ __forceinline__ float run_apply(float p, float l, float h) {
 // meets a state.  A record is one atomic word, so it needs no flag and no fence: the high word
 // tells what it holds, with two NaN patterns that p is never stored as.
 constexpr uint32_t kRecEmpty = 0xffffffffu, kRecState = 0xfffffffeu;
-constexpr int kLook = 8;  // records looked at together
+constexpr int kLook = 8;  // records looked at together (4: 1M tokens 6% slower; 16: more registers, no faster)
 
 typedef unsigned long long u64_t;
 
@@ -259,8 +249,8 @@ __device__ __forceinline__ uint32_t rec_hi(float p) { return p != p ? 0x7fc00000
 // The chain of workgroup i of chains * tiles (the tile within it is the ticket it draws).
 // Workgroups go to the XCDs in turn.  A short chain's tiles are dealt out one chain after the
 // other; a long chain's run over all XCDs, eight at a time, so that no chain waits for one XCD that
-// is behind (1M tokens x 1024 channels: 1750 us, against 2013 us dealt out; the 130M-like layer,
-// 8 tiles a chain, 52.4 us dealt out against 53.1).  Either way every chain gets `tiles`.
+// is behind (as this was chosen, 1M tokens x 1024 channels: 1750 us, against 2013 us dealt out;
+// 8 x 2048 x 1536, 8 tiles a chain: 52.4 us dealt out against 53.1).  Either way every chain gets `tiles`.
 constexpr int kLongChain = 64;
 
 __device__ __forceinline__ int chain_of(unsigned i, int chains, int tiles) {

@@ -4,7 +4,9 @@
 //
 // A team of lanes owns a row, 8 elements a lane and group, read once into registers:
 //   rows of up to 256      8 or 32 lanes, several rows a wave (adjacent groups side by side)
-//   up to 512 * NR         one wave, NR groups a lane: sums without a barrier
+//   513 to 768             32 lanes of 3 groups (forwards; the gated backward over several groups)
+//   up to 2048             one wave of up to 4 groups a lane: sums without a barrier (backwards up
+//                          to 1024, whose column sums take registers too)
 //   up to kBlockRow        one workgroup of as many waves as the row needs, one group a lane
 //   longer                 one workgroup of 1024, reading the row again for each of its passes
 // A team keeps its columns over all its rows, so the weights stay in registers and the
