@@ -20,12 +20,12 @@ namespace ssm {
 namespace {
 
 // r of one group; k: 1 / rms(x) with a post norm.  u is left in `u`.
-template <typename IO, typename RES, bool EXTRA>
-__device__ __forceinline__ void stream8(const Raw8<IO> &x, const Raw8<RES> &res, const float (&pw)[8],
-                                        const float (&sc)[8], bool post, bool scale, float k, float (&u)[8],
-                                        float (&r)[8]) {
+template <typename IO, typename RES, bool EXTRA, int E>
+__device__ __forceinline__ void stream_group(const Raw<IO, E> &x, const Raw<RES, E> &res, const float (&pw)[E],
+                                        const float (&sc)[E], bool post, bool scale, float k, float (&u)[E],
+                                        float (&r)[E]) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
+    for (int e = 0; e < E; ++e) {
         u[e] = x[e];
         if constexpr (EXTRA) {
             if (post) u[e] = u[e] * k * pw[e];
@@ -38,7 +38,7 @@ __device__ __forceinline__ void stream8(const Raw8<IO> &x, const Raw8<RES> &res,
 
 template <typename IO, typename RES, bool EXTRA, typename SH>
 __global__ __launch_bounds__(SH::THREADS) void add_norm_kernel(ssm_add_norm_args_t a, int64_t slots) {
-    constexpr int TEAM = SH::TEAM, NR = SH::NR;
+    constexpr int TEAM = SH::TEAM, NR = SH::NR, E = SH::E;
     __shared__ SumSlots sums;
     int turn = 0;
     const int lane = TEAM == 0 ? threadIdx.x : threadIdx.x % (TEAM ? TEAM : 1), width = TEAM == 0 ? blockDim.x : TEAM;
@@ -46,25 +46,25 @@ __global__ __launch_bounds__(SH::THREADS) void add_norm_kernel(ssm_add_norm_args
     const int D = (int)a.dim;
     const float inv_n = 1.0f / (float)D;
     const bool post = EXTRA && a.post_w, scale = EXTRA && a.scale;
-    float w[NR][8], pw[NR][8] = {}, sc[NR][8] = {};
+    float w[NR][E], pw[NR][E] = {}, sc[NR][E] = {};
     int n[NR];
 #pragma unroll
     for (int c = 0; c < NR; ++c) {
-        const int i = 8 * (lane + c * width);
-        n[c] = max(0, min(8, D - i));
+        const int i = E * (lane + c * width);
+        n[c] = max(0, min(E, D - i));
         load_vec(a.w, i, n[c], w[c]);
         if (post) load_vec(a.post_w, i, n[c], pw[c]);
         if (scale) load_vec(a.scale, i, n[c], sc[c]);
     }
     for (int64_t row = t.row; row < a.rows; row += t.step) {
         const int64_t base = row * D;
-        Raw8<IO> x[NR];
-        Raw8<RES> res[NR];
+        Raw<IO, E> x[NR];
+        Raw<RES, E> res[NR];
 #pragma unroll
         for (int c = 0; c < NR; ++c) {
-            const int i = 8 * (lane + c * width);
-            x[c] = load8<IO>(a.x, base + i, n[c]);
-            res[c] = a.residual ? load8<RES>(a.residual, base + i, n[c]) : Raw8<RES>{};
+            const int i = E * (lane + c * width);
+            x[c] = load_raw<IO, E>(a.x, base + i, n[c]);
+            res[c] = a.residual ? load_raw<RES, E>(a.residual, base + i, n[c]) : Raw<RES, E>{};
         }
         float k = 1.0f;
         if (post) {
@@ -72,31 +72,31 @@ __global__ __launch_bounds__(SH::THREADS) void add_norm_kernel(ssm_add_norm_args
 #pragma unroll
             for (int c = 0; c < NR; ++c)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) s = __builtin_fmaf(x[c][e], x[c][e], s);
+                for (int e = 0; e < E; ++e) s = __builtin_fmaf(x[c][e], x[c][e], s);
             k = inv_rms(team_sum<TEAM>(s, sums, turn), inv_n, a.eps);
         }
-        float r[NR][8], u[8], s = 0.0f;
+        float r[NR][E], u[E], s = 0.0f;
 #pragma unroll
         for (int c = 0; c < NR; ++c) {
-            stream8<IO, RES, EXTRA>(x[c], res[c], pw[c], sc[c], post, scale, k, u, r[c]);
+            stream_group<IO, RES, EXTRA>(x[c], res[c], pw[c], sc[c], post, scale, k, u, r[c]);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) s = __builtin_fmaf(r[c][e], r[c][e], s);
+            for (int e = 0; e < E; ++e) s = __builtin_fmaf(r[c][e], r[c][e], s);
         }
         const float q = inv_rms(team_sum<TEAM>(s, sums, turn), inv_n, a.eps);
 #pragma unroll
         for (int c = 0; c < NR; ++c) {
-            const int i = 8 * (lane + c * width);
-            if (a.res_out) store8<RES>(a.res_out, base + i, n[c], r[c]);
+            const int i = E * (lane + c * width);
+            if (a.res_out) store_raw<RES>(a.res_out, base + i, n[c], r[c]);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) u[e] = r[c][e] * q * w[c][e];
-            store8<IO>(a.y, base + i, n[c], u);
+            for (int e = 0; e < E; ++e) u[e] = r[c][e] * q * w[c][e];
+            store_raw<IO>(a.y, base + i, n[c], u);
         }
     }
 }
 
 template <typename IO, typename RES, bool EXTRA, typename SH>
 __global__ __launch_bounds__(SH::THREADS) void add_norm_bwd_kernel(ssm_add_norm_bwd_args_t a, int64_t slots, float *part, int64_t prows) {
-    constexpr int TEAM = SH::TEAM, NR = SH::NR;
+    constexpr int TEAM = SH::TEAM, NR = SH::NR, E = SH::E;
     __shared__ SumSlots sums;
     int turn = 0;
     const int lane = TEAM == 0 ? threadIdx.x : threadIdx.x % (TEAM ? TEAM : 1), width = TEAM == 0 ? blockDim.x : TEAM;
@@ -104,28 +104,28 @@ __global__ __launch_bounds__(SH::THREADS) void add_norm_bwd_kernel(ssm_add_norm_
     const int D = (int)a.dim;
     const float inv_n = 1.0f / (float)D;
     const bool post = EXTRA && a.post_w, scale = EXTRA && a.scale;
-    float w[NR][8], pw[NR][8] = {}, sc[NR][8] = {};
-    float aw[NR][8] = {}, as[NR][8] = {}, ap[NR][8] = {};
+    float w[NR][E], pw[NR][E] = {}, sc[NR][E] = {};
+    float aw[NR][E] = {}, as[NR][E] = {}, ap[NR][E] = {};
     int n[NR];
 #pragma unroll
     for (int c = 0; c < NR; ++c) {
-        const int i = 8 * (lane + c * width);
-        n[c] = max(0, min(8, D - i));
+        const int i = E * (lane + c * width);
+        n[c] = max(0, min(E, D - i));
         load_vec(a.w, i, n[c], w[c]);
         if (post) load_vec(a.post_w, i, n[c], pw[c]);
         if (scale) load_vec(a.scale, i, n[c], sc[c]);
     }
     for (int64_t row = t.row; row < a.rows; row += t.step) {
         const int64_t base = row * D;
-        Raw8<IO> x[NR], dy[NR];
-        Raw8<RES> res[NR], up[NR];
+        Raw<IO, E> x[NR], dy[NR];
+        Raw<RES, E> res[NR], up[NR];
 #pragma unroll
         for (int c = 0; c < NR; ++c) {
-            const int i = 8 * (lane + c * width);
-            x[c] = load8<IO>(a.x, base + i, n[c]);
-            res[c] = a.residual ? load8<RES>(a.residual, base + i, n[c]) : Raw8<RES>{};
-            dy[c] = load8<IO>(a.dy, base + i, n[c]);
-            up[c] = a.dres_out ? load8<RES>(a.dres_out, base + i, n[c]) : Raw8<RES>{};
+            const int i = E * (lane + c * width);
+            x[c] = load_raw<IO, E>(a.x, base + i, n[c]);
+            res[c] = a.residual ? load_raw<RES, E>(a.residual, base + i, n[c]) : Raw<RES, E>{};
+            dy[c] = load_raw<IO, E>(a.dy, base + i, n[c]);
+            up[c] = a.dres_out ? load_raw<RES, E>(a.dres_out, base + i, n[c]) : Raw<RES, E>{};
         }
         float k = 1.0f;
         if (post) {
@@ -133,15 +133,15 @@ __global__ __launch_bounds__(SH::THREADS) void add_norm_bwd_kernel(ssm_add_norm_
 #pragma unroll
             for (int c = 0; c < NR; ++c)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) s = __builtin_fmaf(x[c][e], x[c][e], s);
+                for (int e = 0; e < E; ++e) s = __builtin_fmaf(x[c][e], x[c][e], s);
             k = inv_rms(team_sum<TEAM>(s, sums, turn), inv_n, a.eps);
         }
-        float u[NR][8], r[NR][8], s = 0.0f, dot = 0.0f;
+        float u[NR][E], r[NR][E], s = 0.0f, dot = 0.0f;
 #pragma unroll
         for (int c = 0; c < NR; ++c) {
-            stream8<IO, RES, EXTRA>(x[c], res[c], pw[c], sc[c], post, scale, k, u[c], r[c]);
+            stream_group<IO, RES, EXTRA>(x[c], res[c], pw[c], sc[c], post, scale, k, u[c], r[c]);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
+            for (int e = 0; e < E; ++e) {
                 s = __builtin_fmaf(r[c][e], r[c][e], s);
                 dot = __builtin_fmaf(dy[c][e] * w[c][e], r[c][e], dot);
             }
@@ -152,7 +152,7 @@ __global__ __launch_bounds__(SH::THREADS) void add_norm_bwd_kernel(ssm_add_norm_
 #pragma unroll
         for (int c = 0; c < NR; ++c)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
+            for (int e = 0; e < E; ++e) {
                 aw[c][e] = __builtin_fmaf(dy[c][e] * q, r[c][e], aw[c][e]);
                 // dr in r's place
                 r[c][e] = __builtin_fmaf(q * w[c][e], dy[c][e], __builtin_fmaf(-m, r[c][e], up[c][e]));
@@ -170,16 +170,16 @@ __global__ __launch_bounds__(SH::THREADS) void add_norm_bwd_kernel(ssm_add_norm_
 #pragma unroll
             for (int c = 0; c < NR; ++c)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) u[c][e] = __builtin_fmaf(k * pw[c][e], u[c][e], -m2 * x[c][e]);
+                for (int e = 0; e < E; ++e) u[c][e] = __builtin_fmaf(k * pw[c][e], u[c][e], -m2 * x[c][e]);
         }
 #pragma unroll
         for (int c = 0; c < NR; ++c) {
-            const int i = 8 * (lane + c * width);
-            if (a.dresidual) store8<RES>(a.dresidual, base + i, n[c], r[c]);
+            const int i = E * (lane + c * width);
+            if (a.dresidual) store_raw<RES>(a.dresidual, base + i, n[c], r[c]);
             if constexpr (EXTRA)
-                store8<IO>(a.dx, base + i, n[c], u[c]);
+                store_raw<IO>(a.dx, base + i, n[c], u[c]);
             else
-                store8<IO>(a.dx, base + i, n[c], r[c]);
+                store_raw<IO>(a.dx, base + i, n[c], r[c]);
         }
     }
     int64_t slot = t.row;
@@ -196,10 +196,10 @@ __global__ __launch_bounds__(SH::THREADS) void add_norm_bwd_kernel(ssm_add_norm_
     if (!writes) return;
 #pragma unroll
     for (int c = 0; c < NR; ++c) {
-        const int i = 8 * (lane + c * width);
-        store8<io_f32>(part, slot * D + i, n[c], aw[c]);
-        if (scale) store8<io_f32>(part, (prows + slot) * D + i, n[c], as[c]);
-        if (post) store8<io_f32>(part, (2 * prows + slot) * D + i, n[c], ap[c]);
+        const int i = E * (lane + c * width);
+        store_raw<io_f32>(part, slot * D + i, n[c], aw[c]);
+        if (scale) store_raw<io_f32>(part, (prows + slot) * D + i, n[c], as[c]);
+        if (post) store_raw<io_f32>(part, (2 * prows + slot) * D + i, n[c], ap[c]);
     }
 }
 
@@ -307,18 +307,25 @@ void with_types(int32_t io, int32_t res, F &&f) {
     }
 }
 
-constexpr int64_t kFwdBlocks = 1024, kBwdBlocks = 512, kLongBlocks = 256;
+constexpr int64_t kFwdBlocks = 1024, kLongBlocks = 256;
+
+// In the backward a lane of a workgroup takes 16 bytes a group from bf16 rows, and also from fp32
+// rows as long as two workgroups of half as many elements a lane, 12 waves at most, fit a CU
+// (8192 x 2560 fp32 with post norm and scale: 134 us, against 176 with 8 elements and 130 registers
+// a lane; of 4096, where one fits either way, 239 against 219).
+bool half_groups(int32_t io, int64_t D) { return io == SSM_F32 && D > 1024 && (D + 255) / 256 <= 12; }
 
 // The launch shape of the backward for rows of D (the forward adds half a wave with NR = 3 and a
 // wave with NR = 4: it holds less per row, and leaves no partial sums).
-RowGrid bwd_grid(int64_t rows, int64_t D) {
+RowGrid bwd_grid(int64_t rows, int64_t D, int32_t io) {
     if (D > kBlockRow) return RowGrid{(unsigned)std::min(rows, kLongBlocks), 1024, std::min(rows, kLongBlocks)};
-    return row_grid(D <= 64 ? 8 : D <= 256 ? 32 : D <= 1024 ? 64 : 0, D, rows, 1, kBwdBlocks);
+    return row_grid(D <= 64 ? 8 : D <= 256 ? 32 : D <= 1024 ? 64 : 0, D, rows, 1, bwd_blocks(D),
+                    half_groups(io, D) ? 4 : 8);
 }
 
 // Rows of partial sums: one per workgroup where its waves add theirs up, else one per team.
-int64_t partial_rows(int64_t rows, int64_t D) {
-    const RowGrid g = bwd_grid(rows, D);
+int64_t partial_rows(int64_t rows, int64_t D, int32_t io) {
+    const RowGrid g = bwd_grid(rows, D, io);
     return D > 256 ? g.blocks : g.slots;
 }
 
@@ -352,13 +359,13 @@ hipError_t launch_add_norm_fwd(const ssm_add_norm_args_t &a, hipStream_t stream)
 }
 
 size_t add_norm_bwd_workspace_bytes(const ssm_add_norm_bwd_args_t &a) {
-    const int64_t n = partial_rows(a.rows, a.dim);
+    const int64_t n = partial_rows(a.rows, a.dim, a.io_dtype);
     return (((size_t)(3 * n * a.dim) * 4 + 255) & ~(size_t)255) + column_sums_scratch_bytes(n, a.dim, 3);
 }
 
 hipError_t launch_add_norm_bwd(const ssm_add_norm_bwd_args_t &a, hipStream_t stream) {
-    const int64_t D = a.dim, n = partial_rows(a.rows, D);
-    const RowGrid g = bwd_grid(a.rows, D);
+    const int64_t D = a.dim, n = partial_rows(a.rows, D, a.io_dtype);
+    const RowGrid g = bwd_grid(a.rows, D, a.io_dtype);
     float *part = static_cast<float *>(a.workspace);
     with_types(a.io_dtype, a.res_dtype, [&](auto io, auto res) {
         using IO = decltype(io);
@@ -374,7 +381,9 @@ hipError_t launch_add_norm_bwd(const ssm_add_norm_bwd_args_t &a, hipStream_t str
         else if (D <= 256) go(Shape<32, 1>{});
         else if (D <= 512) go(Shape<64, 1>{});
         else if (D <= 1024) go(Shape<64, 2>{});
-        else if (D <= 4096) go(Shape<0, 1, 512>{});
+        else if (half_groups(a.io_dtype, D)) {
+            if constexpr (IO::bytes == 4) go(Shape<0, 1, 768, 4>{});
+        } else if (D <= 4096) go(Shape<0, 1, 512>{});
         else if (D <= kBlockRow) go(Shape<0, 1, 1024>{});
         else
             add_norm_bwd_long_kernel<IO, RES><<<g.blocks, 1024, 0, stream>>>(a, part, n);

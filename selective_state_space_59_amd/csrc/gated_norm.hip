@@ -18,7 +18,7 @@ __device__ __forceinline__ float logistic(float z) { return hw_rcp(1.0f + hw_exp
 
 template <typename IO, bool FIRST, typename SH>
 __global__ __launch_bounds__(SH::THREADS) void gated_norm_kernel(ssm_gated_norm_args_t a, int64_t slots) {
-    constexpr int TEAM = SH::TEAM, NR = SH::NR;
+    constexpr int TEAM = SH::TEAM, NR = SH::NR, E = SH::E;
     __shared__ SumSlots sums;
     int turn = 0;
     const int lane = TEAM == 0 ? threadIdx.x : threadIdx.x % (TEAM ? TEAM : 1), width = TEAM == 0 ? blockDim.x : TEAM;
@@ -26,38 +26,38 @@ __global__ __launch_bounds__(SH::THREADS) void gated_norm_kernel(ssm_gated_norm_
     const int S = (int)(a.dim / a.groups);
     const float inv_n = 1.0f / (float)S;
     const int64_t col = t.g * S;
-    float w[NR][8];
+    float w[NR][E];
     int n[NR];
 #pragma unroll
     for (int c = 0; c < NR; ++c) {
-        const int i = 8 * (lane + c * width);
-        n[c] = max(0, min(8, S - i));
+        const int i = E * (lane + c * width);
+        n[c] = max(0, min(E, S - i));
         load_vec(a.w, col + i, n[c], w[c]);
     }
     for (int64_t row = t.row; row < a.rows; row += t.step) {
         const int64_t base = row * a.dim + col;
-        Raw8<IO> x[NR], z[NR];
+        Raw<IO, E> x[NR], z[NR];
 #pragma unroll
         for (int c = 0; c < NR; ++c) {
-            const int i = 8 * (lane + c * width);
-            x[c] = load8<IO>(a.x, base + i, n[c]);
-            z[c] = load8<IO>(a.z, base + i, n[c]);
+            const int i = E * (lane + c * width);
+            x[c] = load_raw<IO, E>(a.x, base + i, n[c]);
+            z[c] = load_raw<IO, E>(a.z, base + i, n[c]);
         }
-        float v[NR][8], s = 0.0f;
+        float v[NR][E], s = 0.0f;
 #pragma unroll
         for (int c = 0; c < NR; ++c)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
+            for (int e = 0; e < E; ++e) {
                 v[c][e] = FIRST ? x[c][e] * silu(z[c][e]) : x[c][e];
                 s = __builtin_fmaf(v[c][e], v[c][e], s);
             }
         const float q = inv_rms(team_sum<TEAM>(s, sums, turn), inv_n, a.eps);
 #pragma unroll
         for (int c = 0; c < NR; ++c) {
-            const int i = 8 * (lane + c * width);
+            const int i = E * (lane + c * width);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[c][e] *= FIRST ? q * w[c][e] : q * w[c][e] * silu(z[c][e]);
-            store8<IO>(a.y, base + i, n[c], v[c]);
+            for (int e = 0; e < E; ++e) v[c][e] *= FIRST ? q * w[c][e] : q * w[c][e] * silu(z[c][e]);
+            store_raw<IO>(a.y, base + i, n[c], v[c]);
         }
     }
 }
@@ -65,7 +65,7 @@ __global__ __launch_bounds__(SH::THREADS) void gated_norm_kernel(ssm_gated_norm_
 template <typename IO, bool FIRST, typename SH>
 __global__ __launch_bounds__(SH::THREADS) void gated_norm_bwd_kernel(
     ssm_gated_norm_bwd_args_t a, int64_t slots, float *part) {
-    constexpr int TEAM = SH::TEAM, NR = SH::NR;
+    constexpr int TEAM = SH::TEAM, NR = SH::NR, E = SH::E;
     __shared__ SumSlots sums;
     int turn = 0;
     const int lane = TEAM == 0 ? threadIdx.x : threadIdx.x % (TEAM ? TEAM : 1), width = TEAM == 0 ? blockDim.x : TEAM;
@@ -73,23 +73,23 @@ __global__ __launch_bounds__(SH::THREADS) void gated_norm_bwd_kernel(
     const int S = (int)(a.dim / a.groups);
     const float inv_n = 1.0f / (float)S;
     const int64_t col = t.g * S;
-    float w[NR][8], aw[NR][8] = {};
+    float w[NR][E], aw[NR][E] = {};
     int n[NR];
 #pragma unroll
     for (int c = 0; c < NR; ++c) {
-        const int i = 8 * (lane + c * width);
-        n[c] = max(0, min(8, S - i));
+        const int i = E * (lane + c * width);
+        n[c] = max(0, min(E, S - i));
         load_vec(a.w, col + i, n[c], w[c]);
     }
-    Raw8<IO> x[NR], z[NR], dy[NR], x1[NR], z1[NR], dy1[NR];
-    auto load_row = [&](int64_t row, Raw8<IO>(&x)[NR], Raw8<IO>(&z)[NR], Raw8<IO>(&dy)[NR]) {
+    Raw<IO, E> x[NR], z[NR], dy[NR], x1[NR], z1[NR], dy1[NR];
+    auto load_row = [&](int64_t row, Raw<IO, E>(&x)[NR], Raw<IO, E>(&z)[NR], Raw<IO, E>(&dy)[NR]) {
         const int64_t base = row * a.dim + col;
 #pragma unroll
         for (int c = 0; c < NR; ++c) {
-            const int i = 8 * (lane + c * width);
-            x[c] = load8<IO>(a.x, base + i, n[c]);
-            z[c] = load8<IO>(a.z, base + i, n[c]);
-            dy[c] = load8<IO>(a.dy, base + i, n[c]);
+            const int i = E * (lane + c * width);
+            x[c] = load_raw<IO, E>(a.x, base + i, n[c]);
+            z[c] = load_raw<IO, E>(a.z, base + i, n[c]);
+            dy[c] = load_raw<IO, E>(a.dy, base + i, n[c]);
         }
     };
     constexpr bool AHEAD = NR <= 2;  // the next row is on its way while this one's sums are formed
@@ -107,11 +107,11 @@ __global__ __launch_bounds__(SH::THREADS) void gated_norm_bwd_kernel(
         } else {
             load_row(row, x, z, dy);
         }
-        float sg[NR][8], s = 0.0f, dot = 0.0f;
+        float sg[NR][E], s = 0.0f, dot = 0.0f;
 #pragma unroll
         for (int c = 0; c < NR; ++c)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
+            for (int e = 0; e < E; ++e) {
                 sg[c][e] = logistic(z[c][e]);
                 const float g = z[c][e] * sg[c][e], v = FIRST ? x[c][e] * g : x[c][e];
                 const float up = FIRST ? dy[c][e] : dy[c][e] * g;
@@ -122,10 +122,10 @@ __global__ __launch_bounds__(SH::THREADS) void gated_norm_bwd_kernel(
         const float q = inv_rms(s, inv_n, a.eps), m = dot * inv_n * q * q * q;
 #pragma unroll
         for (int c = 0; c < NR; ++c) {
-            const int i = 8 * (lane + c * width);
-            float dx[8], dz[8];
+            const int i = E * (lane + c * width);
+            float dx[E], dz[E];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
+            for (int e = 0; e < E; ++e) {
                 const float g = z[c][e] * sg[c][e], slope = sg[c][e] * __builtin_fmaf(z[c][e], 1.0f - sg[c][e], 1.0f);
                 const float qw = q * w[c][e];
                 if constexpr (FIRST) {
@@ -140,8 +140,8 @@ __global__ __launch_bounds__(SH::THREADS) void gated_norm_bwd_kernel(
                     aw[c][e] = __builtin_fmaf(up * q, x[c][e], aw[c][e]);
                 }
             }
-            store8<IO>(a.dx, base + i, n[c], dx);
-            store8<IO>(a.dz, base + i, n[c], dz);
+            store_raw<IO>(a.dx, base + i, n[c], dx);
+            store_raw<IO>(a.dz, base + i, n[c], dz);
         }
     }
     int64_t slot = t.row;
@@ -155,7 +155,7 @@ __global__ __launch_bounds__(SH::THREADS) void gated_norm_bwd_kernel(
     }
     if (!writes) return;
 #pragma unroll
-    for (int c = 0; c < NR; ++c) store8<io_f32>(part, slot * a.dim + col + 8 * (lane + c * width), n[c], aw[c]);
+    for (int c = 0; c < NR; ++c) store_raw<io_f32>(part, slot * a.dim + col + E * (lane + c * width), n[c], aw[c]);
 }
 
 // Groups longer than kBlockRow: a workgroup of 1024 reads the group again for each pass.
@@ -212,7 +212,7 @@ __global__ __launch_bounds__(1024) void gated_norm_bwd_long_kernel(ssm_gated_nor
     }
 }
 
-constexpr int64_t kFwdBlocks = 2048, kBwdBlocks = 512, kLongBlocks = 256;
+constexpr int64_t kFwdBlocks = 2048, kLongBlocks = 256;
 
 // Groups of 513 to 768 channels: half a wave with three groups of 8 a lane leaves fewer lanes idle
 // than a wave with two (16384 x 5120 in 8 groups of 640: forward and backward 262 us against
@@ -227,7 +227,7 @@ int bwd_team(int64_t S, int64_t groups) {
 
 RowGrid bwd_grid(int64_t rows, int64_t S, int64_t groups) {
     return row_grid(bwd_team(S, groups), std::min<int64_t>(S, kBlockRow), rows, groups,
-                    S > kBlockRow ? kLongBlocks : kBwdBlocks);
+                    S > kBlockRow ? kLongBlocks : bwd_blocks(S));
 }
 
 int64_t partial_rows(int64_t rows, int64_t S, int64_t groups) {

@@ -2,7 +2,7 @@
 // shapes.  A "row" here is what one mean square is taken over: a row of the tensor, or a group
 // of its channels.
 //
-// A team of lanes owns a row, 8 elements a lane and group, read once into registers:
+// A team of lanes owns a row, groups of 8 elements (or 4) a lane, read once into registers:
 //   rows of up to 256      8 or 32 lanes, several rows a wave (adjacent groups side by side)
 //   513 to 768             32 lanes of 3 groups (forwards; the gated backward over several groups)
 //   up to 2048             one wave of up to 4 groups a lane: sums without a barrier (backwards up
@@ -23,10 +23,10 @@ namespace ssm {
 constexpr int kBlockRow = 8192;   // longest row held in a workgroup's registers
 constexpr int kTeamThreads = 256; // workgroup of the teams of up to a wave
 
-// TEAM lanes (1 << n up to 64, or 0: the workgroup, of at most THREADS) with NR groups of 8 each.
-template <int TEAM_, int NR_, int THREADS_ = kTeamThreads>
+// TEAM lanes (1 << n up to 64, or 0: the workgroup, of at most THREADS) with NR groups of E each.
+template <int TEAM_, int NR_, int THREADS_ = kTeamThreads, int E_ = 8>
 struct Shape {
-    static constexpr int TEAM = TEAM_, NR = NR_, THREADS = THREADS_;
+    static constexpr int TEAM = TEAM_, NR = NR_, THREADS = THREADS_, E = E_;
 };
 
 template <int TEAM>
@@ -73,11 +73,12 @@ __device__ __forceinline__ float inv_rms(float sum, float inv_n, float eps) {
     return 1.0f / sqrtf(__builtin_fmaf(sum, inv_n, eps));
 }
 
-// Eight weights (the first n of them) as floats.
-__device__ __forceinline__ void load_vec(const float *p, int64_t i, int n, float (&w)[8]) {
-    const Raw8<io_f32> r = load8<io_f32>(p, i, n);
+// E weights (the first n of them) as floats.
+template <int E>
+__device__ __forceinline__ void load_vec(const float *p, int64_t i, int n, float (&w)[E]) {
+    const Raw<io_f32, E> r = load_raw<io_f32, E>(p, i, n);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) w[e] = r[e];
+    for (int e = 0; e < E; ++e) w[e] = r[e];
 }
 
 // Column sums of the waves of a workgroup that hold the same columns: into wave 0's registers.
@@ -124,8 +125,14 @@ __device__ __forceinline__ TeamRows team_rows(int64_t groups, int64_t slots) {
     return {t % groups, slot < slots ? slot : (int64_t)1 << 62, slots};  // spare teams: no rows
 }
 
-// `blocks_wanted`: workgroups that keep the chip busy.
-inline RowGrid row_grid(int team, int64_t len, int64_t rows, int64_t groups, int64_t blocks_wanted) {
+// Workgroups of a backward: as many as run at once, since each walks over rows to its end.  In waves
+// a row of up to 2048 takes at most one of a SIMD, one of up to 4096 two, and the kernels' registers
+// leave room for four (16384 rows of 1280 bf16 with a post norm: 153 us with 512 workgroups, 110 with
+// 1024; of 2560: 184 with 512, 220 with 768; 8192 rows of 5120: 231 with 512, 226 with 256).
+inline int64_t bwd_blocks(int64_t len) { return len <= 1024 ? 512 : len <= 2048 ? 1024 : len <= 4096 ? 512 : 256; }
+
+// `blocks_wanted`: workgroups that keep the chip busy; E: elements of a lane's group.
+inline RowGrid row_grid(int team, int64_t len, int64_t rows, int64_t groups, int64_t blocks_wanted, int E = 8) {
     RowGrid g;
     if (team == 0 || team == 64) {
         const int64_t per = team == 0 ? 1 : kTeamThreads / 64;
@@ -133,7 +140,7 @@ inline RowGrid row_grid(int team, int64_t len, int64_t rows, int64_t groups, int
         const int64_t n = std::min(most, want);
         g.blocks = (unsigned)(n * groups);
         g.slots = n * per;
-        g.threads = team == 0 ? (unsigned)std::min<int64_t>(1024, (len + 511) / 512 * 64) : kTeamThreads;
+        g.threads = team == 0 ? (unsigned)std::min<int64_t>(1024, (len + 64 * E - 1) / (64 * E) * 64) : kTeamThreads;
     } else {
         const int64_t per = kTeamThreads / team;  // teams of a workgroup
         const int64_t most = (rows * groups + per - 1) / per, least = (groups + per - 1) / per;

@@ -10,58 +10,65 @@ typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 // unaligned addresses), so odd widths and shifted tensors run on the same path.
 typedef u32x4_t u32x4_a2 __attribute__((aligned(2)));
 
-// Eight consecutive elements as they lie in memory: 16 bytes of bf16, 32 of fp32.
-template <typename IO>
-struct Raw8 {
-    static constexpr int Q = IO::bytes / 2;
-    u32x4_t q[Q];
+// E consecutive elements as they lie in memory, in pieces of 16 bytes (8 where they are no more).
+template <typename IO, int E>
+struct Raw {
+    static constexpr int WORDS = E * IO::bytes / 4, N = WORDS < 4 ? WORDS : 4, Q = WORDS / N;
+    typedef uint32_t piece_t __attribute__((ext_vector_type(N)));
+    typedef piece_t piece_a2 __attribute__((aligned(2)));
+    piece_t q[Q];
     __device__ __forceinline__ float operator[](int e) const {
-        if constexpr (IO::bytes == 2) return __uint_as_float(e & 1 ? q[0][e / 2] & 0xffff0000u : q[0][e / 2] << 16);
-        return __uint_as_float(q[e / 4][e % 4]);
+        if constexpr (IO::bytes == 2) {
+            const uint32_t w = q[e / 2 / N][e / 2 % N];
+            return __uint_as_float(e & 1 ? w & 0xffff0000u : w << 16);
+        }
+        return __uint_as_float(q[e / N][e % N]);
     }
 };
 
-// Elements i .. i + 7 of p, of which the first n are there (the others read as 0).
-template <typename IO>
-__device__ __forceinline__ Raw8<IO> load8(const void *p, int64_t i, int n) {
+// Elements i .. i + E - 1 of p, of which the first n are there (the others read as 0).
+template <typename IO, int E>
+__device__ __forceinline__ Raw<IO, E> load_raw(const void *p, int64_t i, int n) {
+    using RAW = Raw<IO, E>;
+    constexpr int N = RAW::N;
     const char *at = static_cast<const char *>(p) + i * IO::bytes;
-    Raw8<IO> r;
-    if (n >= 8) {
+    RAW r = {};
+    if (n >= E) {
 #pragma unroll
-        for (int k = 0; k < Raw8<IO>::Q; ++k) r.q[k] = reinterpret_cast<const u32x4_a2 *>(at)[k];
+        for (int k = 0; k < RAW::Q; ++k) r.q[k] = reinterpret_cast<const typename RAW::piece_a2 *>(at)[k];
         return r;
     }
 #pragma unroll
-    for (int k = 0; k < Raw8<IO>::Q; ++k) r.q[k] = u32x4_t{0, 0, 0, 0};
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
+    for (int e = 0; e < E; ++e)
         if (e < n) {
             if constexpr (IO::bytes == 2)
-                r.q[0][e / 2] |= (uint32_t)reinterpret_cast<const uint16_t *>(at)[e] << (16 * (e & 1));
+                r.q[e / 2 / N][e / 2 % N] |= (uint32_t)reinterpret_cast<const uint16_t *>(at)[e] << (16 * (e & 1));
             else
-                r.q[e / 4][e % 4] = reinterpret_cast<const uint32_t *>(at)[e];
+                r.q[e / N][e % N] = reinterpret_cast<const uint32_t *>(at)[e];
         }
     return r;
 }
 
-template <typename IO>
-__device__ __forceinline__ void store8(void *p, int64_t i, int n, const float (&f)[8]) {
+template <typename IO, int E>
+__device__ __forceinline__ void store_raw(void *p, int64_t i, int n, const float (&f)[E]) {
+    using RAW = Raw<IO, E>;
+    constexpr int N = RAW::N;
     char *at = static_cast<char *>(p) + i * IO::bytes;
-    if (n >= 8) {
-        if constexpr (IO::bytes == 2) {
-            *reinterpret_cast<u32x4_a2 *>(at) = u32x4_t{pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
-                                                        pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7])};
-        } else {
+    if (n >= E) {
+        RAW r;
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
-                reinterpret_cast<u32x4_a2 *>(at)[k] =
-                    u32x4_t{__float_as_uint(f[4 * k]), __float_as_uint(f[4 * k + 1]), __float_as_uint(f[4 * k + 2]),
-                            __float_as_uint(f[4 * k + 3])};
+        for (int w = 0; w < RAW::WORDS; ++w) {
+            if constexpr (IO::bytes == 2)
+                r.q[w / N][w % N] = pack_bf16x2(f[2 * w], f[2 * w + 1]);
+            else
+                r.q[w / N][w % N] = __float_as_uint(f[w]);
         }
+#pragma unroll
+        for (int k = 0; k < RAW::Q; ++k) reinterpret_cast<typename RAW::piece_a2 *>(at)[k] = r.q[k];
         return;
     }
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
+    for (int e = 0; e < E; ++e)
         if (e < n) store_io<IO>(at, e, f[e]);
 }
 

@@ -57,6 +57,14 @@ def _gdraw(rows, D, io, seed):
     return [t.to(DEV) for t in (n(rows, D).to(io), n(rows, D).to(io), 1 + 0.1 * n(D), n(rows, D).to(io))]
 
 
+@pytest.mark.parametrize("io,res", TYPES, ids=["f32_f32", "bf16_bf16", "bf16_f32", "f32_bf16"])
+@pytest.mark.parametrize("rows,D", [(1500, 1026), (1100, 2048), (530, 2051), (3, 2999), (300, 4099)])
+def test_add_rmsnorm_rows_of_a_workgroup(rows, D, io, res):
+    """Widths on both sides of where a workgroup takes another form, with more rows than
+    workgroups."""
+    test_add_rmsnorm(rows, D, io, res)
+
+
 @pytest.mark.parametrize("io", [F32, BF], ids=["f32", "bf16"])
 @pytest.mark.parametrize("gate_first", [True, False], ids=["gate_first", "norm_first"])
 @pytest.mark.parametrize("rows,D,groups", [(1, 1, 1), (3, 6, 3), (1, 1536, 1), (5, 768, 8), (300, 128, 2), (7, 515, 5),
@@ -75,6 +83,13 @@ def test_gated_rmsnorm(rows, D, groups, gate_first, io):
     ref = R.gated_rmsnorm_bwd(*a, f64(dy), groups, gate_first)
     for n, v in ref.items():
         check(got[n], v, b[n], "%s %s" % (what, n))
+
+
+@pytest.mark.parametrize("io", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("rows,D,groups", [(1500, 1026, 1), (600, 4098, 2), (530, 2051, 1), (300, 4099, 1), (9, 64, 64)])
+def test_gated_rmsnorm_rows_of_a_workgroup(rows, D, groups, io):
+    """As above; and groups of a single channel."""
+    test_gated_rmsnorm(rows, D, groups, True, io)
 
 
 @pytest.mark.parametrize("io", [F32, BF], ids=["f32", "bf16"])
