@@ -967,15 +967,22 @@ def gated_scan_fwd(x: torch.Tensor, gate: torch.Tensor, mode: str = "rate",
     f32 = torch.float32
     a = GatedScanArgs(batch=B, seqlen=L, dim=D)
     _gates(a, x, gate, mode, A, in_gate, gate_bias, in_bias, dev)
-    a.reset = _resets(reset, (B, L), dev)
-    a.h0 = _arg(h0, "h0", (B, D), f32, dev)
+    if reset is not None:
+        a.reset = _resets(reset, (B, L), dev)
+    if h0 is not None:
+        a.h0 = _arg(h0, "h0", (B, D), f32, dev)
     if y is None:
         y = torch.empty_like(x)
-    a.y = _need(y, "y", (B, L, D), x.dtype, dev)
-    if h_final is None and return_final_state:
+        a.y = y.data_ptr()
+    else:
+        a.y = _need(y, "y", (B, L, D), x.dtype, dev)
+    if h_final is not None:
+        a.h_final = _arg(h_final, "h_final", (B, D), f32, dev)
+    elif return_final_state:
         h_final = torch.empty((B, D), device=dev, dtype=f32)
-    a.h_final = _arg(h_final, "h_final", (B, D), f32, dev)
-    a.checkpoints = _arg(checkpoints, "checkpoints", gated_checkpoint_shape(B, L, D), f32, dev)
+        a.h_final = h_final.data_ptr()
+    if checkpoints is not None:
+        a.checkpoints = _arg(checkpoints, "checkpoints", gated_checkpoint_shape(B, L, D), f32, dev)
     _run("ssm_gated_scan_fwd", a, dev, "ssm_gated_scan_workspace_size", workspace)
     return y, h_final
 
@@ -994,23 +1001,28 @@ def gated_scan_bwd(x: torch.Tensor, gate: torch.Tensor, dy: torch.Tensor, mode: 
     dgate_bias, din_bias, dh0 (float32)."""
     dev = _gpu(x, "x", 3, "(B, L, D)")
     B, L, D = x.shape
-    f32 = dict(device=dev, dtype=torch.float32)
+    f32 = torch.float32
     a = GatedScanBwdArgs(batch=B, seqlen=L, dim=D)
     _gates(a, x, gate, mode, A, in_gate, gate_bias, in_bias, dev)
-    a.reset = _resets(reset, (B, L), dev)
-    a.h0 = _arg(h0, "h0", (B, D), torch.float32, dev)
     a.dy = _need(dy, "dy", (B, L, D), x.dtype, dev)
-    a.dh_final = _arg(dh_final, "dh_final", (B, D), torch.float32, dev)
-    a.checkpoints = _arg(checkpoints, "checkpoints", gated_checkpoint_shape(B, L, D), torch.float32, dev)
     out = dict(dx=torch.empty_like(x), dgate=torch.empty_like(x))
     if in_gate is not None:
         out["din_gate"] = torch.empty_like(x)
-    for name, given in (("dA", mode == "rate"), ("dgate_bias", gate_bias is not None),
-                        ("din_bias", in_bias is not None)):
-        if given:
-            out[name] = torch.empty(D, **f32)
+    if mode == "rate":
+        out["dA"] = torch.empty(D, device=dev, dtype=f32) if A is None else torch.empty_like(A)
+    if gate_bias is not None:
+        out["dgate_bias"] = torch.empty_like(gate_bias)
+    if in_bias is not None:
+        out["din_bias"] = torch.empty_like(in_bias)
+    if reset is not None:
+        a.reset = _resets(reset, (B, L), dev)
     if h0 is not None:
-        out["dh0"] = torch.empty(B, D, **f32)
+        a.h0 = _arg(h0, "h0", (B, D), f32, dev)
+        out["dh0"] = torch.empty_like(h0)
+    if dh_final is not None:
+        a.dh_final = _arg(dh_final, "dh_final", (B, D), f32, dev)
+    if checkpoints is not None:
+        a.checkpoints = _arg(checkpoints, "checkpoints", gated_checkpoint_shape(B, L, D), f32, dev)
     for name, t in out.items():
         setattr(a, name, t.data_ptr())
     _run("ssm_gated_scan_bwd", a, dev, "ssm_gated_scan_bwd_workspace_size", workspace)
@@ -1091,36 +1103,22 @@ def gated_scan(x: torch.Tensor, gate: torch.Tensor, mode: str = "rate", A: Optio
 
 
 # ----------------------------------------------------------------------------- fused norms
-def _add_norm(a, x, w, residual, scale, post_w, eps, dev):
-    R, D = x.shape
-    f32 = torch.float32
-    a.rows, a.dim, a.eps = R, D, float(eps)
-    a.io_dtype = _io_code(x.dtype)
-    res_dtype = x.dtype
+def _add_norm(a, x, w, residual, scale, post_w, eps, shape, dev):
+    D, io, f32 = shape[-1], x.dtype, torch.float32
+    a.rows, a.dim, a.eps = x.numel() // D, D, float(eps)
+    a.io_dtype = a.res_dtype = _io_code(io)
+    a.x = _need(x, "x", shape, io, dev)
+    a.w = _need(w, "w", (D,), f32, dev)
     if residual is not None:
         if not isinstance(residual, torch.Tensor):
             raise TypeError("residual must be a torch.Tensor")
-        res_dtype = residual.dtype
-    a.res_dtype = _io_code(res_dtype)
-    a.x = _need(x, "x", (R, D), x.dtype, dev)
-    a.w = _need(w, "w", (D,), f32, dev)
-    a.residual = _arg(residual, "residual", (R, D), res_dtype, dev)
-    a.scale = _arg(scale, "scale", (D,), f32, dev)
-    a.post_w = _arg(post_w, "post_w", (D,), f32, dev)
-    return res_dtype
-
-
-def _rows_of(t, shape, name):
-    """A (..., D) tensor as (rows, D): a view, so it has to be contiguous."""
-    if t is None:
-        return None
-    if not isinstance(t, torch.Tensor):
-        raise TypeError("%s must be a torch.Tensor" % name)
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
-    if not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % name)
-    return t if t.dim() == 2 else t.view(-1, shape[-1]) if t.numel() else t.new_empty((0, shape[-1]))
+        if residual.dtype is not io:
+            a.res_dtype = _io_code(residual.dtype)
+        a.residual = _arg(residual, "residual", shape, residual.dtype, dev)
+    if scale is not None:
+        a.scale = _arg(scale, "scale", (D,), f32, dev)
+    if post_w is not None:
+        a.post_w = _arg(post_w, "post_w", (D,), f32, dev)
 
 
 def _shape_of(x):
@@ -1140,14 +1138,18 @@ def add_rmsnorm_fwd(x: torch.Tensor, w: torch.Tensor, residual: Optional[torch.T
     shape = _shape_of(x)
     dev = x.device
     a = AddNormArgs()
-    res_dtype = _add_norm(a, _rows_of(x, shape, "x"), w, _rows_of(residual, shape, "residual"), scale, post_w,
-                          eps, dev)
+    _add_norm(a, x, w, residual, scale, post_w, eps, shape, dev)
+    stream = x if residual is None else residual
     if y is None:
         y = torch.empty_like(x)
+        a.y = y.data_ptr()
+    else:
+        a.y = _need(y, "y", shape, x.dtype, dev)
     if res_out is None:
-        res_out = torch.empty(shape, device=dev, dtype=res_dtype)
-    a.y = _need(y, "y", shape, x.dtype, dev)
-    a.res_out = _need(res_out, "res_out", shape, res_dtype, dev)
+        res_out = torch.empty_like(stream)
+        a.res_out = res_out.data_ptr()
+    else:
+        a.res_out = _need(res_out, "res_out", shape, stream.dtype, dev)
     _run("ssm_add_rmsnorm_fwd", a, dev)
     return y, res_out
 
@@ -1164,10 +1166,10 @@ def add_rmsnorm_bwd(x: torch.Tensor, w: torch.Tensor, residual: Optional[torch.T
     shape = _shape_of(x)
     dev = x.device
     a = AddNormBwdArgs()
-    res_dtype = _add_norm(a, _rows_of(x, shape, "x"), w, _rows_of(residual, shape, "residual"), scale, post_w,
-                          eps, dev)
+    _add_norm(a, x, w, residual, scale, post_w, eps, shape, dev)
     a.dy = _need(dy, "dy", shape, x.dtype, dev)
-    a.dres_out = _arg(dres_out, "dres_out", shape, res_dtype, dev)
+    if dres_out is not None:
+        a.dres_out = _arg(dres_out, "dres_out", shape, x.dtype if residual is None else residual.dtype, dev)
     out = dict(dx=torch.empty_like(x), dw=torch.empty_like(w))
     if residual is not None:
         out["dresidual"] = torch.empty_like(residual)
@@ -1229,7 +1231,9 @@ def gated_rmsnorm_fwd(x: torch.Tensor, z: torch.Tensor, w: torch.Tensor, groups:
     _gated_norm(a, x, z, w, groups, gate_first, eps, shape, dev)
     if y is None:
         y = torch.empty_like(x)
-    a.y = _need(y, "y", shape, x.dtype, dev)
+        a.y = y.data_ptr()
+    else:
+        a.y = _need(y, "y", shape, x.dtype, dev)
     _run("ssm_gated_rmsnorm_fwd", a, dev)
     return y
 
