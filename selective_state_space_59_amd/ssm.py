@@ -1206,7 +1206,7 @@ def add_rmsnorm(x: torch.Tensor, w: torch.Tensor, residual: Optional[torch.Tenso
                 scale: Optional[torch.Tensor] = None, post_w: Optional[torch.Tensor] = None,
                 eps: float = 1e-5):
     """The fused residual sum and norm as a differentiable torch op (arguments as in
-    add_rmsnorm_fwd): returns (y, res_out)."""
+    add_rmsnorm_fwd): returns (y, res_out).  A captured backward(): as with gated_scan."""
     return _AddNormFn.apply(x, w, residual, scale, post_w, eps)
 
 
@@ -1274,5 +1274,6 @@ class _GatedNormFn(torch.autograd.Function):
 
 def gated_rmsnorm(x: torch.Tensor, z: torch.Tensor, w: torch.Tensor, groups: int = 1, gate_first: bool = True,
                   eps: float = 1e-5) -> torch.Tensor:
-    """The gated norm as a differentiable torch op (arguments as in gated_rmsnorm_fwd)."""
+    """The gated norm as a differentiable torch op (arguments as in gated_rmsnorm_fwd).  A captured
+    backward(): as with gated_scan."""
     return _GatedNormFn.apply(x, z, w, groups, gate_first, eps)
