@@ -2,8 +2,8 @@
 // decode step, on gfx950 (gated_device.h has the gates, gated_tile.h the hand-over of states).
 //
 // One pass over HBM: x, gate and in_gate are read once, y is written once.  The sequence is cut
-// into tiles of 256 steps by 128 bytes of channels, one workgroup each, so that a layer with few
-// channels still fills the chip.  In a tile a lane owns R consecutive steps of 16 bytes of channels:
+// into tiles of 256 steps (fewer where it is shorter) by 128 bytes of channels, one workgroup each, so
+// that a layer with few channels still fills the chip.  In a tile a lane owns R consecutive steps of 16 bytes of channels:
 // all its loads are issued at once, whole 128-byte lines per 8 lanes, and its steps run in registers
 // from a zero state, with the state l and the product p of the decays.  The lane groups' (p, l) meet
 // in LDS, where all waves combine them in runs and a thread per channel fetches the state that enters
@@ -27,19 +27,22 @@ namespace {
 // bf16 SIGMOID with resets: 130 us, against 142 with p and l kept and 135 with 4 rows).
 template <int MODE>
 constexpr bool kKeep = MODE == SSM_GATE_RATE;
-template <typename IO, int MODE>
-using FwdTile = Tile<IO, 4, kKeep<MODE> ? 4 : 8, kKeep<MODE> ? 512 : 256>;
+// (Short sequences take 4 rows in every mode.)
 constexpr int kFwdSteps = 256;
+template <int MODE, int STEPS>
+constexpr int kFwdRows = kKeep<MODE> || STEPS < kFwdSteps ? 4 : 8;
+template <typename IO, int MODE, int STEPS = kFwdSteps>
+using FwdTile = Tile<IO, 4, kFwdRows<MODE, STEPS>, STEPS / kFwdRows<MODE, STEPS> * 8>;
 template <int MODE>
 constexpr bool kTileOk = FwdTile<io_bf16, MODE>::T == kFwdSteps && FwdTile<io_f32, MODE>::T == kFwdSteps &&
                          SSM_GATED_BLOCK % FwdTile<io_bf16, MODE>::R == 0;
 static_assert(kTileOk<SSM_GATE_DECAY> && kTileOk<SSM_GATE_SIGMOID> && kTileOk<SSM_GATE_RATE>, "tile sizes");
 static_assert(kFwdSteps <= SSM_GATED_TILE, "the longest product of decays");
 
-template <typename IO, int MODE, bool IG, int EDGE>
-__global__ __launch_bounds__((FwdTile<IO, MODE>::THREADS)) void gated_scan_kernel(ssm_gated_scan_args_t a, int chains,
-                                                                         int tiles, u64_t *rec, unsigned *tickets) {
-    using TL = FwdTile<IO, MODE>;
+template <typename IO, int MODE, bool IG, int EDGE, int STEPS>
+__global__ __launch_bounds__((FwdTile<IO, MODE, STEPS>::THREADS)) void gated_scan_kernel(
+    ssm_gated_scan_args_t a, int chains, int tiles, u64_t *rec, unsigned *tickets) {
+    using TL = FwdTile<IO, MODE, STEPS>;
     constexpr int V = TL::V, CB = TL::CB, G = TL::G, T = TL::T, R = TL::R, W = TL::W;
     constexpr int NP = TL::THREADS / CB, GP = G / NP;  // runs of GP lane groups
     __shared__ __attribute__((aligned(16))) float sp[G][CB], sl[G][CB], pp[NP][CB], pl[NP][CB], sc[3][CB];
@@ -272,12 +275,15 @@ hipError_t launch_gated_scan_fwd(const ssm_gated_scan_args_t &a, hipStream_t str
     }
     const unsigned grid = (unsigned)(p.chains * p.tiles);
     gate_dispatch(a.io_dtype, a.mode, a.in_gate != nullptr, [&](auto io, auto mode, auto ig) {
-        using TL = FwdTile<decltype(io), decltype(mode)::value>;
-        auto go = [&](auto edge) {
-            gated_scan_kernel<decltype(io), decltype(mode)::value, decltype(ig)::value, decltype(edge)::value>
-                <<<grid, TL::THREADS, 0, stream>>>(a, (int)p.chains, (int)p.tiles, rec, tickets);
-        };
-        with_edge(edge_of(a.dim, TL::V), go);
+        using IO = decltype(io);
+        constexpr int MODE = decltype(mode)::value;
+        with_steps<kFwdSteps>(a.seqlen, [&](auto steps) {
+            using TL = FwdTile<IO, MODE, decltype(steps)::value>;
+            with_edge(edge_of(a.dim, TL::V), [&](auto edge) {
+                gated_scan_kernel<IO, MODE, decltype(ig)::value, decltype(edge)::value, TL::T>
+                    <<<grid, TL::THREADS, 0, stream>>>(a, (int)p.chains, (int)p.tiles, rec, tickets);
+            });
+        });
     });
     return hipGetLastError();
 }

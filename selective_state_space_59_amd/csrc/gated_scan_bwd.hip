@@ -6,11 +6,11 @@
 //   da_t = lambda_t h_{t-1},  db_t = lambda_t,  and the chain rule of gated_device.h.
 //
 // One pass over HBM: x, gate, in_gate and dy are read once, dx, dgate and din_gate written once.  The
-// tiles are the forward's (gated_tile.h), one checkpoint long, and chained from the last to the
-// first.  A tile recomputes its states from its checkpoint in fp32, so neither y nor any state is
-// read, and both directions share the product p of a lane's decays.  The rows stay in registers
-// as they were read; a channel at a time is widened, its gates formed (once for the lane's run,
-// once for its gradients: arithmetic is cheaper here than registers), and its gradients packed
+// tiles are the forward's (gated_tile.h), one checkpoint long or a whole shorter sequence, and chained
+// from the last to the first.  A tile recomputes its states from its checkpoint in fp32, so neither y
+// nor any state is read, and both directions share the product p of a lane's decays.  The rows stay in
+// registers as they were read; a channel at a time is widened, its gates formed (once for the lane's
+// run, once for its gradients: arithmetic is cheaper here than registers), and its gradients packed
 // into the place of its inputs.
 //
 // Measured in bf16: 8 x 2048 x 1536 RATE with in_gate 91 us, 3.9 TB/s, bound by the issue of its 94
@@ -22,10 +22,11 @@
 namespace ssm {
 namespace {
 
-template <typename IO>
-using BwdTile = Tile<IO, 4, 4, 256>;
-constexpr int T = BwdTile<io_bf16>::T;
-static_assert(T % SSM_GATED_BLOCK == 0 && BwdTile<io_f32>::T == T, "a tile begins at a checkpoint");
+constexpr int kBwdSteps = 128;
+template <typename IO, int STEPS = kBwdSteps>
+using BwdTile = Tile<IO, 4, 4, STEPS * 2>;
+static_assert(BwdTile<io_bf16>::T == kBwdSteps && BwdTile<io_f32>::T == kBwdSteps, "tile sizes");
+static_assert(kBwdSteps % SSM_GATED_BLOCK == 0, "a tile begins at a checkpoint");
 
 template <bool IG>
 __device__ __forceinline__ void pin_row(uint32_t &x, uint32_t &g, uint32_t &i, uint32_t &d) {
@@ -33,12 +34,11 @@ __device__ __forceinline__ void pin_row(uint32_t &x, uint32_t &g, uint32_t &i, u
     if constexpr (IG) asm volatile("" : "+v"(i));
 }
 
-template <typename IO, int MODE, bool IG, bool SPECIAL, int EDGE>
-__global__ __launch_bounds__(BwdTile<IO>::THREADS, 4) void gated_bwd_kernel(ssm_gated_scan_bwd_args_t a, const float *ck,
-                                                                  float *part, int chains, int tiles, u64_t *rec,
-                                                                  unsigned *tickets) {
-    using TL = BwdTile<IO>;
-    constexpr int V = TL::V, CB = TL::CB, G = TL::G, R = TL::R, W = TL::W;
+template <typename IO, int MODE, bool IG, bool SPECIAL, int EDGE, int STEPS>
+__global__ __launch_bounds__((BwdTile<IO, STEPS>::THREADS), 4) void gated_bwd_kernel(
+    ssm_gated_scan_bwd_args_t a, const float *ck, float *part, int chains, int tiles, u64_t *rec, unsigned *tickets) {
+    using TL = BwdTile<IO, STEPS>;
+    constexpr int V = TL::V, CB = TL::CB, G = TL::G, R = TL::R, W = TL::W, T = TL::T;
     constexpr int PER = V / W;  // channels of a word
     // the groups' decay products, forward runs and backward runs; later their entering states
     // and the partial sums
@@ -279,14 +279,14 @@ __global__ __launch_bounds__(BwdTile<IO>::THREADS, 4) void gated_bwd_kernel(ssm_
     if constexpr (MODE != SSM_GATE_DECAY) {
         // this tile's row of the partial sums: gate_bias, then A, then in_bias
         __syncthreads();
-        const int which = tid / CB, ch = tid % CB, d = cblk * CB + ch;
         constexpr int K = MODE == SSM_GATE_SIGMOID ? 1 : IG ? 3 : 2;
-        static_assert(K * CB <= TL::THREADS, "a thread per sum");
-        if (which < K && d < D) {
+        for (int i = tid; i < K * CB; i += TL::THREADS) {
+            const int which = i / CB, ch = i % CB, d = cblk * CB + ch;
+            if (d >= D) continue;
             const float(*s)[CB] = which == 0 ? sp : which == 1 ? sl : sm;
             float v = 0.0f;
 #pragma unroll 8
-            for (int i = 0; i < G; ++i) v += s[i][ch];
+            for (int j = 0; j < G; ++j) v += s[j][ch];
             part[((int64_t)which * a.batch * tiles + b * tiles + tile) * D + d] = v;
         }
     }
@@ -321,7 +321,7 @@ ssm_gated_scan_args_t forward_of(const ssm_gated_scan_bwd_args_t &a) {
 // The workspace is sized without looking at which gradients are asked for.
 BwdPlan plan_of(const ssm_gated_scan_bwd_args_t &a) {
     const int64_t cb = a.io_dtype == SSM_BF16 ? BwdTile<io_bf16>::CB : BwdTile<io_f32>::CB;
-    const int64_t tiles = (a.seqlen + T - 1) / T;
+    const int64_t tiles = (a.seqlen + kBwdSteps - 1) / kBwdSteps;
     BwdPlan p;
     p.chain = ChainPlan{a.batch * ((a.dim + cb - 1) / cb), tiles, cb};
     p.rows = a.batch * tiles;
@@ -365,20 +365,22 @@ hipError_t launch_gated_scan_bwd(const ssm_gated_scan_bwd_args_t &a, hipStream_t
     unsigned *tickets = reinterpret_cast<unsigned *>(ws + p.chain.rec_bytes());
     const unsigned grid = (unsigned)(p.chain.chains * p.chain.tiles);
     gate_dispatch(a.io_dtype, a.mode, a.in_gate != nullptr, [&](auto io, auto mode, auto ig) {
-        using TL = BwdTile<decltype(io)>;
-        auto go = [&](auto special, auto edge) {
+        auto go = [&](auto special, auto edge, auto steps) {
+            using TL = BwdTile<decltype(io), decltype(steps)::value>;
             gated_bwd_kernel<decltype(io), decltype(mode)::value, decltype(ig)::value, decltype(special)::value,
-                             decltype(edge)::value>
+                             decltype(edge)::value, TL::T>
                 <<<grid, TL::THREADS, 0, stream>>>(a, ck, part, (int)p.chain.chains, (int)p.chain.tiles,
                                                    reinterpret_cast<u64_t *>(ws), tickets);
         };
         // the selects for resets and for a cut-off last tile: left out where neither is there and
         // the width is whole
-        const Edge edge = edge_of(a.dim, TL::V);
-        if (edge == kWhole && !a.reset && a.seqlen % T == 0)
-            go(std::false_type{}, std::integral_constant<int, kWhole>{});
+        const Edge edge = edge_of(a.dim, BwdTile<decltype(io)>::V);
+        if (edge == kWhole && !a.reset && a.seqlen % kBwdSteps == 0)
+            go(std::false_type{}, std::integral_constant<int, kWhole>{}, std::integral_constant<int, kBwdSteps>{});
         else
-            with_edge(edge, [&](auto e) { go(std::true_type{}, e); });
+            with_edge(edge, [&](auto e) {
+                with_steps<kBwdSteps>(a.seqlen, [&](auto steps) { go(std::true_type{}, e, steps); });
+            });
     });
     e = hipGetLastError();
     float *out[3] = {a.dgate_bias, a.dA, a.din_bias};

@@ -65,6 +65,16 @@ def test_forward_and_backward(mode, B, L, D, dtype):
         assert torch.equal(got[name], own[name]), name  # the same states, recomputed
 
 
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("mode", MODES)
+@pytest.mark.parametrize("B,L,D", [(300, 4, 40), (5, 32, 72), (3, 33, 130), (2, 64, 67), (2, 65, 8)])
+def test_short_sequences(mode, B, L, D, dtype):
+    """Lengths on both sides of where a sequence takes a larger tile, with and without resets."""
+    for doc in (0, 7):
+        k = scan_case(mode, B, L, D, dtype, seed=L + doc, doc=doc)
+        _check_bwd(k, "doc %d" % doc, _check_fwd(k, "doc %d" % doc))
+
+
 @pytest.mark.parametrize("mode", MODES)
 def test_without_resets_state_or_final_gradient(mode):
     k = scan_case(mode, 2, 600, 40, F32, seed=3, h0=False, bias=False, in_gate=False)
