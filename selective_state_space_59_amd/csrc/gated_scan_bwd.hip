@@ -13,7 +13,7 @@
 // run, once for its gradients: arithmetic is cheaper here than registers), and its gradients packed
 // into the place of its inputs.
 //
-// Measured in bf16: 8 x 2048 x 1536 RATE with in_gate 91 us, 3.9 TB/s, bound by the issue of its 94
+// Measured in bf16: 8 x 2048 x 1536 RATE with in_gate 90 us, 3.9 TB/s, bound by the issue of its 94
 // vector instructions an element (13 of them exponentials, reciprocals and roots); 4 x 4096 x 5120
 // SIGMOID with resets 180 us, 4.7 TB/s, where the waves wait for the tile's phases.
 #include "gated_tile.h"
