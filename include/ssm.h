@@ -517,10 +517,12 @@ ssm_status_t ssm_ssd_step(const ssm_ssd_step_args_t *args, void *stream);
  * behind the other in a row come out as in calls of their own, and a row
  * padded on the left resets at its first token.
  *
- * In SSM_GATE_DECAY the decays are meant to lie in [-1, 1].  Others are
- * computed too, but the products of up to SSM_GATED_TILE decays formed inside
- * must stay below 2^127: growth beyond it gives an infinity or a NaN also
- * where the states themselves stay finite.
+ * The decays are meant to lie in [-1, 1]: in SSM_GATE_DECAY as they are given, in
+ * SSM_GATE_RATE by A <= 0.  Others are computed too, but the products of up to
+ * SSM_GATED_TILE decays formed inside (in the backward too) must stay below 2^127:
+ * growth beyond it gives an infinity or a NaN also where the states themselves
+ * stay finite.  In SSM_GATE_RATE a state of 0 stays 0 all the same, and its
+ * gradients, as long as each decay and each lambda is finite.
  *
  * Arithmetic is fp32 (the hardware's exponential, reciprocal and square root,
  * 1 ulp); y is rounded once.  Results do not change from run to run.

@@ -124,7 +124,7 @@ __global__ __launch_bounds__((FwdTile<IO, MODE, STEPS>::THREADS)) void gated_sca
 #pragma unroll
     for (int i = 0; i < GP; ++i) {
         const float gp = sp[part * GP + i][ch];
-        tl = run_apply(gp, sl[part * GP + i][ch], tl);
+        tl = run_apply<MODE>(gp, sl[part * GP + i][ch], tl);
         tp *= gp;
     }
     pp[part][ch] = tp;
@@ -135,16 +135,16 @@ __global__ __launch_bounds__((FwdTile<IO, MODE, STEPS>::THREADS)) void gated_sca
         tl = 0.0f;
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
-            tl = run_apply(pp[i][ch], pl[i][ch], tl);
+            tl = run_apply<MODE>(pp[i][ch], pl[i][ch], tl);
             tp *= pp[i][ch];
         }
         float h = tile == 0 && a.h0 && d < D ? a.h0[b * D + d] : 0.0f;
         u64_t *mine = rec + ((int64_t)chain * tiles + tile) * CB + ch;
         if (tile > 0) {
             if (tile + 1 < tiles) rec_put(mine, rec_hi(tp), tl);
-            h = chain_enter(mine, CB, tile);
+            h = chain_enter<MODE>(mine, CB, tile);
         }
-        const float after = run_apply(tp, tl, h);
+        const float after = run_apply<MODE>(tp, tl, h);
         if (tile + 1 < tiles)
             rec_put(mine, kRecState, after);
         else if (a.h_final && d < D)
@@ -153,7 +153,7 @@ __global__ __launch_bounds__((FwdTile<IO, MODE, STEPS>::THREADS)) void gated_sca
         for (int i = 0; i < NP; ++i) {
             const float q = pp[i][ch];
             pp[i][ch] = h;
-            h = run_apply(q, pl[i][ch], h);
+            h = run_apply<MODE>(q, pl[i][ch], h);
         }
     }
     __syncthreads();
@@ -165,13 +165,25 @@ __global__ __launch_bounds__((FwdTile<IO, MODE, STEPS>::THREADS)) void gated_sca
             a.checkpoints[((t0 + step) / SSM_GATED_BLOCK * a.batch + b) * D + d] = h;
         const float gp = sp[part * GP + i][ch];
         sp[part * GP + i][ch] = h;
-        h = run_apply(gp, sl[part * GP + i][ch], h);
+        h = run_apply<MODE>(gp, sl[part * GP + i][ch], h);
     }
     __syncthreads();
     if (!a.y) return;
     float e[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) e[v] = sp[g][lc + v];
+    if constexpr (KEEP) {
+        // run_apply's second case, ahead of the rows: a lane needs it only where the product of its decays
+        // is an infinity, and a product of decays above 1 grows from row to row
+        float top = p[R - 1][0];
+#pragma unroll
+        for (int v = 1; v < V; ++v) top = fmaxf(top, p[R - 1][v]);
+        if (__any(top > __FLT_MAX__))
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+#pragma unroll
+                for (int j = 0; j < R; ++j) p[j][v] = e[v] == 0.0f && p[j][v] == p[j][v] ? 0.0f : p[j][v];
+    }
     char *out = static_cast<char *>(a.y) + row0 + col.shift * IO::bytes;
     if constexpr (!KEEP)  // (or the gates of above would be kept after all)
 #pragma unroll
@@ -184,7 +196,7 @@ __global__ __launch_bounds__((FwdTile<IO, MODE, STEPS>::THREADS)) void gated_sca
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             if constexpr (KEEP) {
-                f[v] = a.reset ? run_apply(p[j][v], l[j][v], e[v]) : __builtin_fmaf(p[j][v], e[v], l[j][v]);
+                f[v] = a.reset ? run_apply<MODE>(p[j][v], l[j][v], e[v]) : __builtin_fmaf(p[j][v], e[v], l[j][v]);
             } else {
                 float at, bt;
                 step(j, v, at, bt);

@@ -134,8 +134,8 @@ __global__ __launch_bounds__((BwdTile<IO, STEPS>::THREADS), 4) void gated_bwd_ke
 #pragma unroll
         for (int i = 0; i < GP; ++i) {
             const int f = pt * GP + i, r = pt * GP + GP - 1 - i;
-            tl = run_apply(sp[f][ch], sl[f][ch], tl);
-            tm = run_apply(sp[r][ch], sm[r][ch], tm);
+            tl = run_apply<MODE>(sp[f][ch], sl[f][ch], tl);
+            tm = run_apply<MODE>(sp[r][ch], sm[r][ch], tm);
             tp *= sp[f][ch];
         }
         pp[pt][ch] = tp;
@@ -147,15 +147,15 @@ __global__ __launch_bounds__((BwdTile<IO, STEPS>::THREADS), 4) void gated_bwd_ke
             tm = 0.0f;
 #pragma unroll
             for (int i = NP - 1; i >= 0; --i) {
-                tm = run_apply(pp[i][ch], pm[i][ch], tm);
+                tm = run_apply<MODE>(pp[i][ch], pm[i][ch], tm);
                 tp *= pp[i][ch];
             }
             u64_t *mine = rec + ((int64_t)chain * tiles + k) * CB + ch;
             if (k > 0 && k + 1 < tiles) rec_put(mine, rec_hi(tp), tm);
             float h = d < D ? ck[(t0 / SSM_GATED_BLOCK * a.batch + b) * D + d] : 0.0f;
             float mu = k == 0 && a.dh_final && d < D ? a.dh_final[b * D + d] : 0.0f;
-            if (k > 0) mu = chain_enter(mine, CB, k);
-            const float after = run_apply(tp, tm, mu);
+            if (k > 0) mu = chain_enter<MODE>(mine, CB, k);
+            const float after = run_apply<MODE>(tp, tm, mu);
             if (k + 1 < tiles)
                 rec_put(mine, kRecState, after);
             else if (a.dh0 && d < D)
@@ -164,13 +164,13 @@ __global__ __launch_bounds__((BwdTile<IO, STEPS>::THREADS), 4) void gated_bwd_ke
             for (int i = 0; i < NP; ++i) {
                 const float l = pl[i][ch];
                 pl[i][ch] = h;
-                h = run_apply(pp[i][ch], l, h);
+                h = run_apply<MODE>(pp[i][ch], l, h);
             }
 #pragma unroll
             for (int i = NP - 1; i >= 0; --i) {
                 const float m = pm[i][ch];
                 pm[i][ch] = mu;
-                mu = run_apply(pp[i][ch], m, mu);
+                mu = run_apply<MODE>(pp[i][ch], m, mu);
             }
         }
         __syncthreads();
@@ -179,13 +179,13 @@ __global__ __launch_bounds__((BwdTile<IO, STEPS>::THREADS), 4) void gated_bwd_ke
         for (int i = 0; i < GP; ++i) {
             const float l = sl[pt * GP + i][ch];
             sl[pt * GP + i][ch] = h;
-            h = run_apply(sp[pt * GP + i][ch], l, h);
+            h = run_apply<MODE>(sp[pt * GP + i][ch], l, h);
         }
 #pragma unroll
         for (int i = GP - 1; i >= 0; --i) {
             const float m = sm[pt * GP + i][ch];
             sm[pt * GP + i][ch] = mu;
-            mu = run_apply(sp[pt * GP + i][ch], m, mu);
+            mu = run_apply<MODE>(sp[pt * GP + i][ch], m, mu);
         }
     }
     __syncthreads();

@@ -204,9 +204,15 @@ __device__ __forceinline__ void lds_put(float *p, const float (&f)[V]) {
 // A run of steps maps the state h entering it to p h + l (p the product of its decays, l its
 // states from 0), or to l alone once it holds a reset: p is then NaN, which every later product
 // keeps, and a select drops the entering state whatever it holds.  (A NaN decay makes l NaN too,
-// so it is not lost.)
+// so it is not lost.)  With RATE an entering 0 gives l also where p is an infinity: decays above 1
+// take no input, so every state may be 0 while their product leaves the range.  (The rows of a tile
+// have a branch for it: a select on every element took the 1M-token forward from 1685 to 1725 us.
+// SIGMOID, whose p is at most 1, does without: the second test took its packed backward from 180 to
+// 186 us.)
+template <int MODE>
 __device__ __forceinline__ float run_apply(float p, float l, float h) {
-    return p != p ? l : __builtin_fmaf(p, h, l);
+    const bool alone = MODE == SSM_GATE_RATE ? (p != p) | (h == 0.0f) : p != p;
+    return alone ? l : __builtin_fmaf(p, h, l);
 }
 
 // ---- states between the tiles of one (batch row, channel block): a chain
@@ -232,6 +238,7 @@ __device__ __forceinline__ void rec_put(u64_t *r, uint32_t hi, float lo) {
 // Every wait ends: a tile's number in its chain is a ticket drawn when its workgroup already
 // runs, so the tiles before it belong to workgroups that run or have ended, the first never
 // waits, and a tile leaves its state without waiting for a later one.
+template <int MODE>
 __device__ __forceinline__ float chain_enter(const u64_t *rec, int64_t stride, int k) {
     for (;;) {
         u64_t v[kLook];
@@ -247,7 +254,7 @@ __device__ __forceinline__ float chain_enter(const u64_t *rec, int64_t stride, i
             const uint32_t hi = (uint32_t)(v[j] >> 32);
             const float lo = __uint_as_float((uint32_t)v[j]);
             known = hi == kRecState || (known && hi != kRecEmpty);
-            h = hi == kRecState ? lo : run_apply(__uint_as_float(hi), lo, h);
+            h = hi == kRecState ? lo : run_apply<MODE>(__uint_as_float(hi), lo, h);
         }
         if (__all(known)) return h;
         __builtin_amdgcn_s_sleep(1);

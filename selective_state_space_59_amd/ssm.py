@@ -959,6 +959,8 @@ def gated_scan_fwd(x: torch.Tensor, gate: torch.Tensor, mode: str = "rate",
 
     mode "decay": a = gate, b = x.  "sigmoid": s = sigmoid(gate + gate_bias), a = 1 - s, b = s x.
     "rate": a = exp(A sigmoid(gate + gate_bias)), b = sqrt(1 - a^2) sigmoid(in_gate + in_bias) x.
+    Decays outside [-1, 1] (A > 0) are computed as long as products of up to 256 of them stay below
+    2^127; where A > 0 the input's weight is 0.
 
     Returns (y, h_final or None).  A float32 tensor `checkpoints` of gated_checkpoint_shape(B, L, D)
     also receives the state entering every GATED_BLOCK-step block, for gated_scan_bwd."""

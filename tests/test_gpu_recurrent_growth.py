@@ -1,0 +1,76 @@
+"""Rates above 0 (decays above 1) in the gated recurrence: they take no input, so a state of 0 stays
+0 however large the products of decays formed inside become, and a state that stays in range
+follows its definition (needs an MI355X)."""
+import numpy as np
+import pytest
+import torch
+
+import selective_state_space_59_amd as ssm
+from oracle import recurrent as R
+from tests.recurrent_helpers import check, f64, scan_case, scan_case64
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def _open(L, D, dtype, A, seed, reset=False):
+    """sig(gate) within 2^-40 of 1: every decay is e^A."""
+    k = scan_case("rate", 2, L, D, dtype, seed=seed, bias=False, h0=False)
+    k["gate"] = torch.full_like(k["gate"], 28.0)
+    k["A"] = torch.full((D,), A, device=DEV)
+    if reset:
+        k["reset"] = torch.zeros(2, L, dtype=torch.uint8, device=DEV)
+        k["reset"][0, L // 3] = 1
+    return k
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("reset", [False, True], ids=["plain", "reset"])
+@pytest.mark.parametrize("L,D,A", [(257, 40, 0.5), (700, 67, 0.5), (5000, 24, 2.0), (30, 8, 30.0), (128, 72, 60.0)])
+def test_a_zero_state_stays_zero(L, D, A, dtype, reset):
+    """e^(A 256) is past the fp32 range in every case, and e^(4 A) in the last two."""
+    k = _open(L, D, dtype, A, seed=L, reset=reset)
+    ck = torch.full(ssm.gated_checkpoint_shape(2, L, D), float("nan"), device=DEV)
+    y, hf = ssm.gated_scan_fwd(return_final_state=True, checkpoints=ck, **k)
+    torch.cuda.synchronize()
+    assert not y.any() and not hf.any() and not ck.any()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+def test_gradients_of_a_zero_state(dtype):
+    """dy is 0 but for the first 100 steps, so lambda stays below 100 e^50: every gradient is 0 (the
+    input has no weight and the state is 0), also where a tile's product has left the range."""
+    L = 900
+    k = _open(L, 40, dtype, 0.5, seed=3)
+    dy = torch.zeros_like(k["x"])
+    dy[:, :100] = 1.0
+    got = ssm.gated_scan_bwd(dy=dy, h0=torch.zeros(2, 40, device=DEV), **k)
+    torch.cuda.synchronize()
+    ref = R.gated_scan_bwd(dy=f64(dy), **scan_case64(dict(k, h0=torch.zeros(2, 40, device=DEV))))
+    for n, (v, e) in ref.items():
+        if n != "dh0":
+            assert not np.any(v) and not got[n].any(), n
+    check(got["dh0"], *ref["dh0"], "dh0")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("L", [600, 1500])
+def test_growth_within_the_range(L, dtype):
+    """A of 0.01 to 0.05 over up to 1500 steps, sig(gate) around 1/2: the states stay below e^45 and
+    the products of 256 decays below e^13, within 2^127."""
+    k = scan_case("rate", 2, L, 40, dtype, seed=L, bias=False, in_gate=False)
+    k["A"] = torch.linspace(0.01, 0.05, 40).to(DEV)
+    ck = torch.empty(ssm.gated_checkpoint_shape(2, L, 40), device=DEV)
+    y, hf = ssm.gated_scan_fwd(return_final_state=True, checkpoints=ck, **k)
+    torch.cuda.synchronize()
+    H, _, E = R.gated_scan(**scan_case64(k))
+    check(y, H, E, "y")
+    check(hf, H[:, -1], E[:, -1], "h_final")
+    for j in range(1, ck.shape[0]):
+        check(ck[j], H[:, 128 * j - 1], E[:, 128 * j - 1], "checkpoint %d" % j)
+    dy = torch.randn(k["x"].shape, generator=torch.Generator().manual_seed(1)).to(dtype).to(DEV)
+    got = ssm.gated_scan_bwd(dy=dy, checkpoints=ck, **k)
+    torch.cuda.synchronize()
+    for n, (v, e) in R.gated_scan_bwd(dy=f64(dy), **scan_case64(k)).items():
+        check(got[n], v, e, n)
