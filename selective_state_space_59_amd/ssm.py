@@ -869,6 +869,11 @@ def _need(t, name, shape, dtype, device):
     return _req(t, name, shape, dtype, device).data_ptr()
 
 
+# Autograd does not see the library's writes: a call counts the tensors it was given to write into
+# (those it allocates are new) as changed, so that a backward which saved one of them raises.
+_changed = torch.autograd.graph.increment_version
+
+
 class _Scratch(threading.local):
     """Cached workspaces of the calling thread.  Two threads may use the same stream at once, and
     the launches of their calls then alternate on it: a workspace they shared would be emptied by
@@ -967,6 +972,7 @@ def gated_scan_fwd(x: torch.Tensor, gate: torch.Tensor, mode: str = "rate",
     dev = _gpu(x, "x", 3, "(B, L, D)")
     B, L, D = x.shape
     f32 = torch.float32
+    given = [t for t in (y, h_final, checkpoints) if t is not None]
     a = GatedScanArgs(batch=B, seqlen=L, dim=D)
     _gates(a, x, gate, mode, A, in_gate, gate_bias, in_bias, dev)
     if reset is not None:
@@ -986,6 +992,8 @@ def gated_scan_fwd(x: torch.Tensor, gate: torch.Tensor, mode: str = "rate",
     if checkpoints is not None:
         a.checkpoints = _arg(checkpoints, "checkpoints", gated_checkpoint_shape(B, L, D), f32, dev)
     _run("ssm_gated_scan_fwd", a, dev, "ssm_gated_scan_workspace_size", workspace)
+    if given:
+        _changed(given)
     return y, h_final
 
 
@@ -1038,16 +1046,17 @@ def gated_scan_step(state: torch.Tensor, x: torch.Tensor, gate: torch.Tensor, mo
     """ssm_gated_scan_step: one decode token; advances `state` (B, D) fp32 in place and returns
     y (B, D).  x, gate, in_gate: (B, D) bf16 or fp32; reset: (B,) uint8 or bool, rows whose state
     is taken as 0 (a new sequence); the rest as in gated_scan_fwd."""
-    a, y = gated_scan_step_args(state, x, gate, mode, A, in_gate, gate_bias, in_bias, reset, y)
+    a, out = gated_scan_step_args(state, x, gate, mode, A, in_gate, gate_bias, in_bias, reset, y)
     _run("ssm_gated_scan_step", a, state.device)
-    return y
+    _changed(state if y is None else (state, y))
+    return out
 
 
 def gated_scan_step_args(state, x, gate, mode="rate", A=None, in_gate=None, gate_bias=None, in_bias=None,
                          reset=None, y=None):
     """The checked ssm_gated_step_args_t of a gated_scan_step call, and its y (allocated when not
     given), for callers that launch the same step repeatedly through lib().ssm_gated_scan_step.
-    The tensors must outlive the struct."""
+    The tensors must outlive the struct; autograd does not see what such launches write."""
     dev = _gpu(state, "state", 2, "(B, D) float32")
     shape = state.shape
     if not isinstance(x, torch.Tensor) or x.shape != shape:
@@ -1142,6 +1151,7 @@ def add_rmsnorm_fwd(x: torch.Tensor, w: torch.Tensor, residual: Optional[torch.T
     a = AddNormArgs()
     _add_norm(a, x, w, residual, scale, post_w, eps, shape, dev)
     stream = x if residual is None else residual
+    given = [t for t in (y, res_out) if t is not None]
     if y is None:
         y = torch.empty_like(x)
         a.y = y.data_ptr()
@@ -1153,6 +1163,8 @@ def add_rmsnorm_fwd(x: torch.Tensor, w: torch.Tensor, residual: Optional[torch.T
     else:
         a.res_out = _need(res_out, "res_out", shape, stream.dtype, dev)
     _run("ssm_add_rmsnorm_fwd", a, dev)
+    if given:
+        _changed(given)
     return y, res_out
 
 
@@ -1231,13 +1243,12 @@ def gated_rmsnorm_fwd(x: torch.Tensor, z: torch.Tensor, w: torch.Tensor, groups:
     dev = x.device
     a = GatedNormArgs()
     _gated_norm(a, x, z, w, groups, gate_first, eps, shape, dev)
-    if y is None:
-        y = torch.empty_like(x)
-        a.y = y.data_ptr()
-    else:
-        a.y = _need(y, "y", shape, x.dtype, dev)
+    out = torch.empty_like(x) if y is None else y
+    a.y = out.data_ptr() if y is None else _need(y, "y", shape, x.dtype, dev)
     _run("ssm_gated_rmsnorm_fwd", a, dev)
-    return y
+    if y is not None:
+        _changed(y)
+    return out
 
 
 def gated_rmsnorm_bwd(x: torch.Tensor, z: torch.Tensor, w: torch.Tensor, dy: torch.Tensor, groups: int = 1,
