@@ -281,6 +281,15 @@ def _opt(t, name, shape, dtype, device):
     return t
 
 
+def _changed(*tensors):
+    """Count the given tensors as changed in place.  Autograd does not see the library's writes: a
+    call marks the tensors it was given to write into (those it allocates are new), so that a
+    backward which saved one of them raises."""
+    for t in tensors:
+        if t is not None:
+            torch.autograd.graph.increment_version(t)
+
+
 def _stream(device: torch.device) -> int:
     return torch.cuda.current_stream(device).cuda_stream
 
@@ -394,6 +403,7 @@ def selective_scan_fwd(x: torch.Tensor, delta: torch.Tensor, A: torch.Tensor, Bm
     conv_state_out); conv states are (B, K-1, D) in x's dtype.  A float32 tensor
     `checkpoints` of checkpoint_shape(B, L, D) also receives the state entering every
     SCAN_BLOCK-step block, for selective_scan_bwd(checkpoints=...)."""
+    given = (y, h_final, conv_state_out, checkpoints)
     if y is None:
         y = torch.empty_like(x)
     if return_final_state and h_final is None:
@@ -417,6 +427,7 @@ def selective_scan_fwd(x: torch.Tensor, delta: torch.Tensor, A: torch.Tensor, Bm
         a.workspace = ws.data_ptr()
         a.workspace_bytes = ws.numel() * ws.element_size()
     _check(lib().ssm_selective_scan_fwd(ctypes.byref(a), _stream(dev)), "ssm_selective_scan_fwd")
+    _changed(*given)
     return (y, h_final, conv_state_out) if want_cs else (y, h_final)
 
 
@@ -444,6 +455,7 @@ def selective_scan_fwd_noalloc(x: torch.Tensor, delta: torch.Tensor, A: torch.Te
                         conv_b, h0, y, h_final, conv_state_in, conv_state_out, checkpoints)
     _check(lib().ssm_selective_scan_fwd_noalloc(ctypes.byref(a), _stream(dev)),
            "ssm_selective_scan_fwd_noalloc")
+    _changed(y, h_final, conv_state_out, checkpoints)
     return y, h_final
 
 
@@ -482,12 +494,14 @@ def causal_conv1d_silu(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Te
     _req(x, "x", (Bsz, L, D), x.dtype, dev)
     _req(w, "w", (D, K), torch.float32, dev)
     _opt(bias, "bias", (D,), torch.float32, dev)
+    given = out
     if out is None:
         out = torch.empty_like(x)
     _req(out, "out", (Bsz, L, D), x.dtype, dev)
     _check(lib().ssm_causal_conv1d_silu(Bsz, L, D, K, _io_code(x.dtype), _ptr(x), _ptr(w),
                                         _ptr(bias), _ptr(out), _stream(dev)),
            "ssm_causal_conv1d_silu")
+    _changed(given)
     return out
 
 
@@ -499,10 +513,11 @@ def state_update(state: torch.Tensor, x: torch.Tensor, delta: torch.Tensor, A: t
                  conv_state: Optional[torch.Tensor] = None) -> torch.Tensor:
     """ssm_state_update: advances `state` (B, D, N) -- and with conv_w the conv
     window `conv_state` (B, K-1, D) -- in place and returns y (B, D)."""
-    a, y = state_update_args(state, x, delta, A, Bm, Cm, Dskip, z, delta_bias, delta_softplus, y,
-                             conv_w, conv_b, conv_state)
+    a, out = state_update_args(state, x, delta, A, Bm, Cm, Dskip, z, delta_bias, delta_softplus, y,
+                               conv_w, conv_b, conv_state)
     _check(lib().ssm_state_update(ctypes.byref(a), _stream(state.device)), "ssm_state_update")
-    return y
+    _changed(state, y, conv_state)
+    return out
 
 
 def state_update_args(state, x, delta, A, Bm, Cm, Dskip=None, z=None, delta_bias=None,
@@ -713,6 +728,7 @@ def mamba_block_fwd(h: torch.Tensor, norm_w: torch.Tensor, w_in: torch.Tensor, c
     _req(A, "A", (D, N), f32, dev)
     _opt(Dskip, "Dskip", (D,), f32, dev)
     _req(w_out, "w_out", (dm, D), bf, dev)
+    given = out
     if out is None:
         out = torch.empty_like(h)
     _req(out, "out", (Bsz, L, dm), bf, dev)
@@ -734,6 +750,7 @@ def mamba_block_fwd(h: torch.Tensor, norm_w: torch.Tensor, w_in: torch.Tensor, c
     _check(lib().ssm_block_fwd(plan.handle, ctypes.byref(wts), _ptr(h), _ptr(out), _ptr(workspace),
                                workspace.numel() * workspace.element_size(), _stream(dev)),
            "ssm_block_fwd")
+    _changed(given)
     return out
 
 
@@ -764,6 +781,7 @@ def ssd_fwd(x: torch.Tensor, delta: torch.Tensor, A: torch.Tensor, Bm: torch.Ten
     _opt(z, "z", (Bsz, L, H, P), bf, dev)
     _opt(delta_bias, "delta_bias", (H,), f32, dev)
     _opt(h0, "h0", (Bsz, H, P, N), f32, dev)
+    given = (y, h_final)
     if y is None:
         y = torch.empty_like(x)
     _req(y, "y", (Bsz, L, H, P), bf, dev)
@@ -782,6 +800,7 @@ def ssd_fwd(x: torch.Tensor, delta: torch.Tensor, A: torch.Tensor, Bm: torch.Ten
         a.workspace = ws.data_ptr()
         a.workspace_bytes = ws.numel()
     _check(lib().ssm_ssd_fwd(ctypes.byref(a), _stream(dev)), "ssm_ssd_fwd")
+    _changed(*given)
     return (y, h_final) if h_final is not None else y
 
 
@@ -792,9 +811,10 @@ def ssd_step(state: torch.Tensor, x: torch.Tensor, delta: torch.Tensor, A: torch
     """ssm_ssd_step: one decode step of the SSD layer; advances `state` (B, H, P, N) fp32 in
     place.  x, z: (B, H, P) bf16; delta: (B, H) bf16; A, Dskip, delta_bias: (H,) fp32;
     Bm, Cm: (B, G, N) bf16.  Returns y (B, H, P) bf16."""
-    a, y = ssd_step_args(state, x, delta, A, Bm, Cm, Dskip, z, delta_bias, delta_softplus, y)
+    a, out = ssd_step_args(state, x, delta, A, Bm, Cm, Dskip, z, delta_bias, delta_softplus, y)
     _check(lib().ssm_ssd_step(ctypes.byref(a), _stream(state.device)), "ssm_ssd_step")
-    return y
+    _changed(state, y)
+    return out
 
 
 def ssd_step_args(state, x, delta, A, Bm, Cm, Dskip=None, z=None, delta_bias=None,
@@ -867,11 +887,6 @@ def _need(t, name, shape, dtype, device):
     except AttributeError:
         pass
     return _req(t, name, shape, dtype, device).data_ptr()
-
-
-# Autograd does not see the library's writes: a call counts the tensors it was given to write into
-# (those it allocates are new) as changed, so that a backward which saved one of them raises.
-_changed = torch.autograd.graph.increment_version
 
 
 class _Scratch(threading.local):
@@ -972,7 +987,7 @@ def gated_scan_fwd(x: torch.Tensor, gate: torch.Tensor, mode: str = "rate",
     dev = _gpu(x, "x", 3, "(B, L, D)")
     B, L, D = x.shape
     f32 = torch.float32
-    given = [t for t in (y, h_final, checkpoints) if t is not None]
+    given = (y, h_final, checkpoints)
     a = GatedScanArgs(batch=B, seqlen=L, dim=D)
     _gates(a, x, gate, mode, A, in_gate, gate_bias, in_bias, dev)
     if reset is not None:
@@ -992,8 +1007,7 @@ def gated_scan_fwd(x: torch.Tensor, gate: torch.Tensor, mode: str = "rate",
     if checkpoints is not None:
         a.checkpoints = _arg(checkpoints, "checkpoints", gated_checkpoint_shape(B, L, D), f32, dev)
     _run("ssm_gated_scan_fwd", a, dev, "ssm_gated_scan_workspace_size", workspace)
-    if given:
-        _changed(given)
+    _changed(*given)
     return y, h_final
 
 
@@ -1048,7 +1062,7 @@ def gated_scan_step(state: torch.Tensor, x: torch.Tensor, gate: torch.Tensor, mo
     is taken as 0 (a new sequence); the rest as in gated_scan_fwd."""
     a, out = gated_scan_step_args(state, x, gate, mode, A, in_gate, gate_bias, in_bias, reset, y)
     _run("ssm_gated_scan_step", a, state.device)
-    _changed(state if y is None else (state, y))
+    _changed(state, y)
     return out
 
 
@@ -1151,7 +1165,7 @@ def add_rmsnorm_fwd(x: torch.Tensor, w: torch.Tensor, residual: Optional[torch.T
     a = AddNormArgs()
     _add_norm(a, x, w, residual, scale, post_w, eps, shape, dev)
     stream = x if residual is None else residual
-    given = [t for t in (y, res_out) if t is not None]
+    given = (y, res_out)
     if y is None:
         y = torch.empty_like(x)
         a.y = y.data_ptr()
@@ -1163,8 +1177,7 @@ def add_rmsnorm_fwd(x: torch.Tensor, w: torch.Tensor, residual: Optional[torch.T
     else:
         a.res_out = _need(res_out, "res_out", shape, stream.dtype, dev)
     _run("ssm_add_rmsnorm_fwd", a, dev)
-    if given:
-        _changed(given)
+    _changed(*given)
     return y, res_out
 
 
@@ -1246,8 +1259,7 @@ def gated_rmsnorm_fwd(x: torch.Tensor, z: torch.Tensor, w: torch.Tensor, groups:
     out = torch.empty_like(x) if y is None else y
     a.y = out.data_ptr() if y is None else _need(y, "y", shape, x.dtype, dev)
     _run("ssm_gated_rmsnorm_fwd", a, dev)
-    if y is not None:
-        _changed(y)
+    _changed(y)
     return out
 
 
