@@ -329,6 +329,11 @@ int64_t partial_rows(int64_t rows, int64_t D, int32_t io) {
     return D > 256 ? g.blocks : g.slots;
 }
 
+// Column sums of a call: dw; dscale behind it; dpost_w in the third place.
+int column_sums_of(const ssm_add_norm_bwd_args_t &a) { return a.post_w ? 3 : a.scale ? 2 : 1; }
+
+size_t partial_bytes(int K, int64_t n, int64_t D) { return ((size_t)(K * n * D) * 4 + 255) & ~(size_t)255; }
+
 }  // namespace
 
 hipError_t launch_add_norm_fwd(const ssm_add_norm_args_t &a, hipStream_t stream) {
@@ -360,7 +365,8 @@ hipError_t launch_add_norm_fwd(const ssm_add_norm_args_t &a, hipStream_t stream)
 
 size_t add_norm_bwd_workspace_bytes(const ssm_add_norm_bwd_args_t &a) {
     const int64_t n = partial_rows(a.rows, a.dim, a.io_dtype);
-    return (((size_t)(3 * n * a.dim) * 4 + 255) & ~(size_t)255) + column_sums_scratch_bytes(n, a.dim, 3);
+    const int K = column_sums_of(a);
+    return partial_bytes(K, n, a.dim) + column_sums_scratch_bytes(n, a.dim, K);
 }
 
 hipError_t launch_add_norm_bwd(const ssm_add_norm_bwd_args_t &a, hipStream_t stream) {
@@ -391,8 +397,9 @@ hipError_t launch_add_norm_bwd(const ssm_add_norm_bwd_args_t &a, hipStream_t str
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     float *out[3] = {a.dw, a.scale ? a.dscale : nullptr, a.post_w ? a.dpost_w : nullptr};
-    char *scratch = static_cast<char *>(a.workspace) + (((size_t)(3 * n * D) * 4 + 255) & ~(size_t)255);
-    return launch_column_sums(part, n, D, a.post_w ? 3 : a.scale ? 2 : 1, out, reinterpret_cast<float *>(scratch), stream);
+    const int K = column_sums_of(a);
+    char *scratch = static_cast<char *>(a.workspace) + partial_bytes(K, n, D);
+    return launch_column_sums(part, n, D, K, out, reinterpret_cast<float *>(scratch), stream);
 }
 
 }  // namespace ssm

@@ -69,7 +69,7 @@ size_t column_sums_scratch_bytes(int64_t n, int64_t D, int K);
 hipError_t launch_column_sums(const float *part, int64_t n, int64_t D, int K, float *const out[], float *scratch,
                               hipStream_t stream);
 
-// Fused norms (add_norm.hip, gated_norm.hip).  rows > 0 in the forward; the backward takes rows >= 0.
+// Fused norms (add_norm.hip, gated_norm.hip), rows > 0.
 hipError_t launch_add_norm_fwd(const ssm_add_norm_args_t &a, hipStream_t stream);
 size_t add_norm_bwd_workspace_bytes(const ssm_add_norm_bwd_args_t &a);
 hipError_t launch_add_norm_bwd(const ssm_add_norm_bwd_args_t &a, hipStream_t stream);
