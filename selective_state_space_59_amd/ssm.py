@@ -1239,6 +1239,8 @@ def add_rmsnorm(x: torch.Tensor, w: torch.Tensor, residual: Optional[torch.Tenso
 
 def _gated_norm(a, x, z, w, groups, gate_first, eps, shape, dev):
     D = shape[-1]
+    if int(groups) != groups:
+        raise ValueError("groups must be a whole number, got %r" % (groups,))
     a.rows, a.dim, a.groups, a.eps = x.numel() // D, D, int(groups), float(eps)
     a.io_dtype, a.gate_first = _io_code(x.dtype), int(bool(gate_first))
     a.x = _need(x, "x", shape, x.dtype, dev)
