@@ -215,9 +215,13 @@ __global__ __launch_bounds__(1024) void gated_norm_bwd_long_kernel(ssm_gated_nor
 constexpr int64_t kFwdBlocks = 2048, kLongBlocks = 256;
 
 // Groups of 513 to 768 channels: half a wave with three groups of 8 a lane leaves fewer lanes idle
-// than a wave with two (16384 x 5120 in 8 groups of 640: forward and backward 262 us against
-// 283), but each of its teams leaves a row of partial sums, so in the backward only where several
-// groups share a row (16384 x 768 in one group: 79 against 75).
+// than a wave with two, but each of its teams leaves a row of partial sums, which fall with the
+// number of groups of a row.  Forward and backward in bf16, half waves against waves, in us: 16384 rows
+// of 8 groups of 520 230 and 262, of 640 263 and 276, of 768 310 and 313; 32768 rows of 4 groups 231 and
+// 261, 263 and 275, 311 and 314; of 1, 2 and 3 groups of 520 67, 123, 179 and 72, 137, 199, of 640 79, 141,
+// 204 and 82, 145, 210, of 768 86, 160, 235 and 87, 159, 235.  (The backward's bound of 4 groups gives that
+// much away below 4.)  Forward alone, 16384 rows: one group of 520 13.1 and 13.5, of 768 13.8 and 14.8;
+// 8 groups 85 and 90, 114 and 118.
 bool half_wave(int64_t S) { return S > 512 && S <= 768; }
 
 int bwd_team(int64_t S, int64_t groups) {

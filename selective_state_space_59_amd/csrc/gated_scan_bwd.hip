@@ -13,9 +13,15 @@
 // run, once for its gradients: arithmetic is cheaper here than registers), and its gradients packed
 // into the place of its inputs.
 //
-// Measured in bf16: 8 x 2048 x 1536 RATE with in_gate 90 us, 3.9 TB/s, bound by the issue of its 94
-// vector instructions an element (13 of them exponentials, reciprocals and roots); 4 x 4096 x 5120
-// SIGMOID with resets 180 us, 4.7 TB/s, where the waves wait for the tile's phases.
+// Measured in bf16: 8 x 2048 x 1536 RATE with in_gate 91 us, 3.9 TB/s, bound by the issue of its 92
+// vector instructions an element (13 of them exponentials, reciprocals and roots; 37% of the waves'
+// cycles wait to issue, 33% otherwise); 4 x 4096 x 5120 SIGMOID with resets 180 us, 4.7 TB/s, 97
+// registers, four waves a SIMD, where 52% of the cycles wait for the tile's phases.  Training steps in
+// fp32, 8 x 2048 x 2560: SIGMOID 311 us, RATE with in_gate 431 us, four waves a SIMD.
+//
+// The launch bound holds bf16 RATE with in_gate at 128 registers, four waves a SIMD; of its lanes'
+// words 3 to 8 (12 to 32 bytes) then lie in scratch.  Without the bound or with three waves its layer's
+// training step takes 158 us against 156; the other variants need no more than 123 registers.
 #include "gated_tile.h"
 #include "ssm_internal.h"
 

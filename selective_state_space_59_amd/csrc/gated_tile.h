@@ -44,7 +44,8 @@ __device__ __forceinline__ void store_words(char *p, const Words<W> &q) {
 // How a tile lies over a workgroup: THREADS lanes, W words of R consecutive rows each; the lanes
 // of a row cover kRowBytes.  128 bytes give a layer of 1536 channels 24 blocks a row, and the lanes
 // of a row one whole line; pieces of 256 or 512 bytes, with as many times fewer and larger
-// workgroups, ran the 8 x 2048 x 1536 bf16 forward in 82 and 99 us where 128 took 71.
+// workgroups, ran the 8 x 2048 x 1536 bf16 forward in 82 and 99 us where 128 took 71 (in tiles of
+// 128 steps, ahead of the steps that took it to 52).
 constexpr int kRowBytes = 128;
 
 template <typename IO, int W_, int R_, int THREADS_>
@@ -267,8 +268,12 @@ __device__ __forceinline__ uint32_t rec_hi(float p) { return p != p ? 0x7fc00000
 // The chain of workgroup i of chains * tiles (the tile within it is the ticket it draws).
 // Workgroups go to the XCDs in turn.  A short chain's tiles are dealt out one chain after the
 // other; a long chain's run over all XCDs, eight at a time, so that no chain waits for one XCD that
-// is behind (as this was chosen, 1M tokens x 1024 channels: 1750 us, against 2013 us dealt out;
-// 8 x 2048 x 1536, 8 tiles a chain: 52.4 us dealt out against 53.1).  Either way every chain gets `tiles`.
+// is behind.  Dealt out against spread, bf16 RATE forward, 16384 steps of 1536 channels (131072 in the
+// last): 8 tiles a chain 52.0 and 54.2 us, 16 52.1 and 53.1, 32 53.4 and 53.7, 64 54.8 and 55.1, 128
+// 105.9 and 97.9 (32768 steps), 512 383 and 342; of 5120 channels 16 tiles 166 and 158, 64 169 and 159,
+// so wide layers would gain from a spread of 16 and 32 tiles too.  The backward (tiles of 128
+// steps): even up to 64 tiles, 1134 and 1028 us a training step of 131072.
+// Either way every chain gets `tiles`.
 constexpr int kLongChain = 64;
 
 __device__ __forceinline__ int chain_of(unsigned i, int chains, int tiles) {

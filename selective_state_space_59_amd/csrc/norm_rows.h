@@ -4,7 +4,7 @@
 //
 // A team of lanes owns a row, groups of 8 elements (or 4) a lane, read once into registers:
 //   rows of up to 256      8 or 32 lanes, several rows a wave (adjacent groups side by side)
-//   513 to 768             32 lanes of 3 groups (forwards; the gated backward over several groups)
+//   513 to 768             32 lanes of 3 groups (forwards; the gated backward over four groups or more)
 //   up to 2048             one wave of up to 4 groups a lane: sums without a barrier (backwards up
 //                          to 1024, whose column sums take registers too)
 //   up to kBlockRow        one workgroup of as many waves as the row needs, one group a lane
@@ -125,10 +125,14 @@ __device__ __forceinline__ TeamRows team_rows(int64_t groups, int64_t slots) {
     return {t % groups, slot < slots ? slot : (int64_t)1 << 62, slots};  // spare teams: no rows
 }
 
-// Workgroups of a backward: as many as run at once, since each walks over rows to its end.  In waves
-// a row of up to 2048 takes at most one of a SIMD, one of up to 4096 two, and the kernels' registers
-// leave room for four (16384 rows of 1280 bf16 with a post norm: 153 us with 512 workgroups, 110 with
-// 1024; of 2560: 184 with 512, 220 with 768; 8192 rows of 5120: 231 with 512, 226 with 256).
+// Workgroups of a backward: as many as run at once, since each walks over rows to its end.  With 8
+// elements a lane a row of up to 2048 takes at most one wave of a SIMD, one of up to 4096 two, and the
+// kernels' registers leave room for four.  Training steps of 16384 rows in bf16 with 512, 768, 1024 and
+// 2048 workgroups: 1280 with a post norm and scale 153, 127, 112, 117 us, 2048 156, 138, 138, 149; plain
+// 1280 107, 94, 86, 82, 2048 127, 127, 133, 141; of 2560 184 with 512, 220 with 768; 8192 rows of 5120 231
+// with 512, 226 with 256.  fp32 rows of 1025 to 2048 of the add + norm hold 4 elements a lane, five to
+// eight waves a row, and would be served as well or better by 512: 1280 168 against 173 us with 1024 (with
+// post norm and scale 179, 187), 2048 259 against 272 (260, 282).
 inline int64_t bwd_blocks(int64_t len) { return len <= 1024 ? 512 : len <= 2048 ? 1024 : len <= 4096 ? 512 : 256; }
 
 // `blocks_wanted`: workgroups that keep the chip busy; E: elements of a lane's group.
