@@ -19,9 +19,9 @@
 // registers, four waves a SIMD, where 52% of the cycles wait for the tile's phases.  Training steps in
 // fp32, 8 x 2048 x 2560: SIGMOID 311 us, RATE with in_gate 431 us, four waves a SIMD.
 //
-// The launch bound holds bf16 RATE with in_gate at 128 registers, four waves a SIMD; of its lanes'
-// words 3 to 8 (12 to 32 bytes) then lie in scratch.  Without the bound or with three waves its layer's
-// training step takes 158 us against 156; the other variants need no more than 123 registers.
+// The launch bound holds bf16 RATE with in_gate at 128 registers, four waves a SIMD, and its lanes keep
+// 24 bytes in scratch (32 at most, by width and length).  Without the bound or with three waves the
+// layer's training step takes 158 us against 156; the other variants need at most 123 registers.
 #include "gated_tile.h"
 #include "ssm_internal.h"
 
