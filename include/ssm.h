@@ -521,8 +521,9 @@ ssm_status_t ssm_ssd_step(const ssm_ssd_step_args_t *args, void *stream);
  * SSM_GATE_RATE by A <= 0.  Others are computed too, but the products of up to
  * SSM_GATED_TILE decays formed inside (in the backward too) must stay below 2^127:
  * growth beyond it gives an infinity or a NaN also where the states themselves
- * stay finite.  In SSM_GATE_RATE a state of 0 stays 0 all the same, and its
- * gradients, as long as each decay and each lambda is finite.
+ * stay finite.  In SSM_GATE_RATE a state of 0 stays 0 all the same where each
+ * decay is finite, and so do the gradients through it where each lambda, formed
+ * from such products, is.
  *
  * Arithmetic is fp32 (the hardware's exponential, reciprocal and square root,
  * 1 ulp); y is rounded once.  Results do not change from run to run.

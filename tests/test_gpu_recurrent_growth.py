@@ -74,3 +74,20 @@ def test_growth_within_the_range(L, dtype):
     torch.cuda.synchronize()
     for n, (v, e) in R.gated_scan_bwd(dy=f64(dy), **scan_case64(k)).items():
         check(got[n], v, e, n)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+def test_gradients_of_a_zero_state_across_resets(dtype):
+    """Resets every 90 steps and a dy everywhere: lambda reaches back to a reset at most, below 90 * 10
+    * e^45, while a tile's decays alone would make e^64."""
+    L = 900
+    k = _open(L, 40, dtype, 0.5, seed=5)
+    k["reset"] = torch.zeros(2, L, dtype=torch.uint8, device=DEV)
+    k["reset"][:, ::90] = 1
+    dy = torch.randn(k["x"].shape, generator=torch.Generator().manual_seed(2)).to(dtype).to(DEV)
+    y, hf = ssm.gated_scan_fwd(return_final_state=True, **k)
+    got = ssm.gated_scan_bwd(dy=dy, **k)
+    torch.cuda.synchronize()
+    assert not y.any() and not hf.any()
+    for n, t in got.items():
+        assert not t.any(), n
