@@ -17,7 +17,13 @@
  *   - ssm_add_rmsnorm_fwd, _bwd: the residual sum and the RMSNorm between two
  *     blocks in one pass, with its gradients;
  *   - ssm_gated_rmsnorm_fwd, _bwd: the RMSNorm of a gated layer output over
- *     groups of channels, with its gradients.
+ *     groups of channels, with its gradients;
+ *   - ssm_gated_delta_fwd, _bwd, _step: the gated delta rule, a matrix state
+ *     per head that forgets what it holds for a key before it takes up the
+ *     key's new value, with its gradients and its decode step;
+ *   - ssm_add_rmsnorm_fp8, ssm_quantize_fp8, ssm_matmul_fp8: the norm between
+ *     two blocks with its output in 8 bits, the quantising of any matrix, and
+ *     the product of two such matrices.
  *
  * The operations are defined on these pages (cited by title and section):
  *   [P1] "Mamba: Linear-Time Sequence Modeling with Selective State Spaces"
@@ -69,7 +75,7 @@
 extern "C" {
 #endif
 
-#define SSM_ABI_VERSION 11
+#define SSM_ABI_VERSION 12
 #define SSM_MAX_DSTATE 16 /* largest N the kernels hold in registers */
 #define SSM_MAX_CONV_K 4  /* largest conv1d kernel width */
 
@@ -733,6 +739,190 @@ size_t ssm_gated_rmsnorm_bwd_workspace_size(const ssm_gated_norm_bwd_args_t *arg
 
 /* Outputs must not overlap an input, each other or the workspace. */
 ssm_status_t ssm_gated_rmsnorm_bwd(const ssm_gated_norm_bwd_args_t *args, void *stream);
+
+/*
+ * The gated delta rule: per batch row b and value head h a state S of
+ * (kdim, vdim), read by a query and written by a key.  Per step t
+ *   S' = e^{g_t} S_{t-1}                     (0 where reset[b,t] != 0)
+ *   e_t = v_t - S'^T k_t                     what the state has wrong for k_t
+ *   S_t = S' + beta_t k_t e_t^T,   o_t = scale S_t^T q_t
+ * from S = h0 (or 0); h_final is the state after the last step.  Value head h
+ * uses q and k of head h / (heads / kheads).  With l2norm, q and k stand for
+ * q / sqrt(sum q^2 + 1e-6) and k / sqrt(sum k^2 + 1e-6) over a head's channels.
+ *
+ * g is the log of the decay: usually <= 0, any finite value or -infinity; a step
+ * with g < SSM_DELTA_FORGET (e^g is 0 in fp32) is a reset, with dg = 0.  The
+ * state settles for beta |k|^2 in (0, 2); beyond, it grows as the formulas say.
+ * A reset drops the state whatever it held, an infinity or a NaN included; the
+ * inputs themselves have to be finite, in a row's left padding too (the 64 steps
+ * of a chunk are computed together).
+ *
+ * Arithmetic is fp32: bf16 tensors run on the bf16 matrix cores, with what was
+ * computed carried through the products as the sum of three bf16 numbers (two,
+ * 16 bits, where only a bf16 output follows); outputs are rounded once.  Results
+ * do not change from run to run.  kdim: a multiple of 8 up to SSM_DELTA_MAX_KDIM;
+ * vdim: a multiple of 8 up to SSM_DELTA_MAX_VDIM; kheads divides heads <= 65535;
+ * batch <= 65535; seqlen < 2^30.
+ *
+ * q, k and v may be parts of a wider tensor: x_token is the distance of two steps
+ * and x_batch that of two batch rows, in elements; x_token 0: dense.  A head's
+ * channels and a step's heads are always consecutive.  q and k lie at 16-byte
+ * boundaries, with strides that keep them there.
+ *
+ * A call is several launches and its workspace carries data between them: as
+ * with ssm_gated_scan_fwd.
+ */
+#define SSM_DELTA_CHUNK 64
+#define SSM_DELTA_MAX_KDIM 128
+#define SSM_DELTA_MAX_VDIM 1024
+#define SSM_DELTA_FORGET (-104.0f)
+
+typedef struct ssm_gated_delta_args {
+    int64_t batch, seqlen;  /* B >= 0, L >= 0                                  */
+    int64_t kheads, heads;  /* Hk >= 1, H: a multiple of it                    */
+    int64_t kdim, vdim;     /* K, V                                            */
+    int32_t io_dtype;       /* ssm_dtype_t of q, k, v, beta and o              */
+    int32_t l2norm;         /* 0 or 1                                          */
+    const void *q, *k;      /* (B,L,Hk,K) io_dtype, required                   */
+    const void *v;          /* (B,L,H,V) io_dtype, required                    */
+    const float *g;         /* (B,L,H) fp32, required                          */
+    const void *beta;       /* (B,L,H) io_dtype, required                      */
+    const uint8_t *reset;   /* (B,L) bytes, or NULL (no resets)                */
+    const float *h0;        /* (B,H,K,V) fp32 initial state, or NULL (= 0)     */
+    void *o;                /* (B,L,H,V) io_dtype output, required             */
+    float *h_final;         /* (B,H,K,V) fp32 output, or NULL                  */
+    float *checkpoints;     /* (ceil(L/SSM_DELTA_CHUNK), B, H, K + SSM_DELTA_CHUNK, V) fp32
+                               output, or NULL: for each chunk the state entering it, and
+                               e_t of its steps (0 behind the last)            */
+    int64_t q_token, q_batch, k_token, k_batch, v_token, v_batch;
+    void *workspace;        /* device scratch of workspace_bytes, 256-aligned  */
+    size_t workspace_bytes; /* >= ssm_gated_delta_workspace_size(args)         */
+    float scale;            /* of the outputs; finite                          */
+} ssm_gated_delta_args_t;
+
+/* Workspace bytes (the size fields and io_dtype are read); (size_t)-1 for invalid sizes. */
+size_t ssm_gated_delta_workspace_size(const ssm_gated_delta_args_t *args);
+
+/* Outputs must not overlap any input, each other or the workspace.  L == 0 copies
+ * h0 (or zeros) to h_final. */
+ssm_status_t ssm_gated_delta_fwd(const ssm_gated_delta_args_t *args, void *stream);
+
+/*
+ * Its gradients for dL/do = dout and dL/dh_final = dh_final.  The chunks' inner
+ * matrices are formed again; states and errors come from the forward's
+ * checkpoints (computed once more when none are given).  Gradients of shared
+ * heads are summed in a fixed order; dense outputs.
+ */
+typedef struct ssm_gated_delta_bwd_args {
+    int64_t batch, seqlen, kheads, heads, kdim, vdim; /* as in ssm_gated_delta_args_t */
+    int32_t io_dtype, l2norm;
+    const void *q, *k, *v;  /* forward inputs                                  */
+    const float *g;
+    const void *beta;
+    const uint8_t *reset;
+    const float *h0;
+    const void *dout;       /* (B,L,H,V) io_dtype, dense, required             */
+    const float *dh_final;  /* (B,H,K,V) fp32, or NULL (= 0)                   */
+    const float *checkpoints; /* of an ssm_gated_delta_fwd call on the same inputs, or NULL */
+    void *dq, *dk;          /* (B,L,Hk,K) io_dtype outputs, required           */
+    void *dv;               /* (B,L,H,V) io_dtype output, required             */
+    float *dg;              /* (B,L,H) fp32 output, required                   */
+    void *dbeta;            /* (B,L,H) io_dtype output, required               */
+    float *dh0;             /* (B,H,K,V) fp32 output, or NULL                  */
+    int64_t q_token, q_batch, k_token, k_batch, v_token, v_batch;
+    void *workspace;
+    size_t workspace_bytes; /* >= ssm_gated_delta_bwd_workspace_size(args)     */
+    float scale;
+} ssm_gated_delta_bwd_args_t;
+
+/* Workspace bytes (the size fields, io_dtype and whether checkpoints are given are read);
+ * (size_t)-1 for invalid sizes. */
+size_t ssm_gated_delta_bwd_workspace_size(const ssm_gated_delta_bwd_args_t *args);
+
+/* Outputs must not overlap any input, each other or the workspace; every output
+ * given is overwritten. */
+ssm_status_t ssm_gated_delta_bwd(const ssm_gated_delta_bwd_args_t *args, void *stream);
+
+/*
+ * One decode step on a state kept between calls (h_final of a prefill), advanced
+ * IN PLACE; a row with reset[b] != 0 begins anew.  x_batch: distance of two batch
+ * rows of q, k or v, 0 for dense ones.
+ */
+typedef struct ssm_gated_delta_step_args {
+    int64_t batch, kheads, heads, kdim, vdim;
+    int32_t io_dtype, l2norm;
+    float *state;           /* (B,H,K,V) fp32, 16-byte aligned, required       */
+    const void *q, *k;      /* (B,Hk,K) io_dtype, required                     */
+    const void *v;          /* (B,H,V) io_dtype, required                      */
+    const float *g;         /* (B,H) fp32, required                            */
+    const void *beta;       /* (B,H) io_dtype, required                        */
+    const uint8_t *reset;   /* (B) bytes, or NULL                              */
+    void *o;                /* (B,H,V) io_dtype output, required               */
+    int64_t q_batch, k_batch, v_batch;
+    float scale;
+} ssm_gated_delta_step_args_t;
+
+/* o must not overlap any input or the state, nor the state an input. */
+ssm_status_t ssm_gated_delta_step(const ssm_gated_delta_step_args_t *args, void *stream);
+
+/*
+ * 8-bit values (OCP e4m3: 3 bits behind the leading one, up to 448, no infinity)
+ * with a scale for each block of SSM_FP8_BLOCK consecutive columns and one row, or
+ * as many rows.  For a block with largest magnitude m:
+ *   scale = max(m, 2^-100) / 448,   q = e4m3(x / scale), to nearest even
+ * so q * scale stands for x.  A block that holds an infinity or a NaN has a scale
+ * that is none either, and all of it stands for NaN.  The last blocks of a matrix
+ * may be shorter.
+ */
+#define SSM_FP8_BLOCK 128
+
+typedef struct ssm_quantize_fp8_args {
+    int64_t rows;           /* M >= 0                                          */
+    int64_t dim;            /* D: a multiple of 16, 16 <= D <= 2^20            */
+    int64_t block_rows;     /* 1, or SSM_FP8_BLOCK                             */
+    int32_t io_dtype;       /* ssm_dtype_t of x                                */
+    const void *x;          /* (M,D) io_dtype, required                        */
+    void *q;                /* (M,D) e4m3 bytes, 16-byte aligned, required     */
+    float *scales;          /* (ceil(M/block_rows), ceil(D/128)) fp32, required */
+} ssm_quantize_fp8_args_t;
+
+/* Outputs must not overlap x or each other. */
+ssm_status_t ssm_quantize_fp8(const ssm_quantize_fp8_args_t *args, void *stream);
+
+/*
+ * ssm_add_rmsnorm_fwd with y quantised as by ssm_quantize_fp8 with block_rows 1,
+ * from its fp32 values: q (rows,D) e4m3 bytes and scales (rows, ceil(D/128)) fp32.
+ * `norm` is that function's struct with y NULL, and a dim that is a multiple of 16.
+ */
+typedef struct ssm_add_norm_fp8_args {
+    ssm_add_norm_args_t norm;
+    void *q;                /* 16-byte aligned, required                       */
+    float *scales;          /* required                                        */
+} ssm_add_norm_fp8_args_t;
+
+/* Outputs must not overlap an input (but res_out may be residual) or each other. */
+ssm_status_t ssm_add_rmsnorm_fp8(const ssm_add_norm_fp8_args_t *args, void *stream);
+
+/*
+ * The product of 8-bit matrices, y = x w^T:
+ *   y[m,n] = sum_j x_scales[m,j] w_scales[n/128,j] sum_{k in block j} xq[m,k] wq[n,k]
+ * Sums are fp32; y is rounded once.  For a bf16 y a block's 128 terms are summed by
+ * the 8-bit matrix instruction, which drops what lies 2^14 below the largest of
+ * eight terms (about 1.5e-5 of a result, where the rounding to bf16 is 2e-3); for an
+ * fp32 y they are summed in fp32.  x is quantised by rows of 1, w by rows of 128.
+ */
+typedef struct ssm_matmul_fp8_args {
+    int64_t m, n, k;        /* M >= 0, N >= 1; K a multiple of 16; each < 2^31 */
+    int32_t out_dtype;      /* ssm_dtype_t of y                                */
+    const void *xq;         /* (M,K) e4m3 bytes, 16-byte aligned, required     */
+    const float *x_scales;  /* (M, ceil(K/128)) fp32, required                 */
+    const void *wq;         /* (N,K) e4m3 bytes, 16-byte aligned, required     */
+    const float *w_scales;  /* (ceil(N/128), ceil(K/128)) fp32, required       */
+    void *y;                /* (M,N) out_dtype, required                       */
+} ssm_matmul_fp8_args_t;
+
+/* y must not overlap an input. */
+ssm_status_t ssm_matmul_fp8(const ssm_matmul_fp8_args_t *args, void *stream);
 
 /* Static description of a status code (never NULL). */
 const char *ssm_status_string(ssm_status_t status);

@@ -1,0 +1,253 @@
+// matmul_fp8.hip -- the product of two e4m3 matrices with block scales (ssm_matmul_fp8) on gfx950:
+//   y[m,n] = sum_j sx[m,j] sw[n/128,j] sum_{k in block j} x[m,k] w[n,k]
+// One matrix instruction (16 x 16, 128 deep) sums a block's 128 products of a tile; its result is added to
+// the fp32 sums with the two scales.  w is the left operand, so that a lane holds four neighbouring
+// columns of y and ONE row, whose scale is then one number a tile.
+#include "ssm_device.h"
+#include "ssm_internal.h"
+
+#include <algorithm>
+
+namespace ssm {
+namespace {
+
+typedef float f4 __attribute__((ext_vector_type(4)));
+typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+typedef __bf16 b8 __attribute__((ext_vector_type(8)));
+typedef int i4 __attribute__((ext_vector_type(4)));
+typedef int i8 __attribute__((ext_vector_type(8)));
+
+constexpr int kOne = 0x7f7f7f7f;  // 1.0 in the exponent bytes of the scaled instruction
+
+// 32 bytes of a row as a block's product takes them.  The 8-bit instruction adds the products of a lane in
+// groups of eight, aligned to the largest of each: what lies 2^14 below it is lost (random data: 1.5e-5 of
+// the result).  That is far below a bf16 result's own rounding; for an fp32 result the values are widened
+// to bf16, exactly, and summed by the bf16 instruction at half the rate.
+template <typename OUT>
+struct Operand {
+    i8 v;
+    Operand() = default;
+    __device__ __forceinline__ Operand(i4 a, i4 b) : v{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]} {}
+};
+template <>
+struct Operand<io_f32> {
+    b8 v[4];
+    Operand() = default;
+    __device__ __forceinline__ Operand(i4 a, i4 b) {
+        const int w[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const b2 lo = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[i], 1.0f, false);
+            const b2 hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[i], 1.0f, true);
+            const int e = i % 2 * 4;
+            v[i / 2][e] = lo[0];
+            v[i / 2][e + 1] = lo[1];
+            v[i / 2][e + 2] = hi[0];
+            v[i / 2][e + 3] = hi[1];
+        }
+    }
+};
+
+__device__ __forceinline__ f4 block_product(const Operand<io_bf16> &w, const Operand<io_bf16> &x) {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w.v, x.v, f4{0, 0, 0, 0}, 0, 0, 0, kOne, 0, kOne);
+}
+__device__ __forceinline__ f4 block_product(const Operand<io_f32> &w, const Operand<io_f32> &x) {
+    f4 p = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w.v[i], x.v[i], p, 0, 0, 0);
+    return p;
+}
+
+template <typename OUT>
+__device__ __forceinline__ void store4(const ssm_matmul_fp8_args_t &a, int64_t m, int64_t n, f4 v, bool wide) {
+    if (m >= a.m || n >= a.n) return;
+    const int64_t at = m * a.n + n;
+    if (wide) {
+        if constexpr (OUT::bytes == 2)
+            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.y) + at) =
+                make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+        else
+            *reinterpret_cast<f4 *>(static_cast<float *>(a.y) + at) = v;
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (n + i < a.n) store_io<OUT>(a.y, at + i, v[i]);
+}
+
+// ---------------------------------------------------------------------------------- few rows
+// Up to 16 MT rows: w is read once, straight into registers.  A workgroup owns 16 rows of w; its waves
+// share out the blocks of K and add their sums up in LDS.
+constexpr int kSkinnyWaves = 4;
+
+template <typename OUT, int MT>
+__global__ __launch_bounds__(64 * kSkinnyWaves) void skinny_kernel(ssm_matmul_fp8_args_t a, int blocks, bool wide) {
+    __shared__ __attribute__((aligned(16))) f4 part[kSkinnyWaves][MT][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r16 = lane % 16, grp = lane / 16;
+    const int64_t n0 = (int64_t)blockIdx.x * 16;
+    const char *w = static_cast<const char *>(a.wq) + std::min<int64_t>(n0 + r16, a.n - 1) * a.k;
+    const float *sw = a.w_scales + n0 / 128 * blocks;
+    const char *x[MT];
+    const float *sx[MT];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+        const int64_t m = std::min<int64_t>(16 * t + r16, a.m - 1);
+        x[t] = static_cast<const char *>(a.xq) + m * a.k;
+        sx[t] = a.x_scales + m * blocks;
+    }
+    // 16 bytes at k, 0 behind the row's end
+    const auto piece = [&](const char *row, int64_t k) {
+        return k < a.k ? *reinterpret_cast<const i4 *>(row + k) : i4{0, 0, 0, 0};
+    };
+    f4 acc[MT] = {};
+    for (int j = wave; j < blocks; j += kSkinnyWaves) {
+        const int64_t k = 128 * (int64_t)j + 16 * grp;
+        const Operand<OUT> wv(piece(w, k), piece(w, k + 64));
+        const float s = sw[j];
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+            const f4 p = block_product(wv, Operand<OUT>(piece(x[t], k), piece(x[t], k + 64)));
+            const float st = s * sx[t][j];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[t][i] = __builtin_fmaf(p[i], st, acc[t][i]);
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < MT; ++t) part[wave][t][lane] = acc[t];
+    __syncthreads();
+    for (int t = wave; t < MT; t += kSkinnyWaves) {
+        f4 v = part[0][t][lane];
+#pragma unroll
+        for (int i = 1; i < kSkinnyWaves; ++i) v += part[i][t][lane];
+        store4<OUT>(a, 16 * t + r16, n0 + 4 * grp, v, wide);
+    }
+}
+
+// -------------------------------------------------------------------------------------- tiles
+__device__ const i4 kZeros[1] = {};
+
+typedef __attribute__((address_space(3))) void *lds_ptr;
+typedef const __attribute__((address_space(1))) void *global_ptr;
+
+// BM x BN of y a workgroup, WM x WN a wave (WN divides 128).  Both operands of a block of K go straight
+// from memory to LDS, 16 bytes a lane, one block ahead of the products.  A row's eight pieces of 16 bytes
+// are kept in the order piece ^ (row % 8), by the address each lane loads from, so that the 16 rows of an
+// operand are read without bank conflicts.
+template <typename OUT, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(BM / WM * (BN / WN) * 64) void tile_kernel(ssm_matmul_fp8_args_t a, int blocks, int tiles_m,
+                                                                       int tiles_n, bool wide) {
+    constexpr int WAVES = BM / WM * (BN / WN), MT = WM / 16, NT = WN / 16;
+    constexpr int LOADS = (BM + BN) / 8 / WAVES;  // of 8 rows each
+    __shared__ __attribute__((aligned(1024))) char lds[2][(BM + BN) * 128];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r16 = lane % 16, grp = lane / 16;
+    // Tiles by XCD (workgroups are dealt out to the 8 in turn): each takes a run of tiles, in columns of up
+    // to 8 rows of tiles, so that the tiles it works on at one time share rows of x and w in its L2.
+    const int total = tiles_m * tiles_n, xcd = blockIdx.x % 8, each = total / 8, more = total % 8;
+    const int id = xcd * each + std::min(xcd, more) + (int)blockIdx.x / 8;
+    const int band = id / (8 * tiles_n), high = std::min(8, tiles_m - 8 * band), in = id - band * 8 * tiles_n;
+    const int64_t m0 = (int64_t)(8 * band + in % high) * BM, n0 = (int64_t)(in / high) * BN;
+
+    const char *src[LOADS];
+    const int piece = 16 * (lane % 8 ^ lane / 8);
+#pragma unroll
+    for (int j = 0; j < LOADS; ++j) {
+        const int row = 8 * (wave * LOADS + j) + lane / 8;
+        const bool of_x = row < BM;
+        const int64_t r = of_x ? std::min<int64_t>(m0 + row, a.m - 1) : std::min<int64_t>(n0 + row - BM, a.n - 1);
+        src[j] = static_cast<const char *>(of_x ? a.xq : a.wq) + r * a.k + piece;
+    }
+    const int wm = wave / (BN / WN) * WM, wn = wave % (BN / WN) * WN;
+    const float *sx[MT];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) sx[t] = a.x_scales + std::min<int64_t>(m0 + wm + 16 * t + r16, a.m - 1) * blocks;
+    const float *sw = a.w_scales + std::min<int64_t>(n0 + wn, a.n - 1) / 128 * blocks;
+
+    const auto fetch = [&](int j, int buf) {
+        const bool whole = 128 * (int64_t)(j + 1) <= a.k;
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) {
+            const char *from = src[i] + 128 * (int64_t)j;
+            if (!whole && 128 * (int64_t)j + piece >= a.k) from = reinterpret_cast<const char *>(kZeros);
+            __builtin_amdgcn_global_load_lds((global_ptr)from, (lds_ptr)(lds[buf] + (wave * LOADS + i) * 1024), 16, 0, 0);
+        }
+    };
+    f4 acc[MT][NT] = {};
+    float next[MT], next_w;
+#pragma unroll
+    for (int t = 0; t < MT; ++t) next[t] = sx[t][0];
+    next_w = sw[0];
+    fetch(0, 0);
+    for (int j = 0; j < blocks; ++j) {
+        const char *buf = lds[j % 2];
+        __builtin_amdgcn_s_waitcnt(0);  // this wave's loads have landed; the barrier: everyone's
+        __syncthreads();
+        float s[MT];
+#pragma unroll
+        for (int t = 0; t < MT; ++t) s[t] = next[t] * next_w;
+        if (j + 1 < blocks) {
+#pragma unroll
+            for (int t = 0; t < MT; ++t) next[t] = sx[t][j + 1];
+            next_w = sw[j + 1];
+            fetch(j + 1, (j + 1) % 2);
+        }
+        const auto operand = [&](int row) {
+            const char *at = buf + row * 128;
+            return Operand<OUT>(*reinterpret_cast<const i4 *>(at + 16 * (grp ^ row % 8)),
+                                *reinterpret_cast<const i4 *>(at + 16 * ((grp + 4) ^ row % 8)));
+        };
+        Operand<OUT> x[MT];
+#pragma unroll
+        for (int t = 0; t < MT; ++t) x[t] = operand(wm + 16 * t + r16);
+#pragma unroll
+        for (int u = 0; u < NT; ++u) {
+            const Operand<OUT> w = operand(BM + wn + 16 * u + r16);
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+                const f4 p = block_product(w, x[t]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[t][u][i] = __builtin_fmaf(p[i], s[t], acc[t][u][i]);
+            }
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int u = 0; u < NT; ++u)
+            store4<OUT>(a, m0 + wm + 16 * t + r16, n0 + wn + 16 * u + 4 * grp, acc[t][u], wide);
+}
+
+template <typename OUT>
+void launch(const ssm_matmul_fp8_args_t &a, hipStream_t stream) {
+    const int blocks = (int)((a.k + 127) / 128);
+    const bool wide = a.n % 4 == 0 && reinterpret_cast<uintptr_t>(a.y) % (4 * OUT::bytes) == 0;
+    if (a.m <= 64) {
+        const unsigned grid = (unsigned)((a.n + 15) / 16), threads = 64 * kSkinnyWaves;
+        if (a.m <= 16) skinny_kernel<OUT, 1><<<grid, threads, 0, stream>>>(a, blocks, wide);
+        else if (a.m <= 32) skinny_kernel<OUT, 2><<<grid, threads, 0, stream>>>(a, blocks, wide);
+        else skinny_kernel<OUT, 4><<<grid, threads, 0, stream>>>(a, blocks, wide);
+        return;
+    }
+    const auto tiles = [&](int64_t bm, int64_t bn) { return ((a.m + bm - 1) / bm) * ((a.n + bn - 1) / bn); };
+    if (tiles(256, 256) >= 256) {
+        tile_kernel<OUT, 256, 256, 64, 128><<<(unsigned)tiles(256, 256), 512, 0, stream>>>(
+            a, blocks, (int)((a.m + 255) / 256), (int)((a.n + 255) / 256), wide);
+    } else if (tiles(128, 128) >= 256) {
+        tile_kernel<OUT, 128, 128, 64, 64><<<(unsigned)tiles(128, 128), 256, 0, stream>>>(
+            a, blocks, (int)((a.m + 127) / 128), (int)((a.n + 127) / 128), wide);
+    } else {
+        tile_kernel<OUT, 64, 64, 32, 32><<<(unsigned)tiles(64, 64), 256, 0, stream>>>(
+            a, blocks, (int)((a.m + 63) / 64), (int)((a.n + 63) / 64), wide);
+    }
+}
+
+}  // namespace
+
+hipError_t launch_matmul_fp8(const ssm_matmul_fp8_args_t &a, hipStream_t stream) {
+    if (a.out_dtype == SSM_BF16)
+        launch<io_bf16>(a, stream);
+    else
+        launch<io_f32>(a, stream);
+    return hipGetLastError();
+}
+
+}  // namespace ssm

@@ -1009,3 +1009,306 @@ ssm_status_t ssm_gated_rmsnorm_bwd(const ssm_gated_norm_bwd_args_t *a, void *str
 }
 
 }  // extern "C"
+
+// --------------------------------------------------------------------- gated delta rule
+namespace {
+
+struct DeltaSizes {
+    int64_t B, L, Hk, H, K, V;
+    int32_t io, l2norm;
+    float scale;
+};
+
+ssm_status_t check_delta(const DeltaSizes &z) {
+    if (!io_ok(z.io)) return fail(SSM_ERR_BAD_DTYPE, "io_dtype %d is not SSM_F32 or SSM_BF16", z.io);
+    if (z.B < 0 || z.L < 0)
+        return fail(SSM_ERR_BAD_SHAPE, "negative batch (%lld) or seqlen (%lld)", (long long)z.B, (long long)z.L);
+    if (z.Hk < 1 || z.H < 1 || z.K < 1 || z.V < 1)
+        return fail(SSM_ERR_BAD_SHAPE, "kheads, heads, kdim and vdim must be >= 1");
+    if (z.H % z.Hk != 0)
+        return fail(SSM_ERR_BAD_SHAPE, "kheads (%lld) must divide heads (%lld)", (long long)z.Hk, (long long)z.H);
+    if (z.K > SSM_DELTA_MAX_KDIM || z.K % 8 != 0)
+        return fail(SSM_ERR_UNSUPPORTED, "kdim %lld is not a multiple of 8 up to %d", (long long)z.K,
+                    SSM_DELTA_MAX_KDIM);
+    if (z.V > SSM_DELTA_MAX_VDIM || z.V % 8 != 0)
+        return fail(SSM_ERR_UNSUPPORTED, "vdim %lld is not a multiple of 8 up to %d", (long long)z.V,
+                    SSM_DELTA_MAX_VDIM);
+    if (z.H > 65535 || z.B > 65535)
+        return fail(SSM_ERR_UNSUPPORTED, "heads (%lld) and batch (%lld) go up to 65535", (long long)z.H, (long long)z.B);
+    if (z.L >= (int64_t)1 << 30) return fail(SSM_ERR_UNSUPPORTED, "seqlen %lld is not below 2^30", (long long)z.L);
+    if (z.l2norm != 0 && z.l2norm != 1) return fail(SSM_ERR_UNSUPPORTED, "l2norm must be 0 or 1");
+    if (!(z.scale - z.scale == 0.0f)) return fail(SSM_ERR_BAD_SHAPE, "scale must be finite");
+    // the largest arrays: checkpoints and the backward's workspace, below 2^60 bytes
+    const int64_t chunks = z.L / SSM_DELTA_CHUNK + 1;
+    if (!mul_ok(z.B * z.H, chunks, ((int64_t)1 << 21))) return fail(SSM_ERR_BAD_SHAPE, "sizes overflow");
+    return SSM_OK;
+}
+
+int64_t delta_chunks(int64_t L) { return (L + SSM_DELTA_CHUNK - 1) / SSM_DELTA_CHUNK; }
+
+// The tensor of one of q, k, v: B x L steps of `width` consecutive elements.
+struct Steps {
+    const void *p;
+    int64_t token, batch, width, es;
+    const char *name;
+    bool wide;  // read 16 bytes at a time
+};
+
+// Fills in the strides of a dense tensor and checks those given; `out`: what the tensor spans.
+ssm_status_t check_steps(Steps s, int64_t B, int64_t L, Range &out) {
+    if (s.token == 0) {
+        s.token = s.width;
+        s.batch = L * s.width;
+    }
+    const int64_t most = (int64_t)1 << 40;
+    if (s.token < 0 || s.batch < 0 || s.token > most || s.batch > most)
+        return fail(SSM_ERR_BAD_SHAPE, "%s has a stride that is negative or above 2^40", s.name);
+    if (!mul_ok(L, s.token, 16) || !mul_ok(B, s.batch, 16)) return fail(SSM_ERR_BAD_SHAPE, "sizes overflow");
+    if (s.wide && (!aligned(s.p, 16) || (L > 1 && s.token * s.es % 16 != 0) || (B > 1 && s.batch * s.es % 16 != 0)))
+        return fail(SSM_ERR_ALIGN, "%s does not lie at 16-byte boundaries", s.name);
+    out = range(s.p, B > 0 && L > 0 ? (B - 1) * s.batch + (L - 1) * s.token + s.width : 0, s.es, s.name);
+    return SSM_OK;
+}
+
+template <typename A>
+DeltaSizes delta_sizes(const A &a, int64_t L) {
+    return {a.batch, L, a.kheads, a.heads, a.kdim, a.vdim, a.io_dtype, a.l2norm, a.scale};
+}
+
+struct Named {
+    const void *p;
+    const char *name;
+};
+
+ssm_status_t check_required(const Named *req, int n) {
+    for (int i = 0; i < n; ++i)
+        if (!req[i].p) return fail(SSM_ERR_NULL_ARG, "%s is NULL", req[i].name);
+    return SSM_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t ssm_gated_delta_workspace_size(const ssm_gated_delta_args_t *a) {
+    if (!a) return (size_t)-1;
+    DeltaSizes z = delta_sizes(*a, a->seqlen);
+    z.scale = 1.0f;
+    z.l2norm = 0;
+    if (check_delta(z) != SSM_OK) return (size_t)-1;
+    return a->batch > 0 && a->seqlen > 0 ? ssm::gated_delta_workspace_bytes(*a) : 0;
+}
+
+ssm_status_t ssm_gated_delta_fwd(const ssm_gated_delta_args_t *a, void *stream) {
+    if (!a) return fail(SSM_ERR_NULL_ARG, "args is NULL");
+    ssm_status_t s = check_delta(delta_sizes(*a, a->seqlen));
+    if (s != SSM_OK) return s;
+    const int64_t B = a->batch, L = a->seqlen, H = a->heads, K = a->kdim, V = a->vdim, es = io_bytes(a->io_dtype);
+    const bool work = B > 0 && L > 0;
+    if (work) {
+        const Named req[] = {{a->q, "q"}, {a->k, "k"}, {a->v, "v"}, {a->g, "g"}, {a->beta, "beta"}, {a->o, "o"}};
+        if ((s = check_required(req, COUNT(req))) != SSM_OK) return s;
+    }
+    const void *io[] = {a->q, a->k, a->v, a->beta, a->o};
+    const void *f[] = {a->g, a->h0, a->h_final, a->checkpoints};
+    if ((s = check_align(io, COUNT(io), es, f, COUNT(f))) != SSM_OK) return s;
+    if (!aligned(a->checkpoints, 16)) return fail(SSM_ERR_ALIGN, "checkpoints are not 16-byte aligned");
+    Range rq, rk, rv;
+    if ((s = check_steps({a->q, a->q_token, a->q_batch, a->kheads * K, es, "q", true}, B, L, rq)) != SSM_OK ||
+        (s = check_steps({a->k, a->k_token, a->k_batch, a->kheads * K, es, "k", true}, B, L, rk)) != SSM_OK ||
+        (s = check_steps({a->v, a->v_token, a->v_batch, H * V, es, "v", false}, B, L, rv)) != SSM_OK)
+        return s;
+    const size_t need = work ? ssm::gated_delta_workspace_bytes(*a) : 0;
+    if ((s = check_workspace(a->workspace, a->workspace_bytes, need)) != SSM_OK) return s;
+    const int64_t state = B * H * K * V;
+    const Range in[] = {rq, rk, rv, range(a->g, B * L * H, 4, "g"), range(a->beta, B * L * H, es, "beta"),
+                        range(a->reset, B * L, 1, "reset"), range(a->h0, state, 4, "h0")};
+    const Range out[] = {range(a->o, B * L * H * V, es, "o"), range(a->h_final, state, 4, "h_final"),
+                         range(a->checkpoints, delta_chunks(L) * B * H * (K + SSM_DELTA_CHUNK) * V, 4, "checkpoints")};
+    const Range ws = range(need ? a->workspace : nullptr, (int64_t)need, 1, "workspace");
+    if ((s = check_overlaps(in, COUNT(in), out, COUNT(out), ws)) != SSM_OK) return s;
+    if (B == 0) return ok();
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    hipError_t e = hipSuccess;
+    if (L > 0)
+        e = ssm::launch_gated_delta_fwd(*a, st);
+    else if (a->h_final)
+        e = ssm::launch_copy_or_zero(a->h_final, a->h0, state, st);
+    if (e != hipSuccess) return fail(SSM_ERR_HIP, "HIP error: %s", hipGetErrorString(e));
+    return ok();
+}
+
+size_t ssm_gated_delta_bwd_workspace_size(const ssm_gated_delta_bwd_args_t *a) {
+    if (!a) return (size_t)-1;
+    DeltaSizes z = delta_sizes(*a, a->seqlen);
+    z.scale = 1.0f;
+    z.l2norm = 0;
+    if (check_delta(z) != SSM_OK) return (size_t)-1;
+    return a->batch > 0 && a->seqlen > 0 ? ssm::gated_delta_bwd_workspace_bytes(*a) : 0;
+}
+
+ssm_status_t ssm_gated_delta_bwd(const ssm_gated_delta_bwd_args_t *a, void *stream) {
+    if (!a) return fail(SSM_ERR_NULL_ARG, "args is NULL");
+    ssm_status_t s = check_delta(delta_sizes(*a, a->seqlen));
+    if (s != SSM_OK) return s;
+    const int64_t B = a->batch, L = a->seqlen, H = a->heads, K = a->kdim, V = a->vdim, es = io_bytes(a->io_dtype);
+    const bool work = B > 0 && L > 0;
+    if (work) {
+        const Named req[] = {{a->q, "q"}, {a->k, "k"}, {a->v, "v"}, {a->g, "g"}, {a->beta, "beta"}, {a->dout, "dout"},
+                             {a->dq, "dq"}, {a->dk, "dk"}, {a->dv, "dv"}, {a->dg, "dg"}, {a->dbeta, "dbeta"}};
+        if ((s = check_required(req, COUNT(req))) != SSM_OK) return s;
+    }
+    const void *io[] = {a->q, a->k, a->v, a->beta, a->dout, a->dq, a->dk, a->dv, a->dbeta};
+    const void *f[] = {a->g, a->h0, a->dh_final, a->checkpoints, a->dg, a->dh0};
+    if ((s = check_align(io, COUNT(io), es, f, COUNT(f))) != SSM_OK) return s;
+    if (!aligned(a->checkpoints, 16)) return fail(SSM_ERR_ALIGN, "checkpoints are not 16-byte aligned");
+    Range rq, rk, rv;
+    if ((s = check_steps({a->q, a->q_token, a->q_batch, a->kheads * K, es, "q", true}, B, L, rq)) != SSM_OK ||
+        (s = check_steps({a->k, a->k_token, a->k_batch, a->kheads * K, es, "k", true}, B, L, rk)) != SSM_OK ||
+        (s = check_steps({a->v, a->v_token, a->v_batch, H * V, es, "v", false}, B, L, rv)) != SSM_OK)
+        return s;
+    const size_t need = work ? ssm::gated_delta_bwd_workspace_bytes(*a) : 0;
+    if ((s = check_workspace(a->workspace, a->workspace_bytes, need)) != SSM_OK) return s;
+    const int64_t state = B * H * K * V, steps = B * L;
+    const Range in[] = {rq, rk, rv, range(a->g, steps * H, 4, "g"), range(a->beta, steps * H, es, "beta"),
+                        range(a->reset, steps, 1, "reset"), range(a->h0, state, 4, "h0"),
+                        range(a->dout, steps * H * V, es, "dout"), range(a->dh_final, state, 4, "dh_final"),
+                        range(a->checkpoints, delta_chunks(L) * B * H * (K + SSM_DELTA_CHUNK) * V, 4, "checkpoints")};
+    const Range out[] = {range(a->dq, steps * a->kheads * K, es, "dq"), range(a->dk, steps * a->kheads * K, es, "dk"),
+                         range(a->dv, steps * H * V, es, "dv"), range(a->dg, steps * H, 4, "dg"),
+                         range(a->dbeta, steps * H, es, "dbeta"), range(a->dh0, state, 4, "dh0")};
+    const Range ws = range(need ? a->workspace : nullptr, (int64_t)need, 1, "workspace");
+    if ((s = check_overlaps(in, COUNT(in), out, COUNT(out), ws)) != SSM_OK) return s;
+    if (B == 0) return ok();
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    hipError_t e = hipSuccess;
+    if (L > 0)
+        e = ssm::launch_gated_delta_bwd(*a, st);
+    else if (a->dh0)
+        e = ssm::launch_copy_or_zero(a->dh0, a->dh_final, state, st);
+    if (e != hipSuccess) return fail(SSM_ERR_HIP, "HIP error: %s", hipGetErrorString(e));
+    return ok();
+}
+
+ssm_status_t ssm_gated_delta_step(const ssm_gated_delta_step_args_t *a, void *stream) {
+    if (!a) return fail(SSM_ERR_NULL_ARG, "args is NULL");
+    ssm_status_t s = check_delta(delta_sizes(*a, 1));
+    if (s != SSM_OK) return s;
+    const int64_t B = a->batch, Hk = a->kheads, H = a->heads, K = a->kdim, V = a->vdim, es = io_bytes(a->io_dtype);
+    if (B == 0) return ok();
+    const Named req[] = {{a->state, "state"}, {a->q, "q"}, {a->k, "k"}, {a->v, "v"},
+                         {a->g, "g"}, {a->beta, "beta"}, {a->o, "o"}};
+    if ((s = check_required(req, COUNT(req))) != SSM_OK) return s;
+    const void *io[] = {a->q, a->k, a->v, a->beta, a->o};
+    const void *f[] = {a->g};
+    if ((s = check_align(io, COUNT(io), es, f, COUNT(f))) != SSM_OK) return s;
+    if (!aligned(a->state, 16)) return fail(SSM_ERR_ALIGN, "state is not 16-byte aligned");
+    Range rq, rk, rv;  // each batch row is a step here
+    if ((s = check_steps({a->q, a->q_batch, 0, Hk * K, es, "q", false}, 1, B, rq)) != SSM_OK ||
+        (s = check_steps({a->k, a->k_batch, 0, Hk * K, es, "k", false}, 1, B, rk)) != SSM_OK ||
+        (s = check_steps({a->v, a->v_batch, 0, H * V, es, "v", false}, 1, B, rv)) != SSM_OK)
+        return s;
+    const Range in[] = {rq, rk, rv, range(a->g, B * H, 4, "g"), range(a->beta, B * H, es, "beta"),
+                        range(a->reset, B, 1, "reset")};
+    const Range out[] = {range(a->state, B * H * K * V, 4, "state"), range(a->o, B * H * V, es, "o")};
+    if ((s = check_overlaps(in, COUNT(in), out, COUNT(out), range(nullptr, 0, 1, ""))) != SSM_OK) return s;
+    const hipError_t e = ssm::launch_gated_delta_step(*a, static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return fail(SSM_ERR_HIP, "HIP error: %s", hipGetErrorString(e));
+    return ok();
+}
+
+// ------------------------------------------------------------------------------ e4m3
+static ssm_status_t check_fp8_width(int64_t rows, int64_t D) {
+    if (rows < 0) return fail(SSM_ERR_BAD_SHAPE, "negative rows (%lld)", (long long)rows);
+    if (D < 1) return fail(SSM_ERR_BAD_SHAPE, "dim must be >= 1 (got %lld)", (long long)D);
+    if (D > kMaxWidth || D % 16 != 0)
+        return fail(SSM_ERR_UNSUPPORTED, "dim %lld is not a multiple of 16 up to 2^20", (long long)D);
+    // 16 blocks a workgroup of 256 threads, fewer than 2^32 threads a launch
+    const int64_t blocks = (D + SSM_FP8_BLOCK - 1) / SSM_FP8_BLOCK;
+    if (rows >= ((int64_t)1 << 28) / blocks)
+        return fail(SSM_ERR_UNSUPPORTED, "rows * ceil(dim / 128) is not below 2^28");
+    return SSM_OK;
+}
+
+ssm_status_t ssm_quantize_fp8(const ssm_quantize_fp8_args_t *a, void *stream) {
+    if (!a) return fail(SSM_ERR_NULL_ARG, "args is NULL");
+    if (!io_ok(a->io_dtype)) return fail(SSM_ERR_BAD_DTYPE, "io_dtype %d is not SSM_F32 or SSM_BF16", a->io_dtype);
+    ssm_status_t s = check_fp8_width(a->rows, a->dim);
+    if (s != SSM_OK) return s;
+    if (a->block_rows != 1 && a->block_rows != SSM_FP8_BLOCK)
+        return fail(SSM_ERR_UNSUPPORTED, "block_rows must be 1 or %d", SSM_FP8_BLOCK);
+    if (a->rows == 0) return ok();
+    const Named req[] = {{a->x, "x"}, {a->q, "q"}, {a->scales, "scales"}};
+    if ((s = check_required(req, COUNT(req))) != SSM_OK) return s;
+    const int64_t n = a->rows * a->dim, es = io_bytes(a->io_dtype);
+    const void *io[] = {a->x}, *f[] = {a->scales};
+    if ((s = check_align(io, 1, es, f, 1)) != SSM_OK) return s;
+    if (!aligned(a->q, 16)) return fail(SSM_ERR_ALIGN, "q is not 16-byte aligned");
+    const Range in[] = {range(a->x, n, es, "x")};
+    const int64_t blocks = (a->rows + a->block_rows - 1) / a->block_rows * ((a->dim + 127) / 128);
+    const Range out[] = {range(a->q, n, 1, "q"), range(a->scales, blocks, 4, "scales")};
+    if ((s = check_overlaps(in, 1, out, COUNT(out), range(nullptr, 0, 1, ""))) != SSM_OK) return s;
+    const hipError_t e = ssm::launch_quantize_fp8(*a, static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return fail(SSM_ERR_HIP, "HIP error: %s", hipGetErrorString(e));
+    return ok();
+}
+
+ssm_status_t ssm_add_rmsnorm_fp8(const ssm_add_norm_fp8_args_t *p, void *stream) {
+    if (!p) return fail(SSM_ERR_NULL_ARG, "args is NULL");
+    const ssm_add_norm_args_t *a = &p->norm;
+    if (!io_ok(a->io_dtype) || !io_ok(a->res_dtype))
+        return fail(SSM_ERR_BAD_DTYPE, "io_dtype (%d) and res_dtype (%d) must be SSM_F32 or SSM_BF16", a->io_dtype,
+                    a->res_dtype);
+    ssm_status_t s = check_norm(a->rows, a->dim, a->eps);
+    if (s == SSM_OK) s = check_fp8_width(a->rows, a->dim);
+    if (s != SSM_OK) return s;
+    if (a->y) return fail(SSM_ERR_BAD_SHAPE, "y must be NULL: the norm's output is q");
+    if (a->rows == 0) return ok();
+    const Named req[] = {{a->x, "x"}, {a->w, "w"}, {p->q, "q"}, {p->scales, "scales"}};
+    if ((s = check_required(req, COUNT(req))) != SSM_OK) return s;
+    const int64_t D = a->dim, n = a->rows * D, es = io_bytes(a->io_dtype), rs = io_bytes(a->res_dtype);
+    const void *io[] = {a->x}, *res[] = {a->residual, a->res_out}, *f[] = {a->scale, a->post_w, a->w, p->scales};
+    if ((s = check_align(io, COUNT(io), es, f, COUNT(f))) != SSM_OK) return s;
+    if ((s = check_align(res, COUNT(res), rs, nullptr, 0)) != SSM_OK) return s;
+    if (!aligned(p->q, 16)) return fail(SSM_ERR_ALIGN, "q is not 16-byte aligned");
+    const Range in[] = {range(a->x, n, es, "x"), range(a->residual, n, rs, "residual"),
+                        range(a->scale, D, 4, "scale"), range(a->post_w, D, 4, "post_w"), range(a->w, D, 4, "w")};
+    const Range out[] = {range(a->res_out, n, rs, "res_out"), range(p->q, n, 1, "q"),
+                         range(p->scales, a->rows * ((D + 127) / 128), 4, "scales")};
+    s = check_overlaps(in, COUNT(in), out, COUNT(out), range(nullptr, 0, 1, ""), SameOk{a->res_out, a->residual});
+    if (s != SSM_OK) return s;
+    const hipError_t e = ssm::launch_add_norm_fp8(*p, static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return fail(SSM_ERR_HIP, "HIP error: %s", hipGetErrorString(e));
+    return ok();
+}
+
+ssm_status_t ssm_matmul_fp8(const ssm_matmul_fp8_args_t *a, void *stream) {
+    if (!a) return fail(SSM_ERR_NULL_ARG, "args is NULL");
+    if (!io_ok(a->out_dtype)) return fail(SSM_ERR_BAD_DTYPE, "out_dtype %d is not SSM_F32 or SSM_BF16", a->out_dtype);
+    const int64_t M = a->m, N = a->n, K = a->k;
+    if (M < 0 || N < 1 || K < 1)
+        return fail(SSM_ERR_BAD_SHAPE, "sizes m %lld, n %lld, k %lld", (long long)M, (long long)N, (long long)K);
+    if (K % 16 != 0 || K > kMaxWidth)
+        return fail(SSM_ERR_UNSUPPORTED, "k %lld is not a multiple of 16 up to 2^20", (long long)K);
+    // a workgroup of 512 threads per 256 x 256 of y, fewer than 2^32 threads a launch
+    if (N >= (int64_t)1 << 24 || M >= (int64_t)1 << 31 || !mul_ok(M + 256, N + 256) ||
+        (M + 255) / 256 * ((N + 255) / 256) >= (int64_t)1 << 22)
+        return fail(SSM_ERR_UNSUPPORTED, "n is not below 2^24, or ceil(m / 256) * ceil(n / 256) not below 2^22");
+    if (M == 0) return ok();
+    ssm_status_t s;
+    const Named req[] = {{a->xq, "xq"}, {a->x_scales, "x_scales"}, {a->wq, "wq"}, {a->w_scales, "w_scales"}, {a->y, "y"}};
+    if ((s = check_required(req, COUNT(req))) != SSM_OK) return s;
+    const int64_t es = io_bytes(a->out_dtype), blocks = (K + 127) / 128;
+    const void *io[] = {a->y}, *f[] = {a->x_scales, a->w_scales};
+    if ((s = check_align(io, 1, es, f, COUNT(f))) != SSM_OK) return s;
+    if (!aligned(a->xq, 16) || !aligned(a->wq, 16)) return fail(SSM_ERR_ALIGN, "xq or wq is not 16-byte aligned");
+    const Range in[] = {range(a->xq, M * K, 1, "xq"), range(a->x_scales, M * blocks, 4, "x_scales"),
+                        range(a->wq, N * K, 1, "wq"), range(a->w_scales, (N + 127) / 128 * blocks, 4, "w_scales")};
+    const Range out[] = {range(a->y, M * N, es, "y")};
+    if ((s = check_overlaps(in, COUNT(in), out, 1, range(nullptr, 0, 1, ""))) != SSM_OK) return s;
+    const hipError_t e = ssm::launch_matmul_fp8(*a, static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return fail(SSM_ERR_HIP, "HIP error: %s", hipGetErrorString(e));
+    return ok();
+}
+
+}  // extern "C"

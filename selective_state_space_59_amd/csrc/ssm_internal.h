@@ -77,6 +77,18 @@ hipError_t launch_gated_norm_fwd(const ssm_gated_norm_args_t &a, hipStream_t str
 size_t gated_norm_bwd_workspace_bytes(const ssm_gated_norm_bwd_args_t &a);
 hipError_t launch_gated_norm_bwd(const ssm_gated_norm_bwd_args_t &a, hipStream_t stream);
 
+// Gated delta rule (gated_delta.hip, gated_delta_bwd.hip): batch, seqlen > 0; the step batch > 0.
+size_t gated_delta_workspace_bytes(const ssm_gated_delta_args_t &a);
+hipError_t launch_gated_delta_fwd(const ssm_gated_delta_args_t &a, hipStream_t stream);
+size_t gated_delta_bwd_workspace_bytes(const ssm_gated_delta_bwd_args_t &a);
+hipError_t launch_gated_delta_bwd(const ssm_gated_delta_bwd_args_t &a, hipStream_t stream);
+hipError_t launch_gated_delta_step(const ssm_gated_delta_step_args_t &a, hipStream_t stream);
+
+// e4m3 with block scales (quant_fp8.hip, matmul_fp8.hip): rows, m > 0.
+hipError_t launch_quantize_fp8(const ssm_quantize_fp8_args_t &a, hipStream_t stream);
+hipError_t launch_add_norm_fp8(const ssm_add_norm_fp8_args_t &a, hipStream_t stream);
+hipError_t launch_matmul_fp8(const ssm_matmul_fp8_args_t &a, hipStream_t stream);
+
 // Copy or zero-fill the final state for an empty (L == 0) scan.
 hipError_t launch_empty_scan_state(const ssm_scan_args_t &a, hipStream_t stream);
 

@@ -45,7 +45,9 @@ EXPORTED_SYMBOLS = ("ssm_selective_scan_workspace_size", "ssm_selective_scan_fwd
                     "ssm_gated_scan_bwd_workspace_size", "ssm_gated_scan_bwd", "ssm_gated_scan_step",
                     "ssm_add_rmsnorm_fwd", "ssm_add_rmsnorm_bwd_workspace_size", "ssm_add_rmsnorm_bwd",
                     "ssm_gated_rmsnorm_fwd", "ssm_gated_rmsnorm_bwd_workspace_size",
-                    "ssm_gated_rmsnorm_bwd")
+                    "ssm_gated_rmsnorm_bwd", "ssm_gated_delta_workspace_size", "ssm_gated_delta_fwd",
+                    "ssm_gated_delta_bwd_workspace_size", "ssm_gated_delta_bwd", "ssm_gated_delta_step",
+                    "ssm_quantize_fp8", "ssm_add_rmsnorm_fp8", "ssm_matmul_fp8")
 NOALLOC_SCRATCH_BYTES = 32 << 20
 
 _P = ctypes.c_void_p
@@ -168,6 +170,52 @@ class GatedNormBwdArgs(ctypes.Structure):
                 ("workspace", _P), ("workspace_bytes", ctypes.c_size_t), ("eps", ctypes.c_float)]
 
 
+class GatedDeltaArgs(ctypes.Structure):
+    """Mirror of ssm_gated_delta_args_t."""
+    _fields_ = [("batch", _I64), ("seqlen", _I64), ("kheads", _I64), ("heads", _I64), ("kdim", _I64),
+                ("vdim", _I64), ("io_dtype", _I32), ("l2norm", _I32), ("q", _P), ("k", _P), ("v", _P), ("g", _P),
+                ("beta", _P), ("reset", _P), ("h0", _P), ("o", _P), ("h_final", _P), ("checkpoints", _P),
+                ("q_token", _I64), ("q_batch", _I64), ("k_token", _I64), ("k_batch", _I64), ("v_token", _I64),
+                ("v_batch", _I64), ("workspace", _P), ("workspace_bytes", ctypes.c_size_t),
+                ("scale", ctypes.c_float)]
+
+
+class GatedDeltaBwdArgs(ctypes.Structure):
+    """Mirror of ssm_gated_delta_bwd_args_t."""
+    _fields_ = [("batch", _I64), ("seqlen", _I64), ("kheads", _I64), ("heads", _I64), ("kdim", _I64),
+                ("vdim", _I64), ("io_dtype", _I32), ("l2norm", _I32), ("q", _P), ("k", _P), ("v", _P), ("g", _P),
+                ("beta", _P), ("reset", _P), ("h0", _P), ("dout", _P), ("dh_final", _P), ("checkpoints", _P),
+                ("dq", _P), ("dk", _P), ("dv", _P), ("dg", _P), ("dbeta", _P), ("dh0", _P),
+                ("q_token", _I64), ("q_batch", _I64), ("k_token", _I64), ("k_batch", _I64), ("v_token", _I64),
+                ("v_batch", _I64), ("workspace", _P), ("workspace_bytes", ctypes.c_size_t),
+                ("scale", ctypes.c_float)]
+
+
+class GatedDeltaStepArgs(ctypes.Structure):
+    """Mirror of ssm_gated_delta_step_args_t."""
+    _fields_ = [("batch", _I64), ("kheads", _I64), ("heads", _I64), ("kdim", _I64), ("vdim", _I64),
+                ("io_dtype", _I32), ("l2norm", _I32), ("state", _P), ("q", _P), ("k", _P), ("v", _P), ("g", _P),
+                ("beta", _P), ("reset", _P), ("o", _P), ("q_batch", _I64), ("k_batch", _I64), ("v_batch", _I64),
+                ("scale", ctypes.c_float)]
+
+
+class QuantizeFp8Args(ctypes.Structure):
+    """Mirror of ssm_quantize_fp8_args_t."""
+    _fields_ = [("rows", _I64), ("dim", _I64), ("block_rows", _I64), ("io_dtype", _I32), ("x", _P), ("q", _P),
+                ("scales", _P)]
+
+
+class AddNormFp8Args(ctypes.Structure):
+    """Mirror of ssm_add_norm_fp8_args_t."""
+    _fields_ = [("norm", AddNormArgs), ("q", _P), ("scales", _P)]
+
+
+class MatmulFp8Args(ctypes.Structure):
+    """Mirror of ssm_matmul_fp8_args_t."""
+    _fields_ = [("m", _I64), ("n", _I64), ("k", _I64), ("out_dtype", _I32), ("xq", _P), ("x_scales", _P),
+                ("wq", _P), ("w_scales", _P), ("y", _P)]
+
+
 class SSMError(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__(message)
@@ -222,11 +270,15 @@ def lib() -> ctypes.CDLL:
         for name, args in (("gated_scan_fwd", GatedScanArgs), ("gated_scan_bwd", GatedScanBwdArgs),
                            ("gated_scan_step", GatedStepArgs), ("add_rmsnorm_fwd", AddNormArgs),
                            ("add_rmsnorm_bwd", AddNormBwdArgs), ("gated_rmsnorm_fwd", GatedNormArgs),
-                           ("gated_rmsnorm_bwd", GatedNormBwdArgs)):
+                           ("gated_rmsnorm_bwd", GatedNormBwdArgs), ("gated_delta_fwd", GatedDeltaArgs),
+                           ("gated_delta_bwd", GatedDeltaBwdArgs), ("gated_delta_step", GatedDeltaStepArgs),
+                           ("quantize_fp8", QuantizeFp8Args), ("add_rmsnorm_fp8", AddNormFp8Args),
+                           ("matmul_fp8", MatmulFp8Args)):
             f = getattr(L, "ssm_" + name)
             f.argtypes, f.restype = [ctypes.POINTER(args), _P], ctypes.c_int
         for name, args in (("gated_scan", GatedScanArgs), ("gated_scan_bwd", GatedScanBwdArgs),
-                           ("add_rmsnorm_bwd", AddNormBwdArgs), ("gated_rmsnorm_bwd", GatedNormBwdArgs)):
+                           ("add_rmsnorm_bwd", AddNormBwdArgs), ("gated_rmsnorm_bwd", GatedNormBwdArgs),
+                           ("gated_delta", GatedDeltaArgs), ("gated_delta_bwd", GatedDeltaBwdArgs)):
             f = getattr(L, "ssm_%s_workspace_size" % name)
             f.argtypes, f.restype = [ctypes.POINTER(args)], ctypes.c_size_t
         _lib = L
@@ -1304,3 +1356,302 @@ def gated_rmsnorm(x: torch.Tensor, z: torch.Tensor, w: torch.Tensor, groups: int
     """The gated norm as a differentiable torch op (arguments as in gated_rmsnorm_fwd).  A captured
     backward(): as with gated_scan."""
     return _GatedNormFn.apply(x, z, w, groups, gate_first, eps)
+
+
+# ------------------------------------------------------------------------- gated delta rule
+DELTA_CHUNK = 64  # SSM_DELTA_CHUNK
+
+
+def gated_delta_checkpoint_shape(batch: int, seqlen: int, heads: int, kdim: int, vdim: int) -> tuple:
+    """Shape of the fp32 checkpoint tensor of gated_delta_fwd: for every chunk of DELTA_CHUNK steps the
+    state entering it and the errors e_t of its steps, (ceil(L / DELTA_CHUNK), B, H, K + DELTA_CHUNK, V)."""
+    return ((seqlen + DELTA_CHUNK - 1) // DELTA_CHUNK, batch, heads, kdim + DELTA_CHUNK, vdim)
+
+
+def _steps(a, t, name, shape, dtype, dev):
+    """Put a (..., heads, channels) tensor that may be part of a wider one into `a`: its address, and its
+    strides where it is not dense."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == dev.index and t.is_contiguous():
+            setattr(a, name, t.data_ptr())
+            return
+    except AttributeError:
+        pass
+    if t is None:
+        raise ValueError("%s is required" % name)
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.shape == shape and t.numel() and t.stride(-1) == 1 and (shape[-2] == 1 or t.stride(-2) == shape[-1]):
+        width = shape[-2] * shape[-1]
+        batch = t.stride(0)
+        if len(shape) == 3:
+            if shape[0] == 1:
+                batch = 0  # dense: there is no second row
+            if (shape[0] == 1 or batch >= width) and t.dtype is dtype and t.device == dev:
+                setattr(a, name, t.data_ptr())
+                setattr(a, name + "_batch", batch)
+                return
+        else:
+            token = t.stride(1) if shape[1] > 1 else width
+            if shape[0] == 1:
+                batch = 0
+            if token >= width and (shape[0] == 1 or batch >= width) and t.dtype is dtype and t.device == dev:
+                setattr(a, name, t.data_ptr())
+                setattr(a, name + "_token", token)
+                setattr(a, name + "_batch", batch)
+                return
+    _opt(t, name, shape, dtype, dev)
+
+
+def _delta(a, q, k, v, g, beta, scale, l2norm, dev):
+    """Check the inputs of a gated delta call against q and v and put them into `a`."""
+    if not isinstance(v, torch.Tensor) or v.dim() != q.dim():
+        raise ValueError("v must be a tensor of %d dimensions like q" % q.dim())
+    lead, io = q.shape[:-2], q.dtype
+    a.kheads, a.kdim = q.shape[-2:]
+    a.heads, a.vdim = H, V = v.shape[-2:]
+    a.io_dtype, a.l2norm = _io_code(io), int(bool(l2norm))
+    a.scale = q.shape[-1] ** -0.5 if scale is None else float(scale)
+    _steps(a, q, "q", q.shape, io, dev)
+    _steps(a, k, "k", q.shape, io, dev)
+    _steps(a, v, "v", (*lead, H, V), io, dev)
+    a.g = _need(g, "g", (*lead, H), torch.float32, dev)
+    a.beta = _need(beta, "beta", (*lead, H), io, dev)
+
+
+def _delta_q(q):
+    dev = _gpu(q, "q", 4, "(B, L, Hk, K)")
+    if q.shape[-1] < 1 or q.shape[-2] < 1:
+        raise ValueError("q must have heads and channels")
+    return dev
+
+
+def gated_delta_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor,
+                    scale: Optional[float] = None, l2norm: bool = False, reset: Optional[torch.Tensor] = None,
+                    h0: Optional[torch.Tensor] = None, return_final_state: bool = False,
+                    o: Optional[torch.Tensor] = None, h_final: Optional[torch.Tensor] = None,
+                    checkpoints: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
+    """ssm_gated_delta_fwd: per value head, S' = exp(g_t) S, e_t = v_t - S'^T k_t,
+    S = S' + beta_t k_t e_t^T, o_t = scale S^T q_t.  q, k: (B, L, Hk, K); v: (B, L, H, V), bf16 or fp32,
+    dense or parts of a wider tensor (steps and rows any distance apart); Hk divides H; g: (B, L, H) fp32
+    log decays; beta: (B, L, H) in q's dtype; scale: K ** -0.5 unless given; l2norm: q and k are divided by
+    their norms first; reset: (B, L) uint8 or bool; h0: (B, H, K, V) fp32.
+
+    Returns (o, h_final or None).  A float32 tensor `checkpoints` of gated_delta_checkpoint_shape(B, L, H,
+    K, V) also receives what gated_delta_bwd needs of the states."""
+    dev = _delta_q(q)
+    B, L = q.shape[:2]
+    f32 = torch.float32
+    given = (o, h_final, checkpoints)
+    a = GatedDeltaArgs(batch=B, seqlen=L)
+    _delta(a, q, k, v, g, beta, scale, l2norm, dev)
+    H, K, V = a.heads, a.kdim, a.vdim
+    if reset is not None:
+        a.reset = _resets(reset, (B, L), dev)
+    if h0 is not None:
+        a.h0 = _arg(h0, "h0", (B, H, K, V), f32, dev)
+    if o is None:
+        o = torch.empty((B, L, H, V), device=dev, dtype=q.dtype)
+        a.o = o.data_ptr()
+    else:
+        a.o = _need(o, "o", (B, L, H, V), q.dtype, dev)
+    if h_final is not None:
+        a.h_final = _arg(h_final, "h_final", (B, H, K, V), f32, dev)
+    elif return_final_state:
+        h_final = torch.empty((B, H, K, V), device=dev, dtype=f32)
+        a.h_final = h_final.data_ptr()
+    if checkpoints is not None:
+        a.checkpoints = _arg(checkpoints, "checkpoints", gated_delta_checkpoint_shape(B, L, H, K, V), f32, dev)
+    _run("ssm_gated_delta_fwd", a, dev, "ssm_gated_delta_workspace_size", workspace)
+    _changed(*given)
+    return o, h_final
+
+
+def gated_delta_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor,
+                    do: torch.Tensor, scale: Optional[float] = None, l2norm: bool = False,
+                    reset: Optional[torch.Tensor] = None, h0: Optional[torch.Tensor] = None,
+                    dh_final: Optional[torch.Tensor] = None, checkpoints: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None) -> dict:
+    """ssm_gated_delta_bwd: the gradients of gated_delta_fwd for dL/do = do, dL/dh_final = dh_final.
+    `checkpoints` are the ones a gated_delta_fwd call with the same inputs wrote (else the backward
+    computes them).
+
+    Returns a dict with dq, dk, dv, dbeta (q's dtype), dg and, with h0, dh0 (float32), all dense."""
+    dev = _delta_q(q)
+    B, L = q.shape[:2]
+    f32, io = torch.float32, q.dtype
+    a = GatedDeltaBwdArgs(batch=B, seqlen=L)
+    _delta(a, q, k, v, g, beta, scale, l2norm, dev)
+    H, K, V = a.heads, a.kdim, a.vdim
+    a.dout = _need(do, "do", (B, L, H, V), io, dev)
+    out = dict(dq=torch.empty(q.shape, device=dev, dtype=io), dk=torch.empty(q.shape, device=dev, dtype=io),
+               dv=torch.empty((B, L, H, V), device=dev, dtype=io), dg=torch.empty((B, L, H), device=dev, dtype=f32),
+               dbeta=torch.empty((B, L, H), device=dev, dtype=io))
+    if reset is not None:
+        a.reset = _resets(reset, (B, L), dev)
+    if h0 is not None:
+        a.h0 = _arg(h0, "h0", (B, H, K, V), f32, dev)
+        out["dh0"] = torch.empty_like(h0)
+    if dh_final is not None:
+        a.dh_final = _arg(dh_final, "dh_final", (B, H, K, V), f32, dev)
+    if checkpoints is not None:
+        a.checkpoints = _arg(checkpoints, "checkpoints", gated_delta_checkpoint_shape(B, L, H, K, V), f32, dev)
+    for name, t in out.items():
+        setattr(a, name, t.data_ptr())
+    _run("ssm_gated_delta_bwd", a, dev, "ssm_gated_delta_bwd_workspace_size", workspace)
+    return out
+
+
+def gated_delta_step(state: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor,
+                     beta: torch.Tensor, scale: Optional[float] = None, l2norm: bool = False,
+                     reset: Optional[torch.Tensor] = None, o: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """ssm_gated_delta_step: one decode token; advances `state` (B, H, K, V) fp32 in place and returns
+    o (B, H, V).  q, k: (B, Hk, K), v: (B, H, V), dense or parts of wider rows; g: (B, H) fp32; beta:
+    (B, H) in q's dtype; reset: (B,) uint8 or bool, rows whose state is taken as 0 (a new sequence); the
+    rest as in gated_delta_fwd."""
+    a, out = gated_delta_step_args(state, q, k, v, g, beta, scale, l2norm, reset, o)
+    _run("ssm_gated_delta_step", a, state.device)
+    _changed(state, o)
+    return out
+
+
+def gated_delta_step_args(state, q, k, v, g, beta, scale=None, l2norm=False, reset=None, o=None):
+    """The checked ssm_gated_delta_step_args_t of a gated_delta_step call, and its o (allocated when not
+    given), for callers that launch the same step repeatedly through lib().ssm_gated_delta_step.  The
+    tensors must outlive the struct; autograd does not see what such launches write."""
+    dev = _gpu(state, "state", 4, "(B, H, K, V) float32")
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be a (B, Hk, K) tensor")
+    B, H, K, V = state.shape
+    a = GatedDeltaStepArgs(batch=B)
+    a.state = _need(state, "state", state.shape, torch.float32, dev)
+    if q.shape[0] != B or q.shape[2] != K or not isinstance(v, torch.Tensor) or v.shape != (B, H, V):
+        raise ValueError("a state of %s takes q and k of (%d, Hk, %d) and v of (%d, %d, %d)"
+                         % (tuple(state.shape), B, K, B, H, V))
+    _delta(a, q, k, v, g, beta, scale, l2norm, dev)
+    if reset is not None:
+        a.reset = _resets(reset, (B,), dev)
+    if o is None:
+        o = torch.empty((B, H, V), device=dev, dtype=q.dtype)
+        a.o = o.data_ptr()
+    else:
+        a.o = _need(o, "o", (B, H, V), q.dtype, dev)
+    return a, o
+
+
+class _GatedDeltaFn(torch.autograd.Function):
+    """gated_delta as a torch autograd function: the forward writes the checkpoints, the backward
+    reads them (ssm_gated_delta_fwd / _bwd)."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, g, beta, h0, scale, l2norm, reset):
+        _delta_q(q)
+        ck = None
+        if any(ctx.needs_input_grad) and isinstance(v, torch.Tensor) and v.dim() == 4:
+            shape = gated_delta_checkpoint_shape(*q.shape[:2], v.shape[2], q.shape[3], v.shape[3])
+            ck = torch.empty(shape, device=q.device, dtype=torch.float32)
+        o, hf = gated_delta_fwd(q, k, v, g, beta, scale, l2norm, reset=reset, h0=h0, return_final_state=True,
+                                checkpoints=ck)
+        ctx.save_for_backward(q, k, v, g, beta, h0, reset, ck)
+        ctx.opts = dict(scale=scale, l2norm=l2norm)
+        return o, hf
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, do, dh_final):
+        q, k, v, g, beta, h0, reset, ck = ctx.saved_tensors
+        d = gated_delta_bwd(q, k, v, g, beta, do.contiguous(), reset=reset, h0=h0, dh_final=dh_final.contiguous(),
+                            checkpoints=ck, **ctx.opts)
+        return d["dq"], d["dk"], d["dv"], d["dg"], d["dbeta"], d.get("dh0"), None, None, None
+
+
+def gated_delta(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor,
+                scale: Optional[float] = None, l2norm: bool = False, reset: Optional[torch.Tensor] = None,
+                h0: Optional[torch.Tensor] = None):
+    """The gated delta rule as a differentiable torch op (arguments as in gated_delta_fwd): returns
+    (o, h_final), and backward() runs ssm_gated_delta_bwd from the checkpoints the forward kept.  A
+    captured backward(): as with gated_scan."""
+    return _GatedDeltaFn.apply(q, k, v, g, beta, h0, scale, l2norm, reset)
+
+
+# ------------------------------------------------------------------------ e4m3 with block scales
+FP8_BLOCK = 128  # SSM_FP8_BLOCK
+_E4M3 = torch.float8_e4m3fn
+
+
+def _blocks(n: int) -> int:
+    return (n + FP8_BLOCK - 1) // FP8_BLOCK
+
+
+def quantize_fp8(x: torch.Tensor, block_rows: int = 1, q: Optional[torch.Tensor] = None,
+                 scales: Optional[torch.Tensor] = None):
+    """ssm_quantize_fp8: x (..., D) bf16 or fp32, D a multiple of 16, in e4m3 with a scale for each row and
+    128 columns, or (block_rows=128, x of two dimensions) for each 128 x 128 block, as matmul_fp8 takes its
+    weights.  q * scale stands for x.
+
+    Returns (q, scales): float8_e4m3fn of x's shape, and float32 (..., ceil(D / 128)) or (ceil(M / 128),
+    ceil(D / 128))."""
+    shape = _shape_of(x)
+    dev, D = x.device, shape[-1]
+    if int(block_rows) != block_rows:
+        raise ValueError("block_rows must be a whole number, got %r" % (block_rows,))
+    if block_rows != 1 and len(shape) != 2:
+        raise ValueError("x must be (M, D) with block_rows %d" % block_rows)
+    a = QuantizeFp8Args(rows=x.numel() // D, dim=D, block_rows=int(block_rows), io_dtype=_io_code(x.dtype))
+    a.x = _need(x, "x", shape, x.dtype, dev)
+    of = (*shape[:-1], _blocks(D)) if block_rows == 1 else (_blocks(shape[0]), _blocks(D))
+    given = (q, scales)
+    q = torch.empty(shape, device=dev, dtype=_E4M3) if q is None else q
+    scales = torch.empty(of, device=dev, dtype=torch.float32) if scales is None else scales
+    a.q = _need(q, "q", shape, _E4M3, dev)
+    a.scales = _need(scales, "scales", of, torch.float32, dev)
+    _run("ssm_quantize_fp8", a, dev)
+    _changed(*given)
+    return q, scales
+
+
+def add_rmsnorm_fp8(x: torch.Tensor, w: torch.Tensor, residual: Optional[torch.Tensor] = None,
+                    scale: Optional[torch.Tensor] = None, post_w: Optional[torch.Tensor] = None,
+                    eps: float = 1e-5, q: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None,
+                    res_out: Optional[torch.Tensor] = None):
+    """ssm_add_rmsnorm_fp8: add_rmsnorm_fwd with y in e4m3, quantised from its fp32 values as by
+    quantize_fp8; D a multiple of 16.  For serving: it has no gradients.  Returns (q, scales, res_out)."""
+    shape = _shape_of(x)
+    dev = x.device
+    a = AddNormFp8Args()
+    _add_norm(a.norm, x, w, residual, scale, post_w, eps, shape, dev)
+    stream = x if residual is None else residual
+    given = (q, scales, res_out)
+    of = (*shape[:-1], _blocks(shape[-1]))
+    q = torch.empty(shape, device=dev, dtype=_E4M3) if q is None else q
+    scales = torch.empty(of, device=dev, dtype=torch.float32) if scales is None else scales
+    res_out = torch.empty_like(stream) if res_out is None else res_out
+    a.q = _need(q, "q", shape, _E4M3, dev)
+    a.scales = _need(scales, "scales", of, torch.float32, dev)
+    a.norm.res_out = _need(res_out, "res_out", shape, stream.dtype, dev)
+    _run("ssm_add_rmsnorm_fp8", a, dev)
+    _changed(*given)
+    return q, scales, res_out
+
+
+def matmul_fp8(xq: torch.Tensor, x_scales: torch.Tensor, wq: torch.Tensor, w_scales: torch.Tensor,
+               out_dtype: torch.dtype = torch.bfloat16, y: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """ssm_matmul_fp8: y (..., N) = x w^T of e4m3 matrices, xq (..., K) with scales (..., ceil(K / 128)), as
+    quantize_fp8 or add_rmsnorm_fp8 give them, wq (N, K) with scales (ceil(N / 128), ceil(K / 128)), as
+    quantize_fp8(w, block_rows=128) does; K a multiple of 16; y in bf16 or fp32.  For serving: it has no
+    gradients."""
+    shape = _shape_of(xq)
+    dev, K = xq.device, shape[-1]
+    if not isinstance(wq, torch.Tensor) or wq.dim() != 2:
+        raise ValueError("wq must be an (N, K) tensor")
+    N = wq.shape[0]
+    a = MatmulFp8Args(m=xq.numel() // K, n=N, k=K, out_dtype=_io_code(out_dtype if y is None else y.dtype))
+    a.xq = _need(xq, "xq", shape, _E4M3, dev)
+    a.x_scales = _need(x_scales, "x_scales", (*shape[:-1], _blocks(K)), torch.float32, dev)
+    a.wq = _need(wq, "wq", (N, K), _E4M3, dev)
+    a.w_scales = _need(w_scales, "w_scales", (_blocks(N), _blocks(K)), torch.float32, dev)
+    out = torch.empty((*shape[:-1], N), device=dev, dtype=out_dtype) if y is None else y
+    a.y = _need(out, "y", (*shape[:-1], N), out.dtype, dev)
+    _run("ssm_matmul_fp8", a, dev)
+    _changed(y)
+    return out

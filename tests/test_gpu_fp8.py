@@ -1,0 +1,143 @@
+"""e4m3 with block scales on the GPU against its fp64 definition (needs an MI355X)."""
+import numpy as np
+import pytest
+import torch
+
+import selective_state_space_59_amd as ssm
+from oracle import delta as R
+from oracle import recurrent as N
+from tests.recurrent_helpers import check, f64, norm_bound
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+BF, F32 = torch.bfloat16, torch.float32
+IDS = dict(argvalues=[F32, BF], ids=["f32", "bf16"])
+U = 2.0 ** -24
+
+
+def _randn(*shape, seed, dtype=F32, std=1.0):
+    return (std * torch.randn(*shape, generator=torch.Generator().manual_seed(seed))).to(dtype)
+
+
+def _values(q):
+    return q.float().cpu().double().numpy()
+
+
+@pytest.mark.parametrize("dtype", **IDS)
+@pytest.mark.parametrize("block_rows", [1, 128])
+@pytest.mark.parametrize("M,D", [(1, 16), (3, 128), (1, 2560), (129, 144), (200, 400), (1000, 1040), (5, 16384)])
+def test_quantize(M, D, block_rows, dtype):
+    """Scales to the bit; the values those of the rounded quotient.  (The quotient itself is rounded to
+    fp32: that decides where it lies within 2^-24 of a border.)"""
+    x = _randn(M, D, seed=M + D, dtype=dtype)
+    x[0, ::5] = 0
+    x[M // 2] *= torch.exp(3 * _randn(D, seed=1)).to(dtype)
+    q, s = ssm.quantize_fp8(x.to(DEV), block_rows)
+    x64 = f64(x)
+    scales = R.block_scales(x64, block_rows)
+    assert np.array_equal(f64(s), scales)
+    quotient = (x64 / R.spread(scales, block_rows, M, D)).astype(np.float32).astype(np.float64)
+    assert np.array_equal(_values(q), R.e4m3(quotient))
+
+
+@pytest.mark.parametrize("block_rows", [1, 128])
+def test_quantize_extremes(block_rows):
+    """Zeros, the smallest and the largest numbers, infinities and NaNs: a block that holds one of the
+    latter stands for NaN, the others do not notice."""
+    x = _randn(130, 512, seed=2)
+    x[0] = 0
+    x[1, :128] *= 2.0 ** -120
+    x[2, :128] *= 2.0 ** 120
+    x[129, 300] = float("inf")
+    x[129, 400] = float("nan")
+    q, s = ssm.quantize_fp8(x.to(DEV), block_rows)
+    rows = R.spread(f64(s), block_rows, 130, 512)
+    with np.errstate(invalid="ignore"):
+        back = _values(q) * rows
+    band = slice(129, 130) if block_rows == 1 else slice(128, 130)
+    assert np.isnan(back[band, 256:]).all()
+    fine = np.ones((130, 512), bool)
+    fine[band, 256:] = False
+    # half a step of 2^-3 of the value, or of the smallest normal value's binade: 2^-4 and 2^-10
+    err = np.abs(back - f64(x)) - 2.0 ** -4 * np.abs(f64(x)) - 2.0 ** -10 * rows - 4 * U * np.abs(f64(x))
+    assert (err[fine] <= 0).all()
+    if block_rows == 1:
+        assert (back[0] == 0).all() and (f64(s)[0] == np.float64(np.float32(2.0 ** -100 / 448))).all()
+
+
+@pytest.mark.parametrize("io,res", [(F32, F32), (BF, BF), (BF, F32), (F32, BF)])
+@pytest.mark.parametrize("rows,D", [(1, 16), (3, 48), (300, 128), (41, 144), (7, 512), (70, 656), (5, 768), (9, 1024),
+                                    (33, 2048), (5, 2560), (4, 5136), (2, 8192), (3, 20000), (2, 69984)])
+def test_add_rmsnorm_fp8(rows, D, io, res):
+    """The residual sum to its bound; scales and values to what the norm's bound allows: q * scale within
+    half a step of e4m3 (2^-4 of the value, 2^-10 below 2^-6) of the fp32 value, which is within the bound."""
+    for i, (post, scale, residual) in enumerate([(False, False, True), (True, True, True), (False, True, False)]):
+        if D > 10000 and i == 2:
+            continue
+        x = _randn(rows, D, seed=D + i, dtype=io)
+        w, sc, pw = 1 + 0.1 * _randn(D, seed=5), 0.5 + 0.1 * _randn(D, seed=6), 1 + 0.1 * _randn(D, seed=7)
+        r0 = _randn(rows, D, seed=D + i + 50, std=2.0, dtype=res)
+        k = dict(x=x, w=w, residual=r0 if residual else None, scale=sc if scale else None, post_w=pw if post else None)
+        what = "%dx%d %d" % (rows, D, i)
+        print(what, flush=True)
+        q, s, r = ssm.add_rmsnorm_fp8(**{m: None if v is None else v.to(DEV) for m, v in k.items()})
+        k64 = {m: f64(v) for m, v in k.items()}
+        y, rr = N.add_rmsnorm(**k64)
+        b = norm_bound(k64["x"], k64["w"], k64["residual"], k64["scale"], k64["post_w"])
+        check(r, rr, b["res_out"], what + " res_out")
+        want = R.block_scales(y, 1)
+        per = np.stack([c.max(1) for c in np.split(np.pad(b["y"], ((0, 0), (0, -D % 128))), want.shape[1], 1)], 1)
+        got = f64(s)
+        assert (np.abs(got - want) <= per / 448 + 4 * U * want).all(), what
+        at = R.spread(got, 1, rows, D)
+        off = np.abs(_values(q) * at - y) - (2.0 ** -4 * (np.abs(y) + b["y"]) + 2.0 ** -10 * at + b["y"] + 4 * U * np.abs(y))
+        assert (off <= 0).all(), (what, off.max())
+
+
+def _operands(M, N_, K, seed):
+    q = lambda m, s: R.e4m3(np.clip(s * f64(_randn(m, K, seed=seed + int(s))), -448, 448))  # noqa: E731
+    xq, wq = q(M, 100), q(N_, 90)
+    kb = -(-K // 128)
+    sx = f64(torch.exp(_randn(M, kb, seed=seed + 2)))
+    sw = f64(torch.exp(_randn(-(-N_ // 128), kb, seed=seed + 3)))
+    dev = lambda t, d: torch.from_numpy(t).to(F32).to(d).to(DEV)  # noqa: E731
+    f8 = torch.float8_e4m3fn
+    return (xq, sx, wq, sw), (dev(xq, f8), dev(sx, F32), dev(wq, f8), dev(sw, F32))
+
+
+# the skinny kernel's and the three tiles' ranges, edges that are no multiple of anything, K within a block
+MATS = [(1, 16, 16), (1, 1, 128), (2, 130, 272), (16, 300, 512), (17, 129, 2560), (33, 100, 144), (64, 257, 400),
+        (65, 64, 64), (65, 1000, 1040), (200, 333, 256), (1237, 1331, 2000), (1100, 4100, 128), (4096, 1027, 272),
+        (4200, 4000, 400), (4097, 4097, 160)]
+
+
+@pytest.mark.parametrize("dtype", **IDS)
+@pytest.mark.parametrize("M,N_,K", MATS)
+def test_matmul(M, N_, K, dtype):
+    """Within the bound of a sum in fp32: K terms of exact products, each partial sum and each scale's
+    product rounded to 2^-24 (a matrix instruction may cut its terms off at 2^-23 of the largest instead of
+    rounding them: twice that).  For a bf16 result the 8-bit matrix instruction cuts each of eight products
+    it aligns to the largest of them, p, at a unit of 2^-14 of p's power of two (448 x 448 = 1.53 2^17 beside
+    2^3 keeps it, beside 2^2 does not): seven of them lose less than 2^-14 |p| each, and the |p| of the groups
+    add up to no more than the sum of all magnitudes."""
+    ref, args = _operands(M, N_, K, seed=M + N_ + K)
+    y = ssm.matmul_fp8(*args, out_dtype=dtype)
+    assert y.dtype == dtype
+    want, size = R.matmul_blocks(*ref)
+    cut = 7 * 2.0 ** -14 if dtype is BF else 0.0
+    check(y, want, (2 * (K + 4) * U + cut) * size, "%dx%dx%d" % (M, N_, K))
+
+
+def test_quantised_linear():
+    """A layer's product with both operands quantised from the weights and inputs a user has: within what
+    the two roundings to e4m3 allow, 2^-4 of each value and 2^-10 of its block's scale."""
+    x, w = _randn(3, 70, 400, seed=3, dtype=BF), _randn(300, 400, seed=4, std=0.05)
+    wq, ws = ssm.quantize_fp8(w.to(DEV), block_rows=128)
+    xq, xs = ssm.quantize_fp8(x.to(DEV))
+    y = ssm.matmul_fp8(xq, xs, wq, ws, out_dtype=F32)
+    assert y.shape == (3, 70, 300)
+    x64, w64 = f64(x).reshape(210, 400), f64(w)
+    sx, sw = R.spread(f64(xs).reshape(210, 4), 1, 210, 400), R.spread(f64(ws), 128, 300, 400)
+    dx, dw = 2.0 ** -4 * np.abs(x64) + 2.0 ** -10 * sx, 2.0 ** -4 * np.abs(w64) + 2.0 ** -10 * sw
+    off = dx @ np.abs(w64).T + np.abs(x64) @ dw.T + dx @ dw.T
+    assert (np.abs(f64(y).reshape(210, 300) - x64 @ w64.T) <= off * (1 + 1e-3)).all()
