@@ -217,7 +217,8 @@ __device__ __forceinline__ float decay(const Gates &s, int t, int u) {
 }
 
 // 64 rows of K channels (rows from t0 on of one head) between memory, registers and LDS, 16 bytes a
-// piece: lane = row, so that a transposed copy is written without conflicts.
+// piece: lane = row, so that a transposed copy is written without conflicts.  Loads have no condition (a
+// conditional one is waited for where its branch ends, and the next chunk's are to stay in flight).
 template <typename IO, int KP>
 struct HeadRows {
     using E = typename Op<IO>::elem;
@@ -232,11 +233,23 @@ struct HeadRows {
     static __device__ __forceinline__ void load(Regs<WAVES> &r, const void *base, int64_t off, int64_t token, int64_t t0,
                                                 int64_t L, int K) {
         const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-        const char *row = static_cast<const char *>(base) + (off + (t0 + lane) * token) * IO::bytes;
+        const int64_t t = t0 + lane < L ? t0 + lane : L - 1;
+        const char *row = static_cast<const char *>(base) + (off + t * token) * IO::bytes;
 #pragma unroll
         for (int i = 0; i < KP / PER / WAVES; ++i) {
             const int c = (wave * (KP / PER / WAVES) + i) * PER;
-            r.r[i] = t0 + lane < L && c < K ? *reinterpret_cast<const u4 *>(row + c * IO::bytes) : u4{0, 0, 0, 0};
+            r.r[i] = *reinterpret_cast<const u4 *>(row + (c < K ? c : 0) * IO::bytes);
+        }
+    }
+    // The steps past the end and the channels past K, which were loaded from elsewhere, as 0.
+    template <int WAVES>
+    static __device__ __forceinline__ void cut(Regs<WAVES> &r, int64_t t0, int64_t L, int K) {
+        const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+        if (t0 + kC <= L && K == KP) return;
+#pragma unroll
+        for (int i = 0; i < KP / PER / WAVES; ++i) {
+            const int c = (wave * (KP / PER / WAVES) + i) * PER;
+            if (t0 + lane >= L || c >= K) r.r[i] = u4{0, 0, 0, 0};
         }
     }
     template <int WAVES>
@@ -329,6 +342,34 @@ struct ChunkBlock {
     static constexpr size_t kInvBytes = Inv::ELEMS * IO::bytes;
     static constexpr size_t kBytes = kVecBytes + kInvBytes + AttT::ELEMS * IO::bytes;
 };
+
+// A state's column (rows of `to`, V apart) from a wave's registers.
+template <int KT>
+__device__ __forceinline__ void store_state(float *to, int K, int V, int grp, const f4 (&s)[KT]) {
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int k = pair_row(kt, grp, i);
+            if (K == 16 * KT || k < K) to[k * V] = s[kt][i];
+        }
+}
+
+// An element as it lies in memory, kept so until it is used.
+template <typename IO>
+struct RawOne {
+    typename IO::storage v;
+    __device__ __forceinline__ float get() const {
+        if constexpr (IO::bytes == 2)
+            return bf16_bits_to_f32(v);
+        else
+            return v;
+    }
+};
+template <typename IO>
+__device__ __forceinline__ RawOne<IO> load_one(const void *p, int64_t i) {
+    return {static_cast<const typename IO::storage *>(p)[i]};
+}
 
 // Enqueue the chunks' kernel (gated_delta.hip); `blocks`: ChunkBlock<IO>::kBytes a chunk.
 hipError_t launch_prepare(const Call &a, int io_dtype, bool backward, char *blocks, hipStream_t stream);

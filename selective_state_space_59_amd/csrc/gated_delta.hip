@@ -22,9 +22,9 @@ namespace {
 template <typename IO, int KP>
 struct PrepareLds {
     using Rows = HeadRows<IO, KP>;
-    typename Op<IO>::elem q[kC * Rows::STRIDE], k[kC * Rows::STRIDE];
-    float a[kC][kC + 4];    // B diag(beta)
-    float inv[kC][20];      // the inverses of its diagonal blocks, side by side: row, column within the block
+    alignas(16) typename Op<IO>::elem q[kC * Rows::STRIDE], k[kC * Rows::STRIDE];
+    alignas(16) float a[kC][kC + 4];    // B diag(beta)
+    alignas(16) float inv[kC][20];      // the inverses of its diagonal blocks, side by side: row, column within the block
     Gates gates;
 };
 
@@ -64,6 +64,8 @@ __global__ __launch_bounds__(kThreads) void prepare_kernel(Call a, char *blocks)
         Rows::template load<4>(rq, a.q, b * a.q_batch + (int64_t)hk * a.K, a.q_token, t0, a.L, a.K);
         Rows::template load<4>(rk, a.k, b * a.k_batch + (int64_t)hk * a.K, a.k_token, t0, a.L, a.K);
         load_gates<IO>(a, b, h, t0, s.gates);
+        Rows::template cut<4>(rq, t0, a.L, a.K);
+        Rows::template cut<4>(rk, t0, a.L, a.K);
         Rows::template store<4>(rq, s.q);
         Rows::template store<4>(rk, s.k);
     }
@@ -175,10 +177,10 @@ struct ChainLds {
     using Block = ChunkBlock<IO>;
     using E = typename Op<IO>::elem;
     static constexpr bool kTransposed = IO::bytes == 2;
-    E q[kC * Rows::STRIDE], k[kC * Rows::STRIDE];
-    E kt[kTransposed ? KP * Rows::TSTRIDE : 8];
-    E inv[Block::Inv::PLANES * Block::Inv::PLANE], att[Block::Att::PLANES * Block::Att::PLANE];
-    float vec[kVecs * kC];
+    alignas(16) E q[kC * Rows::STRIDE], k[kC * Rows::STRIDE];
+    alignas(16) E kt[kTransposed ? KP * Rows::TSTRIDE : 8];
+    alignas(16) E inv[Block::Inv::PLANES * Block::Inv::PLANE], att[Block::Att::PLANES * Block::Att::PLANE];
+    alignas(16) float vec[kVecs * kC];
 };
 
 struct ChainArgs {
@@ -203,8 +205,9 @@ __global__ __launch_bounds__(kThreads) void chain_kernel(ChainArgs p) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r16 = lane % 16, grp = lane / 16;
     const int64_t b = blockIdx.z;
     const int h = blockIdx.y, hk = h / (a.H / a.Hk);
-    const int v = (blockIdx.x * (kThreads / 64) + wave) * 16 + r16;
-    const bool live = v < a.V;
+    // lanes past the last channel repeat it and store nothing
+    const int vw = (blockIdx.x * (kThreads / 64) + wave) * 16 + r16, v = min(vw, a.V - 1);
+    const bool live = vw < a.V;
     const int64_t head = b * a.H + h;
     const char *blocks = p.blocks + head * a.n * Block::kBytes;
     const int64_t q_off = b * a.q_batch + (int64_t)hk * a.K, k_off = b * a.k_batch + (int64_t)hk * a.K;
@@ -216,7 +219,7 @@ __global__ __launch_bounds__(kThreads) void chain_kernel(ChainArgs p) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int k = pair_row(kt, grp, i);
-            state[kt][i] = p.h0 && live && k < a.K ? p.h0[(head * a.K + k) * a.V + v] : 0.0f;
+            state[kt][i] = p.h0 && k < a.K ? p.h0[(head * a.K + k) * a.V + v] : 0.0f;
         }
 
     // the next chunk's tiles, on their way while this one is computed
@@ -224,7 +227,7 @@ __global__ __launch_bounds__(kThreads) void chain_kernel(ChainArgs p) {
     typename Block::Inv::template Regs<kThreads> rinv;
     typename Block::Att::template Regs<kThreads> ratt;
     float rvec[2];
-    f4 rv[4];
+    RawOne<IO> rv[4][4];
     const auto fetch = [&](int64_t c) {
         const char *block = blocks + c * Block::kBytes;
         Rows::template load<4>(rq, a.q, q_off, a.q_token, c * kC, a.L, a.K);
@@ -234,20 +237,23 @@ __global__ __launch_bounds__(kThreads) void chain_kernel(ChainArgs p) {
             ratt, reinterpret_cast<const E *>(block + Block::kVecBytes + Block::kInvBytes));
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const int at = threadIdx.x + kThreads * i;
-            rvec[i] = at < kVecs * kC ? reinterpret_cast<const float *>(block)[at] : 0.0f;
+            const int at = min((int)threadIdx.x + kThreads * i, kVecs * kC - 1);
+            rvec[i] = reinterpret_cast<const float *>(block)[at];
         }
 #pragma unroll
         for (int tt = 0; tt < 4; ++tt)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int64_t t = c * kC + pair_row(tt, grp, i);
-                rv[tt][i] = live && t < a.L ? load_io<IO>(a.v, v_off + t * a.v_token) : 0.0f;
+                rv[tt][i] = load_one<IO>(a.v, v_off + (t < a.L ? t : a.L - 1) * a.v_token);
             }
     };
     fetch(0);
     for (int64_t c = 0; c < a.n; ++c) {
         __syncthreads();  // the last chunk's tiles have been read
+        const bool whole = (c + 1) * kC <= a.L;
+        Rows::template cut<4>(rq, c * kC, a.L, a.K);
+        Rows::template cut<4>(rk, c * kC, a.L, a.K);
         Rows::template store<4>(rq, s.q);
         Rows::template store<4>(rk, s.k);
         if constexpr (Lds::kTransposed) Rows::template store_transposed<4>(rk, s.kt);
@@ -260,19 +266,15 @@ __global__ __launch_bounds__(kThreads) void chain_kernel(ChainArgs p) {
         }
         f4 val[4];
 #pragma unroll
-        for (int tt = 0; tt < 4; ++tt) val[tt] = rv[tt];
+        for (int tt = 0; tt < 4; ++tt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                val[tt][i] = whole || c * kC + pair_row(tt, grp, i) < a.L ? rv[tt][i].get() : 0.0f;
         __syncthreads();
         if (c + 1 < a.n) fetch(c + 1);
 
         float *ck = p.ck ? p.ck + (((c * a.B + b) * a.H + h) * (a.K + kC)) * a.V + v : nullptr;
-        if (ck && live)
-#pragma unroll
-            for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int k = pair_row(kt, grp, i);
-                    if (k < a.K) ck[(int64_t)k * a.V] = state[kt][i];
-                }
+        if (ck && live) store_state<KT>(ck, a.K, a.V, grp, state);
 
         // K S and Q S
         f4 ks[4] = {}, qs[4] = {};
@@ -364,22 +366,21 @@ __global__ __launch_bounds__(kThreads) void chain_kernel(ChainArgs p) {
                                         s.att + pair_row16(tt, r16) * Block::Att::STRIDE + 32 * y + 8 * grp,
                                         Block::Att::PLANE),
                                     us[y]);
+            }
+            if (live) {
+                const int64_t at = ((b * a.L + c * kC) * a.H + h) * a.V + v;
+                const int step = a.H * a.V;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int64_t t = c * kC + pair_row(tt, grp, i);
-                    if (live && t < a.L) store_io<IO>(p.o, ((b * a.L + t) * a.H + h) * a.V + v, qs[tt][i]);
-                }
+                for (int tt = 0; tt < 4; ++tt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int t = pair_row(tt, grp, i);
+                        if (whole || c * kC + t < a.L) store_io<IO>(p.o, at + (int64_t)t * step, qs[tt][i]);
+                    }
             }
         }
     }
-    if (p.h_final && live)
-#pragma unroll
-        for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int k = pair_row(kt, grp, i);
-                if (k < a.K) p.h_final[(head * a.K + k) * a.V + v] = state[kt][i];
-            }
+    if (p.h_final && live) store_state<KT>(p.h_final + head * a.K * a.V + v, a.K, a.V, grp, state);
 }
 
 // ------------------------------------------------------------------------------------ step

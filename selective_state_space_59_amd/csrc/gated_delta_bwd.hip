@@ -13,6 +13,7 @@
 //   Z = dP P + dB B;   dG_end += sum_t k.(leave U dS^T) + through <dS, S>;   dg = suffix sums of dG
 // dbeta never divides by beta: E is kept in place of U.
 #include "delta_tile.h"
+#include "wide_io.h"
 
 #include <algorithm>
 
@@ -36,11 +37,11 @@ struct BackLds {
     using Block = ChunkBlock<IO>;
     using E = typename Op<IO>::elem;
     static constexpr bool kTransposed = IO::bytes == 2;
-    E k[kC * Rows::STRIDE];
-    E q[kTransposed ? 8 : kC * Rows::STRIDE];
-    E kt[kTransposed ? KP * Rows::TSTRIDE : 8], qt[kTransposed ? KP * Rows::TSTRIDE : 8];
-    E inv[Block::Inv::PLANES * Block::Inv::PLANE], att[Block::AttT::PLANES * Block::AttT::PLANE];
-    float vec[kVecs * kC];
+    alignas(16) E k[kC * Rows::STRIDE];
+    alignas(16) E q[kTransposed ? 8 : kC * Rows::STRIDE];
+    alignas(16) E kt[kTransposed ? KP * Rows::TSTRIDE : 8], qt[kTransposed ? KP * Rows::TSTRIDE : 8];
+    alignas(16) E inv[Block::Inv::PLANES * Block::Inv::PLANE], att[Block::AttT::PLANES * Block::AttT::PLANE];
+    alignas(16) float vec[kVecs * kC];
 };
 
 template <typename IO, int KP>
@@ -58,8 +59,9 @@ __global__ __launch_bounds__(kThreads) void back_chain_kernel(BackArgs p) {
     const int64_t b = blockIdx.z;
     const int h = blockIdx.y, hk = h / (a.H / a.Hk);
     const int strip = blockIdx.x * (kThreads / 64) + wave, strips = (a.V + 15) / 16;
-    const int v = strip * 16 + r16;
-    const bool live = v < a.V;
+    // lanes past the last channel repeat it, store nothing and count for nothing
+    const int vw = strip * 16 + r16, v = min(vw, a.V - 1);
+    const bool live = vw < a.V;
     const int64_t head = b * a.H + h;
     const char *blocks = p.blocks + head * a.n * Block::kBytes;
     const int64_t q_off = b * a.q_batch + (int64_t)hk * a.K, k_off = b * a.k_batch + (int64_t)hk * a.K;
@@ -70,13 +72,14 @@ __global__ __launch_bounds__(kThreads) void back_chain_kernel(BackArgs p) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int k = pair_row(kt, grp, i);
-            ds[kt][i] = p.dh_final && live && k < a.K ? p.dh_final[(head * a.K + k) * a.V + v] : 0.0f;
+            ds[kt][i] = p.dh_final && k < a.K ? p.dh_final[(head * a.K + k) * a.V + v] : 0.0f;
         }
     typename Rows::template Regs<4> rq, rk;
     typename Block::Inv::template Regs<kThreads> rinv;
     typename Block::AttT::template Regs<kThreads> ratt;
     float rvec[2];
-    f4 rdo[4], rerr[4];
+    RawOne<IO> rdo[4][4];
+    f4 rerr[4];
     const auto fetch = [&](int64_t c) {
         const char *block = blocks + c * Block::kBytes;
         Rows::template load<4>(rq, a.q, q_off, a.q_token, c * kC, a.L, a.K);
@@ -86,8 +89,8 @@ __global__ __launch_bounds__(kThreads) void back_chain_kernel(BackArgs p) {
             ratt, reinterpret_cast<const E *>(block + Block::kVecBytes + Block::kInvBytes));
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const int at = threadIdx.x + kThreads * i;
-            rvec[i] = at < kVecs * kC ? reinterpret_cast<const float *>(block)[at] : 0.0f;
+            const int at = min((int)threadIdx.x + kThreads * i, kVecs * kC - 1);
+            rvec[i] = reinterpret_cast<const float *>(block)[at];
         }
         const float *err = p.ck + (((c * a.B + b) * a.H + h) * (a.K + kC) + a.K) * a.V + v;
 #pragma unroll
@@ -96,13 +99,16 @@ __global__ __launch_bounds__(kThreads) void back_chain_kernel(BackArgs p) {
             for (int i = 0; i < 4; ++i) {
                 const int r = pair_row(tt, grp, i);
                 const int64_t t = c * kC + r;
-                rdo[tt][i] = live && t < a.L ? load_io<IO>(p.dout, ((b * a.L + t) * a.H + h) * a.V + v) : 0.0f;
-                rerr[tt][i] = live ? err[(int64_t)r * a.V] : 0.0f;
+                rdo[tt][i] = load_one<IO>(p.dout, ((b * a.L + (t < a.L ? t : a.L - 1)) * a.H + h) * a.V + v);
+                rerr[tt][i] = err[r * a.V];
             }
     };
     fetch(a.n - 1);
     for (int64_t c = a.n - 1; c >= 0; --c) {
         __syncthreads();
+        const bool whole = (c + 1) * kC <= a.L;
+        Rows::template cut<4>(rq, c * kC, a.L, a.K);
+        Rows::template cut<4>(rk, c * kC, a.L, a.K);
         Rows::template store<4>(rk, s.k);
         if constexpr (Lds::kTransposed) {
             Rows::template store_transposed<4>(rk, s.kt);
@@ -120,21 +126,17 @@ __global__ __launch_bounds__(kThreads) void back_chain_kernel(BackArgs p) {
         f4 dout[4], err[4];
 #pragma unroll
         for (int tt = 0; tt < 4; ++tt) {
-            dout[tt] = rdo[tt];
-            err[tt] = rerr[tt];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                dout[tt][i] = whole || c * kC + pair_row(tt, grp, i) < a.L ? rdo[tt][i].get() : 0.0f;
+                err[tt][i] = live ? rerr[tt][i] : 0.0f;
+            }
         }
         __syncthreads();
         if (c > 0) fetch(c - 1);
 
         const int64_t chunk = head * a.n + c;
-        if (live)
-#pragma unroll
-            for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int k = pair_row(kt, grp, i);
-                    if (k < a.K) p.after[(chunk * a.K + k) * a.V + v] = ds[kt][i];
-                }
+        if (live) store_state<KT>(p.after + chunk * a.K * a.V + v, a.K, a.V, grp, ds);
         // dU = P^T dO + leave K dS
         f4 du[4] = {};
 #pragma unroll
@@ -188,16 +190,19 @@ __global__ __launch_bounds__(kThreads) void back_chain_kernel(BackArgs p) {
                                         Block::Inv::PLANE),
                                     us[y]);
         }
-        if (live)
+        if (live) {
+            float *to = p.dx + chunk * kC * a.V + v;
+            const int64_t at = ((b * a.L + c * kC) * a.H + h) * a.V + v;
+            const int step = a.H * a.V;
 #pragma unroll
             for (int tt = 0; tt < 4; ++tt)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int r = pair_row(tt, grp, i);
-                    const int64_t t = c * kC + r;
-                    p.dx[(chunk * kC + r) * a.V + v] = dx[tt][i];
-                    if (t < a.L) store_io<IO>(p.dv, ((b * a.L + t) * a.H + h) * a.V + v, dx[tt][i]);
+                    const int t = pair_row(tt, grp, i);
+                    to[t * a.V] = dx[tt][i];
+                    if (whole || c * kC + t < a.L) store_io<IO>(p.dv, at + (int64_t)t * step, dx[tt][i]);
                 }
+        }
         // dS <- through dS + (scale enter Q)^T dO - (enter K)^T dX
         typename O::template Sum<PL> qs[2], xs[2];
 #pragma unroll
@@ -233,14 +238,7 @@ __global__ __launch_bounds__(kThreads) void back_chain_kernel(BackArgs p) {
             }
         }
     }
-    if (p.dh0 && live)
-#pragma unroll
-        for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int k = pair_row(kt, grp, i);
-                if (k < a.K) p.dh0[(head * a.K + k) * a.V + v] = ds[kt][i];
-            }
+    if (p.dh0 && live) store_state<KT>(p.dh0 + head * a.K * a.V + v, a.K, a.V, grp, ds);
 }
 
 // --------------------------------------------------------------------------- all chunks at once
@@ -260,7 +258,7 @@ struct Slab {
     using E = typename Op<IO>::elem;
     static constexpr int PLANES = IO::bytes == 2 ? P : 1;
     static constexpr int STRIDE = kVB + 16 / IO::bytes, PLANE = ROWS * STRIDE;
-    E e[PLANES * PLANE];
+    alignas(16) E e[PLANES * PLANE];
     __device__ __forceinline__ void put4(int row, int col, f4 v) {
         if constexpr (IO::bytes == 4) {
             *reinterpret_cast<f4 *>(e + row * STRIDE + col) = v;
@@ -288,20 +286,20 @@ struct GradLds {
     using E = typename Op<IO>::elem;
     using Mat = ChunkMatrix<IO, 2>;  // these feed outputs of the tensors' type alone
     static constexpr bool kTransposed = IO::bytes == 2;
-    E q[kC * Rows::STRIDE], k[kC * Rows::STRIDE];
+    alignas(16) E q[kC * Rows::STRIDE], k[kC * Rows::STRIDE];
     Gates gates;
     float row_z[4][kC], col_z[4][kC], col_by[4][kC];
     float row_a[KP / 16][kC], row_b[KP / 16][kC];
     float dots[kGradThreads / 64];
-    union {
+    alignas(16) union {
         struct {
             Slab<IO, kC, 1> dout;
             Slab<IO, kC, 3> dx, err;
             Slab<IO, KP, 3> before, after;
         } in;
         struct {
-            E kt[kTransposed ? KP * Rows::TSTRIDE : 8], qt[kTransposed ? KP * Rows::TSTRIDE : 8];
-            E m1[Mat::PLANES * Mat::PLANE], m2[Mat::PLANES * Mat::PLANE], m3[Mat::PLANES * Mat::PLANE];
+            alignas(16) E kt[kTransposed ? KP * Rows::TSTRIDE : 8], qt[kTransposed ? KP * Rows::TSTRIDE : 8];
+            alignas(16) E m1[Mat::PLANES * Mat::PLANE], m2[Mat::PLANES * Mat::PLANE], m3[Mat::PLANES * Mat::PLANE];
         } out;
     };
 };
@@ -331,20 +329,20 @@ __global__ __launch_bounds__(kGradThreads) void grads_kernel(GradArgs p) {
     extern __shared__ __attribute__((aligned(16))) char raw[];
     Lds &s = *reinterpret_cast<Lds *>(raw);
     const Call &a = p.a;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r16 = lane % 16, grp = lane / 16;
-    const int kd = wave % KT, first = wave / KT * NT;
     const int64_t c = blockIdx.x, b = blockIdx.z, t0 = c * kC;
     const int hk = blockIdx.y, share = a.H / a.Hk;
     {
         typename Rows::template Regs<8> rq, rk;
         Rows::template load<8>(rq, a.q, b * a.q_batch + (int64_t)hk * a.K, a.q_token, t0, a.L, a.K);
         Rows::template load<8>(rk, a.k, b * a.k_batch + (int64_t)hk * a.K, a.k_token, t0, a.L, a.K);
+        Rows::template cut<8>(rq, t0, a.L, a.K);
+        Rows::template cut<8>(rk, t0, a.L, a.K);
         Rows::template store<8>(rq, s.q);
         Rows::template store<8>(rk, s.k);
     }
     __syncthreads();
-    if (tid < 256) {
-        const int row = tid / 4, part = tid % 4;
+    if (threadIdx.x < 256) {
+        const int row = threadIdx.x / 4, part = threadIdx.x % 4;
 #pragma unroll
         for (int which = 0; which < 2; ++which) {
             const E *x = (which ? s.k : s.q) + row * Rows::STRIDE + part * (KP / 4);
@@ -359,30 +357,31 @@ __global__ __launch_bounds__(kGradThreads) void grads_kernel(GradArgs p) {
 
     f4 dq[NT] = {}, dk[NT] = {};
     for (int h = hk * share; h < (hk + 1) * share; ++h) {
+        // The thread's place, formed anew for each head: the compiler would else keep hundreds of addresses
+        // that depend on nothing but it across the heads, in scratch memory.
+        int tid = threadIdx.x;
+        asm volatile("" : "+v"(tid));
+        const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), r16 = lane % 16, grp = lane / 16;
+        const int kd = wave % KT, first = wave / KT * NT;
         const int64_t chunk = (b * a.H + h) * a.n + c;
         const float *before = p.ck + ((c * a.B + b) * a.H + h) * (a.K + kC) * a.V, *err = before + (int64_t)a.K * a.V;
         const float *after = p.after + chunk * a.K * a.V, *dx = p.dx + chunk * kC * a.V;
         const int row = tid / 8, col = tid % 8 * 4;
-        f4 rdo, rdx, rerr, rs[SR], ra[SR];
+        Raw<IO, 4> rdo;
+        f4 rdx, rerr, rs[SR], ra[SR];
+        // (rows and channels past the ends come from elsewhere and are cleared when they are put down)
+        const bool step_in = t0 + row < a.L;
+        const int64_t o_row = ((b * a.L + (step_in ? t0 + row : a.L - 1)) * a.H + h) * a.V;
         const auto fetch = [&](int v0) {
-            const int v = v0 + col;
-            const bool in = v < a.V;
-            const int64_t at = (int64_t)row * a.V + v;
-            rdo = f4{0, 0, 0, 0};
-            if (in && t0 + row < a.L) {
-                const int64_t o = ((b * a.L + t0 + row) * a.H + h) * a.V + v;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) rdo[i] = load_io<IO>(p.dout, o + i);
-            }
-            const f4 zero = {0, 0, 0, 0};
-            rdx = in ? *reinterpret_cast<const f4 *>(dx + at) : zero;
-            rerr = in ? *reinterpret_cast<const f4 *>(err + at) : zero;
+            const int v = v0 + col < a.V ? v0 + col : 0;
+            rdo = load_raw<IO, 4>(p.dout, o_row + v, 4);
+            rdx = *reinterpret_cast<const f4 *>(dx + row * a.V + v);
+            rerr = *reinterpret_cast<const f4 *>(err + row * a.V + v);
 #pragma unroll
             for (int j = 0; j < SR; ++j) {
-                const int k = row + 64 * j;
-                const int64_t ks = (int64_t)k * a.V + v;
-                rs[j] = in && k < a.K ? *reinterpret_cast<const f4 *>(before + ks) : zero;
-                ra[j] = in && k < a.K ? *reinterpret_cast<const f4 *>(after + ks) : zero;
+                const int k = row + 64 * j, at = (k < a.K ? k : 0) * a.V + v;
+                rs[j] = *reinterpret_cast<const f4 *>(before + at);
+                ra[j] = *reinterpret_cast<const f4 *>(after + at);
             }
         };
         fetch(0);
@@ -391,11 +390,14 @@ __global__ __launch_bounds__(kGradThreads) void grads_kernel(GradArgs p) {
         float dot = 0.0f;
         for (int v0 = 0; v0 < a.V; v0 += kVB) {
             __syncthreads();
-            s.in.dout.put4(row, col, rdo);
-            s.in.dx.put4(row, col, rdx);
-            s.in.err.put4(row, col, rerr);
+            const f4 zero = {0, 0, 0, 0};
+            const bool in = v0 + col < a.V;
+            s.in.dout.put4(row, col, in && step_in ? f4{rdo[0], rdo[1], rdo[2], rdo[3]} : zero);
+            s.in.dx.put4(row, col, in ? rdx : zero);
+            s.in.err.put4(row, col, in ? rerr : zero);
 #pragma unroll
             for (int j = 0; j < SR; ++j) {
+                if (!in || row + 64 * j >= a.K) rs[j] = ra[j] = zero;
                 s.in.before.put4(row + 64 * j, col, rs[j]);
                 s.in.after.put4(row + 64 * j, col, ra[j]);
 #pragma unroll
@@ -569,6 +571,8 @@ __global__ __launch_bounds__(kGradThreads) void grads_kernel(GradArgs p) {
         __syncthreads();
     }
     // through the norms: dx = r (dxhat - xhat (xhat . dxhat))
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r16 = lane % 16, grp = lane / 16;
+    const int kd = wave % KT, first = wave / KT * NT;
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
