@@ -2,10 +2,7 @@
 //
 // A chunk is 64 steps.  All products run on 16 x 16 result tiles of the matrix cores, contracted 32 at
 // a time: lane l holds row (A) or column (B) l % 16 and the eight consecutive contraction indices
-// 8 (l / 16) .. + 7; the result has column l % 16 and, in register i, row 4 (l / 16) + i.  Where a result
-// is the right operand of the next product its tiles come in pairs whose rows are dealt out so that
-// the two results of a lane ARE the eight values the next product wants of it (pair_row): states, value
-// errors and gradients go from one product to the next without leaving their registers.
+// 8 (l / 16) .. + 7; the result has column l % 16 and, in register i, row 4 (l / 16) + i.
 //
 // Precision.  q, k, v, do in bf16 are exact operands.  What was computed in fp32 enters a bf16 product as
 // the sum of three bf16 numbers (8 significant bits each, 24 in all: the value itself to 2^-24), an exact
@@ -31,13 +28,6 @@ typedef __bf16 b8 __attribute__((ext_vector_type(8)));
 typedef __bf16 b4 __attribute__((ext_vector_type(4)));
 typedef __bf16 b2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u4 __attribute__((ext_vector_type(4)));
-
-// Row of a result's register i in tile `tile` of a run of pairs, for lane group `grp` (lane / 16).
-__device__ __forceinline__ constexpr int pair_row(int tile, int grp, int i) {
-    return 32 * (tile / 2) + 8 * grp + 4 * (tile & 1) + i;
-}
-// The same for row r = 0..15 of that tile (rows of the left operand).
-__device__ __forceinline__ constexpr int pair_row16(int tile, int r) { return pair_row(tile, r / 4, r % 4); }
 
 // The operands of one contraction over 32, for fp32 and bf16 tensors.
 template <typename IO>
@@ -68,10 +58,9 @@ struct Op<io_f32> {
         return load(p);
     }
     template <int P>
-    static __device__ __forceinline__ Ex sum(f4 a, f4 b) {
-        return {{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]}};
+    static __device__ __forceinline__ Ex first(const Ex &a) {
+        return a;
     }
-    static __device__ __forceinline__ Ex exact(f4 a, f4 b) { return sum<1>(a, b); }
     static __device__ __forceinline__ f4 mul(f4 c, const Ex &a, const Ex &b) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.v[i], b.v[i], c, 0, 0, 0);
@@ -99,33 +88,12 @@ struct Op<io_bf16> {
         for (int i = 0; i < P; ++i) r.p[i] = *reinterpret_cast<const b8 *>(p + i * stride);
         return r;
     }
-    static __device__ __forceinline__ b8 narrow(const float (&x)[8]) {
-        b8 r;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const b2 t = __builtin_convertvector((f2){x[2 * i], x[2 * i + 1]}, b2);
-            r[2 * i] = t[0];
-            r[2 * i + 1] = t[1];
-        }
-        return r;
-    }
-    template <int P>
-    static __device__ __forceinline__ Sum<P> sum(f4 a, f4 b) {
-        float x[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+    template <int P, int Q>
+    static __device__ __forceinline__ Sum<P> first(const Sum<Q> &a) {
         Sum<P> r;
 #pragma unroll
-        for (int p = 0; p < P; ++p) {
-            r.p[p] = narrow(x);
-            if (p + 1 < P)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] -= (float)r.p[p][i];
-        }
+        for (int i = 0; i < P; ++i) r.p[i] = a.p[i];
         return r;
-    }
-    // values that are bf16 numbers
-    static __device__ __forceinline__ Ex exact(f4 a, f4 b) {
-        const float x[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-        return {narrow(x)};
     }
     static __device__ __forceinline__ f4 one(f4 c, b8 a, b8 b) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
@@ -153,11 +121,6 @@ struct Op<io_bf16> {
         return c;
     }
 };
-
-template <typename IO>
-__device__ __forceinline__ float widen(typename Op<IO>::elem v) {
-    return (float)v;
-}
 
 // One call's tensors as its kernels see them.  Strides in elements; a head's K (or V) channels are
 // consecutive, its heads too.
@@ -217,7 +180,7 @@ __device__ __forceinline__ float decay(const Gates &s, int t, int u) {
 }
 
 // 64 rows of K channels (rows from t0 on of one head) between memory, registers and LDS, 16 bytes a
-// piece: lane = row, so that a transposed copy is written without conflicts.  Loads have no condition (a
+// piece: lane = row.  Loads have no condition (a
 // conditional one is waited for where its branch ends, and the next chunk's are to stay in flight).
 template <typename IO, int KP>
 struct HeadRows {
@@ -261,98 +224,124 @@ struct HeadRows {
             *reinterpret_cast<u4 *>(lds + lane * STRIDE + c) = r.r[i];
         }
     }
-    template <int WAVES>
-    static __device__ __forceinline__ void store_transposed(const Regs<WAVES> &r, E *lds) {
-        const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-#pragma unroll
-        for (int i = 0; i < KP / PER / WAVES; ++i) {
-            const int c = (wave * (KP / PER / WAVES) + i) * PER;
-            E e[PER];
-            __builtin_memcpy(e, &r.r[i], 16);
-#pragma unroll
-            for (int j = 0; j < PER; ++j) lds[(c + j) * TSTRIDE + lane] = e[j];
-        }
-    }
 };
 
-// A 64 x 64 matrix of a chunk in the workspace: fp32, or bf16 planes.
-template <typename IO, int P>
-struct ChunkMatrix {
+// Planes of a matrix whose rows are `STRIDE` elements apart and whose planes are `PLANE` apart: the value
+// itself in fp32, the sum of `P` bf16 numbers else.  Four consecutive values of a row, or one.
+template <typename IO, int P, int PLANE>
+__device__ __forceinline__ void put_planes4(typename Op<IO>::elem *to, f4 v) {
+    if constexpr (IO::bytes == 4) {
+        *reinterpret_cast<f4 *>(to) = v;
+    } else {
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            b4 q;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const b2 w = __builtin_convertvector((f2){v[2 * i], v[2 * i + 1]}, b2);
+                q[2 * i] = w[0];
+                q[2 * i + 1] = w[1];
+            }
+            if (p + 1 < P)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] -= (float)q[i];
+            *reinterpret_cast<b4 *>(to + p * PLANE) = q;
+        }
+    }
+}
+template <typename IO, int P, int PLANE>
+__device__ __forceinline__ void put_planes(typename Op<IO>::elem *to, float v) {
+#pragma unroll
+    for (int p = 0; p < (IO::bytes == 2 ? P : 1); ++p) {
+        const typename Op<IO>::elem q = (typename Op<IO>::elem)v;
+        to[p * PLANE] = q;
+        v -= (float)q;
+    }
+}
+
+// ROWS x WIDTH numbers in LDS as `P` planes (one in fp32), rows padded by 16 bytes.
+template <typename IO, int ROWS, int WIDTH, int P>
+struct Slab {
     using E = typename Op<IO>::elem;
     static constexpr int PLANES = IO::bytes == 2 ? P : 1;
-    static constexpr int PER = 16 / IO::bytes;
-    static constexpr int STRIDE = kC + PER, PLANE = kC * STRIDE;  // in LDS
-    static constexpr int ELEMS = PLANES * kC * kC;                // in the workspace
-    static constexpr int PIECES = ELEMS / PER;
-    template <int THREADS>
-    struct Regs {
-        u4 r[PIECES / THREADS];
-    };
-    template <int THREADS>
-    static __device__ __forceinline__ void load(Regs<THREADS> &r, const E *from) {
-#pragma unroll
-        for (int i = 0; i < PIECES / THREADS; ++i)
-            r.r[i] = reinterpret_cast<const u4 *>(from)[threadIdx.x + THREADS * i];
+    static constexpr int STRIDE = WIDTH + 16 / IO::bytes, PLANE = ROWS * STRIDE;
+    alignas(16) E e[PLANES * PLANE];
+    __device__ __forceinline__ void put4(int row, int col, f4 v) {
+        put_planes4<IO, PLANES, PLANE>(e + row * STRIDE + col, v);
     }
-    template <int THREADS>
-    static __device__ __forceinline__ void store(const Regs<THREADS> &r, E *lds) {
-#pragma unroll
-        for (int i = 0; i < PIECES / THREADS; ++i) {
-            const int at = threadIdx.x + THREADS * i, row = at / (kC / PER), c = at % (kC / PER);
-            *reinterpret_cast<u4 *>(lds + row * STRIDE + c * PER) = r.r[i];
-        }
+    __device__ __forceinline__ void put(int row, int col, float v) {
+        put_planes<IO, PLANES, PLANE>(e + row * STRIDE + col, v);
     }
-    // four values of one row of the matrix (or column, where it is kept transposed), at row and col .. + 3
-    static __device__ __forceinline__ void put4(E *to, int row, int col, f4 v) {
-        if constexpr (IO::bytes == 4) {
-            *reinterpret_cast<f4 *>(to + row * kC + col) = v;
-        } else {
-#pragma unroll
-            for (int p = 0; p < PLANES; ++p) {
-                b4 q;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    q[i] = (__bf16)v[i];
-                    v[i] -= (float)q[i];
-                }
-                *reinterpret_cast<b4 *>(to + p * kC * kC + row * kC + col) = q;
-            }
-        }
+    // the first N planes of the eight numbers at row, col
+    template <int N = PLANES>
+    __device__ __forceinline__ auto get(int row, int col) const {
+        return Op<IO>::template planes<N>(e + row * STRIDE + col, PLANE);
     }
-    static __device__ __forceinline__ void put(E *to, int row, int col, float v) {
-#pragma unroll
-        for (int p = 0; p < PLANES; ++p) {
-            const E q = (E)v;
-            to[p * kC * kC + row * kC + col] = q;
-            v -= (float)q;
-        }
-    }
+    __device__ __forceinline__ auto get_exact(int row, int col) const { return Op<IO>::load(e + row * STRIDE + col); }
 };
 
-// What the chunks hand to the chains, one block per (row, head, chunk): the row vectors, the inverse and
-// the attention matrix, both transposed for the backward chain.
+// What the chunks hand to the chains, one block per (row, head, chunk) in the workspace: vectors over the
+// steps; the inverse and the attention matrix (transposed for the backward chain), planes of 64 x 64; the
+// keys, and for the backward the queries, transposed (KP x 64).
 enum { kVecKEnter, kVecKLeave, kVecQEnter, kVecBeta, kVecThrough, kVecs };
 
-template <typename IO>
+template <typename IO, int KP, bool BWD>
 struct ChunkBlock {
-    using Inv = ChunkMatrix<IO, 3>;
-    using Att = ChunkMatrix<IO, 2>;   // forward: for the outputs alone
-    using AttT = ChunkMatrix<IO, 3>;  // backward
-    static constexpr size_t kVecBytes = kVecs * kC * sizeof(float);
-    static constexpr size_t kInvBytes = Inv::ELEMS * IO::bytes;
-    static constexpr size_t kBytes = kVecBytes + kInvBytes + AttT::ELEMS * IO::bytes;
+    using E = typename Op<IO>::elem;
+    static constexpr int PLANE = kC * kC;
+    static constexpr int INV = IO::bytes == 2 ? 3 : 1;            // planes of the inverse
+    static constexpr int ATT = IO::bytes == 2 ? (BWD ? 3 : 2) : 1;  // forward: for the outputs alone
+    static constexpr size_t kInv = kVecs * kC * sizeof(float);    // byte offsets
+    static constexpr size_t kAtt = kInv + (size_t)INV * PLANE * IO::bytes;
+    static constexpr size_t kKt = kAtt + (size_t)ATT * PLANE * IO::bytes;
+    static constexpr size_t kQt = kKt + (size_t)KP * kC * IO::bytes;
+    static constexpr size_t kBytes = BWD ? kQt + (size_t)KP * kC * IO::bytes : kQt;
 };
 
-// A state's column (rows of `to`, V apart) from a wave's registers.
-template <int KT>
-__device__ __forceinline__ void store_state(float *to, int K, int V, int grp, const f4 (&s)[KT]) {
+// The chains' workgroups: one head's 16 NC value channels each, heads dealt out to the 8 XCDs (workgroups
+// go to them in turn), so that the workgroups that read the same chunks share an L2.
+struct ChainPlace {
+    int64_t head;
+    int slice;
+    bool any;
+};
+__device__ __forceinline__ ChainPlace chain_place(int64_t heads, int slices) {
+    const int64_t turn = blockIdx.x / 8;
+    ChainPlace p;
+    p.head = turn / slices * 8 + blockIdx.x % 8;
+    p.slice = (int)(turn % slices);
+    p.any = p.head < heads;
+    return p;
+}
+inline unsigned chain_grid(int64_t heads, int slices) { return (unsigned)((heads + 7) / 8 * 8 * slices); }
+
+// Value channels of a chain's workgroup: 32, or 16 where 32 would leave CUs without one.  Measured: see the
+// chain kernel.
+inline int chain_columns(const Call &a) { return a.B * a.H * ((a.V + 31) / 32) >= 256 ? 2 : 1; }
+
+// A tensor's place for a whole wave and a lane's distance from it in bytes: one address register a lane.
+template <typename T>
+__device__ __forceinline__ T &at(const void *base, uint32_t off) {
+    return *reinterpret_cast<T *>(const_cast<char *>(static_cast<const char *>(base)) + off);
+}
+template <typename T>
+__device__ __forceinline__ const char *bytes(const T *p, int64_t elements, int64_t size) {
+    return reinterpret_cast<const char *>(p) + elements * size;
+}
+
+// A wave's rows of a state (from k0 on, V floats each) into memory.
+template <int ST, int NC>
+__device__ __forceinline__ void store_rows(char *to, uint32_t v_row, int K, int k0, bool every, const uint32_t (&v)[NC],
+                                           const bool (&live)[NC], const f4 (&s)[ST][NC]) {
 #pragma unroll
-    for (int kt = 0; kt < KT; ++kt)
+    for (int n = 0; n < NC; ++n)
+        if (live[n])
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int k = pair_row(kt, grp, i);
-            if (K == 16 * KT || k < K) to[k * V] = s[kt][i];
-        }
+            for (int j = 0; j < ST; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (every || k0 + 16 * j + i < K)
+                        at<float>(to + (16 * j + i) * (int64_t)v_row, k0 * v_row + v[n] * 4) = s[j][n][i];
 }
 
 // An element as it lies in memory, kept so until it is used.
@@ -366,14 +355,9 @@ struct RawOne {
             return v;
     }
 };
-template <typename IO>
-__device__ __forceinline__ RawOne<IO> load_one(const void *p, int64_t i) {
-    return {static_cast<const typename IO::storage *>(p)[i]};
-}
-
-// Enqueue the chunks' kernel (gated_delta.hip); `blocks`: ChunkBlock<IO>::kBytes a chunk.
+// Enqueue the chunks' kernel (gated_delta.hip); `blocks`: block_bytes a chunk.
 hipError_t launch_prepare(const Call &a, int io_dtype, bool backward, char *blocks, hipStream_t stream);
-size_t block_bytes(int io_dtype);
+size_t block_bytes(int io_dtype, int64_t kdim, bool backward);
 // The forward chain; o, h_final and ck may be NULL.
 hipError_t launch_chain(const Call &a, int io_dtype, const char *blocks, const float *h0, void *o, float *h_final,
                         float *ck, hipStream_t stream);

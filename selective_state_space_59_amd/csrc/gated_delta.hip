@@ -8,8 +8,7 @@
 //   O  = scale enter Q S + P diag(beta) E
 //   S <- through S + (leave K)^T diag(beta) E
 // prepare_kernel forms the inverse of I + B diag(beta) and P for every chunk at once; chain_kernel
-// then carries the states from chunk to chunk, each wave the 16 value channels whose states it holds in
-// registers, apart from the others.
+// then carries the states from chunk to chunk, each workgroup 16 or 32 value channels apart from the others.
 #include "delta_tile.h"
 
 #include <algorithm>
@@ -53,7 +52,7 @@ __global__ __launch_bounds__(kThreads) void prepare_kernel(Call a, char *blocks)
     using O = Op<IO>;
     using E = typename O::elem;
     using Rows = HeadRows<IO, KP>;
-    using Block = ChunkBlock<IO>;
+    using Block = ChunkBlock<IO, KP, BWD>;
     __shared__ __attribute__((aligned(16))) PrepareLds<IO, KP> s;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r16 = lane % 16, grp = lane / 16;
     const int64_t c = blockIdx.x, b = blockIdx.z;
@@ -76,8 +75,21 @@ __global__ __launch_bounds__(kThreads) void prepare_kernel(Call a, char *blocks)
 
     char *block = blocks + ((b * a.H + h) * a.n + c) * Block::kBytes;
     float *vec = reinterpret_cast<float *>(block);
-    E *inv = reinterpret_cast<E *>(block + Block::kVecBytes);
-    E *att = reinterpret_cast<E *>(block + Block::kVecBytes + Block::kInvBytes);
+    E *inv = reinterpret_cast<E *>(block + Block::kInv), *att = reinterpret_cast<E *>(block + Block::kAtt);
+    // keys and queries transposed, 16 bytes (of consecutive steps) a piece
+    constexpr int PER = Rows::PER;
+    for (int i = threadIdx.x; i < KP * kC / PER; i += kThreads) {
+        const int k = i % KP, t = i / KP * PER;
+        E x[PER];
+#pragma unroll
+        for (int j = 0; j < PER; ++j) x[j] = s.k[(t + j) * Rows::STRIDE + k];
+        __builtin_memcpy(block + Block::kKt + (k * kC + t) * sizeof(E), x, 16);
+        if constexpr (BWD) {
+#pragma unroll
+            for (int j = 0; j < PER; ++j) x[j] = s.q[(t + j) * Rows::STRIDE + k];
+            __builtin_memcpy(block + Block::kQt + (k * kC + t) * sizeof(E), x, 16);
+        }
+    }
     if (threadIdx.x < kC) {
         const int t = threadIdx.x;
         vec[kVecKEnter * kC + t] = s.gates.enter[t] * s.gates.rk[t];
@@ -114,10 +126,11 @@ __global__ __launch_bounds__(kThreads) void prepare_kernel(Call a, char *blocks)
             continue;  // above the pairs of tiles that are read
         }
         if constexpr (BWD) {
-            Block::AttT::put4(att, u, 16 * wave + 4 * grp, qk);
+            put_planes4<IO, Block::ATT, Block::PLANE>(att + u * kC + 16 * wave + 4 * grp, qk);
         } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) Block::Att::put(att, 16 * wave + 4 * grp + i, u, qk[i]);
+            for (int i = 0; i < 4; ++i)
+                put_planes<IO, Block::ATT, Block::PLANE>(att + (16 * wave + 4 * grp + i) * kC + u, qk[i]);
         }
     }
     __syncthreads();
@@ -161,26 +174,23 @@ __global__ __launch_bounds__(kThreads) void prepare_kernel(Call a, char *blocks)
         col[i] = v;
         if (i >= wave || i == (wave ^ 1)) {
             if constexpr (BWD) {
-                Block::Inv::put4(inv, 16 * wave + r16, 16 * i + 4 * grp, v);
+                put_planes4<IO, Block::INV, Block::PLANE>(inv + (16 * wave + r16) * kC + 16 * i + 4 * grp, v);
             } else {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) Block::Inv::put(inv, 16 * i + 4 * grp + e, 16 * wave + r16, v[e]);
+                for (int e = 0; e < 4; ++e)
+                    put_planes<IO, Block::INV, Block::PLANE>(inv + (16 * i + 4 * grp + e) * kC + 16 * wave + r16, v[e]);
             }
         }
     }
 }
 
 // ----------------------------------------------------------------------------------- chain
-template <typename IO, int KP>
+template <typename IO, int KP, int NC>
 struct ChainLds {
-    using Rows = HeadRows<IO, KP>;
-    using Block = ChunkBlock<IO>;
-    using E = typename Op<IO>::elem;
-    static constexpr bool kTransposed = IO::bytes == 2;
-    alignas(16) E q[kC * Rows::STRIDE], k[kC * Rows::STRIDE];
-    alignas(16) E kt[kTransposed ? KP * Rows::TSTRIDE : 8];
-    alignas(16) E inv[Block::Inv::PLANES * Block::Inv::PLANE], att[Block::Att::PLANES * Block::Att::PLANE];
-    alignas(16) float vec[kVecs * kC];
+    static constexpr int PL = Op<IO>::kPlanes, OUT = PL == 1 ? 1 : 2;
+    Slab<IO, 16 * NC, KP, PL> state;  // column by column, as right operands
+    Slab<IO, 16 * NC, kC, PL> x, w;   // X; leave diag(beta) E
+    Slab<IO, 16 * NC, kC, OUT> u;     // diag(beta) E
 };
 
 struct ChainArgs {
@@ -189,198 +199,209 @@ struct ChainArgs {
     const float *h0;
     void *o;
     float *h_final, *ck;
+    int slices;
 };
 
-template <typename IO, int KP>
-__global__ __launch_bounds__(kThreads) void chain_kernel(ChainArgs p) {
+// Four waves carry 16 NC value channels of one head along the chunks.  Wave w has the steps 16 w .. + 15 of
+// the chunk in every product over steps and the rows KP/4 w .. of the state.  What it needs of the keys,
+// queries and the chunk's matrices no other wave of the workgroup reads, so it comes from memory straight
+// into registers, reloaded for the next chunk as soon as it has been used; only states, X and E go round
+// through LDS, split into their planes once, by the wave that owns them.  Three barriers a chunk.
+template <typename IO, int KP, int NC>
+__global__ __launch_bounds__(kThreads, 2) void chain_kernel(ChainArgs p) {
     using O = Op<IO>;
     using E = typename O::elem;
-    using Rows = HeadRows<IO, KP>;
-    using Block = ChunkBlock<IO>;
-    using Lds = ChainLds<IO, KP>;
-    constexpr int KT = KP / 16, PL = O::kPlanes, OUT = PL == 1 ? 1 : 2;
+    using Block = ChunkBlock<IO, KP, false>;
+    using Lds = ChainLds<IO, KP, NC>;
+    constexpr int KX = KP / 32, ST = KP / 64, PL = Lds::PL, OUT = Lds::OUT;
     extern __shared__ __attribute__((aligned(16))) char raw[];
     Lds &s = *reinterpret_cast<Lds *>(raw);
     const Call &a = p.a;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r16 = lane % 16, grp = lane / 16;
-    const int64_t b = blockIdx.z;
-    const int h = blockIdx.y, hk = h / (a.H / a.Hk);
-    // lanes past the last channel repeat it and store nothing
-    const int vw = (blockIdx.x * (kThreads / 64) + wave) * 16 + r16, v = min(vw, a.V - 1);
-    const bool live = vw < a.V;
-    const int64_t head = b * a.H + h;
+    const ChainPlace place = chain_place(a.B * a.H, p.slices);
+    if (!place.any) return;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int r16 = lane % 16, grp = lane / 16;
+    const int64_t head = place.head, b = head / a.H;
+    const int h = (int)(head % a.H), hk = h / (a.H / a.Hk);
+    const int row = 16 * wave + r16, mine = 16 * wave + 4 * grp;  // left operands' row; results' first row
     const char *blocks = p.blocks + head * a.n * Block::kBytes;
-    const int64_t q_off = b * a.q_batch + (int64_t)hk * a.K, k_off = b * a.k_batch + (int64_t)hk * a.K;
-    const int64_t v_off = b * a.v_batch + (int64_t)h * a.V + v;
-
-    f4 state[KT];
+    const char *q_base = bytes(static_cast<const char *>(a.q), b * a.q_batch + (int64_t)hk * a.K, IO::bytes);
+    const char *k_base = bytes(static_cast<const char *>(a.k), b * a.k_batch + (int64_t)hk * a.K, IO::bytes);
+    const char *v_base = bytes(static_cast<const char *>(a.v), b * a.v_batch + (int64_t)h * a.V, IO::bytes);
+    char *o_base = static_cast<char *>(p.o) + (b * a.L * a.H + h) * a.V * IO::bytes;
+    const uint32_t q_step = (uint32_t)a.q_token * IO::bytes, k_step = (uint32_t)a.k_token * IO::bytes;
+    const uint32_t v_step = (uint32_t)a.v_token * IO::bytes, o_step = (uint32_t)(a.H * a.V) * IO::bytes;
+    // lanes past the last channel repeat it and store nothing
+    uint32_t v[NC];
+    bool live[NC];
 #pragma unroll
-    for (int kt = 0; kt < KT; ++kt)
+    for (int n = 0; n < NC; ++n) {
+        const int vw = 16 * (place.slice * NC + n) + r16;
+        v[n] = min(vw, a.V - 1);
+        live[n] = vw < a.V;
+    }
+
+    f4 state[ST][NC];
+#pragma unroll
+    for (int j = 0; j < ST; ++j)
+#pragma unroll
+        for (int n = 0; n < NC; ++n) {
+            const int k0 = 16 * (ST * wave + j) + 4 * grp;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                state[j][n][i] = p.h0 && k0 + i < a.K ? p.h0[(head * a.K + k0 + i) * a.V + v[n]] : 0.0f;
+            s.state.put4(16 * n + r16, k0, state[j][n]);
+        }
+
+    typename O::Ex kf[KX], qf[KX], ktf[ST][2];
+    typename O::template Sum<PL> inv[2];
+    typename O::template Sum<OUT> att[2];
+    f4 k_enter, k_leave, q_enter, beta;
+    float through;
+    RawOne<IO> val[NC][4];
+    // (no load has a condition: one that has is waited for where its branch ends)
+    // a step of the chunk that is there
+    const auto step_of = [&](int64_t c, int t) { return (uint32_t)min((int64_t)t, a.L - 1 - c * kC); };
+    const auto load_qk = [&](int64_t c) {
+        const char *kc = k_base + c * kC * (int64_t)k_step, *qc = q_base + c * kC * (int64_t)q_step;
+        const uint32_t t = step_of(c, row);
+#pragma unroll
+        for (int x = 0; x < KX; ++x) {
+            const uint32_t off = (32 * x + 8 * grp < a.K ? 32 * x + 8 * grp : 0) * IO::bytes;
+            kf[x] = O::load(&at<E>(kc, t * k_step + off));
+            qf[x] = O::load(&at<E>(qc, t * q_step + off));
+        }
+    };
+    const auto load_vec = [&](int64_t c) {
+        const char *vec = blocks + c * Block::kBytes;
+        k_enter = at<f4>(vec, (kVecKEnter * kC + mine) * 4);
+        k_leave = at<f4>(vec, (kVecKLeave * kC + mine) * 4);
+        q_enter = at<f4>(vec, (kVecQEnter * kC + mine) * 4);
+        beta = at<f4>(vec, (kVecBeta * kC + mine) * 4);
+        through = at<float>(vec, kVecThrough * kC * 4);
+    };
+    const auto load_val = [&](int64_t c) {
+        const char *vc = v_base + c * kC * (int64_t)v_step;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int k = pair_row(kt, grp, i);
-            state[kt][i] = p.h0 && k < a.K ? p.h0[(head * a.K + k) * a.V + v] : 0.0f;
-        }
-
-    // the next chunk's tiles, on their way while this one is computed
-    typename Rows::template Regs<4> rq, rk;
-    typename Block::Inv::template Regs<kThreads> rinv;
-    typename Block::Att::template Regs<kThreads> ratt;
-    float rvec[2];
-    RawOne<IO> rv[4][4];
-    const auto fetch = [&](int64_t c) {
-        const char *block = blocks + c * Block::kBytes;
-        Rows::template load<4>(rq, a.q, q_off, a.q_token, c * kC, a.L, a.K);
-        Rows::template load<4>(rk, a.k, k_off, a.k_token, c * kC, a.L, a.K);
-        Block::Inv::template load<kThreads>(rinv, reinterpret_cast<const E *>(block + Block::kVecBytes));
-        Block::Att::template load<kThreads>(
-            ratt, reinterpret_cast<const E *>(block + Block::kVecBytes + Block::kInvBytes));
+            const uint32_t t = step_of(c, mine + i) * v_step;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int at = min((int)threadIdx.x + kThreads * i, kVecs * kC - 1);
-            rvec[i] = reinterpret_cast<const float *>(block)[at];
+            for (int n = 0; n < NC; ++n) val[n][i] = at<RawOne<IO>>(vc, t + v[n] * IO::bytes);
         }
+    };
+    // (the waves of the upper half have no second block of columns: they load the first twice)
+    const int y1 = wave / 2 * 32;
+    const uint32_t m_off = (row * kC + 8 * grp) * IO::bytes;
+    const auto load_inv = [&](int64_t c) {
+        const char *m = blocks + c * Block::kBytes + Block::kInv;
+        inv[0] = O::template planes<PL>(&at<E>(m, m_off), Block::PLANE);
+        inv[1] = O::template planes<PL>(&at<E>(m + y1 * IO::bytes, m_off), Block::PLANE);
+    };
+    const auto load_att = [&](int64_t c) {
+        const char *m = blocks + c * Block::kBytes + Block::kAtt;
+        att[0] = O::template planes<OUT>(&at<E>(m, m_off), Block::PLANE);
+        att[1] = O::template planes<OUT>(&at<E>(m + y1 * IO::bytes, m_off), Block::PLANE);
+    };
+    const auto load_kt = [&](int64_t c) {
+        const char *m = blocks + c * Block::kBytes + Block::kKt + 16 * ST * wave * kC * IO::bytes;
 #pragma unroll
-        for (int tt = 0; tt < 4; ++tt)
+        for (int j = 0; j < ST; ++j)
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+                ktf[j][y] = O::load(&at<E>(m + (16 * j * kC + 32 * y) * IO::bytes, (r16 * kC + 8 * grp) * IO::bytes));
+    };
+    const uint32_t v_row = (uint32_t)a.V * 4;  // a state's row in bytes
+    load_qk(0);
+    load_vec(0);
+    load_val(0);
+    load_inv(0);
+    load_kt(0);
+    load_att(0);
+    __syncthreads();
+    for (int64_t c = 0; c < a.n; ++c) {
+        const int64_t next = min(c + 1, a.n - 1);
+        const bool whole = (c + 1) * kC <= a.L;
+        char *ck = reinterpret_cast<char *>(p.ck) + (c * a.B * a.H + head) * (a.K + kC) * (int64_t)v_row;
+        if (!whole || a.K != KP)  // steps past the end and channels past K, which were loaded from elsewhere
+#pragma unroll
+            for (int x = 0; x < KX; ++x)
+                if (c * kC + row >= a.L || 32 * x + 8 * grp >= a.K) kf[x] = qf[x] = typename O::Ex{};
+        // K S and Q S
+        f4 ks[NC] = {}, o[NC] = {};
+#pragma unroll
+        for (int x = 0; x < KX; ++x)
+#pragma unroll
+            for (int n = 0; n < NC; ++n) {
+                const auto st = s.state.template get<PL>(16 * n + r16, 32 * x + 8 * grp);
+                ks[n] = O::mul(ks[n], kf[x], st);
+                o[n] = O::mul(o[n], qf[x], O::template first<OUT>(st));
+            }
+        load_qk(next);
+        // X = V - enter K S (a state that does not reach a step has no part in it, whatever it holds)
+#pragma unroll
+        for (int n = 0; n < NC; ++n) {
+            f4 x;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int64_t t = c * kC + pair_row(tt, grp, i);
-                rv[tt][i] = load_one<IO>(a.v, v_off + (t < a.L ? t : a.L - 1) * a.v_token);
+                x[i] = whole || c * kC + mine + i < a.L ? val[n][i].get() : 0.0f;
+                x[i] = k_enter[i] != 0.0f ? __builtin_fmaf(-k_enter[i], ks[n][i], x[i]) : x[i];
+                o[n][i] = q_enter[i] != 0.0f ? q_enter[i] * o[n][i] : 0.0f;
             }
-    };
-    fetch(0);
-    for (int64_t c = 0; c < a.n; ++c) {
-        __syncthreads();  // the last chunk's tiles have been read
-        const bool whole = (c + 1) * kC <= a.L;
-        Rows::template cut<4>(rq, c * kC, a.L, a.K);
-        Rows::template cut<4>(rk, c * kC, a.L, a.K);
-        Rows::template store<4>(rq, s.q);
-        Rows::template store<4>(rk, s.k);
-        if constexpr (Lds::kTransposed) Rows::template store_transposed<4>(rk, s.kt);
-        Block::Inv::template store<kThreads>(rinv, s.inv);
-        Block::Att::template store<kThreads>(ratt, s.att);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int at = threadIdx.x + kThreads * i;
-            if (at < kVecs * kC) s.vec[at] = rvec[i];
+            s.x.put4(16 * n + r16, mine, x);
         }
-        f4 val[4];
-#pragma unroll
-        for (int tt = 0; tt < 4; ++tt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                val[tt][i] = whole || c * kC + pair_row(tt, grp, i) < a.L ? rv[tt][i].get() : 0.0f;
+        load_val(next);
+        if (p.ck) store_rows<ST, NC>(ck, v_row, a.K, 16 * ST * wave + 4 * grp, a.K == KP, v, live, state);
         __syncthreads();
-        if (c + 1 < a.n) fetch(c + 1);
-
-        float *ck = p.ck ? p.ck + (((c * a.B + b) * a.H + h) * (a.K + kC)) * a.V + v : nullptr;
-        if (ck && live) store_state<KT>(ck, a.K, a.V, grp, state);
-
-        // K S and Q S
-        f4 ks[4] = {}, qs[4] = {};
+        // (I + B diag(beta)) E = X
 #pragma unroll
-        for (int x = 0; x < KT / 2; ++x) {
-            const auto st = O::template sum<PL>(state[2 * x], state[2 * x + 1]);
-            typename O::template Sum<OUT> so;
-            if constexpr (PL == 1) {
-                so = st;
-            } else {
-                so.p[0] = st.p[0];
-                so.p[1] = st.p[1];
-            }
+        for (int n = 0; n < NC; ++n) {
+            f4 err = O::mul(f4{0, 0, 0, 0}, inv[0], s.x.get(16 * n + r16, 8 * grp));
+            if (wave >= 2) err = O::mul(err, inv[1], s.x.get(16 * n + r16, 32 + 8 * grp));
+            const f4 u = beta * err;
+            s.w.put4(16 * n + r16, mine, k_leave * u);
+            s.u.put4(16 * n + r16, mine, u);
+            if (p.ck && live[n])
 #pragma unroll
-            for (int tt = 0; tt < 4; ++tt) {
-                const int row = pair_row16(tt, r16);
-                ks[tt] = O::mul(ks[tt], O::load(s.k + row * Rows::STRIDE + 32 * x + 8 * grp), st);
-                qs[tt] = O::mul(qs[tt], O::load(s.q + row * Rows::STRIDE + 32 * x + 8 * grp), so);
-            }
+                for (int i = 0; i < 4; ++i) at<float>(ck + (a.K + i) * (int64_t)v_row, mine * v_row + v[n] * 4) = err[i];
         }
-        // X = V - enter K S (a state that does not reach a step has no part in it, whatever it holds)
-        f4 err[4] = {};
-        typename O::template Sum<PL> xs[2];
-#pragma unroll
-        for (int tt = 0; tt < 4; ++tt) {
-            const f4 en = *reinterpret_cast<const f4 *>(s.vec + kVecKEnter * kC + pair_row(tt, grp, 0));
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (en[i] != 0.0f) val[tt][i] = __builtin_fmaf(-en[i], ks[tt][i], val[tt][i]);
-        }
-#pragma unroll
-        for (int y = 0; y < 2; ++y) xs[y] = O::template sum<PL>(val[2 * y], val[2 * y + 1]);
-#pragma unroll
-        for (int tt = 0; tt < 4; ++tt)
-#pragma unroll
-            for (int y = 0; y <= tt / 2; ++y)
-                err[tt] = O::mul(err[tt],
-                                 O::template planes<PL>(s.inv + pair_row16(tt, r16) * Block::Inv::STRIDE + 32 * y + 8 * grp,
-                                                        Block::Inv::PLANE),
-                                 xs[y]);
-        if (ck && live)
-#pragma unroll
-            for (int tt = 0; tt < 4; ++tt)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) ck[(int64_t)(a.K + pair_row(tt, grp, i)) * a.V] = err[tt][i];
+        load_inv(next);
+        const float pass = through;
+        load_vec(next);
+        __syncthreads();
         // S <- through S + (leave K)^T diag(beta) E
-        f4 u[4];
 #pragma unroll
-        for (int tt = 0; tt < 4; ++tt)
-            u[tt] = err[tt] * *reinterpret_cast<const f4 *>(s.vec + kVecBeta * kC + pair_row(tt, grp, 0));
-        {
-            typename O::template Sum<PL> ws[2];
+        for (int n = 0; n < NC; ++n) {
+            const auto w0 = s.w.get(16 * n + r16, 8 * grp), w1 = s.w.get(16 * n + r16, 32 + 8 * grp);
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
-                const f4 l0 = *reinterpret_cast<const f4 *>(s.vec + kVecKLeave * kC + pair_row(2 * y, grp, 0));
-                const f4 l1 = *reinterpret_cast<const f4 *>(s.vec + kVecKLeave * kC + pair_row(2 * y + 1, grp, 0));
-                ws[y] = O::template sum<PL>(u[2 * y] * l0, u[2 * y + 1] * l1);
-            }
-            const float through = s.vec[kVecThrough * kC];
+            for (int j = 0; j < ST; ++j) {
+                f4 &st = state[j][n];
 #pragma unroll
-            for (int kt = 0; kt < KT; ++kt) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) state[kt][i] = through != 0.0f ? through * state[kt][i] : 0.0f;
-#pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    typename O::Ex left;
-                    if constexpr (Lds::kTransposed)
-                        left = O::load(s.kt + pair_row16(kt, r16) * Rows::TSTRIDE + 32 * y + 8 * grp);
-                    else
-                        left = Op<IO>::gather(s.k + (32 * y + 8 * grp) * Rows::STRIDE + pair_row16(kt, r16), Rows::STRIDE);
-                    state[kt] = O::mul(state[kt], left, ws[y]);
-                }
+                for (int i = 0; i < 4; ++i) st[i] = pass != 0.0f ? pass * st[i] : 0.0f;
+                st = O::mul(O::mul(st, ktf[j][0], w0), ktf[j][1], w1);
+                s.state.put4(16 * n + r16, 16 * (ST * wave + j) + 4 * grp, st);
             }
         }
+        load_kt(next);
         // O = scale enter Q S + P diag(beta) E
         if (p.o) {
-            typename O::template Sum<OUT> us[2];
+            char *oc = o_base + (c * kC + 16 * wave) * (int64_t)o_step;
 #pragma unroll
-            for (int y = 0; y < 2; ++y) us[y] = O::template sum<OUT>(u[2 * y], u[2 * y + 1]);
+            for (int n = 0; n < NC; ++n) {
+                o[n] = O::mul(o[n], att[0], s.u.get(16 * n + r16, 8 * grp));
+                if (wave >= 2) o[n] = O::mul(o[n], att[1], s.u.get(16 * n + r16, 32 + 8 * grp));
+                if (live[n])
 #pragma unroll
-            for (int tt = 0; tt < 4; ++tt) {
-                const f4 en = *reinterpret_cast<const f4 *>(s.vec + kVecQEnter * kC + pair_row(tt, grp, 0));
-#pragma unroll
-                for (int i = 0; i < 4; ++i) qs[tt][i] = en[i] != 0.0f ? en[i] * qs[tt][i] : 0.0f;
-#pragma unroll
-                for (int y = 0; y <= tt / 2; ++y)
-                    qs[tt] = O::mul(qs[tt],
-                                    O::template planes<OUT>(
-                                        s.att + pair_row16(tt, r16) * Block::Att::STRIDE + 32 * y + 8 * grp,
-                                        Block::Att::PLANE),
-                                    us[y]);
-            }
-            if (live) {
-                const int64_t at = ((b * a.L + c * kC) * a.H + h) * a.V + v;
-                const int step = a.H * a.V;
-#pragma unroll
-                for (int tt = 0; tt < 4; ++tt)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int t = pair_row(tt, grp, i);
-                        if (whole || c * kC + t < a.L) store_io<IO>(p.o, at + (int64_t)t * step, qs[tt][i]);
-                    }
+                    for (int i = 0; i < 4; ++i)
+                        if (whole || c * kC + mine + i < a.L)
+                            store_io<IO>(&at<char>(oc + i * (int64_t)o_step, 4 * grp * o_step + v[n] * IO::bytes), 0, o[n][i]);
             }
         }
+        load_att(next);
+        __syncthreads();
     }
-    if (p.h_final && live) store_state<KT>(p.h_final + head * a.K * a.V + v, a.K, a.V, grp, state);
+    if (p.h_final)
+        store_rows<ST, NC>(reinterpret_cast<char *>(p.h_final) + head * a.K * (int64_t)v_row, v_row, a.K,
+                           16 * ST * wave + 4 * grp, a.K == KP, v, live, state);
 }
 
 // ------------------------------------------------------------------------------------ step
@@ -505,10 +526,14 @@ hipError_t prepare(const Call &a, bool backward, char *blocks, hipStream_t strea
 }
 
 template <typename IO, int KP>
-hipError_t chain(const ChainArgs &p, hipStream_t stream) {
-    const unsigned per = 16 * (kThreads / 64);
-    const dim3 grid(((unsigned)p.a.V + per - 1) / per, (unsigned)p.a.H, (unsigned)p.a.B);
-    chain_kernel<IO, KP><<<grid, kThreads, sizeof(ChainLds<IO, KP>), stream>>>(p);
+hipError_t chain(ChainArgs p, hipStream_t stream) {
+    const int nc = chain_columns(p.a);
+    p.slices = (p.a.V + 16 * nc - 1) / (16 * nc);
+    const unsigned grid = chain_grid(p.a.B * p.a.H, p.slices);
+    if (nc == 2)
+        chain_kernel<IO, KP, 2><<<grid, kThreads, sizeof(ChainLds<IO, KP, 2>), stream>>>(p);
+    else
+        chain_kernel<IO, KP, 1><<<grid, kThreads, sizeof(ChainLds<IO, KP, 1>), stream>>>(p);
     return hipGetLastError();
 }
 
@@ -521,8 +546,13 @@ hipError_t step(const StepArgs &p, hipStream_t stream) {
 
 }  // namespace
 
-size_t block_bytes(int io_dtype) {
-    return io_dtype == SSM_BF16 ? ChunkBlock<io_bf16>::kBytes : ChunkBlock<io_f32>::kBytes;
+size_t block_bytes(int io_dtype, int64_t kdim, bool backward) {
+    const auto of = [&](auto io) {
+        using IO = decltype(io);
+        if (kdim <= 64) return backward ? ChunkBlock<IO, 64, true>::kBytes : ChunkBlock<IO, 64, false>::kBytes;
+        return backward ? ChunkBlock<IO, 128, true>::kBytes : ChunkBlock<IO, 128, false>::kBytes;
+    };
+    return io_dtype == SSM_BF16 ? of(io_bf16{}) : of(io_f32{});
 }
 
 hipError_t launch_prepare(const Call &a, int io_dtype, bool backward, char *blocks, hipStream_t stream) {
@@ -535,7 +565,7 @@ hipError_t launch_prepare(const Call &a, int io_dtype, bool backward, char *bloc
 
 hipError_t launch_chain(const Call &a, int io_dtype, const char *blocks, const float *h0, void *o, float *h_final,
                         float *ck, hipStream_t stream) {
-    const ChainArgs p{a, blocks, h0, o, h_final, ck};
+    const ChainArgs p{a, blocks, h0, o, h_final, ck, 0};
     if (io_dtype == SSM_BF16) return a.K <= 64 ? chain<io_bf16, 64>(p, stream) : chain<io_bf16, 128>(p, stream);
     return a.K <= 64 ? chain<io_f32, 64>(p, stream) : chain<io_f32, 128>(p, stream);
 }
@@ -575,7 +605,7 @@ delta::Call call_of(const A &a) {
 
 size_t gated_delta_workspace_bytes(const ssm_gated_delta_args_t &a) {
     const int64_t n = (a.seqlen + delta::kC - 1) / delta::kC;
-    return (size_t)(a.batch * a.heads * n) * delta::block_bytes(a.io_dtype);
+    return (size_t)(a.batch * a.heads * n) * delta::block_bytes(a.io_dtype, a.kdim, false);
 }
 
 hipError_t launch_gated_delta_fwd(const ssm_gated_delta_args_t &a, hipStream_t stream) {

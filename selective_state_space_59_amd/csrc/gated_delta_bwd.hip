@@ -29,216 +29,231 @@ struct BackArgs {
     void *dv;
     float *dh0;
     float *after, *dx, *edu;  // workspace: (B,H,n,K,V), (B,H,n,64,V), (B,H,n,ceil(V/16),64)
+    int slices;
 };
 
-template <typename IO, int KP>
+template <typename IO, int KP, int NC>
 struct BackLds {
-    using Rows = HeadRows<IO, KP>;
-    using Block = ChunkBlock<IO>;
-    using E = typename Op<IO>::elem;
-    static constexpr bool kTransposed = IO::bytes == 2;
-    alignas(16) E k[kC * Rows::STRIDE];
-    alignas(16) E q[kTransposed ? 8 : kC * Rows::STRIDE];
-    alignas(16) E kt[kTransposed ? KP * Rows::TSTRIDE : 8], qt[kTransposed ? KP * Rows::TSTRIDE : 8];
-    alignas(16) E inv[Block::Inv::PLANES * Block::Inv::PLANE], att[Block::AttT::PLANES * Block::AttT::PLANE];
-    alignas(16) float vec[kVecs * kC];
+    static constexpr int PL = Op<IO>::kPlanes;
+    Slab<IO, 16 * NC, KP, PL> ds;       // column by column, as right operands
+    Slab<IO, 16 * NC, kC, PL> u, w, q;  // diag(beta) dU; -enter dX; scale enter dO
+    Slab<IO, 16 * NC, kC, 1> dout;
 };
 
-template <typename IO, int KP>
-__global__ __launch_bounds__(kThreads) void back_chain_kernel(BackArgs p) {
+// The forward's chain (chain_kernel) backwards: wave w has the steps 16 w .. + 15 and the rows KP/4 w .. of
+// the state's gradient.
+template <typename IO, int KP, int NC>
+__global__ __launch_bounds__(kThreads, 2) void back_chain_kernel(BackArgs p) {
     using O = Op<IO>;
     using E = typename O::elem;
-    using Rows = HeadRows<IO, KP>;
-    using Block = ChunkBlock<IO>;
-    using Lds = BackLds<IO, KP>;
-    constexpr int KT = KP / 16, PL = O::kPlanes;
+    using Block = ChunkBlock<IO, KP, true>;
+    using Lds = BackLds<IO, KP, NC>;
+    constexpr int KX = KP / 32, ST = KP / 64, PL = Lds::PL;
     extern __shared__ __attribute__((aligned(16))) char raw[];
     Lds &s = *reinterpret_cast<Lds *>(raw);
     const Call &a = p.a;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r16 = lane % 16, grp = lane / 16;
-    const int64_t b = blockIdx.z;
-    const int h = blockIdx.y, hk = h / (a.H / a.Hk);
-    const int strip = blockIdx.x * (kThreads / 64) + wave, strips = (a.V + 15) / 16;
-    // lanes past the last channel repeat it, store nothing and count for nothing
-    const int vw = strip * 16 + r16, v = min(vw, a.V - 1);
-    const bool live = vw < a.V;
-    const int64_t head = b * a.H + h;
+    const ChainPlace place = chain_place(a.B * a.H, p.slices);
+    if (!place.any) return;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int r16 = lane % 16, grp = lane / 16;
+    const int64_t head = place.head, b = head / a.H;
+    const int h = (int)(head % a.H), hk = h / (a.H / a.Hk);
+    const int row = 16 * wave + r16, mine = 16 * wave + 4 * grp;
+    const int strips = (a.V + 15) / 16;
     const char *blocks = p.blocks + head * a.n * Block::kBytes;
-    const int64_t q_off = b * a.q_batch + (int64_t)hk * a.K, k_off = b * a.k_batch + (int64_t)hk * a.K;
-
-    f4 ds[KT];
+    const char *k_base = bytes(static_cast<const char *>(a.k), b * a.k_batch + (int64_t)hk * a.K, IO::bytes);
+    const int64_t o_first = (b * a.L * a.H + h) * a.V * IO::bytes;
+    const char *do_base = static_cast<const char *>(p.dout) + o_first;
+    char *dv_base = static_cast<char *>(p.dv) + o_first;
+    const uint32_t k_step = (uint32_t)a.k_token * IO::bytes, o_step = (uint32_t)(a.H * a.V) * IO::bytes;
+    const uint32_t v_row = (uint32_t)a.V * 4;  // a state's row in bytes
+    // lanes past the last channel repeat it, store nothing and count for nothing
+    uint32_t v[NC];
+    bool live[NC];
 #pragma unroll
-    for (int kt = 0; kt < KT; ++kt)
+    for (int n = 0; n < NC; ++n) {
+        const int vw = 16 * (place.slice * NC + n) + r16;
+        v[n] = min(vw, a.V - 1);
+        live[n] = vw < a.V;
+    }
+
+    f4 ds[ST][NC];
+#pragma unroll
+    for (int j = 0; j < ST; ++j)
+#pragma unroll
+        for (int n = 0; n < NC; ++n) {
+            const int k0 = 16 * (ST * wave + j) + 4 * grp;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                ds[j][n][i] = p.dh_final && k0 + i < a.K ? p.dh_final[(head * a.K + k0 + i) * a.V + v[n]] : 0.0f;
+            s.ds.put4(16 * n + r16, k0, ds[j][n]);
+        }
+
+    typename O::Ex kf[KX], ktf[ST][2], qtf[ST][2];
+    typename O::template Sum<PL> inv[2], att[2];
+    f4 k_enter, k_leave, q_enter, beta;
+    float through;
+    RawOne<IO> rdo[NC][4];
+    f4 rerr[NC];
+    // a step of the chunk that is there
+    const auto step_of = [&](int64_t c, int t) { return (uint32_t)min((int64_t)t, a.L - 1 - c * kC); };
+    const auto load_k = [&](int64_t c) {
+        const char *kc = k_base + c * kC * (int64_t)k_step;
+        const uint32_t t = step_of(c, row) * k_step;
+#pragma unroll
+        for (int x = 0; x < KX; ++x)
+            kf[x] = O::load(&at<E>(kc, t + (32 * x + 8 * grp < a.K ? 32 * x + 8 * grp : 0) * IO::bytes));
+    };
+    const auto load_vec = [&](int64_t c) {
+        const char *vec = blocks + c * Block::kBytes;
+        k_enter = at<f4>(vec, (kVecKEnter * kC + mine) * 4);
+        k_leave = at<f4>(vec, (kVecKLeave * kC + mine) * 4);
+        q_enter = at<f4>(vec, (kVecQEnter * kC + mine) * 4);
+        beta = at<f4>(vec, (kVecBeta * kC + mine) * 4);
+        through = at<float>(vec, kVecThrough * kC * 4);
+    };
+    const auto load_dout = [&](int64_t c) {
+        const char *dc = do_base + c * kC * (int64_t)o_step;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int k = pair_row(kt, grp, i);
-            ds[kt][i] = p.dh_final && k < a.K ? p.dh_final[(head * a.K + k) * a.V + v] : 0.0f;
+            const uint32_t t = step_of(c, 4 * grp + 16 * wave + i) * o_step;
+#pragma unroll
+            for (int n = 0; n < NC; ++n) rdo[n][i] = at<RawOne<IO>>(dc, t + v[n] * IO::bytes);
         }
-    typename Rows::template Regs<4> rq, rk;
-    typename Block::Inv::template Regs<kThreads> rinv;
-    typename Block::AttT::template Regs<kThreads> ratt;
-    float rvec[2];
-    RawOne<IO> rdo[4][4];
-    f4 rerr[4];
-    const auto fetch = [&](int64_t c) {
-        const char *block = blocks + c * Block::kBytes;
-        Rows::template load<4>(rq, a.q, q_off, a.q_token, c * kC, a.L, a.K);
-        Rows::template load<4>(rk, a.k, k_off, a.k_token, c * kC, a.L, a.K);
-        Block::Inv::template load<kThreads>(rinv, reinterpret_cast<const E *>(block + Block::kVecBytes));
-        Block::AttT::template load<kThreads>(
-            ratt, reinterpret_cast<const E *>(block + Block::kVecBytes + Block::kInvBytes));
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int at = min((int)threadIdx.x + kThreads * i, kVecs * kC - 1);
-            rvec[i] = reinterpret_cast<const float *>(block)[at];
-        }
-        const float *err = p.ck + (((c * a.B + b) * a.H + h) * (a.K + kC) + a.K) * a.V + v;
-#pragma unroll
-        for (int tt = 0; tt < 4; ++tt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int r = pair_row(tt, grp, i);
-                const int64_t t = c * kC + r;
-                rdo[tt][i] = load_one<IO>(p.dout, ((b * a.L + (t < a.L ? t : a.L - 1)) * a.H + h) * a.V + v);
-                rerr[tt][i] = err[r * a.V];
-            }
     };
-    fetch(a.n - 1);
-    for (int64_t c = a.n - 1; c >= 0; --c) {
-        __syncthreads();
+    const auto load_err = [&](int64_t c) {
+        const char *err = reinterpret_cast<const char *>(p.ck) + ((c * a.B * a.H + head) * (a.K + kC) + a.K) * (int64_t)v_row;
+#pragma unroll
+        for (int n = 0; n < NC; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) rerr[n][i] = at<float>(err + i * (int64_t)v_row, mine * v_row + v[n] * 4);
+    };
+    // (the waves of the lower half have no first block of columns: they load the second twice)
+    const int y0 = wave / 2 * 32;
+    const uint32_t m_off = (row * kC + 8 * grp) * IO::bytes;
+    const auto load_matrix = [&](typename O::template Sum<PL> (&m)[2], int64_t c, size_t off) {
+        const char *from = blocks + c * Block::kBytes + off;
+        m[0] = O::template planes<PL>(&at<E>(from + y0 * IO::bytes, m_off), Block::PLANE);
+        m[1] = O::template planes<PL>(&at<E>(from + 32 * IO::bytes, m_off), Block::PLANE);
+    };
+    const auto load_rows = [&](typename O::Ex (&m)[ST][2], int64_t c, size_t off) {
+        const char *from = blocks + c * Block::kBytes + off + 16 * ST * wave * kC * IO::bytes;
+#pragma unroll
+        for (int j = 0; j < ST; ++j)
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+                m[j][y] = O::load(&at<E>(from + (16 * j * kC + 32 * y) * IO::bytes, (r16 * kC + 8 * grp) * IO::bytes));
+    };
+    // this chunk's dO, as an operand and against the state; steps past the end as 0
+    f4 dout[NC];
+    const auto put_dout = [&](int64_t c) {
+#pragma unroll
+        for (int n = 0; n < NC; ++n) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                dout[n][i] = (c + 1) * kC <= a.L || c * kC + mine + i < a.L ? rdo[n][i].get() : 0.0f;
+            s.dout.put4(16 * n + r16, mine, dout[n]);
+        }
+    };
+    const int64_t last = a.n - 1;
+    load_dout(last);
+    load_k(last);
+    load_vec(last);
+    load_matrix(att, last, Block::kAtt);
+    load_err(last);
+    load_matrix(inv, last, Block::kInv);
+    load_rows(ktf, last, Block::kKt);
+    load_rows(qtf, last, Block::kQt);
+    put_dout(last);
+    load_dout(last > 0 ? last - 1 : 0);
+    __syncthreads();
+    for (int64_t c = last; c >= 0; --c) {
+        const int64_t next = c > 0 ? c - 1 : 0, chunk = head * a.n + c;
         const bool whole = (c + 1) * kC <= a.L;
-        Rows::template cut<4>(rq, c * kC, a.L, a.K);
-        Rows::template cut<4>(rk, c * kC, a.L, a.K);
-        Rows::template store<4>(rk, s.k);
-        if constexpr (Lds::kTransposed) {
-            Rows::template store_transposed<4>(rk, s.kt);
-            Rows::template store_transposed<4>(rq, s.qt);
-        } else {
-            Rows::template store<4>(rq, s.q);
+        if (!whole || a.K != KP)
+#pragma unroll
+            for (int x = 0; x < KX; ++x)
+                if (c * kC + row >= a.L || 32 * x + 8 * grp >= a.K) kf[x] = typename O::Ex{};
+        // dU = leave K dS + P^T dO
+        f4 du[NC] = {};
+#pragma unroll
+        for (int x = 0; x < KX; ++x)
+#pragma unroll
+            for (int n = 0; n < NC; ++n)
+                du[n] = O::mul(du[n], kf[x], s.ds.get(16 * n + r16, 32 * x + 8 * grp));
+        load_k(next);
+#pragma unroll
+        for (int n = 0; n < NC; ++n) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) du[n][i] = k_leave[i] != 0.0f ? k_leave[i] * du[n][i] : 0.0f;
+            if (wave < 2) du[n] = O::mul(du[n], att[0], s.dout.get_exact(16 * n + r16, 8 * grp));
+            du[n] = O::mul(du[n], att[1], s.dout.get_exact(16 * n + r16, 32 + 8 * grp));
+            s.u.put4(16 * n + r16, mine, beta * du[n]);
+            s.q.put4(16 * n + r16, mine, q_enter * dout[n]);
         }
-        Block::Inv::template store<kThreads>(rinv, s.inv);
-        Block::AttT::template store<kThreads>(ratt, s.att);
+        load_matrix(att, next, Block::kAtt);
+        // E . dU over each strip's channels
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int at = threadIdx.x + kThreads * i;
-            if (at < kVecs * kC) s.vec[at] = rvec[i];
-        }
-        f4 dout[4], err[4];
+        for (int n = 0; n < NC; ++n) {
+            f4 e;
 #pragma unroll
-        for (int tt = 0; tt < 4; ++tt) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                dout[tt][i] = whole || c * kC + pair_row(tt, grp, i) < a.L ? rdo[tt][i].get() : 0.0f;
-                err[tt][i] = live ? rerr[tt][i] : 0.0f;
-            }
-        }
-        __syncthreads();
-        if (c > 0) fetch(c - 1);
-
-        const int64_t chunk = head * a.n + c;
-        if (live) store_state<KT>(p.after + chunk * a.K * a.V + v, a.K, a.V, grp, ds);
-        // dU = P^T dO + leave K dS
-        f4 du[4] = {};
-#pragma unroll
-        for (int x = 0; x < KT / 2; ++x) {
-            const auto st = O::template sum<PL>(ds[2 * x], ds[2 * x + 1]);
-#pragma unroll
-            for (int tt = 0; tt < 4; ++tt)
-                du[tt] = O::mul(du[tt], O::load(s.k + pair_row16(tt, r16) * Rows::STRIDE + 32 * x + 8 * grp), st);
-        }
-        const typename O::Ex dx_in[2] = {O::exact(dout[0], dout[1]), O::exact(dout[2], dout[3])};
-#pragma unroll
-        for (int tt = 0; tt < 4; ++tt) {
-            const f4 lv = *reinterpret_cast<const f4 *>(s.vec + kVecKLeave * kC + pair_row(tt, grp, 0));
-#pragma unroll
-            for (int i = 0; i < 4; ++i) du[tt][i] = lv[i] != 0.0f ? lv[i] * du[tt][i] : 0.0f;
-#pragma unroll
-            for (int y = tt / 2; y < 2; ++y)
-                du[tt] = O::mul(du[tt],
-                                O::template planes<PL>(s.att + pair_row16(tt, r16) * Block::AttT::STRIDE + 32 * y + 8 * grp,
-                                                       Block::AttT::PLANE),
-                                dx_in[y]);
-        }
-        // E . dU over this wave's channels
-#pragma unroll
-        for (int tt = 0; tt < 4; ++tt) {
-            f4 e = err[tt] * du[tt];
+            for (int i = 0; i < 4; ++i) e[i] = live[n] ? rerr[n][i] * du[n][i] : 0.0f;
 #pragma unroll
             for (int d = 1; d < 16; d *= 2)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) e[i] += __shfl_xor(e[i], d, 64);
-            if (r16 == 0 && strip < strips)
-                *reinterpret_cast<f4 *>(p.edu + (chunk * strips + strip) * kC + pair_row(tt, grp, 0)) = e;
+            const int strip = place.slice * NC + n;
+            if (r16 == 0 && strip < strips) *reinterpret_cast<f4 *>(p.edu + (chunk * strips + strip) * kC + mine) = e;
         }
+        load_err(next);
+        store_rows<ST, NC>(reinterpret_cast<char *>(p.after) + chunk * a.K * (int64_t)v_row, v_row, a.K,
+                           16 * ST * wave + 4 * grp, a.K == KP, v, live, ds);
+        __syncthreads();
         // dX = N^T diag(beta) dU
-        f4 dx[4] = {};
-        {
-            typename O::template Sum<PL> us[2];
+        char *dvc = dv_base + (c * kC + 16 * wave) * (int64_t)o_step;
+        char *dxc = reinterpret_cast<char *>(p.dx) + chunk * kC * (int64_t)v_row;
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
-                const f4 b0 = *reinterpret_cast<const f4 *>(s.vec + kVecBeta * kC + pair_row(2 * y, grp, 0));
-                const f4 b1 = *reinterpret_cast<const f4 *>(s.vec + kVecBeta * kC + pair_row(2 * y + 1, grp, 0));
-                us[y] = O::template sum<PL>(du[2 * y] * b0, du[2 * y + 1] * b1);
-            }
-#pragma unroll
-            for (int tt = 0; tt < 4; ++tt)
-#pragma unroll
-                for (int y = tt / 2; y < 2; ++y)
-                    dx[tt] = O::mul(dx[tt],
-                                    O::template planes<PL>(
-                                        s.inv + pair_row16(tt, r16) * Block::Inv::STRIDE + 32 * y + 8 * grp,
-                                        Block::Inv::PLANE),
-                                    us[y]);
-        }
-        if (live) {
-            float *to = p.dx + chunk * kC * a.V + v;
-            const int64_t at = ((b * a.L + c * kC) * a.H + h) * a.V + v;
-            const int step = a.H * a.V;
-#pragma unroll
-            for (int tt = 0; tt < 4; ++tt)
+        for (int n = 0; n < NC; ++n) {
+            f4 dx = {0, 0, 0, 0};
+            if (wave < 2) dx = O::mul(dx, inv[0], s.u.get(16 * n + r16, 8 * grp));
+            dx = O::mul(dx, inv[1], s.u.get(16 * n + r16, 32 + 8 * grp));
+            s.w.put4(16 * n + r16, mine, -k_enter * dx);
+            if (live[n])
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int t = pair_row(tt, grp, i);
-                    to[t * a.V] = dx[tt][i];
-                    if (whole || c * kC + t < a.L) store_io<IO>(p.dv, at + (int64_t)t * step, dx[tt][i]);
+                    at<float>(dxc + i * (int64_t)v_row, mine * v_row + v[n] * 4) = dx[i];
+                    if (whole || c * kC + mine + i < a.L)
+                        store_io<IO>(&at<char>(dvc + i * (int64_t)o_step, 4 * grp * o_step + v[n] * IO::bytes), 0, dx[i]);
                 }
         }
+        load_matrix(inv, next, Block::kInv);
+        const float pass = through;
+        load_vec(next);
+        __syncthreads();
         // dS <- through dS + (scale enter Q)^T dO - (enter K)^T dX
-        typename O::template Sum<PL> qs[2], xs[2];
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {
-            f4 qo[2], kx[2];
+        for (int n = 0; n < NC; ++n) {
+            const auto w0 = s.w.get(16 * n + r16, 8 * grp), w1 = s.w.get(16 * n + r16, 32 + 8 * grp);
+            const auto q0 = s.q.get(16 * n + r16, 8 * grp), q1 = s.q.get(16 * n + r16, 32 + 8 * grp);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                qo[j] = dout[2 * y + j] *
-                        *reinterpret_cast<const f4 *>(s.vec + kVecQEnter * kC + pair_row(2 * y + j, grp, 0));
-                kx[j] = -dx[2 * y + j] *
-                        *reinterpret_cast<const f4 *>(s.vec + kVecKEnter * kC + pair_row(2 * y + j, grp, 0));
-            }
-            qs[y] = O::template sum<PL>(qo[0], qo[1]);
-            xs[y] = O::template sum<PL>(kx[0], kx[1]);
-        }
-        const float through = s.vec[kVecThrough * kC];
+            for (int j = 0; j < ST; ++j) {
+                f4 &d = ds[j][n];
 #pragma unroll
-        for (int kt = 0; kt < KT; ++kt) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) ds[kt][i] = through != 0.0f ? through * ds[kt][i] : 0.0f;
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-                typename O::Ex lq, lk;
-                if constexpr (Lds::kTransposed) {
-                    lq = O::load(s.qt + pair_row16(kt, r16) * Rows::TSTRIDE + 32 * y + 8 * grp);
-                    lk = O::load(s.kt + pair_row16(kt, r16) * Rows::TSTRIDE + 32 * y + 8 * grp);
-                } else {
-                    lq = Op<IO>::gather(s.q + (32 * y + 8 * grp) * Rows::STRIDE + pair_row16(kt, r16), Rows::STRIDE);
-                    lk = Op<IO>::gather(s.k + (32 * y + 8 * grp) * Rows::STRIDE + pair_row16(kt, r16), Rows::STRIDE);
-                }
-                ds[kt] = O::mul(ds[kt], lq, qs[y]);
-                ds[kt] = O::mul(ds[kt], lk, xs[y]);
+                for (int i = 0; i < 4; ++i) d[i] = pass != 0.0f ? pass * d[i] : 0.0f;
+                d = O::mul(O::mul(d, qtf[j][0], q0), qtf[j][1], q1);
+                d = O::mul(O::mul(d, ktf[j][0], w0), ktf[j][1], w1);
+                s.ds.put4(16 * n + r16, 16 * (ST * wave + j) + 4 * grp, d);
             }
         }
+        load_rows(ktf, next, Block::kKt);
+        load_rows(qtf, next, Block::kQt);
+        put_dout(next);
+        load_dout(next > 0 ? next - 1 : 0);
+        __syncthreads();
     }
-    if (p.dh0 && live) store_state<KT>(p.dh0 + head * a.K * a.V + v, a.K, a.V, grp, ds);
+    if (p.dh0)
+        store_rows<ST, NC>(reinterpret_cast<char *>(p.dh0) + head * a.K * (int64_t)v_row, v_row, a.K,
+                           16 * ST * wave + 4 * grp, a.K == KP, v, live, ds);
 }
 
 // --------------------------------------------------------------------------- all chunks at once
@@ -252,39 +267,11 @@ struct GradArgs {
     float *dg;
 };
 
-// `P` planes of ROWS x 32 numbers in LDS.
-template <typename IO, int ROWS, int P>
-struct Slab {
-    using E = typename Op<IO>::elem;
-    static constexpr int PLANES = IO::bytes == 2 ? P : 1;
-    static constexpr int STRIDE = kVB + 16 / IO::bytes, PLANE = ROWS * STRIDE;
-    alignas(16) E e[PLANES * PLANE];
-    __device__ __forceinline__ void put4(int row, int col, f4 v) {
-        if constexpr (IO::bytes == 4) {
-            *reinterpret_cast<f4 *>(e + row * STRIDE + col) = v;
-        } else {
-#pragma unroll
-            for (int p = 0; p < PLANES; ++p) {
-                b4 q;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    q[i] = (__bf16)v[i];
-                    v[i] -= (float)q[i];
-                }
-                *reinterpret_cast<b4 *>(e + p * PLANE + row * STRIDE + col) = q;
-            }
-        }
-    }
-    __device__ __forceinline__ auto get(int row, int col) const {
-        return Op<IO>::template planes<PLANES>(e + row * STRIDE + col, PLANE);
-    }
-};
-
 template <typename IO, int KP>
 struct GradLds {
     using Rows = HeadRows<IO, KP>;
     using E = typename Op<IO>::elem;
-    using Mat = ChunkMatrix<IO, 2>;  // these feed outputs of the tensors' type alone
+    static constexpr int TSTRIDE = kC + 16 / IO::bytes;
     static constexpr bool kTransposed = IO::bytes == 2;
     alignas(16) E q[kC * Rows::STRIDE], k[kC * Rows::STRIDE];
     Gates gates;
@@ -293,13 +280,13 @@ struct GradLds {
     float dots[kGradThreads / 64];
     alignas(16) union {
         struct {
-            Slab<IO, kC, 1> dout;
-            Slab<IO, kC, 3> dx, err;
-            Slab<IO, KP, 3> before, after;
+            Slab<IO, kC, kVB, 1> dout;
+            Slab<IO, kC, kVB, 3> dx, err;
+            Slab<IO, KP, kVB, 3> before, after;
         } in;
         struct {
-            alignas(16) E kt[kTransposed ? KP * Rows::TSTRIDE : 8], qt[kTransposed ? KP * Rows::TSTRIDE : 8];
-            alignas(16) E m1[Mat::PLANES * Mat::PLANE], m2[Mat::PLANES * Mat::PLANE], m3[Mat::PLANES * Mat::PLANE];
+            alignas(16) E kt[kTransposed ? KP * TSTRIDE : 8], qt[kTransposed ? KP * TSTRIDE : 8];
+            Slab<IO, kC, kC, 2> m1, m2, m3;  // these feed outputs of the tensors' type alone
         } out;
     };
 };
@@ -324,7 +311,6 @@ __global__ __launch_bounds__(kGradThreads) void grads_kernel(GradArgs p) {
     using E = typename O::elem;
     using Rows = HeadRows<IO, KP>;
     using Lds = GradLds<IO, KP>;
-    using Mat = typename Lds::Mat;
     constexpr int KT = KP / 16, NT = KT / 2, SR = KP / 64;  // SR: state rows' pieces a thread
     extern __shared__ __attribute__((aligned(16))) char raw[];
     Lds &s = *reinterpret_cast<Lds *>(raw);
@@ -409,7 +395,7 @@ __global__ __launch_bounds__(kGradThreads) void grads_kernel(GradArgs p) {
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
                 const int t = 16 * (first + j) + r16;
-                os[j] = O::mul(os[j], O::load(s.in.dout.e + t * Slab<IO, kC, 1>::STRIDE + 8 * grp), sb);
+                os[j] = O::mul(os[j], s.in.dout.get_exact(t, 8 * grp), sb);
                 xs[j] = O::mul(xs[j], s.in.dx.get(t, 8 * grp), sb);
                 es[j] = O::mul(es[j], s.in.err.get(t, 8 * grp), sa);
             }
@@ -419,7 +405,7 @@ __global__ __launch_bounds__(kGradThreads) void grads_kernel(GradArgs p) {
                     int ti, tj;
                     lower_tile(wave + 8 * j, ti, tj);
                     const auto e = s.in.err.get(16 * tj + r16, 8 * grp);
-                    dp[j] = O::mul(dp[j], O::load(s.in.dout.e + (16 * ti + r16) * Slab<IO, kC, 1>::STRIDE + 8 * grp), e);
+                    dp[j] = O::mul(dp[j], s.in.dout.get_exact(16 * ti + r16, 8 * grp), e);
                     yy[j] = O::mul(yy[j], s.in.dx.get(16 * ti + r16, 8 * grp), e);
                 }
         }
@@ -430,23 +416,13 @@ __global__ __launch_bounds__(kGradThreads) void grads_kernel(GradArgs p) {
         if constexpr (Lds::kTransposed)
             for (int i = tid; i < kC * KP; i += kGradThreads) {
                 const int t = i % kC, k = i / kC;
-                s.out.kt[k * Rows::TSTRIDE + t] = s.k[t * Rows::STRIDE + k];
-                s.out.qt[k * Rows::TSTRIDE + t] = s.q[t * Rows::STRIDE + k];
+                s.out.kt[k * Lds::TSTRIDE + t] = s.k[t * Rows::STRIDE + k];
+                s.out.qt[k * Lds::TSTRIDE + t] = s.q[t * Rows::STRIDE + k];
             }
-        for (int i = tid; i < Mat::PLANES * Mat::PLANE; i += kGradThreads) {
-            s.out.m1[i] = (E)0.0f;
-            s.out.m2[i] = (E)0.0f;
-            s.out.m3[i] = (E)0.0f;
-        }
+        // (the three matrices lie side by side; what the tiles below do not write is 0)
+        for (int i = tid; i < (int)(3 * sizeof(s.out.m1) / 16); i += kGradThreads)
+            reinterpret_cast<u4 *>(&s.out.m1)[i] = u4{0, 0, 0, 0};
         __syncthreads();
-        const auto put = [](E *m, int r, int q, float v) {
-#pragma unroll
-            for (int i = 0; i < Mat::PLANES; ++i) {
-                const E e = (E)v;
-                m[i * Mat::PLANE + r * Mat::STRIDE + q] = e;
-                v -= (float)e;
-            }
-        };
 #pragma unroll
         for (int j = 0; j < 2; ++j)
             if (wave + 8 * j < 10) {
@@ -472,12 +448,12 @@ __global__ __launch_bounds__(kGradThreads) void grads_kernel(GradArgs p) {
                     const float z = dpv * att + db * bm, by = bm * y;
                     const float sq = a.scale * d * dpv, sb = d * db;
                     if (u <= t) {
-                        put(s.out.m1, t, u, sq * rku);
-                        put(s.out.m2, u, t, sq * rqt);
+                        s.out.m1.put(t, u, sq * rku);
+                        s.out.m2.put(u, t, sq * rqt);
                     }
                     if (u < t) {
-                        put(s.out.m3, t, u, sb * rku);
-                        put(s.out.m3, u, t, sb * rkt);
+                        s.out.m3.put(t, u, sb * rku);
+                        s.out.m3.put(u, t, sb * rkt);
                     }
                     cz += z;
                     cby += by;
@@ -556,16 +532,16 @@ __global__ __launch_bounds__(kGradThreads) void grads_kernel(GradArgs p) {
             for (int y = 0; y < 2; ++y) {
                 typename O::Ex kr, qr;
                 if constexpr (Lds::kTransposed) {
-                    kr = O::load(s.out.kt + (16 * kd + r16) * Rows::TSTRIDE + 32 * y + 8 * grp);
-                    qr = O::load(s.out.qt + (16 * kd + r16) * Rows::TSTRIDE + 32 * y + 8 * grp);
+                    kr = O::load(s.out.kt + (16 * kd + r16) * Lds::TSTRIDE + 32 * y + 8 * grp);
+                    qr = O::load(s.out.qt + (16 * kd + r16) * Lds::TSTRIDE + 32 * y + 8 * grp);
                 } else {
                     kr = Op<IO>::gather(s.k + (32 * y + 8 * grp) * Rows::STRIDE + 16 * kd + r16, Rows::STRIDE);
                     qr = Op<IO>::gather(s.q + (32 * y + 8 * grp) * Rows::STRIDE + 16 * kd + r16, Rows::STRIDE);
                 }
-                const int at = (16 * ti + r16) * Mat::STRIDE + 32 * y + 8 * grp;
-                if (y <= ti / 2) dq[j] = O::mul(dq[j], O::template planes<Mat::PLANES>(s.out.m1 + at, Mat::PLANE), kr);
-                if (y >= ti / 2) dk[j] = O::mul(dk[j], O::template planes<Mat::PLANES>(s.out.m2 + at, Mat::PLANE), qr);
-                dk[j] = O::mul(dk[j], O::template planes<Mat::PLANES>(s.out.m3 + at, Mat::PLANE), kr);
+                const int at = 32 * y + 8 * grp;
+                if (y <= ti / 2) dq[j] = O::mul(dq[j], s.out.m1.get(16 * ti + r16, at), kr);
+                if (y >= ti / 2) dk[j] = O::mul(dk[j], s.out.m2.get(16 * ti + r16, at), qr);
+                dk[j] = O::mul(dk[j], s.out.m3.get(16 * ti + r16, at), kr);
             }
         }
         __syncthreads();
@@ -611,10 +587,14 @@ __global__ __launch_bounds__(kGradThreads) void grads_kernel(GradArgs p) {
 }
 
 template <typename IO, int KP>
-hipError_t backward(const BackArgs &p, const GradArgs &g, hipStream_t stream) {
-    const unsigned per = 16 * (kThreads / 64);
-    const dim3 grid(((unsigned)p.a.V + per - 1) / per, (unsigned)p.a.H, (unsigned)p.a.B);
-    back_chain_kernel<IO, KP><<<grid, kThreads, sizeof(BackLds<IO, KP>), stream>>>(p);
+hipError_t backward(BackArgs p, const GradArgs &g, hipStream_t stream) {
+    const int nc = chain_columns(p.a);
+    p.slices = (p.a.V + 16 * nc - 1) / (16 * nc);
+    const unsigned grid = chain_grid(p.a.B * p.a.H, p.slices);
+    if (nc == 2)
+        back_chain_kernel<IO, KP, 2><<<grid, kThreads, sizeof(BackLds<IO, KP, 2>), stream>>>(p);
+    else
+        back_chain_kernel<IO, KP, 1><<<grid, kThreads, sizeof(BackLds<IO, KP, 1>), stream>>>(p);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const dim3 chunks((unsigned)p.a.n, (unsigned)p.a.Hk, (unsigned)p.a.B);
@@ -632,7 +612,7 @@ BackPlan back_plan(const ssm_gated_delta_bwd_args_t &a) {
     const size_t n = (size_t)((a.seqlen + kC - 1) / kC), chunks = n * a.batch * a.heads;
     BackPlan p;
     p.blocks = 0;
-    p.after = up256(chunks * block_bytes(a.io_dtype));
+    p.after = up256(chunks * std::max(block_bytes(a.io_dtype, a.kdim, false), block_bytes(a.io_dtype, a.kdim, true)));
     p.dx = p.after + up256(chunks * a.kdim * a.vdim * 4);
     p.edu = p.dx + up256(chunks * kC * a.vdim * 4);
     p.ck = p.edu + up256(chunks * ((a.vdim + 15) / 16) * kC * 4);
@@ -658,7 +638,7 @@ hipError_t launch_backward(const Call &c, const ssm_gated_delta_bwd_args_t &a, h
     if (e != hipSuccess) return e;
     float *after = reinterpret_cast<float *>(ws + plan.after), *dx = reinterpret_cast<float *>(ws + plan.dx);
     float *edu = reinterpret_cast<float *>(ws + plan.edu);
-    const BackArgs p{c, ws, ck, a.dh_final, a.dout, a.dv, a.dh0, after, dx, edu};
+    const BackArgs p{c, ws, ck, a.dh_final, a.dout, a.dv, a.dh0, after, dx, edu, 0};
     const GradArgs g{c, ck, after, dx, edu, a.dout, a.dq, a.dk, a.dbeta, a.dg};
     if (a.io_dtype == SSM_BF16)
         return a.kdim <= 64 ? backward<io_bf16, 64>(p, g, stream) : backward<io_bf16, 128>(p, g, stream);

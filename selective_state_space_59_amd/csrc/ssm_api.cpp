@@ -1036,6 +1036,11 @@ ssm_status_t check_delta(const DeltaSizes &z) {
     if (z.H > 65535 || z.B > 65535)
         return fail(SSM_ERR_UNSUPPORTED, "heads (%lld) and batch (%lld) go up to 65535", (long long)z.H, (long long)z.B);
     if (z.L >= (int64_t)1 << 30) return fail(SSM_ERR_UNSUPPORTED, "seqlen %lld is not below 2^30", (long long)z.L);
+    if (z.H * z.V >= (int64_t)1 << 24 || z.Hk * z.K >= (int64_t)1 << 24)
+        return fail(SSM_ERR_UNSUPPORTED, "heads * vdim and kheads * kdim have to be below 2^24");
+    // 512 threads for each 16 channels of a head, fewer than 2^32 threads a launch
+    if ((z.B * z.H + 8) * ((z.V + 15) / 16) >= (int64_t)1 << 23)
+        return fail(SSM_ERR_UNSUPPORTED, "batch * heads * ceil(vdim / 16) is not below 2^23");
     if (z.l2norm != 0 && z.l2norm != 1) return fail(SSM_ERR_UNSUPPORTED, "l2norm must be 0 or 1");
     if (!(z.scale - z.scale == 0.0f)) return fail(SSM_ERR_BAD_SHAPE, "scale must be finite");
     // the largest arrays: checkpoints and the backward's workspace, below 2^60 bytes
@@ -1060,9 +1065,10 @@ ssm_status_t check_steps(Steps s, int64_t B, int64_t L, Range &out) {
         s.token = s.width;
         s.batch = L * s.width;
     }
-    const int64_t most = (int64_t)1 << 40;
-    if (s.token < 0 || s.batch < 0 || s.token > most || s.batch > most)
-        return fail(SSM_ERR_BAD_SHAPE, "%s has a stride that is negative or above 2^40", s.name);
+    // (a lane's way to its step of a chunk, up to 63 steps of 4 bytes an element, is a number of 32 bits)
+    if (s.token < 0 || s.batch < 0 || s.token >= (int64_t)1 << 24 || s.batch > (int64_t)1 << 40)
+        return fail(SSM_ERR_BAD_SHAPE, "%s has a stride that is negative, 2^24 or more (steps) or above 2^40 (rows)",
+                    s.name);
     if (!mul_ok(L, s.token, 16) || !mul_ok(B, s.batch, 16)) return fail(SSM_ERR_BAD_SHAPE, "sizes overflow");
     if (s.wide && (!aligned(s.p, 16) || (L > 1 && s.token * s.es % 16 != 0) || (B > 1 && s.batch * s.es % 16 != 0)))
         return fail(SSM_ERR_ALIGN, "%s does not lie at 16-byte boundaries", s.name);
