@@ -280,9 +280,15 @@ struct Slab {
     __device__ __forceinline__ auto get_exact(int row, int col) const { return Op<IO>::load(e + row * STRIDE + col); }
 };
 
+// Element (row, col) of a matrix of 64 columns kept as the left operands of its 16 x 32 tiles, 64 lanes of
+// eight elements each: a wave loads a tile as one run of memory.
+__device__ __forceinline__ constexpr int tiled(int row, int col) {
+    return ((row / 16 * 2 + col / 32) * 64 + row % 16 + col % 32 / 8 * 16) * 8 + col % 8;
+}
+
 // What the chunks hand to the chains, one block per (row, head, chunk) in the workspace: vectors over the
 // steps; the inverse and the attention matrix (transposed for the backward chain), planes of 64 x 64; the
-// keys, and for the backward the queries, transposed (KP x 64).
+// keys, and for the backward the queries, transposed (KP x 64).  All matrices tiled.
 enum { kVecKEnter, kVecKLeave, kVecQEnter, kVecBeta, kVecThrough, kVecs };
 
 template <typename IO, int KP, bool BWD>
@@ -314,10 +320,6 @@ __device__ __forceinline__ ChainPlace chain_place(int64_t heads, int slices) {
     return p;
 }
 inline unsigned chain_grid(int64_t heads, int slices) { return (unsigned)((heads + 7) / 8 * 8 * slices); }
-
-// Value channels of a chain's workgroup: 32, or 16 where 32 would leave CUs without one.  Measured: see the
-// chain kernel.
-inline int chain_columns(const Call &a) { return a.B * a.H * ((a.V + 31) / 32) >= 256 ? 2 : 1; }
 
 // A tensor's place for a whole wave and a lane's distance from it in bytes: one address register a lane.
 template <typename T>

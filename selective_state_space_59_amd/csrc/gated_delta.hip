@@ -76,18 +76,17 @@ __global__ __launch_bounds__(kThreads) void prepare_kernel(Call a, char *blocks)
     char *block = blocks + ((b * a.H + h) * a.n + c) * Block::kBytes;
     float *vec = reinterpret_cast<float *>(block);
     E *inv = reinterpret_cast<E *>(block + Block::kInv), *att = reinterpret_cast<E *>(block + Block::kAtt);
-    // keys and queries transposed, 16 bytes (of consecutive steps) a piece
-    constexpr int PER = Rows::PER;
-    for (int i = threadIdx.x; i < KP * kC / PER; i += kThreads) {
-        const int k = i % KP, t = i / KP * PER;
-        E x[PER];
+    // keys and queries transposed, a lane's eight steps a piece
+    for (int i = threadIdx.x; i < KP * kC / 8; i += kThreads) {
+        const int k = i / 128 * 16 + i % 16, t = i / 64 % 2 * 32 + i / 16 % 4 * 8;
+        alignas(16) E x[8];
 #pragma unroll
-        for (int j = 0; j < PER; ++j) x[j] = s.k[(t + j) * Rows::STRIDE + k];
-        __builtin_memcpy(block + Block::kKt + (k * kC + t) * sizeof(E), x, 16);
+        for (int j = 0; j < 8; ++j) x[j] = s.k[(t + j) * Rows::STRIDE + k];
+        __builtin_memcpy(block + Block::kKt + i * 8 * sizeof(E), x, 8 * sizeof(E));
         if constexpr (BWD) {
 #pragma unroll
-            for (int j = 0; j < PER; ++j) x[j] = s.q[(t + j) * Rows::STRIDE + k];
-            __builtin_memcpy(block + Block::kQt + (k * kC + t) * sizeof(E), x, 16);
+            for (int j = 0; j < 8; ++j) x[j] = s.q[(t + j) * Rows::STRIDE + k];
+            __builtin_memcpy(block + Block::kQt + i * 8 * sizeof(E), x, 8 * sizeof(E));
         }
     }
     if (threadIdx.x < kC) {
@@ -126,11 +125,11 @@ __global__ __launch_bounds__(kThreads) void prepare_kernel(Call a, char *blocks)
             continue;  // above the pairs of tiles that are read
         }
         if constexpr (BWD) {
-            put_planes4<IO, Block::ATT, Block::PLANE>(att + u * kC + 16 * wave + 4 * grp, qk);
+            put_planes4<IO, Block::ATT, Block::PLANE>(att + tiled(u, 16 * wave + 4 * grp), qk);
         } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                put_planes<IO, Block::ATT, Block::PLANE>(att + (16 * wave + 4 * grp + i) * kC + u, qk[i]);
+                put_planes<IO, Block::ATT, Block::PLANE>(att + tiled(16 * wave + 4 * grp + i, u), qk[i]);
         }
     }
     __syncthreads();
@@ -174,11 +173,11 @@ __global__ __launch_bounds__(kThreads) void prepare_kernel(Call a, char *blocks)
         col[i] = v;
         if (i >= wave || i == (wave ^ 1)) {
             if constexpr (BWD) {
-                put_planes4<IO, Block::INV, Block::PLANE>(inv + (16 * wave + r16) * kC + 16 * i + 4 * grp, v);
+                put_planes4<IO, Block::INV, Block::PLANE>(inv + tiled(16 * wave + r16, 16 * i + 4 * grp), v);
             } else {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    put_planes<IO, Block::INV, Block::PLANE>(inv + (16 * i + 4 * grp + e) * kC + 16 * wave + r16, v[e]);
+                    put_planes<IO, Block::INV, Block::PLANE>(inv + tiled(16 * i + 4 * grp + e, 16 * wave + r16), v[e]);
             }
         }
     }
@@ -289,26 +288,26 @@ __global__ __launch_bounds__(kThreads, 2) void chain_kernel(ChainArgs p) {
             for (int n = 0; n < NC; ++n) val[n][i] = at<RawOne<IO>>(vc, t + v[n] * IO::bytes);
         }
     };
+    constexpr int TILE = 512 * IO::bytes;
+    const uint32_t in_tile = lane * 8 * IO::bytes;
     // (the waves of the upper half have no second block of columns: they load the first twice)
-    const int y1 = wave / 2 * 32;
-    const uint32_t m_off = (row * kC + 8 * grp) * IO::bytes;
+    const int tile0 = 2 * wave * TILE, tile1 = tile0 + wave / 2 * TILE;
     const auto load_inv = [&](int64_t c) {
         const char *m = blocks + c * Block::kBytes + Block::kInv;
-        inv[0] = O::template planes<PL>(&at<E>(m, m_off), Block::PLANE);
-        inv[1] = O::template planes<PL>(&at<E>(m + y1 * IO::bytes, m_off), Block::PLANE);
+        inv[0] = O::template planes<PL>(&at<E>(m + tile0, in_tile), Block::PLANE);
+        inv[1] = O::template planes<PL>(&at<E>(m + tile1, in_tile), Block::PLANE);
     };
     const auto load_att = [&](int64_t c) {
         const char *m = blocks + c * Block::kBytes + Block::kAtt;
-        att[0] = O::template planes<OUT>(&at<E>(m, m_off), Block::PLANE);
-        att[1] = O::template planes<OUT>(&at<E>(m + y1 * IO::bytes, m_off), Block::PLANE);
+        att[0] = O::template planes<OUT>(&at<E>(m + tile0, in_tile), Block::PLANE);
+        att[1] = O::template planes<OUT>(&at<E>(m + tile1, in_tile), Block::PLANE);
     };
     const auto load_kt = [&](int64_t c) {
-        const char *m = blocks + c * Block::kBytes + Block::kKt + 16 * ST * wave * kC * IO::bytes;
+        const char *m = blocks + c * Block::kBytes + Block::kKt + 2 * ST * wave * TILE;
 #pragma unroll
         for (int j = 0; j < ST; ++j)
 #pragma unroll
-            for (int y = 0; y < 2; ++y)
-                ktf[j][y] = O::load(&at<E>(m + (16 * j * kC + 32 * y) * IO::bytes, (r16 * kC + 8 * grp) * IO::bytes));
+            for (int y = 0; y < 2; ++y) ktf[j][y] = O::load(&at<E>(m + (2 * j + y) * TILE, in_tile));
     };
     const uint32_t v_row = (uint32_t)a.V * 4;  // a state's row in bytes
     load_qk(0);
@@ -527,7 +526,9 @@ hipError_t prepare(const Call &a, bool backward, char *blocks, hipStream_t strea
 
 template <typename IO, int KP>
 hipError_t chain(ChainArgs p, hipStream_t stream) {
-    const int nc = chain_columns(p.a);
+    // 32 channels a workgroup where every CU gets one all the same (8 x 2048 x 12 heads: 197 us, 230 with 16;
+    // where checkpoints are written as well 312 either way)
+    const int nc = p.a.B * p.a.H * ((p.a.V + 31) / 32) >= 256 ? 2 : 1;
     p.slices = (p.a.V + 16 * nc - 1) / (16 * nc);
     const unsigned grid = chain_grid(p.a.B * p.a.H, p.slices);
     if (nc == 2)
