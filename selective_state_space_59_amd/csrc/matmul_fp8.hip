@@ -48,6 +48,8 @@ struct Operand<io_f32> {
     }
 };
 
+__device__ __forceinline__ int64_t least(int64_t a, int64_t b) { return a < b ? a : b; }
+
 __device__ __forceinline__ f4 block_product(const Operand<io_bf16> &w, const Operand<io_bf16> &x) {
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w.v, x.v, f4{0, 0, 0, 0}, 0, 0, 0, kOne, 0, kOne);
 }
@@ -85,13 +87,13 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void skinny_kernel(ssm_matmul_fp
     __shared__ __attribute__((aligned(16))) f4 part[kSkinnyWaves][MT][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r16 = lane % 16, grp = lane / 16;
     const int64_t n0 = (int64_t)blockIdx.x * 16;
-    const char *w = static_cast<const char *>(a.wq) + std::min<int64_t>(n0 + r16, a.n - 1) * a.k;
+    const char *w = static_cast<const char *>(a.wq) + least(n0 + r16, a.n - 1) * a.k;
     const float *sw = a.w_scales + n0 / 128 * blocks;
     const char *x[MT];
     const float *sx[MT];
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
-        const int64_t m = std::min<int64_t>(16 * t + r16, a.m - 1);
+        const int64_t m = least(16 * t + r16, a.m - 1);
         x[t] = static_cast<const char *>(a.xq) + m * a.k;
         sx[t] = a.x_scales + m * blocks;
     }
@@ -143,8 +145,8 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64) void tile_kernel(ssm_matm
     // Tiles by XCD (workgroups are dealt out to the 8 in turn): each takes a run of tiles, in columns of up
     // to 8 rows of tiles, so that the tiles it works on at one time share rows of x and w in its L2.
     const int total = tiles_m * tiles_n, xcd = blockIdx.x % 8, each = total / 8, more = total % 8;
-    const int id = xcd * each + std::min(xcd, more) + (int)blockIdx.x / 8;
-    const int band = id / (8 * tiles_n), high = std::min(8, tiles_m - 8 * band), in = id - band * 8 * tiles_n;
+    const int id = xcd * each + min(xcd, more) + (int)blockIdx.x / 8;
+    const int band = id / (8 * tiles_n), high = min(8, tiles_m - 8 * band), in = id - band * 8 * tiles_n;
     const int64_t m0 = (int64_t)(8 * band + in % high) * BM, n0 = (int64_t)(in / high) * BN;
 
     const char *src[LOADS];
@@ -153,14 +155,14 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64) void tile_kernel(ssm_matm
     for (int j = 0; j < LOADS; ++j) {
         const int row = 8 * (wave * LOADS + j) + lane / 8;
         const bool of_x = row < BM;
-        const int64_t r = of_x ? std::min<int64_t>(m0 + row, a.m - 1) : std::min<int64_t>(n0 + row - BM, a.n - 1);
+        const int64_t r = of_x ? least(m0 + row, a.m - 1) : least(n0 + row - BM, a.n - 1);
         src[j] = static_cast<const char *>(of_x ? a.xq : a.wq) + r * a.k + piece;
     }
     const int wm = wave / (BN / WN) * WM, wn = wave % (BN / WN) * WN;
     const float *sx[MT];
 #pragma unroll
-    for (int t = 0; t < MT; ++t) sx[t] = a.x_scales + std::min<int64_t>(m0 + wm + 16 * t + r16, a.m - 1) * blocks;
-    const float *sw = a.w_scales + std::min<int64_t>(n0 + wn, a.n - 1) / 128 * blocks;
+    for (int t = 0; t < MT; ++t) sx[t] = a.x_scales + least(m0 + wm + 16 * t + r16, a.m - 1) * blocks;
+    const float *sw = a.w_scales + least(n0 + wn, a.n - 1) / 128 * blocks;
 
     const auto fetch = [&](int j, int buf) {
         const bool whole = 128 * (int64_t)(j + 1) <= a.k;
@@ -198,15 +200,31 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64) void tile_kernel(ssm_matm
         Operand<OUT> x[MT];
 #pragma unroll
         for (int t = 0; t < MT; ++t) x[t] = operand(wm + 16 * t + r16);
+        // Column u's products are under way while those of u - 1 are added: an instruction's result takes as
+        // long as the next one needs to run, and a wave waits where it asks for it earlier.
+        Operand<OUT> w = operand(BM + wn + r16);
+        f4 p[MT];
 #pragma unroll
-        for (int u = 0; u < NT; ++u) {
-            const Operand<OUT> w = operand(BM + wn + 16 * u + r16);
+        for (int u = 0; u <= NT; ++u) {
+            f4 q[MT];
+            if (u < NT) {
 #pragma unroll
-            for (int t = 0; t < MT; ++t) {
-                const f4 p = block_product(w, x[t]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) acc[t][u][i] = __builtin_fmaf(p[i], s[t], acc[t][u][i]);
+                for (int t = 0; t < MT; ++t) q[t] = block_product(w, x[t]);
+                if (u + 1 < NT) w = operand(BM + wn + 16 * (u + 1) + r16);
             }
+            if (u > 0)
+#pragma unroll
+                for (int t = 0; t < MT; ++t)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[t][u - 1][i] = __builtin_fmaf(p[t][i], s[t], acc[t][u - 1][i]);
+            if (u > 0 && u < NT && OUT::bytes == 2)
+#pragma unroll
+                for (int t = 0; t < MT; ++t) {
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // a matrix instruction,
+                    __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);  // the four sums of an earlier one
+                }
+#pragma unroll
+            for (int t = 0; t < MT; ++t) p[t] = q[t];
         }
     }
 #pragma unroll
