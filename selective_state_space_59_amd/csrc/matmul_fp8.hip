@@ -131,6 +131,8 @@ __device__ const i4 kZeros[1] = {};
 typedef __attribute__((address_space(3))) void *lds_ptr;
 typedef const __attribute__((address_space(1))) void *global_ptr;
 
+constexpr int kRun = 8;
+
 // BM x BN of y a workgroup, WM x WN a wave (WN divides 128).  Both operands of a block of K go straight
 // from memory to LDS, 16 bytes a lane, one block ahead of the products.  A row's eight pieces of 16 bytes
 // are kept in the order piece ^ (row % 8), by the address each lane loads from, so that the 16 rows of an
@@ -140,8 +142,10 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64) void tile_kernel(ssm_matm
                                                                        int tiles_n, bool wide) {
     constexpr int WAVES = BM / WM * (BN / WN), MT = WM / 16, NT = WN / 16;
     constexpr int LOADS = (BM + BN) / 8 / WAVES;  // of 8 rows each
+    constexpr int THREADS = 64 * WAVES, NB = (BN + 127) / 128;  // w's blocks a workgroup meets
     __shared__ __attribute__((aligned(1024))) char lds[2][(BM + BN) * 128];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r16 = lane % 16, grp = lane / 16;
+    __shared__ float scales[2][kRun][BM], w_scales[2][kRun][NB];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r16 = lane % 16, grp = lane / 16;
     // Tiles by XCD (workgroups are dealt out to the 8 in turn): each takes a run of tiles, in columns of up
     // to 8 rows of tiles, so that the tiles it works on at one time share rows of x and w in its L2.
     const int total = tiles_m * tiles_n, xcd = blockIdx.x % 8, each = total / 8, more = total % 8;
@@ -149,49 +153,74 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64) void tile_kernel(ssm_matm
     const int band = id / (8 * tiles_n), high = min(8, tiles_m - 8 * band), in = id - band * 8 * tiles_n;
     const int64_t m0 = (int64_t)(8 * band + in % high) * BM, n0 = (int64_t)(in / high) * BN;
 
-    const char *src[LOADS];
+    // x's loads of a wave come first, then w's: a wave has one kind only (BM and BN are multiples of its rows)
+    static_assert(BM % (8 * LOADS) == 0 && BN % (8 * LOADS) == 0, "");
+    const bool of_x = wave * LOADS * 8 < BM;
+    const int first = wave * LOADS * 8 - (of_x ? 0 : BM);
+    const int64_t row0 = of_x ? m0 : n0, left = (of_x ? a.m : a.n) - 1 - row0;
+    const char *src = static_cast<const char *>(of_x ? a.xq : a.wq) + row0 * a.k;
     const int piece = 16 * (lane % 8 ^ lane / 8);
+    uint32_t off[LOADS];
 #pragma unroll
-    for (int j = 0; j < LOADS; ++j) {
-        const int row = 8 * (wave * LOADS + j) + lane / 8;
-        const bool of_x = row < BM;
-        const int64_t r = of_x ? least(m0 + row, a.m - 1) : least(n0 + row - BM, a.n - 1);
-        src[j] = static_cast<const char *>(of_x ? a.xq : a.wq) + r * a.k + piece;
-    }
+    for (int j = 0; j < LOADS; ++j) off[j] = (uint32_t)least(first + 8 * j + lane / 8, left) * (uint32_t)a.k + piece;
     const int wm = wave / (BN / WN) * WM, wn = wave % (BN / WN) * WN;
-    const float *sx[MT];
+    // The scales go through LDS, kRun blocks of K at a time: a row's lie side by side, and fetching one
+    // for each of 16 rows every block cost more than the operands (3000 cycles of a block's 6700).
+    constexpr int PER = kRun * BM / THREADS;
+    const int s_row = threadIdx.x / (kRun / PER), s_at = threadIdx.x % (kRun / PER) * PER;
+    const float *sx = a.x_scales + least(m0 + s_row, a.m - 1) * blocks;
+    const int w_at = threadIdx.x % (kRun * NB) / NB;
+    const float *sw = a.w_scales + least(n0 / 128 + threadIdx.x % NB, (a.n - 1) / 128) * blocks;
+    float ahead[PER], ahead_w;
+    const auto load_scales = [&](int j) {
 #pragma unroll
-    for (int t = 0; t < MT; ++t) sx[t] = a.x_scales + least(m0 + wm + 16 * t + r16, a.m - 1) * blocks;
-    const float *sw = a.w_scales + least(n0 + wn, a.n - 1) / 128 * blocks;
+        for (int i = 0; i < PER; ++i) ahead[i] = sx[min(j + s_at + i, blocks - 1)];
+        ahead_w = sw[min(j + w_at, blocks - 1)];
+    };
+    const auto keep_scales = [&](int run) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) scales[run % 2][s_at + i][s_row] = ahead[i];
+        if (threadIdx.x < kRun * NB) w_scales[run % 2][w_at][threadIdx.x % NB] = ahead_w;
+    };
 
     const auto fetch = [&](int j, int buf) {
-        const bool whole = 128 * (int64_t)(j + 1) <= a.k;
+        const char *from = src + 128 * (int64_t)j;
+        char *to = lds[buf] + wave * LOADS * 1024;
+        if (128 * (int64_t)(j + 1) <= a.k) {
 #pragma unroll
-        for (int i = 0; i < LOADS; ++i) {
-            const char *from = src[i] + 128 * (int64_t)j;
-            if (!whole && 128 * (int64_t)j + piece >= a.k) from = reinterpret_cast<const char *>(kZeros);
-            __builtin_amdgcn_global_load_lds((global_ptr)from, (lds_ptr)(lds[buf] + (wave * LOADS + i) * 1024), 16, 0, 0);
+            for (int i = 0; i < LOADS; ++i) {
+                // (kept a base and a distance: the sums, formed once, would take two registers each)
+                uint32_t o = off[i];
+                asm volatile("" : "+v"(o));
+                __builtin_amdgcn_global_load_lds((global_ptr)(from + o), (lds_ptr)(to + i * 1024), 16, 0, 0);
+            }
+        } else {  // behind a row's end: zeros
+            const bool in = 128 * (int64_t)j + piece < a.k;
+#pragma unroll
+            for (int i = 0; i < LOADS; ++i) {
+                uint32_t o = off[i];
+                asm volatile("" : "+v"(o));
+                const char *p = in ? from + o : reinterpret_cast<const char *>(kZeros);
+                __builtin_amdgcn_global_load_lds((global_ptr)p, (lds_ptr)(to + i * 1024), 16, 0, 0);
+            }
         }
     };
     f4 acc[MT][NT] = {};
-    float next[MT], next_w;
-#pragma unroll
-    for (int t = 0; t < MT; ++t) next[t] = sx[t][0];
-    next_w = sw[0];
     fetch(0, 0);
+    load_scales(0);
+    keep_scales(0);
     for (int j = 0; j < blocks; ++j) {
         const char *buf = lds[j % 2];
+        // (ahead of the barrier: the run before the last was read up to the block before)
+        if (j % kRun == 0 && j > 0) keep_scales(j / kRun);
         __builtin_amdgcn_s_waitcnt(0);  // this wave's loads have landed; the barrier: everyone's
         __syncthreads();
+        if (j % kRun == 0) load_scales(j + kRun);
+        if (j + 1 < blocks) fetch(j + 1, (j + 1) % 2);
         float s[MT];
+        const float s_w = w_scales[j / kRun % 2][j % kRun][wn / 128];
 #pragma unroll
-        for (int t = 0; t < MT; ++t) s[t] = next[t] * next_w;
-        if (j + 1 < blocks) {
-#pragma unroll
-            for (int t = 0; t < MT; ++t) next[t] = sx[t][j + 1];
-            next_w = sw[j + 1];
-            fetch(j + 1, (j + 1) % 2);
-        }
+        for (int t = 0; t < MT; ++t) s[t] = scales[j / kRun % 2][j % kRun][wm + 16 * t + r16] * s_w;
         const auto operand = [&](int row) {
             const char *at = buf + row * 128;
             return Operand<OUT>(*reinterpret_cast<const i4 *>(at + 16 * (grp ^ row % 8)),
@@ -223,6 +252,7 @@ __global__ __launch_bounds__(BM / WM * (BN / WN) * 64) void tile_kernel(ssm_matm
                     __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // a matrix instruction,
                     __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);  // the four sums of an earlier one
                 }
+            __builtin_amdgcn_sched_barrier(0);  // (or every operand would be read ahead, beyond the registers)
 #pragma unroll
             for (int t = 0; t < MT; ++t) p[t] = q[t];
         }
