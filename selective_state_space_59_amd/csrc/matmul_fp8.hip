@@ -276,9 +276,13 @@ void launch(const ssm_matmul_fp8_args_t &a, hipStream_t stream) {
         return;
     }
     const auto tiles = [&](int64_t bm, int64_t bn) { return ((a.m + bm - 1) / bm) * ((a.n + bn - 1) / bn); };
-    if (tiles(256, 256) >= 256) {
-        tile_kernel<OUT, 256, 256, 64, 128><<<(unsigned)tiles(256, 256), 512, 0, stream>>>(
-            a, blocks, (int)((a.m + 255) / 256), (int)((a.n + 255) / 256), wide);
+    // The largest tile that still gives every CU a workgroup.  16384 x 10240 x 2560 in bf16: tiles of 256 490 us,
+    // of 128 624; fp32 results, whose widened operands would not fit the registers beside 256 x 256 of sums,
+    // stay with 128.
+    if (OUT::bytes == 2 && tiles(256, 256) >= 256) {
+        if constexpr (OUT::bytes == 2)
+            tile_kernel<OUT, 256, 256, 64, 128><<<(unsigned)tiles(256, 256), 512, 0, stream>>>(
+                a, blocks, (int)((a.m + 255) / 256), (int)((a.n + 255) / 256), wide);
     } else if (tiles(128, 128) >= 256) {
         tile_kernel<OUT, 128, 128, 64, 64><<<(unsigned)tiles(128, 128), 256, 0, stream>>>(
             a, blocks, (int)((a.m + 127) / 128), (int)((a.n + 127) / 128), wide);
