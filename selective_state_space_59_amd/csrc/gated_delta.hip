@@ -336,14 +336,17 @@ __global__ __launch_bounds__(kThreads, 2) void chain_kernel(ChainArgs p) {
                 o[n] = O::mul(o[n], qf[x], O::template first<OUT>(st));
             }
         load_qk(next);
-        // X = V - enter K S (a state that does not reach a step has no part in it, whatever it holds)
+        // X = V - enter K S (a state that does not reach a step has no part in it, whatever it holds; one that
+        // holds infinities or NaNs and ends in this chunk shows in its own outputs through Q S, and must not
+        // meet, in the products over steps, the zeros that keep it from the steps behind its end)
 #pragma unroll
         for (int n = 0; n < NC; ++n) {
             f4 x;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 x[i] = whole || c * kC + mine + i < a.L ? val[n][i].get() : 0.0f;
-                x[i] = k_enter[i] != 0.0f ? __builtin_fmaf(-k_enter[i], ks[n][i], x[i]) : x[i];
+                const bool seen = k_enter[i] != 0.0f && (through != 0.0f || ks[n][i] - ks[n][i] == 0.0f);
+                x[i] = seen ? __builtin_fmaf(-k_enter[i], ks[n][i], x[i]) : x[i];
                 o[n][i] = q_enter[i] != 0.0f ? q_enter[i] * o[n][i] : 0.0f;
             }
             s.x.put4(16 * n + r16, mine, x);

@@ -35,13 +35,14 @@ def case64(k):
     return {m: f64(v) if isinstance(v, torch.Tensor) else v for m, v in k.items()}
 
 
-def close(got, ref, rel, what):
-    """|got - ref| <= rel max|ref| + half a step of got's type."""
+def close(got, ref, rel, what, roundings=1):
+    """|got - ref| <= rel max|ref| + half a step of got's type for each of `roundings` (two where ref was
+    rounded to that type as well)."""
     g = f64(got)
     assert g.shape == ref.shape, (what, g.shape, ref.shape)
     if not ref.size:
         return
-    tol = rel * np.abs(ref).max() + HALF_STEP[got.dtype] * np.abs(ref) + 1e-37
+    tol = rel * np.abs(ref).max() + roundings * HALF_STEP[got.dtype] * np.abs(ref) + 1e-37
     off = np.abs(g - ref)
     bad = ~(off <= tol)
     if bad.any():
