@@ -122,6 +122,19 @@ struct Op<io_bf16> {
     }
 };
 
+// Sum over the 16 lanes of a row of results, in each of them: rotations within the row (ror 8, 4, 2, 1) in the
+// vector unit, where shuffles would go through LDS.
+template <int CTRL>
+__device__ __forceinline__ float rotated(float x) {
+    return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), CTRL, 0xf, 0xf, false));
+}
+__device__ __forceinline__ float sum16(float x) {
+    x += rotated<0x128>(x);
+    x += rotated<0x124>(x);
+    x += rotated<0x122>(x);
+    return x + rotated<0x121>(x);
+}
+
 // One call's tensors as its kernels see them.  Strides in elements; a head's K (or V) channels are
 // consecutive, its heads too.
 struct Call {

@@ -21,8 +21,11 @@ namespace {
 template <typename IO, int KP>
 struct PrepareLds {
     using Rows = HeadRows<IO, KP>;
-    alignas(16) typename Op<IO>::elem q[kC * Rows::STRIDE], k[kC * Rows::STRIDE];
-    alignas(16) float a[kC][kC + 4];    // B diag(beta)
+    alignas(16) typename Op<IO>::elem k[kC * Rows::STRIDE];
+    union {
+        alignas(16) typename Op<IO>::elem q[kC * Rows::STRIDE];
+        alignas(16) float a[kC][kC + 4];  // B diag(beta), when the queries are in registers
+    };
     alignas(16) float inv[kC][20];      // the inverses of its diagonal blocks, side by side: row, column within the block
     Gates gates;
 };
@@ -104,6 +107,7 @@ __global__ __launch_bounds__(kThreads) void prepare_kernel(Call a, char *blocks)
         qa[x] = O::load(s.q + (16 * wave + r16) * Rows::STRIDE + 32 * x + 8 * grp);
         ka[x] = O::load(s.k + (16 * wave + r16) * Rows::STRIDE + 32 * x + 8 * grp);
     }
+    __syncthreads();
     for (int j = 0; j < 4; ++j) {
         f4 kk = {0, 0, 0, 0}, qk = {0, 0, 0, 0};
         const int u = 16 * j + r16;
@@ -136,10 +140,15 @@ __global__ __launch_bounds__(kThreads) void prepare_kernel(Call a, char *blocks)
     float x[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-        float v = i == r16 ? 1.0f : 0.0f;
+        float v[4] = {i == r16 ? 1.0f : 0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int k = 0; k < i; ++k) v = __builtin_fmaf(-s.a[16 * wave + i][16 * wave + k], x[k], v);
-        x[i] = v;
+        for (int k = 0; k < i; k += 4) {
+            const f4 left = *reinterpret_cast<const f4 *>(&s.a[16 * wave + i][16 * wave + k]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (k + e < i) v[e] = __builtin_fmaf(-left[e], x[k + e], v[e]);
+        }
+        x[i] = (v[0] + v[1]) + (v[2] + v[3]);
     }
     if (grp == 0)
 #pragma unroll

@@ -197,11 +197,7 @@ __global__ __launch_bounds__(kThreads, 2) void back_chain_kernel(BackArgs p) {
         for (int n = 0; n < NC; ++n) {
             f4 e;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) e[i] = live[n] ? rerr[n][i] * du[n][i] : 0.0f;
-#pragma unroll
-            for (int d = 1; d < 16; d *= 2)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) e[i] += __shfl_xor(e[i], d, 64);
+            for (int i = 0; i < 4; ++i) e[i] = sum16(live[n] ? rerr[n][i] * du[n][i] : 0.0f);
             const int strip = place.slice * NC + n;
             if (r16 == 0 && strip < strips) *reinterpret_cast<f4 *>(p.edu + (chunk * strips + strip) * kC + mine) = e;
         }
@@ -275,8 +271,8 @@ struct GradLds {
     static constexpr bool kTransposed = IO::bytes == 2;
     alignas(16) E q[kC * Rows::STRIDE], k[kC * Rows::STRIDE];
     Gates gates;
-    float row_z[4][kC], col_z[4][kC], col_by[4][kC];
-    float row_a[KP / 16][kC], row_b[KP / 16][kC];
+    float row_z[4][kC], col_z[4][kC], col_by[4][kC], edu[kC];
+    alignas(16) float row_a[KP / 16][kC], row_b[KP / 16][kC];
     float dots[kGradThreads / 64];
     alignas(16) union {
         struct {
@@ -295,12 +291,6 @@ struct GradLds {
 __device__ __forceinline__ void lower_tile(int i, int &ti, int &tj) {
     ti = i < 1 ? 0 : i < 3 ? 1 : i < 6 ? 2 : 3;
     tj = i - ti * (ti + 1) / 2;
-}
-
-__device__ __forceinline__ float sum16(float x) {
-#pragma unroll
-    for (int d = 1; d < 16; d *= 2) x += __shfl_xor(x, d, 64);
-    return x;
 }
 
 // One chunk of one key head, over the value heads that share it.  Wave w has the result columns
@@ -414,15 +404,25 @@ __global__ __launch_bounds__(kGradThreads) void grads_kernel(GradArgs p) {
         for (int d = 1; d < 64; d *= 2) dot += __shfl_xor(dot, d, 64);
         if (lane == 0) s.dots[wave] = dot;
         if constexpr (Lds::kTransposed)
-            for (int i = tid; i < kC * KP; i += kGradThreads) {
-                const int t = i % kC, k = i / kC;
-                s.out.kt[k * Lds::TSTRIDE + t] = s.k[t * Rows::STRIDE + k];
-                s.out.qt[k * Lds::TSTRIDE + t] = s.q[t * Rows::STRIDE + k];
+            for (int i = tid; i < kC * KP / 8; i += kGradThreads) {
+                const int t = i % kC, k = i / kC * 8;
+                const auto kv = O::load(s.k + t * Rows::STRIDE + k), qv = O::load(s.q + t * Rows::STRIDE + k);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    s.out.kt[(k + j) * Lds::TSTRIDE + t] = kv.v[j];
+                    s.out.qt[(k + j) * Lds::TSTRIDE + t] = qv.v[j];
+                }
             }
         // (the three matrices lie side by side; what the tiles below do not write is 0)
         for (int i = tid; i < (int)(3 * sizeof(s.out.m1) / 16); i += kGradThreads)
             reinterpret_cast<u4 *>(&s.out.m1)[i] = u4{0, 0, 0, 0};
         __syncthreads();
+        if (wave == kGradThreads / 64 - 1) {  // (one of those with one tile)
+            const int strips = (a.V + 15) / 16;
+            float e = 0.0f;
+            for (int i = 0; i < strips; ++i) e += p.edu[(chunk * strips + i) * kC + lane];
+            s.edu[lane] = e;
+        }
 #pragma unroll
         for (int j = 0; j < 2; ++j)
             if (wave + 8 * j < 10) {
@@ -516,8 +516,7 @@ __global__ __launch_bounds__(kGradThreads) void grads_kernel(GradArgs p) {
                 const double down = __shfl_down(dG, d, 64);
                 if (t + d < 64) dG += down;
             }
-            const int strips = (a.V + 15) / 16;
-            for (int i = 0; i < strips; ++i) dbeta += p.edu[(chunk * strips + i) * kC + t];
+            dbeta += s.edu[t];
             const bool cut = s.gates.doc[t] != (t ? s.gates.doc[t - 1] : 0);
             if (t0 + t < a.L) {
                 const int64_t at = (b * a.L + t0 + t) * a.H + h;
@@ -563,27 +562,29 @@ __global__ __launch_bounds__(kGradThreads) void grads_kernel(GradArgs p) {
         }
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
+    for (int j = 0; j < NT; ++j) {
+        const int first_t = 16 * (first + j) + 4 * grp, k = 16 * kd + r16;
+        f4 q_dot = {0, 0, 0, 0}, k_dot = {0, 0, 0, 0};
+#pragma unroll
+        for (int w = 0; w < KT; ++w) {
+            q_dot += *reinterpret_cast<const f4 *>(&s.row_a[w][first_t]);
+            k_dot += *reinterpret_cast<const f4 *>(&s.row_b[w][first_t]);
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int t = 16 * (first + j) + 4 * grp + i, k = 16 * kd + r16;
+            const int t = first_t + i;
             if (t0 + t >= a.L || k >= a.K) continue;
             float oq = dq[j][i], ok = dk[j][i];
             if (a.l2norm) {
-                float qd = 0.0f, kdot = 0.0f;
-#pragma unroll
-                for (int w = 0; w < KT; ++w) {
-                    qd += s.row_a[w][t];
-                    kdot += s.row_b[w][t];
-                }
                 const float rq = s.gates.rq[t], rk = s.gates.rk[t];
-                oq = rq * (oq - rq * (float)s.q[t * Rows::STRIDE + k] * qd);
-                ok = rk * (ok - rk * (float)s.k[t * Rows::STRIDE + k] * kdot);
+                oq = rq * (oq - rq * (float)s.q[t * Rows::STRIDE + k] * q_dot[i]);
+                ok = rk * (ok - rk * (float)s.k[t * Rows::STRIDE + k] * k_dot[i]);
             }
             const int64_t at = ((b * a.L + t0 + t) * a.Hk + hk) * a.K + k;
             store_io<IO>(p.dq, at, oq);
             store_io<IO>(p.dk, at, ok);
         }
+    }
 }
 
 template <typename IO, int KP>
