@@ -301,7 +301,8 @@ __device__ __forceinline__ constexpr int tiled(int row, int col) {
 
 // What the chunks hand to the chains, one block per (row, head, chunk) in the workspace: vectors over the
 // steps; the inverse and the attention matrix (transposed for the backward chain), planes of 64 x 64; the
-// keys, and for the backward the queries, transposed (KP x 64).  All matrices tiled.
+// keys, and for the backward the queries, transposed (KP x 64).  All matrices tiled.  For the backward the
+// chunk's gates as well.
 enum { kVecKEnter, kVecKLeave, kVecQEnter, kVecBeta, kVecThrough, kVecs };
 
 template <typename IO, int KP, bool BWD>
@@ -314,7 +315,8 @@ struct ChunkBlock {
     static constexpr size_t kAtt = kInv + (size_t)INV * PLANE * IO::bytes;
     static constexpr size_t kKt = kAtt + (size_t)ATT * PLANE * IO::bytes;
     static constexpr size_t kQt = kKt + (size_t)KP * kC * IO::bytes;
-    static constexpr size_t kBytes = BWD ? kQt + (size_t)KP * kC * IO::bytes : kQt;
+    static constexpr size_t kGates = kQt + (size_t)KP * kC * IO::bytes;  // backward: the gates, for the gradients
+    static constexpr size_t kBytes = BWD ? kGates + (sizeof(Gates) + 15) / 16 * 16 : kQt;
 };
 
 // The chains' workgroups: one head's 16 NC value channels each, heads dealt out to the 8 XCDs (workgroups

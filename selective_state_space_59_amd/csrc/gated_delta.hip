@@ -79,6 +79,11 @@ __global__ __launch_bounds__(kThreads) void prepare_kernel(Call a, char *blocks)
     char *block = blocks + ((b * a.H + h) * a.n + c) * Block::kBytes;
     float *vec = reinterpret_cast<float *>(block);
     E *inv = reinterpret_cast<E *>(block + Block::kInv), *att = reinterpret_cast<E *>(block + Block::kAtt);
+    if constexpr (BWD) {
+        static_assert(sizeof(Gates) % 4 == 0, "");
+        for (int i = threadIdx.x; i < (int)sizeof(Gates) / 4; i += kThreads)
+            reinterpret_cast<uint32_t *>(block + Block::kGates)[i] = reinterpret_cast<const uint32_t *>(&s.gates)[i];
+    }
     // keys and queries transposed, a lane's eight steps a piece
     for (int i = threadIdx.x; i < KP * kC / 8; i += kThreads) {
         const int k = i / 128 * 16 + i % 16, t = i / 64 % 2 * 32 + i / 16 % 4 * 8;

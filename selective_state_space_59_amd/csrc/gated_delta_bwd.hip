@@ -257,6 +257,7 @@ constexpr int kGradThreads = 512, kVB = 32;  // value channels of a pass
 
 struct GradArgs {
     Call a;
+    const char *blocks;
     const float *ck, *after, *dx, *edu;
     const void *dout;
     void *dq, *dk, *dbeta;
@@ -316,21 +317,6 @@ __global__ __launch_bounds__(kGradThreads) void grads_kernel(GradArgs p) {
         Rows::template store<8>(rq, s.q);
         Rows::template store<8>(rk, s.k);
     }
-    __syncthreads();
-    if (threadIdx.x < 256) {
-        const int row = threadIdx.x / 4, part = threadIdx.x % 4;
-#pragma unroll
-        for (int which = 0; which < 2; ++which) {
-            const E *x = (which ? s.k : s.q) + row * Rows::STRIDE + part * (KP / 4);
-            float t = 0.0f;
-#pragma unroll
-            for (int i = 0; i < KP / 4; ++i) t = __builtin_fmaf((float)x[i], (float)x[i], t);
-            t += __shfl_xor(t, 1, 64);
-            t += __shfl_xor(t, 2, 64);
-            if (part == 0) (which ? s.gates.rk : s.gates.rq)[row] = a.l2norm ? 1.0f / sqrtf(t + kL2Eps) : 1.0f;
-        }
-    }
-
     f4 dq[NT] = {}, dk[NT] = {};
     for (int h = hk * share; h < (hk + 1) * share; ++h) {
         // The thread's place, formed anew for each head: the compiler would else keep hundreds of addresses
@@ -361,7 +347,12 @@ __global__ __launch_bounds__(kGradThreads) void grads_kernel(GradArgs p) {
             }
         };
         fetch(0);
-        load_gates<IO>(a, b, h, t0, s.gates);
+        {  // the chunk's gates, as prepare_kernel formed them
+            using Block = ChunkBlock<IO, KP, true>;
+            const uint32_t *from = reinterpret_cast<const uint32_t *>(p.blocks + chunk * Block::kBytes + Block::kGates);
+            for (int i = tid; i < (int)sizeof(Gates) / 4; i += kGradThreads)
+                reinterpret_cast<uint32_t *>(&s.gates)[i] = from[i];
+        }
         f4 os[NT] = {}, xs[NT] = {}, es[NT] = {}, dp[2] = {}, yy[2] = {};
         float dot = 0.0f;
         for (int v0 = 0; v0 < a.V; v0 += kVB) {
@@ -573,17 +564,25 @@ __global__ __launch_bounds__(kGradThreads) void grads_kernel(GradArgs p) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int t = first_t + i;
-            if (t0 + t >= a.L || k >= a.K) continue;
             float oq = dq[j][i], ok = dk[j][i];
+            E &qe = s.q[t * Rows::STRIDE + k], &ke = s.k[t * Rows::STRIDE + k];  // this lane's alone by now
             if (a.l2norm) {
                 const float rq = s.gates.rq[t], rk = s.gates.rk[t];
-                oq = rq * (oq - rq * (float)s.q[t * Rows::STRIDE + k] * q_dot[i]);
-                ok = rk * (ok - rk * (float)s.k[t * Rows::STRIDE + k] * k_dot[i]);
+                oq = rq * (oq - rq * (float)qe * q_dot[i]);
+                ok = rk * (ok - rk * (float)ke * k_dot[i]);
             }
-            const int64_t at = ((b * a.L + t0 + t) * a.Hk + hk) * a.K + k;
-            store_io<IO>(p.dq, at, oq);
-            store_io<IO>(p.dk, at, ok);
+            qe = (E)oq;
+            ke = (E)ok;
         }
+    }
+    __syncthreads();
+    // out by rows, 16 bytes a lane
+    for (int i = threadIdx.x; i < kC * KP / Rows::PER; i += kGradThreads) {
+        const int t = i / (KP / Rows::PER), k = i % (KP / Rows::PER) * Rows::PER;
+        if (t0 + t >= a.L || k >= a.K) continue;
+        const int64_t at = ((b * a.L + t0 + t) * a.Hk + hk) * a.K + k;
+        reinterpret_cast<u32x4_a2 *>(static_cast<E *>(p.dq) + at)[0] = *reinterpret_cast<const u4 *>(s.q + t * Rows::STRIDE + k);
+        reinterpret_cast<u32x4_a2 *>(static_cast<E *>(p.dk) + at)[0] = *reinterpret_cast<const u4 *>(s.k + t * Rows::STRIDE + k);
     }
 }
 
@@ -637,7 +636,7 @@ hipError_t launch_backward(const Call &c, const ssm_gated_delta_bwd_args_t &a, h
     float *after = reinterpret_cast<float *>(ws + plan.after), *dx = reinterpret_cast<float *>(ws + plan.dx);
     float *edu = reinterpret_cast<float *>(ws + plan.edu);
     const BackArgs p{c, ws, ck, a.dh_final, a.dout, a.dv, a.dh0, after, dx, edu, 0};
-    const GradArgs g{c, ck, after, dx, edu, a.dout, a.dq, a.dk, a.dbeta, a.dg};
+    const GradArgs g{c, ws, ck, after, dx, edu, a.dout, a.dq, a.dk, a.dbeta, a.dg};
     if (a.io_dtype == SSM_BF16)
         return a.kdim <= 64 ? backward<io_bf16, 64>(p, g, stream) : backward<io_bf16, 128>(p, g, stream);
     return a.kdim <= 64 ? backward<io_f32, 64>(p, g, stream) : backward<io_f32, 128>(p, g, stream);
