@@ -346,32 +346,80 @@ __device__ __forceinline__ const char *bytes(const T *p, int64_t elements, int64
     return reinterpret_cast<const char *>(p) + elements * size;
 }
 
-// A wave's rows of a state (from k0 on, V floats each) into memory.
-template <int ST, int NC>
-__device__ __forceinline__ void store_rows(char *to, uint32_t v_row, int K, int k0, bool every, const uint32_t (&v)[NC],
-                                           const bool (&live)[NC], const f4 (&s)[ST][NC]) {
-#pragma unroll
-    for (int n = 0; n < NC; ++n)
-        if (live[n])
-#pragma unroll
-            for (int j = 0; j < ST; ++j)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (every || k0 + 16 * j + i < K)
-                        at<float>(to + (16 * j + i) * (int64_t)v_row, k0 * v_row + v[n] * 4) = s[j][n][i];
+// A lane's value channels in a chain's workgroup: with two of them side by side, so that they are loaded and
+// stored together (V is even: both are there or neither).  Channels past the last repeat it.
+template <int NC>
+__device__ __forceinline__ int channel(int slice, int r16, int n) {
+    return NC * (16 * slice + r16) + n;
+}
+typedef f2 f2_a4 __attribute__((aligned(4)));
+typedef uint32_t u1_a2 __attribute__((aligned(2)));
+
+// NC neighbouring floats, or elements, at a lane's channels.
+template <int NC>
+__device__ __forceinline__ void store_floats(void *row, uint32_t off, const float (&x)[NC]) {
+    if constexpr (NC == 2)
+        at<f2_a4>(row, off) = f2{x[0], x[1]};
+    else
+        at<float>(row, off) = x[0];
+}
+template <typename IO, int NC>
+__device__ __forceinline__ void store_elements(void *row, uint32_t off, const float (&x)[NC]) {
+    if constexpr (IO::bytes == 4)
+        store_floats<NC>(row, off, x);
+    else if constexpr (NC == 2)
+        at<u1_a2>(row, off) = pack_bf16x2(x[0], x[1]);
+    else
+        store_io<IO>(&at<char>(row, off), 0, x[0]);
 }
 
-// An element as it lies in memory, kept so until it is used.
-template <typename IO>
-struct RawOne {
-    typename IO::storage v;
-    __device__ __forceinline__ float get() const {
+// A wave's rows of a state (from k0 on, V floats each) into memory.
+template <int ST, int NC>
+__device__ __forceinline__ void store_rows(char *to, uint32_t v_row, int K, int k0, bool every, uint32_t v0, bool live,
+                                           const f4 (&s)[ST][NC]) {
+    if (!live) return;
+#pragma unroll
+    for (int j = 0; j < ST; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (every || k0 + 16 * j + i < K) {
+                float x[NC];
+#pragma unroll
+                for (int n = 0; n < NC; ++n) x[n] = s[j][n][i];
+                store_floats<NC>(to + (16 * j + i) * (int64_t)v_row, k0 * v_row + v0 * 4, x);
+            }
+}
+
+// NC neighbouring elements as they lie in memory, kept so until they are used.
+template <typename IO, int NC>
+struct Elements {
+    typedef typename IO::storage one;
+    struct Two {
+        one v[NC];
+    };
+    Two e;
+    static __device__ __forceinline__ Elements load(const void *row, uint32_t off) {
+        Elements r;
+        if constexpr (NC == 2 && IO::bytes == 2) {
+            const uint32_t w = at<u1_a2>(row, off);
+            __builtin_memcpy(&r.e, &w, 4);
+        } else if constexpr (NC == 2) {
+            const f2 w = at<f2_a4>(row, off);
+            r.e.v[0] = w[0];
+            r.e.v[1] = w[1];
+        } else {
+            r.e.v[0] = at<one>(row, off);
+        }
+        return r;
+    }
+    __device__ __forceinline__ float get(int n) const {
         if constexpr (IO::bytes == 2)
-            return bf16_bits_to_f32(v);
+            return bf16_bits_to_f32(e.v[n]);
         else
-            return v;
+            return e.v[n];
     }
 };
+
 // Enqueue the chunks' kernel (gated_delta.hip); `blocks`: block_bytes a chunk.
 hipError_t launch_prepare(const Call &a, int io_dtype, bool backward, char *blocks, hipStream_t stream);
 size_t block_bytes(int io_dtype, int64_t kdim, bool backward);

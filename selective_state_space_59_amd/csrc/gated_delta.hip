@@ -244,15 +244,10 @@ __global__ __launch_bounds__(kThreads, 2) void chain_kernel(ChainArgs p) {
     char *o_base = static_cast<char *>(p.o) + (b * a.L * a.H + h) * a.V * IO::bytes;
     const uint32_t q_step = (uint32_t)a.q_token * IO::bytes, k_step = (uint32_t)a.k_token * IO::bytes;
     const uint32_t v_step = (uint32_t)a.v_token * IO::bytes, o_step = (uint32_t)(a.H * a.V) * IO::bytes;
-    // lanes past the last channel repeat it and store nothing
-    uint32_t v[NC];
-    bool live[NC];
-#pragma unroll
-    for (int n = 0; n < NC; ++n) {
-        const int vw = 16 * (place.slice * NC + n) + r16;
-        v[n] = min(vw, a.V - 1);
-        live[n] = vw < a.V;
-    }
+    // lanes past the last channels repeat them and store nothing
+    const int vw = channel<NC>(place.slice, r16, 0);
+    const uint32_t v0 = min(vw, a.V - NC);
+    const bool live = vw < a.V;
 
     f4 state[ST][NC];
 #pragma unroll
@@ -262,7 +257,7 @@ __global__ __launch_bounds__(kThreads, 2) void chain_kernel(ChainArgs p) {
             const int k0 = 16 * (ST * wave + j) + 4 * grp;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                state[j][n][i] = p.h0 && k0 + i < a.K ? p.h0[(head * a.K + k0 + i) * a.V + v[n]] : 0.0f;
+                state[j][n][i] = p.h0 && k0 + i < a.K ? p.h0[(head * a.K + k0 + i) * a.V + v0 + n] : 0.0f;
             s.state.put4(16 * n + r16, k0, state[j][n]);
         }
 
@@ -271,7 +266,7 @@ __global__ __launch_bounds__(kThreads, 2) void chain_kernel(ChainArgs p) {
     typename O::template Sum<OUT> att[2];
     f4 k_enter, k_leave, q_enter, beta;
     float through;
-    RawOne<IO> val[NC][4];
+    Elements<IO, NC> val[4];
     // (no load has a condition: one that has is waited for where its branch ends)
     // a step of the chunk that is there
     const auto step_of = [&](int64_t c, int t) { return (uint32_t)min((int64_t)t, a.L - 1 - c * kC); };
@@ -296,11 +291,8 @@ __global__ __launch_bounds__(kThreads, 2) void chain_kernel(ChainArgs p) {
     const auto load_val = [&](int64_t c) {
         const char *vc = v_base + c * kC * (int64_t)v_step;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t t = step_of(c, mine + i) * v_step;
-#pragma unroll
-            for (int n = 0; n < NC; ++n) val[n][i] = at<RawOne<IO>>(vc, t + v[n] * IO::bytes);
-        }
+        for (int i = 0; i < 4; ++i)
+            val[i] = Elements<IO, NC>::load(vc, step_of(c, mine + i) * v_step + v0 * IO::bytes);
     };
     constexpr int TILE = 512 * IO::bytes;
     const uint32_t in_tile = lane * 8 * IO::bytes;
@@ -358,7 +350,7 @@ __global__ __launch_bounds__(kThreads, 2) void chain_kernel(ChainArgs p) {
             f4 x;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                x[i] = whole || c * kC + mine + i < a.L ? val[n][i].get() : 0.0f;
+                x[i] = whole || c * kC + mine + i < a.L ? val[i].get(n) : 0.0f;
                 const bool seen = k_enter[i] != 0.0f && (through != 0.0f || ks[n][i] - ks[n][i] == 0.0f);
                 x[i] = seen ? __builtin_fmaf(-k_enter[i], ks[n][i], x[i]) : x[i];
                 o[n][i] = q_enter[i] != 0.0f ? q_enter[i] * o[n][i] : 0.0f;
@@ -366,9 +358,10 @@ __global__ __launch_bounds__(kThreads, 2) void chain_kernel(ChainArgs p) {
             s.x.put4(16 * n + r16, mine, x);
         }
         load_val(next);
-        if (p.ck) store_rows<ST, NC>(ck, v_row, a.K, 16 * ST * wave + 4 * grp, a.K == KP, v, live, state);
+        if (p.ck) store_rows<ST, NC>(ck, v_row, a.K, 16 * ST * wave + 4 * grp, a.K == KP, v0, live, state);
         __syncthreads();
         // (I + B diag(beta)) E = X
+        f4 errs[NC];
 #pragma unroll
         for (int n = 0; n < NC; ++n) {
             f4 err = O::mul(f4{0, 0, 0, 0}, inv[0], s.x.get(16 * n + r16, 8 * grp));
@@ -376,10 +369,16 @@ __global__ __launch_bounds__(kThreads, 2) void chain_kernel(ChainArgs p) {
             const f4 u = beta * err;
             s.w.put4(16 * n + r16, mine, k_leave * u);
             s.u.put4(16 * n + r16, mine, u);
-            if (p.ck && live[n])
-#pragma unroll
-                for (int i = 0; i < 4; ++i) at<float>(ck + (a.K + i) * (int64_t)v_row, mine * v_row + v[n] * 4) = err[i];
+            errs[n] = err;
         }
+        if (p.ck && live)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float x[NC];
+#pragma unroll
+                for (int n = 0; n < NC; ++n) x[n] = errs[n][i];
+                store_floats<NC>(ck + (a.K + i) * (int64_t)v_row, mine * v_row + v0 * 4, x);
+            }
         load_inv(next);
         const float pass = through;
         load_vec(next);
@@ -405,19 +404,23 @@ __global__ __launch_bounds__(kThreads, 2) void chain_kernel(ChainArgs p) {
             for (int n = 0; n < NC; ++n) {
                 o[n] = O::mul(o[n], att[0], s.u.get(16 * n + r16, 8 * grp));
                 if (wave >= 2) o[n] = O::mul(o[n], att[1], s.u.get(16 * n + r16, 32 + 8 * grp));
-                if (live[n])
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (whole || c * kC + mine + i < a.L)
-                            store_io<IO>(&at<char>(oc + i * (int64_t)o_step, 4 * grp * o_step + v[n] * IO::bytes), 0, o[n][i]);
             }
+            if (live)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (whole || c * kC + mine + i < a.L) {
+                        float x[NC];
+#pragma unroll
+                        for (int n = 0; n < NC; ++n) x[n] = o[n][i];
+                        store_elements<IO, NC>(oc + i * (int64_t)o_step, 4 * grp * o_step + v0 * IO::bytes, x);
+                    }
         }
         load_att(next);
         __syncthreads();
     }
     if (p.h_final)
         store_rows<ST, NC>(reinterpret_cast<char *>(p.h_final) + head * a.K * (int64_t)v_row, v_row, a.K,
-                           16 * ST * wave + 4 * grp, a.K == KP, v, live, state);
+                           16 * ST * wave + 4 * grp, a.K == KP, v0, live, state);
 }
 
 // ------------------------------------------------------------------------------------ step

@@ -67,15 +67,10 @@ __global__ __launch_bounds__(kThreads, 2) void back_chain_kernel(BackArgs p) {
     char *dv_base = static_cast<char *>(p.dv) + o_first;
     const uint32_t k_step = (uint32_t)a.k_token * IO::bytes, o_step = (uint32_t)(a.H * a.V) * IO::bytes;
     const uint32_t v_row = (uint32_t)a.V * 4;  // a state's row in bytes
-    // lanes past the last channel repeat it, store nothing and count for nothing
-    uint32_t v[NC];
-    bool live[NC];
-#pragma unroll
-    for (int n = 0; n < NC; ++n) {
-        const int vw = 16 * (place.slice * NC + n) + r16;
-        v[n] = min(vw, a.V - 1);
-        live[n] = vw < a.V;
-    }
+    // lanes past the last channels repeat them, store nothing and count for nothing
+    const int vw = channel<NC>(place.slice, r16, 0);
+    const uint32_t v0 = min(vw, a.V - NC);
+    const bool live = vw < a.V;
 
     f4 ds[ST][NC];
 #pragma unroll
@@ -85,7 +80,7 @@ __global__ __launch_bounds__(kThreads, 2) void back_chain_kernel(BackArgs p) {
             const int k0 = 16 * (ST * wave + j) + 4 * grp;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                ds[j][n][i] = p.dh_final && k0 + i < a.K ? p.dh_final[(head * a.K + k0 + i) * a.V + v[n]] : 0.0f;
+                ds[j][n][i] = p.dh_final && k0 + i < a.K ? p.dh_final[(head * a.K + k0 + i) * a.V + v0 + n] : 0.0f;
             s.ds.put4(16 * n + r16, k0, ds[j][n]);
         }
 
@@ -93,7 +88,7 @@ __global__ __launch_bounds__(kThreads, 2) void back_chain_kernel(BackArgs p) {
     typename O::template Sum<PL> inv[2], att[2];
     f4 k_enter, k_leave, q_enter, beta;
     float through;
-    RawOne<IO> rdo[NC][4];
+    Elements<IO, NC> rdo[4];
     f4 rerr[NC];
     // a step of the chunk that is there
     const auto step_of = [&](int64_t c, int t) { return (uint32_t)min((int64_t)t, a.L - 1 - c * kC); };
@@ -115,18 +110,15 @@ __global__ __launch_bounds__(kThreads, 2) void back_chain_kernel(BackArgs p) {
     const auto load_dout = [&](int64_t c) {
         const char *dc = do_base + c * kC * (int64_t)o_step;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t t = step_of(c, 4 * grp + 16 * wave + i) * o_step;
-#pragma unroll
-            for (int n = 0; n < NC; ++n) rdo[n][i] = at<RawOne<IO>>(dc, t + v[n] * IO::bytes);
-        }
+        for (int i = 0; i < 4; ++i)
+            rdo[i] = Elements<IO, NC>::load(dc, step_of(c, mine + i) * o_step + v0 * IO::bytes);
     };
     const auto load_err = [&](int64_t c) {
         const char *err = reinterpret_cast<const char *>(p.ck) + ((c * a.B * a.H + head) * (a.K + kC) + a.K) * (int64_t)v_row;
 #pragma unroll
         for (int n = 0; n < NC; ++n)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) rerr[n][i] = at<float>(err + i * (int64_t)v_row, mine * v_row + v[n] * 4);
+            for (int i = 0; i < 4; ++i) rerr[n][i] = at<float>(err + i * (int64_t)v_row, mine * v_row + (v0 + n) * 4);
     };
     constexpr int TILE = 512 * IO::bytes;
     const uint32_t in_tile = lane * 8 * IO::bytes;
@@ -151,7 +143,7 @@ __global__ __launch_bounds__(kThreads, 2) void back_chain_kernel(BackArgs p) {
         for (int n = 0; n < NC; ++n) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                dout[n][i] = (c + 1) * kC <= a.L || c * kC + mine + i < a.L ? rdo[n][i].get() : 0.0f;
+                dout[n][i] = (c + 1) * kC <= a.L || c * kC + mine + i < a.L ? rdo[i].get(n) : 0.0f;
             s.dout.put4(16 * n + r16, mine, dout[n]);
         }
     };
@@ -197,13 +189,13 @@ __global__ __launch_bounds__(kThreads, 2) void back_chain_kernel(BackArgs p) {
         for (int n = 0; n < NC; ++n) {
             f4 e;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) e[i] = sum16(live[n] ? rerr[n][i] * du[n][i] : 0.0f);
+            for (int i = 0; i < 4; ++i) e[i] = sum16(live ? rerr[n][i] * du[n][i] : 0.0f);
             const int strip = place.slice * NC + n;
             if (r16 == 0 && strip < strips) *reinterpret_cast<f4 *>(p.edu + (chunk * strips + strip) * kC + mine) = e;
         }
         load_err(next);
         store_rows<ST, NC>(reinterpret_cast<char *>(p.after) + chunk * a.K * (int64_t)v_row, v_row, a.K,
-                           16 * ST * wave + 4 * grp, a.K == KP, v, live, ds);
+                           16 * ST * wave + 4 * grp, a.K == KP, v0, live, ds);
         __syncthreads();
         // dX = N^T diag(beta) dU
         char *dvc = dv_base + (c * kC + 16 * wave) * (int64_t)o_step;
@@ -214,12 +206,12 @@ __global__ __launch_bounds__(kThreads, 2) void back_chain_kernel(BackArgs p) {
             if (wave < 2) dx = O::mul(dx, inv[0], s.u.get(16 * n + r16, 8 * grp));
             dx = O::mul(dx, inv[1], s.u.get(16 * n + r16, 32 + 8 * grp));
             s.w.put4(16 * n + r16, mine, -k_enter * dx);
-            if (live[n])
+            if (live)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    at<float>(dxc + i * (int64_t)v_row, mine * v_row + v[n] * 4) = dx[i];
+                    at<float>(dxc + i * (int64_t)v_row, mine * v_row + (v0 + n) * 4) = dx[i];
                     if (whole || c * kC + mine + i < a.L)
-                        store_io<IO>(&at<char>(dvc + i * (int64_t)o_step, 4 * grp * o_step + v[n] * IO::bytes), 0, dx[i]);
+                        store_io<IO>(&at<char>(dvc + i * (int64_t)o_step, 4 * grp * o_step + (v0 + n) * IO::bytes), 0, dx[i]);
                 }
         }
         load_matrix(inv, next, Block::kInv);
@@ -249,7 +241,7 @@ __global__ __launch_bounds__(kThreads, 2) void back_chain_kernel(BackArgs p) {
     }
     if (p.dh0)
         store_rows<ST, NC>(reinterpret_cast<char *>(p.dh0) + head * a.K * (int64_t)v_row, v_row, a.K,
-                           16 * ST * wave + 4 * grp, a.K == KP, v, live, ds);
+                           16 * ST * wave + 4 * grp, a.K == KP, v0, live, ds);
 }
 
 // --------------------------------------------------------------------------- all chunks at once
