@@ -335,6 +335,8 @@ __device__ __forceinline__ ChainPlace chain_place(int64_t heads, int slices) {
     return p;
 }
 inline unsigned chain_grid(int64_t heads, int slices) { return (unsigned)((heads + 7) / 8 * 8 * slices); }
+// Whether slices of 32 value channels leave a workgroup for each CU.
+inline bool wide_slices(const Call &a) { return a.B * a.H * ((a.V + 31) / 32) >= 256; }
 
 // A tensor's place for a whole wave and a lane's distance from it in bytes: one address register a lane.
 template <typename T>

@@ -547,8 +547,8 @@ hipError_t prepare(const Call &a, bool backward, char *blocks, hipStream_t strea
 template <typename IO, int KP>
 hipError_t chain(ChainArgs p, hipStream_t stream) {
     // 32 channels a workgroup where every CU gets one all the same (8 x 2048 x 12 heads: 197 us, 230 with 16;
-    // where checkpoints are written as well 312 either way)
-    const int nc = p.a.B * p.a.H * ((p.a.V + 31) / 32) >= 256 ? 2 : 1;
+    // where checkpoints are written as well 259 and 312)
+    const int nc = wide_slices(p.a) ? 2 : 1;
     p.slices = (p.a.V + 16 * nc - 1) / (16 * nc);
     const unsigned grid = chain_grid(p.a.B * p.a.H, p.slices);
     if (nc == 2)

@@ -28,7 +28,7 @@ struct BackArgs {
     const void *dout;
     void *dv;
     float *dh0;
-    float *after, *dx, *edu;  // workspace: (B,H,n,K,V), (B,H,n,64,V), (B,H,n,ceil(V/16),64)
+    float *after, *dx, *edu;  // workspace: (B,H,n,K,V), (B,H,n,64,V), (B,H,n,slices,64)
     int slices;
 };
 
@@ -59,7 +59,6 @@ __global__ __launch_bounds__(kThreads, 2) void back_chain_kernel(BackArgs p) {
     const int64_t head = place.head, b = head / a.H;
     const int h = (int)(head % a.H), hk = h / (a.H / a.Hk);
     const int row = 16 * wave + r16, mine = 16 * wave + 4 * grp;
-    const int strips = (a.V + 15) / 16;
     const char *blocks = p.blocks + head * a.n * Block::kBytes;
     const char *k_base = bytes(static_cast<const char *>(a.k), b * a.k_batch + (int64_t)hk * a.K, IO::bytes);
     const int64_t o_first = (b * a.L * a.H + h) * a.V * IO::bytes;
@@ -89,7 +88,7 @@ __global__ __launch_bounds__(kThreads, 2) void back_chain_kernel(BackArgs p) {
     f4 k_enter, k_leave, q_enter, beta;
     float through;
     Elements<IO, NC> rdo[4];
-    f4 rerr[NC];
+    Elements<io_f32, NC> rerr[4];
     // a step of the chunk that is there
     const auto step_of = [&](int64_t c, int t) { return (uint32_t)min((int64_t)t, a.L - 1 - c * kC); };
     const auto load_k = [&](int64_t c) {
@@ -116,9 +115,8 @@ __global__ __launch_bounds__(kThreads, 2) void back_chain_kernel(BackArgs p) {
     const auto load_err = [&](int64_t c) {
         const char *err = reinterpret_cast<const char *>(p.ck) + ((c * a.B * a.H + head) * (a.K + kC) + a.K) * (int64_t)v_row;
 #pragma unroll
-        for (int n = 0; n < NC; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) rerr[n][i] = at<float>(err + i * (int64_t)v_row, mine * v_row + (v0 + n) * 4);
+        for (int i = 0; i < 4; ++i)
+            rerr[i] = Elements<io_f32, NC>::load(err + i * (int64_t)v_row, mine * v_row + v0 * 4);
     };
     constexpr int TILE = 512 * IO::bytes;
     const uint32_t in_tile = lane * 8 * IO::bytes;
@@ -184,15 +182,16 @@ __global__ __launch_bounds__(kThreads, 2) void back_chain_kernel(BackArgs p) {
             s.q.put4(16 * n + r16, mine, q_enter * dout[n]);
         }
         load_matrix(att, next, Block::kAtt);
-        // E . dU over each strip's channels
+        // E . dU over the slice's channels
+        f4 e;
 #pragma unroll
-        for (int n = 0; n < NC; ++n) {
-            f4 e;
+        for (int i = 0; i < 4; ++i) {
+            float own = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) e[i] = sum16(live ? rerr[n][i] * du[n][i] : 0.0f);
-            const int strip = place.slice * NC + n;
-            if (r16 == 0 && strip < strips) *reinterpret_cast<f4 *>(p.edu + (chunk * strips + strip) * kC + mine) = e;
+            for (int n = 0; n < NC; ++n) own = __builtin_fmaf(rerr[i].get(n), du[n][i], own);
+            e[i] = sum16(live ? own : 0.0f);
         }
+        if (r16 == 0) *reinterpret_cast<f4 *>(p.edu + (chunk * p.slices + place.slice) * kC + mine) = e;
         load_err(next);
         store_rows<ST, NC>(reinterpret_cast<char *>(p.after) + chunk * a.K * (int64_t)v_row, v_row, a.K,
                            16 * ST * wave + 4 * grp, a.K == KP, v0, live, ds);
@@ -200,20 +199,23 @@ __global__ __launch_bounds__(kThreads, 2) void back_chain_kernel(BackArgs p) {
         // dX = N^T diag(beta) dU
         char *dvc = dv_base + (c * kC + 16 * wave) * (int64_t)o_step;
         char *dxc = reinterpret_cast<char *>(p.dx) + chunk * kC * (int64_t)v_row;
+        f4 dx[NC] = {};
 #pragma unroll
         for (int n = 0; n < NC; ++n) {
-            f4 dx = {0, 0, 0, 0};
-            if (wave < 2) dx = O::mul(dx, inv[0], s.u.get(16 * n + r16, 8 * grp));
-            dx = O::mul(dx, inv[1], s.u.get(16 * n + r16, 32 + 8 * grp));
-            s.w.put4(16 * n + r16, mine, -k_enter * dx);
-            if (live)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    at<float>(dxc + i * (int64_t)v_row, mine * v_row + (v0 + n) * 4) = dx[i];
-                    if (whole || c * kC + mine + i < a.L)
-                        store_io<IO>(&at<char>(dvc + i * (int64_t)o_step, 4 * grp * o_step + (v0 + n) * IO::bytes), 0, dx[i]);
-                }
+            if (wave < 2) dx[n] = O::mul(dx[n], inv[0], s.u.get(16 * n + r16, 8 * grp));
+            dx[n] = O::mul(dx[n], inv[1], s.u.get(16 * n + r16, 32 + 8 * grp));
+            s.w.put4(16 * n + r16, mine, -k_enter * dx[n]);
         }
+        if (live)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float x[NC];
+#pragma unroll
+                for (int n = 0; n < NC; ++n) x[n] = dx[n][i];
+                store_floats<NC>(dxc + i * (int64_t)v_row, mine * v_row + v0 * 4, x);
+                if (whole || c * kC + mine + i < a.L)
+                    store_elements<IO, NC>(dvc + i * (int64_t)o_step, 4 * grp * o_step + v0 * IO::bytes, x);
+            }
         load_matrix(inv, next, Block::kInv);
         const float pass = through;
         load_vec(next);
@@ -254,6 +256,7 @@ struct GradArgs {
     const void *dout;
     void *dq, *dk, *dbeta;
     float *dg;
+    int slices;
 };
 
 template <typename IO, int KP>
@@ -401,9 +404,8 @@ __global__ __launch_bounds__(kGradThreads) void grads_kernel(GradArgs p) {
             reinterpret_cast<u4 *>(&s.out.m1)[i] = u4{0, 0, 0, 0};
         __syncthreads();
         if (wave == kGradThreads / 64 - 1) {  // (one of those with one tile)
-            const int strips = (a.V + 15) / 16;
             float e = 0.0f;
-            for (int i = 0; i < strips; ++i) e += p.edu[(chunk * strips + i) * kC + lane];
+            for (int i = 0; i < p.slices; ++i) e += p.edu[(chunk * p.slices + i) * kC + lane];
             s.edu[lane] = e;
         }
 #pragma unroll
@@ -578,17 +580,25 @@ __global__ __launch_bounds__(kGradThreads) void grads_kernel(GradArgs p) {
     }
 }
 
-template <typename IO, int KP>
-hipError_t backward(BackArgs p, const GradArgs &g, hipStream_t stream) {
-    // 16 channels a workgroup: 32 would not fit the registers (8 x 2048 x 12 heads: 333 us, 541 with 32)
-    p.slices = (p.a.V + 15) / 16;
-    const unsigned grid = chain_grid(p.a.B * p.a.H, p.slices);
-    back_chain_kernel<IO, KP, 1><<<grid, kThreads, sizeof(BackLds<IO, KP, 1>), stream>>>(p);
+template <typename IO, int KP, int NC>
+hipError_t back_chain(BackArgs p, GradArgs g, hipStream_t stream) {
+    p.slices = g.slices = (p.a.V + 16 * NC - 1) / (16 * NC);
+    back_chain_kernel<IO, KP, NC>
+        <<<chain_grid(p.a.B * p.a.H, p.slices), kThreads, sizeof(BackLds<IO, KP, NC>), stream>>>(p);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const dim3 chunks((unsigned)p.a.n, (unsigned)p.a.Hk, (unsigned)p.a.B);
     grads_kernel<IO, KP><<<chunks, kGradThreads, sizeof(GradLds<IO, KP>), stream>>>(g);
     return hipGetLastError();
+}
+
+template <typename IO, int KP>
+hipError_t backward(const BackArgs &p, const GradArgs &g, hipStream_t stream) {
+    // 32 value channels a workgroup where that leaves one for each CU, as forwards (8 x 2048 x 12 heads: 277 us, 340
+    // with 16); floats keep to 16, as 32 would not fit the registers
+    if constexpr (IO::bytes == 2)
+        if (wide_slices(p.a)) return back_chain<IO, KP, 2>(p, g, stream);
+    return back_chain<IO, KP, 1>(p, g, stream);
 }
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
@@ -628,7 +638,7 @@ hipError_t launch_backward(const Call &c, const ssm_gated_delta_bwd_args_t &a, h
     float *after = reinterpret_cast<float *>(ws + plan.after), *dx = reinterpret_cast<float *>(ws + plan.dx);
     float *edu = reinterpret_cast<float *>(ws + plan.edu);
     const BackArgs p{c, ws, ck, a.dh_final, a.dout, a.dv, a.dh0, after, dx, edu, 0};
-    const GradArgs g{c, ws, ck, after, dx, edu, a.dout, a.dq, a.dk, a.dbeta, a.dg};
+    const GradArgs g{c, ws, ck, after, dx, edu, a.dout, a.dq, a.dk, a.dbeta, a.dg, 0};
     if (a.io_dtype == SSM_BF16)
         return a.kdim <= 64 ? backward<io_bf16, 64>(p, g, stream) : backward<io_bf16, 128>(p, g, stream);
     return a.kdim <= 64 ? backward<io_f32, 64>(p, g, stream) : backward<io_f32, 128>(p, g, stream);
