@@ -48,7 +48,8 @@ def _same(got, want, what):
 @pytest.mark.parametrize("dtype", **IDS)
 def test_stores_of_the_chain_stay_inside(dtype):
     """Every output and a workspace of exactly the size asked for lie in marked memory."""
-    for B, L, Hk, H, K, V in [(1, 1, 1, 1, 8, 8), (2, 65, 1, 2, 72, 24), (1, 64, 2, 2, 64, 72), (1, 130, 2, 6, 128, 136)]:
+    for B, L, Hk, H, K, V in [(1, 1, 1, 1, 8, 8), (2, 65, 1, 2, 72, 24), (1, 64, 2, 2, 64, 72), (1, 130, 2, 6, 128, 136),
+                               (32, 66, 2, 8, 72, 24), (16, 65, 8, 8, 128, 40)]:
         what = "%dx%d %d/%d heads %dx%d" % (B, L, Hk, H, K, V)
         print(what, flush=True)
         k = delta_case(B, L, Hk, H, K, V, dtype, seed=L, doc=20)

@@ -54,6 +54,15 @@ def test_forward_and_gradients(shape, dtype):
 
 
 @pytest.mark.parametrize("dtype", **IDS)
+@pytest.mark.parametrize("shape", [(64, 70, 2, 4, 16, 8), (32, 3, 8, 8, 128, 24), (16, 65, 4, 8, 72, 40), (86, 66, 1, 1, 64, 72)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_slices_of_32_channels(shape, dtype):
+    """Chains enough for a workgroup to take 32 value channels, the last slice of 8, 24, 8 and 8 of them."""
+    k = delta_case(*shape, dtype, seed=sum(shape), doc=40)
+    _check(k, "%s" % (shape,))
+
+
+@pytest.mark.parametrize("dtype", **IDS)
 @pytest.mark.parametrize("shape", [(1, 1, 1, 8, 8), (3, 2, 4, 128, 128), (5, 1, 3, 72, 40), (2, 4, 4, 64, 136),
                                    (130, 2, 2, 24, 32)], ids=lambda s: "x".join(map(str, s)))
 def test_step(shape, dtype):
