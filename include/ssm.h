@@ -762,12 +762,14 @@ ssm_status_t ssm_gated_rmsnorm_bwd(const ssm_gated_norm_bwd_args_t *args, void *
  * 16 bits, where only a bf16 output follows); outputs are rounded once.  Results
  * do not change from run to run.  kdim: a multiple of 8 up to SSM_DELTA_MAX_KDIM;
  * vdim: a multiple of 8 up to SSM_DELTA_MAX_VDIM; kheads divides heads <= 65535;
- * batch <= 65535; seqlen < 2^30.
+ * batch <= 65535; seqlen < 2^30; heads * vdim and kheads * kdim < 2^24;
+ * (batch * heads + 8) * ceil(vdim / 16) < 2^23.
  *
  * q, k and v may be parts of a wider tensor: x_token is the distance of two steps
  * and x_batch that of two batch rows, in elements; x_token 0: dense.  A head's
- * channels and a step's heads are always consecutive.  q and k lie at 16-byte
- * boundaries, with strides that keep them there.
+ * channels and a step's heads are always consecutive.  Strides are not negative,
+ * x_token < 2^24 and x_batch <= 2^40.  q and k lie at 16-byte boundaries, with
+ * strides that keep them there (ssm_gated_delta_step: at their elements').
  *
  * A call is several launches and its workspace carries data between them: as
  * with ssm_gated_scan_fwd.
@@ -792,8 +794,8 @@ typedef struct ssm_gated_delta_args {
     void *o;                /* (B,L,H,V) io_dtype output, required             */
     float *h_final;         /* (B,H,K,V) fp32 output, or NULL                  */
     float *checkpoints;     /* (ceil(L/SSM_DELTA_CHUNK), B, H, K + SSM_DELTA_CHUNK, V) fp32
-                               output, or NULL: for each chunk the state entering it, and
-                               e_t of its steps (0 behind the last)            */
+                               output, 16-byte aligned, or NULL: for each chunk the state
+                               entering it, and e_t of its steps (0 behind the last) */
     int64_t q_token, q_batch, k_token, k_batch, v_token, v_batch;
     void *workspace;        /* device scratch of workspace_bytes, 256-aligned  */
     size_t workspace_bytes; /* >= ssm_gated_delta_workspace_size(args)         */
@@ -823,7 +825,8 @@ typedef struct ssm_gated_delta_bwd_args {
     const float *h0;
     const void *dout;       /* (B,L,H,V) io_dtype, dense, required             */
     const float *dh_final;  /* (B,H,K,V) fp32, or NULL (= 0)                   */
-    const float *checkpoints; /* of an ssm_gated_delta_fwd call on the same inputs, or NULL */
+    const float *checkpoints; /* of an ssm_gated_delta_fwd call on the same inputs, 16-byte
+                                 aligned, or NULL                              */
     void *dq, *dk;          /* (B,L,Hk,K) io_dtype outputs, required           */
     void *dv;               /* (B,L,H,V) io_dtype output, required             */
     float *dg;              /* (B,L,H) fp32 output, required                   */
@@ -846,7 +849,7 @@ ssm_status_t ssm_gated_delta_bwd(const ssm_gated_delta_bwd_args_t *args, void *s
 /*
  * One decode step on a state kept between calls (h_final of a prefill), advanced
  * IN PLACE; a row with reset[b] != 0 begins anew.  x_batch: distance of two batch
- * rows of q, k or v, 0 for dense ones.
+ * rows of q, k or v, < 2^24; 0 for dense ones.
  */
 typedef struct ssm_gated_delta_step_args {
     int64_t batch, kheads, heads, kdim, vdim;
@@ -877,7 +880,7 @@ ssm_status_t ssm_gated_delta_step(const ssm_gated_delta_step_args_t *args, void 
 #define SSM_FP8_BLOCK 128
 
 typedef struct ssm_quantize_fp8_args {
-    int64_t rows;           /* M >= 0                                          */
+    int64_t rows;           /* M >= 0; M * ceil(D/128) < 2^28                  */
     int64_t dim;            /* D: a multiple of 16, 16 <= D <= 2^20            */
     int64_t block_rows;     /* 1, or SSM_FP8_BLOCK                             */
     int32_t io_dtype;       /* ssm_dtype_t of x                                */
@@ -892,7 +895,8 @@ ssm_status_t ssm_quantize_fp8(const ssm_quantize_fp8_args_t *args, void *stream)
 /*
  * ssm_add_rmsnorm_fwd with y quantised as by ssm_quantize_fp8 with block_rows 1,
  * from its fp32 values: q (rows,D) e4m3 bytes and scales (rows, ceil(D/128)) fp32.
- * `norm` is that function's struct with y NULL, and a dim that is a multiple of 16.
+ * `norm` is that function's struct with y NULL, and a dim that is a multiple of 16;
+ * rows * ceil(D/128) < 2^28.
  */
 typedef struct ssm_add_norm_fp8_args {
     ssm_add_norm_args_t norm;
@@ -912,7 +916,8 @@ ssm_status_t ssm_add_rmsnorm_fp8(const ssm_add_norm_fp8_args_t *args, void *stre
  * fp32 y they are summed in fp32.  x is quantised by rows of 1, w by rows of 128.
  */
 typedef struct ssm_matmul_fp8_args {
-    int64_t m, n, k;        /* M >= 0, N >= 1; K a multiple of 16; each < 2^31 */
+    int64_t m, n, k;        /* M >= 0; 1 <= N < 2^24; K: a multiple of 16 up to 2^20;
+                               ceil(M/256) * ceil(N/256) < 2^22                */
     int32_t out_dtype;      /* ssm_dtype_t of y                                */
     const void *xq;         /* (M,K) e4m3 bytes, 16-byte aligned, required     */
     const float *x_scales;  /* (M, ceil(K/128)) fp32, required                 */

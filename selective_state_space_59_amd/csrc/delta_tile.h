@@ -425,9 +425,11 @@ struct Elements {
 // Enqueue the chunks' kernel (gated_delta.hip); `blocks`: block_bytes a chunk.
 hipError_t launch_prepare(const Call &a, int io_dtype, bool backward, char *blocks, hipStream_t stream);
 size_t block_bytes(int io_dtype, int64_t kdim, bool backward);
-// The forward chain; o, h_final and ck may be NULL.
-hipError_t launch_chain(const Call &a, int io_dtype, const char *blocks, const float *h0, void *o, float *h_final,
-                        float *ck, hipStream_t stream);
+// The forward chain; o, h_final and ck may be NULL.  `blocks`: chain_bytes, the chunks' blocks first.
+hipError_t launch_chain(const Call &a, int io_dtype, char *blocks, const float *h0, void *o, float *h_final, float *ck,
+                        hipStream_t stream);
+size_t chain_bytes(int io_dtype, int64_t heads, int64_t n, int64_t kdim, int64_t vdim);
+inline size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 // The backward of a call (gated_delta_bwd.hip).
 hipError_t launch_backward(const Call &c, const ssm_gated_delta_bwd_args_t &a, hipStream_t stream);
 size_t backward_bytes(const ssm_gated_delta_bwd_args_t &a);

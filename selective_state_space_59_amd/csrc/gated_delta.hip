@@ -212,7 +212,9 @@ struct ChainArgs {
     const float *h0;
     void *o;
     float *h_final, *ck;
-    int slices;
+    float *parts;  // (heads, segments - 1): Z, K x V floats, and T transposed, K x K
+    int64_t per;   // chunks of a segment
+    int segments, slices;
 };
 
 // Four waves carry 16 NC value channels of one head along the chunks.  Wave w has the steps 16 w .. + 15 of
@@ -220,7 +222,12 @@ struct ChainArgs {
 // queries and the chunk's matrices no other wave of the workgroup reads, so it comes from memory straight
 // into registers, reloaded for the next chunk as soon as it has been used; only states, X and E go round
 // through LDS, split into their planes once, by the wave that owns them.  Three barriers a chunk.
-template <typename IO, int KP, int NC>
+//
+// A long sequence of few heads runs in segments.  The state that leaves a segment is T S + Z for the state S
+// entering it; first (FIRST) all segments but the last form, without outputs, their Z (from a state of zeros,
+// the first one's from h0) and, as K more columns without values, their T (from the identity); join_kernel
+// turns these into the states entering the segments, and the chains run again from there.
+template <typename IO, int KP, int NC, bool FIRST>
 __global__ __launch_bounds__(kThreads, 2) void chain_kernel(ChainArgs p) {
     using O = Op<IO>;
     using E = typename O::elem;
@@ -230,11 +237,14 @@ __global__ __launch_bounds__(kThreads, 2) void chain_kernel(ChainArgs p) {
     extern __shared__ __attribute__((aligned(16))) char raw[];
     Lds &s = *reinterpret_cast<Lds *>(raw);
     const Call &a = p.a;
-    const ChainPlace place = chain_place(a.B * a.H, p.slices);
+    const int running = FIRST ? p.segments - 1 : p.segments;
+    const ChainPlace place = chain_place(a.B * a.H * running, p.slices);
     if (!place.any) return;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r16 = lane % 16, grp = lane / 16;
-    const int64_t head = place.head, b = head / a.H;
+    const int64_t head = place.head / running, b = head / a.H;
+    const int segment = (int)(place.head % running);
+    const int64_t begin = segment * p.per, end = min(begin + p.per, a.n);
     const int h = (int)(head % a.H), hk = h / (a.H / a.Hk);
     const int row = 16 * wave + r16, mine = 16 * wave + 4 * grp;  // left operands' row; results' first row
     const char *blocks = p.blocks + head * a.n * Block::kBytes;
@@ -245,9 +255,15 @@ __global__ __launch_bounds__(kThreads, 2) void chain_kernel(ChainArgs p) {
     const uint32_t q_step = (uint32_t)a.q_token * IO::bytes, k_step = (uint32_t)a.k_token * IO::bytes;
     const uint32_t v_step = (uint32_t)a.v_token * IO::bytes, o_step = (uint32_t)(a.H * a.V) * IO::bytes;
     // lanes past the last channels repeat them and store nothing
-    const int vw = channel<NC>(place.slice, r16, 0);
-    const uint32_t v0 = min(vw, a.V - NC);
-    const bool live = vw < a.V;
+    const int value_slices = (a.V + 16 * NC - 1) / (16 * NC);
+    const bool matrix = FIRST && place.slice >= value_slices;  // columns of T
+    if (matrix && segment == 0) return;
+    const int width = matrix ? a.K : a.V, vw = channel<NC>(place.slice - (matrix ? value_slices : 0), r16, 0);
+    const uint32_t v0 = min(vw, width - NC);
+    const bool live = vw < width;
+    const auto part = [&](int i) { return p.parts + (head * (p.segments - 1) + i) * a.K * (int64_t)(a.V + a.K); };
+    const float *from = p.h0 ? p.h0 + head * a.K * a.V : nullptr;
+    if (segment > 0) from = FIRST ? nullptr : part(segment - 1);
 
     f4 state[ST][NC];
 #pragma unroll
@@ -257,7 +273,10 @@ __global__ __launch_bounds__(kThreads, 2) void chain_kernel(ChainArgs p) {
             const int k0 = 16 * (ST * wave + j) + 4 * grp;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                state[j][n][i] = p.h0 && k0 + i < a.K ? p.h0[(head * a.K + k0 + i) * a.V + v0 + n] : 0.0f;
+                {
+                state[j][n][i] = from && k0 + i < a.K ? from[(k0 + i) * a.V + v0 + n] : 0.0f;
+                if (matrix) state[j][n][i] = k0 + i == (int)v0 + n ? 1.0f : 0.0f;
+            }
             s.state.put4(16 * n + r16, k0, state[j][n]);
         }
 
@@ -277,7 +296,7 @@ __global__ __launch_bounds__(kThreads, 2) void chain_kernel(ChainArgs p) {
         for (int x = 0; x < KX; ++x) {
             const uint32_t off = (32 * x + 8 * grp < a.K ? 32 * x + 8 * grp : 0) * IO::bytes;
             kf[x] = O::load(&at<E>(kc, t * k_step + off));
-            qf[x] = O::load(&at<E>(qc, t * q_step + off));
+            if constexpr (!FIRST) qf[x] = O::load(&at<E>(qc, t * q_step + off));
         }
     };
     const auto load_vec = [&](int64_t c) {
@@ -292,7 +311,7 @@ __global__ __launch_bounds__(kThreads, 2) void chain_kernel(ChainArgs p) {
         const char *vc = v_base + c * kC * (int64_t)v_step;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            val[i] = Elements<IO, NC>::load(vc, step_of(c, mine + i) * v_step + v0 * IO::bytes);
+            val[i] = Elements<IO, NC>::load(vc, step_of(c, mine + i) * v_step + (matrix ? 0 : v0) * IO::bytes);
     };
     constexpr int TILE = 512 * IO::bytes;
     const uint32_t in_tile = lane * 8 * IO::bytes;
@@ -304,6 +323,7 @@ __global__ __launch_bounds__(kThreads, 2) void chain_kernel(ChainArgs p) {
         inv[1] = O::template planes<PL>(&at<E>(m + tile1, in_tile), Block::PLANE);
     };
     const auto load_att = [&](int64_t c) {
+        if constexpr (FIRST) return;
         const char *m = blocks + c * Block::kBytes + Block::kAtt;
         att[0] = O::template planes<OUT>(&at<E>(m + tile0, in_tile), Block::PLANE);
         att[1] = O::template planes<OUT>(&at<E>(m + tile1, in_tile), Block::PLANE);
@@ -316,15 +336,15 @@ __global__ __launch_bounds__(kThreads, 2) void chain_kernel(ChainArgs p) {
             for (int y = 0; y < 2; ++y) ktf[j][y] = O::load(&at<E>(m + (2 * j + y) * TILE, in_tile));
     };
     const uint32_t v_row = (uint32_t)a.V * 4;  // a state's row in bytes
-    load_qk(0);
-    load_vec(0);
-    load_val(0);
-    load_inv(0);
-    load_kt(0);
-    load_att(0);
+    load_qk(begin);
+    load_vec(begin);
+    load_val(begin);
+    load_inv(begin);
+    load_kt(begin);
+    load_att(begin);
     __syncthreads();
-    for (int64_t c = 0; c < a.n; ++c) {
-        const int64_t next = min(c + 1, a.n - 1);
+    for (int64_t c = begin; c < end; ++c) {
+        const int64_t next = min(c + 1, end - 1);
         const bool whole = (c + 1) * kC <= a.L;
         char *ck = reinterpret_cast<char *>(p.ck) + (c * a.B * a.H + head) * (a.K + kC) * (int64_t)v_row;
         if (!whole || a.K != KP)  // steps past the end and channels past K, which were loaded from elsewhere
@@ -339,7 +359,7 @@ __global__ __launch_bounds__(kThreads, 2) void chain_kernel(ChainArgs p) {
             for (int n = 0; n < NC; ++n) {
                 const auto st = s.state.template get<PL>(16 * n + r16, 32 * x + 8 * grp);
                 ks[n] = O::mul(ks[n], kf[x], st);
-                o[n] = O::mul(o[n], qf[x], O::template first<OUT>(st));
+                if constexpr (!FIRST) o[n] = O::mul(o[n], qf[x], O::template first<OUT>(st));
             }
         load_qk(next);
         // X = V - enter K S (a state that does not reach a step has no part in it, whatever it holds; one that
@@ -350,7 +370,7 @@ __global__ __launch_bounds__(kThreads, 2) void chain_kernel(ChainArgs p) {
             f4 x;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                x[i] = whole || c * kC + mine + i < a.L ? val[i].get(n) : 0.0f;
+                x[i] = !matrix && (whole || c * kC + mine + i < a.L) ? val[i].get(n) : 0.0f;
                 const bool seen = k_enter[i] != 0.0f && (through != 0.0f || ks[n][i] - ks[n][i] == 0.0f);
                 x[i] = seen ? __builtin_fmaf(-k_enter[i], ks[n][i], x[i]) : x[i];
                 o[n][i] = q_enter[i] != 0.0f ? q_enter[i] * o[n][i] : 0.0f;
@@ -358,7 +378,7 @@ __global__ __launch_bounds__(kThreads, 2) void chain_kernel(ChainArgs p) {
             s.x.put4(16 * n + r16, mine, x);
         }
         load_val(next);
-        if (p.ck) store_rows<ST, NC>(ck, v_row, a.K, 16 * ST * wave + 4 * grp, a.K == KP, v0, live, state);
+        if (!FIRST && p.ck) store_rows<ST, NC>(ck, v_row, a.K, 16 * ST * wave + 4 * grp, a.K == KP, v0, live, state);
         __syncthreads();
         // (I + B diag(beta)) E = X
         f4 errs[NC];
@@ -368,10 +388,10 @@ __global__ __launch_bounds__(kThreads, 2) void chain_kernel(ChainArgs p) {
             if (wave >= 2) err = O::mul(err, inv[1], s.x.get(16 * n + r16, 32 + 8 * grp));
             const f4 u = beta * err;
             s.w.put4(16 * n + r16, mine, k_leave * u);
-            s.u.put4(16 * n + r16, mine, u);
+            if constexpr (!FIRST) s.u.put4(16 * n + r16, mine, u);
             errs[n] = err;
         }
-        if (p.ck && live)
+        if (!FIRST && p.ck && live)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 float x[NC];
@@ -398,7 +418,7 @@ __global__ __launch_bounds__(kThreads, 2) void chain_kernel(ChainArgs p) {
         }
         load_kt(next);
         // O = scale enter Q S + P diag(beta) E
-        if (p.o) {
+        if (!FIRST && p.o) {
             char *oc = o_base + (c * kC + 16 * wave) * (int64_t)o_step;
 #pragma unroll
             for (int n = 0; n < NC; ++n) {
@@ -418,9 +438,92 @@ __global__ __launch_bounds__(kThreads, 2) void chain_kernel(ChainArgs p) {
         load_att(next);
         __syncthreads();
     }
-    if (p.h_final)
+    if (matrix) {  // transposed
+#pragma unroll
+        for (int j = 0; j < ST; ++j)
+#pragma unroll
+            for (int n = 0; n < NC; ++n) {
+                const int k0 = 16 * (ST * wave + j) + 4 * grp;
+                if (live && k0 < a.K)
+                    *reinterpret_cast<f4 *>(part(segment) + a.K * a.V + (v0 + n) * a.K + k0) = state[j][n];
+            }
+    } else if constexpr (FIRST)
+        store_rows<ST, NC>(reinterpret_cast<char *>(part(segment)), v_row, a.K, 16 * ST * wave + 4 * grp, a.K == KP, v0,
+                           live, state);
+    else if (p.h_final && segment == p.segments - 1)
         store_rows<ST, NC>(reinterpret_cast<char *>(p.h_final) + head * a.K * (int64_t)v_row, v_row, a.K,
                            16 * ST * wave + 4 * grp, a.K == KP, v0, live, state);
+}
+
+// The states entering the segments, each put in the place of the Z before it: kJoinV value channels of a head
+// a workgroup, for each thread four rows and 16 of the columns of T S, summed over the eight threads of a row
+// through LDS.  A segment's T is loaded while the one before it is worked on.  What T does not take up, or S
+// does not hold, has no part in T S (T is 0 behind a reset, and S may hold infinities or NaNs): sums that come
+// out as NaN are formed again without the terms that have a zero.  (Rows of T behind K repeat others, where S
+// is put as 0.)
+constexpr int kJoinV = 4;
+
+__global__ __launch_bounds__(kThreads, 2) void join_kernel(ChainArgs p) {
+    constexpr int KM = SSM_DELTA_MAX_KDIM, COLS = KM / 8;
+    static_assert(kThreads == KM / 4 * 8 && kThreads == KM * kJoinV / 2, "threads of a row, outputs of a thread");
+    __shared__ f4 s[KM], sums[8][KM];
+    const Call &a = p.a;
+    const int slices = a.V / kJoinV;  // V is a multiple of 8
+    const int64_t head = blockIdx.x / slices, size = a.K * (int64_t)(a.V + a.K);
+    const int v0 = (int)(blockIdx.x % slices) * kJoinV;
+    float *part = p.parts + head * (p.segments - 1) * size;
+    const int quad = threadIdx.x % (KM / 4), eighth = threadIdx.x / (KM / 4);
+    const float *column = part + a.K * a.V + min(4 * quad, a.K - 4);
+    const int row = threadIdx.x / 2, half = threadIdx.x % 2 * 2, at = min(row, a.K - 1) * a.V + v0 + half;
+    f4 t[COLS], m[COLS];
+    f2 z;
+    const auto load = [&](int g) {
+#pragma unroll
+        for (int j = 0; j < COLS; ++j)
+            t[j] = *reinterpret_cast<const f4 *>(column + g * size + min(COLS * eighth + j, a.K - 1) * a.K);
+        z = *reinterpret_cast<const f2 *>(part + g * size + at);
+    };
+    const auto put = [&](f2 x) {
+        if (row >= a.K) x = f2{0, 0};
+        float *to = reinterpret_cast<float *>(&s[row]) + half;
+        to[0] = x[0];
+        to[1] = x[1];
+    };
+    put(*reinterpret_cast<const f2 *>(part + at));
+    load(1);
+    __syncthreads();
+    for (int g = 1; g < p.segments - 1; ++g) {
+#pragma unroll
+        for (int j = 0; j < COLS; ++j) m[j] = t[j];
+        f2 out = z;
+        load(min(g + 1, p.segments - 2));
+        f4 sum[4];  // a row's channels each
+        const auto add_up = [&](auto with_zeros) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) sum[r] = f4{0, 0, 0, 0};
+#pragma unroll
+            for (int j = 0; j < COLS; ++j) {
+                const f4 x = s[COLS * eighth + j];
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+#pragma unroll
+                    for (int n = 0; n < kJoinV; ++n)
+                        if (with_zeros.value || (m[j][r] != 0.0f && x[n] != 0.0f))
+                            sum[r][n] = __builtin_fmaf(m[j][r], x[n], sum[r][n]);
+            }
+        };
+        add_up(std::true_type{});
+        f4 all = sum[0] + sum[1] + sum[2] + sum[3];
+        if (!(all[0] + all[1] + all[2] + all[3] < __builtin_inff())) add_up(std::false_type{});
+#pragma unroll
+        for (int r = 0; r < 4; ++r) sums[eighth][4 * quad + r] = sum[r];
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < 8; ++e) out += *reinterpret_cast<const f2 *>(reinterpret_cast<const float *>(&sums[e][row]) + half);
+        put(out);
+        if (row < a.K) *reinterpret_cast<f2 *>(part + g * size + at) = out;
+        __syncthreads();
+    }
 }
 
 // ------------------------------------------------------------------------------------ step
@@ -544,18 +647,27 @@ hipError_t prepare(const Call &a, bool backward, char *blocks, hipStream_t strea
     return hipGetLastError();
 }
 
+template <typename IO, int KP, int NC, bool FIRST>
+hipError_t chain_pass(ChainArgs p, hipStream_t stream) {
+    p.slices = (p.a.V + 16 * NC - 1) / (16 * NC) + (FIRST ? (p.a.K + 16 * NC - 1) / (16 * NC) : 0);
+    const unsigned grid = chain_grid(p.a.B * p.a.H * (p.segments - FIRST), p.slices);
+    chain_kernel<IO, KP, NC, FIRST><<<grid, kThreads, sizeof(ChainLds<IO, KP, NC>), stream>>>(p);
+    return hipGetLastError();
+}
+
 template <typename IO, int KP>
-hipError_t chain(ChainArgs p, hipStream_t stream) {
+hipError_t chain(const ChainArgs &p, hipStream_t stream) {
+    if (p.segments > 1) {
+        hipError_t e = chain_pass<IO, KP, 1, true>(p, stream);
+        if (e != hipSuccess) return e;
+        if (p.segments > 2)
+            join_kernel<<<(unsigned)(p.a.B * p.a.H * (p.a.V / kJoinV)), kThreads, 0, stream>>>(p);
+        e = hipGetLastError();
+        return e != hipSuccess ? e : chain_pass<IO, KP, 1, false>(p, stream);
+    }
     // 32 channels a workgroup where every CU gets one all the same (8 x 2048 x 12 heads: 197 us, 230 with 16;
     // where checkpoints are written as well 259 and 312)
-    const int nc = wide_slices(p.a) ? 2 : 1;
-    p.slices = (p.a.V + 16 * nc - 1) / (16 * nc);
-    const unsigned grid = chain_grid(p.a.B * p.a.H, p.slices);
-    if (nc == 2)
-        chain_kernel<IO, KP, 2><<<grid, kThreads, sizeof(ChainLds<IO, KP, 2>), stream>>>(p);
-    else
-        chain_kernel<IO, KP, 1><<<grid, kThreads, sizeof(ChainLds<IO, KP, 1>), stream>>>(p);
-    return hipGetLastError();
+    return wide_slices(p.a) ? chain_pass<IO, KP, 2, false>(p, stream) : chain_pass<IO, KP, 1, false>(p, stream);
 }
 
 template <typename IO, int KP>
@@ -584,9 +696,34 @@ hipError_t launch_prepare(const Call &a, int io_dtype, bool backward, char *bloc
                      : prepare<io_f32, 128>(a, backward, blocks, stream);
 }
 
-hipError_t launch_chain(const Call &a, int io_dtype, const char *blocks, const float *h0, void *o, float *h_final,
-                        float *ck, hipStream_t stream) {
-    const ChainArgs p{a, blocks, h0, o, h_final, ck, 0};
+// Segments of a sequence of n chunks: as many as run at once, two workgroups a CU with outputs and three
+// without; of at least eight chunks, as each costs a step of join_kernel and its state once more.  bf16, K = V =
+// 128, whole calls, in segments and in one piece: 32768 steps of 12 heads 992 us in 5 segments and 1407, of 4
+// heads 340 in 13 and 1165, of one head 152 in 32 and 1026; 4096 steps of 4 heads 80 in 8 and 164; 2048 steps of
+// 12 heads 100 in 4 and 98; 1024 steps of 12 heads 73 in 3 and 60, and two segments of them 59.
+static int segments_of(int64_t heads, int64_t n, int64_t K, int64_t V) {
+    const int64_t values = heads * ((V + 15) / 16), matrices = heads * ((K + 15) / 16);
+    const auto fits = [&](int64_t s) {
+        return s <= n / 8 && s * s <= 2 * n && values * s <= 512 && values * (s - 1) + matrices * (s - 2) <= 768;
+    };
+    int64_t s = 3;
+    if (!fits(s) || n < 32) return 1;
+    while (fits(s + 1)) ++s;
+    const int64_t per = (n + s - 1) / s;
+    return (int)((n + per - 1) / per);
+}
+
+size_t chain_bytes(int io_dtype, int64_t heads, int64_t n, int64_t K, int64_t V) {
+    return up256((size_t)(heads * n) * block_bytes(io_dtype, K, false)) +
+           up256((size_t)(heads * (segments_of(heads, n, K, V) - 1) * K * (V + K)) * sizeof(float));
+}
+
+hipError_t launch_chain(const Call &a, int io_dtype, char *blocks, const float *h0, void *o, float *h_final, float *ck,
+                        hipStream_t stream) {
+    const int64_t heads = a.B * a.H;
+    const int segments = segments_of(heads, a.n, a.K, a.V);
+    float *parts = reinterpret_cast<float *>(blocks + up256((size_t)(heads * a.n) * block_bytes(io_dtype, a.K, false)));
+    const ChainArgs p{a, blocks, h0, o, h_final, ck, parts, (a.n + segments - 1) / segments, segments, 0};
     if (io_dtype == SSM_BF16) return a.K <= 64 ? chain<io_bf16, 64>(p, stream) : chain<io_bf16, 128>(p, stream);
     return a.K <= 64 ? chain<io_f32, 64>(p, stream) : chain<io_f32, 128>(p, stream);
 }
@@ -626,7 +763,7 @@ delta::Call call_of(const A &a) {
 
 size_t gated_delta_workspace_bytes(const ssm_gated_delta_args_t &a) {
     const int64_t n = (a.seqlen + delta::kC - 1) / delta::kC;
-    return (size_t)(a.batch * a.heads * n) * delta::block_bytes(a.io_dtype, a.kdim, false);
+    return delta::chain_bytes(a.io_dtype, a.batch * a.heads, n, a.kdim, a.vdim);
 }
 
 hipError_t launch_gated_delta_fwd(const ssm_gated_delta_args_t &a, hipStream_t stream) {

@@ -601,8 +601,6 @@ hipError_t backward(const BackArgs &p, const GradArgs &g, hipStream_t stream) {
     return back_chain<IO, KP, 1>(p, g, stream);
 }
 
-size_t up256(size_t n) { return (n + 255) / 256 * 256; }
-
 struct BackPlan {
     size_t blocks, after, dx, edu, ck, total;
 };
@@ -611,7 +609,9 @@ BackPlan back_plan(const ssm_gated_delta_bwd_args_t &a) {
     const size_t n = (size_t)((a.seqlen + kC - 1) / kC), chunks = n * a.batch * a.heads;
     BackPlan p;
     p.blocks = 0;
-    p.after = up256(chunks * std::max(block_bytes(a.io_dtype, a.kdim, false), block_bytes(a.io_dtype, a.kdim, true)));
+    p.after = up256(chunks * block_bytes(a.io_dtype, a.kdim, true));
+    if (!a.checkpoints)
+        p.after = std::max(p.after, chain_bytes(a.io_dtype, a.batch * a.heads, (int64_t)n, a.kdim, a.vdim));
     p.dx = p.after + up256(chunks * a.kdim * a.vdim * 4);
     p.edu = p.dx + up256(chunks * kC * a.vdim * 4);
     p.ck = p.edu + up256(chunks * ((a.vdim + 15) / 16) * kC * 4);

@@ -49,7 +49,8 @@ def _same(got, want, what):
 def test_stores_of_the_chain_stay_inside(dtype):
     """Every output and a workspace of exactly the size asked for lie in marked memory."""
     for B, L, Hk, H, K, V in [(1, 1, 1, 1, 8, 8), (2, 65, 1, 2, 72, 24), (1, 64, 2, 2, 64, 72), (1, 130, 2, 6, 128, 136),
-                               (32, 66, 2, 8, 72, 24), (16, 65, 8, 8, 128, 40)]:
+                               (32, 66, 2, 8, 72, 24), (16, 65, 8, 8, 128, 40),
+                               (1, 2050, 1, 2, 72, 40)]:
         what = "%dx%d %d/%d heads %dx%d" % (B, L, Hk, H, K, V)
         print(what, flush=True)
         k = delta_case(B, L, Hk, H, K, V, dtype, seed=L, doc=20)
@@ -234,17 +235,23 @@ def test_growing_decays():
     close(hf, rs, 20 * bound(k), "h_final")
 
 
-def test_long_sequences_carry_their_state():
-    """Two halves with the state handed over give what one call does, to the rounding of the state's own
-    order: the halves meet at a chunk's border, so to the bit."""
-    k = delta_case(1, 64 * 40, 2, 2, 64, 64, BF, seed=9)
+@pytest.mark.parametrize("chunks,cut", [(31, 13), (80, 35)])
+def test_long_sequences_carry_their_state(chunks, cut):
+    """Two halves with the state handed over give what one call does: the halves meet at a chunk's border, so
+    to the bit where no call is split into segments (31 chunks).  A long call and its halves are split in other
+    places; each is then within the bound of the definition, and within two of one another, and both were
+    rounded."""
+    L, cut = 64 * chunks, 64 * cut
+    k = delta_case(1, L, 2, 2, 64, 64, BF, seed=9)
     o, hf = ssm.gated_delta_fwd(return_final_state=True, **k)
-    cut = 64 * 17
     part = lambda a, b: {n: t[:, a:b].contiguous() for n, t in k.items()  # noqa: E731
                          if isinstance(t, torch.Tensor) and n != "h0"}
     o1, h1 = ssm.gated_delta_fwd(return_final_state=True, l2norm=True, h0=k["h0"], **part(0, cut))
-    o2, h2 = ssm.gated_delta_fwd(return_final_state=True, l2norm=True, h0=h1, **part(cut, 64 * 40))
-    assert torch.equal(torch.cat([o1, o2], 1), o) and torch.equal(h2, hf)
+    o2, h2 = ssm.gated_delta_fwd(return_final_state=True, l2norm=True, h0=h1, **part(cut, L))
+    if chunks == 31:
+        assert torch.equal(torch.cat([o1, o2], 1), o) and torch.equal(h2, hf)
+    close(torch.cat([o1, o2], 1), f64(o), 2 * bound(k), "o", roundings=2)
+    close(h2, f64(hf), 2 * bound(k), "h_final")
 
 
 def test_offsets_past_32_bits():

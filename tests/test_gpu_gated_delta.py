@@ -63,6 +63,37 @@ def test_slices_of_32_channels(shape, dtype):
 
 
 @pytest.mark.parametrize("dtype", **IDS)
+@pytest.mark.parametrize("shape", [(1, 2048, 1, 1, 128, 128), (1, 2100, 2, 2, 72, 24), (2, 2090, 1, 3, 40, 136),
+                                   (1, 4100, 1, 2, 8, 8), (1, 2049, 4, 4, 128, 264)], ids=lambda s: "x".join(map(str, s)))
+def test_segments(shape, dtype):
+    """Sequences of 32 to 65 chunks and few heads, which are run in segments; memories of more steps than a
+    segment, resets in all, some and none of the segments."""
+    for i, (l2norm, doc, h0, beta, ck) in enumerate([(True, 0, True, 2.0, True), (True, 600, True, 1.0, False),
+                                                     (False, 40, False, 1.0, True)]):
+        k = delta_case(*shape, dtype, seed=i, l2norm=l2norm, doc=doc, h0=h0, beta=beta)
+        k["g"] = k["g"] * 0.02
+        _check(k, "%s l2norm=%d doc=%d h0=%d ck=%d" % (shape, l2norm, doc, h0, ck), checkpoints=ck)
+
+
+@pytest.mark.parametrize("dtype", **IDS)
+def test_segments_of_states_that_are_dropped(dtype):
+    """A state of infinities and NaNs, dropped in the first, a middle or the last segment, stays out of what
+    follows; what comes before holds them, as the definition's does."""
+    L = 64 * 39 + 20
+    for at in (0, 70, 64 * 13 + 5, 64 * 38 + 1):
+        k = delta_case(1, L, 1, 2, 64, 48, dtype, seed=at)
+        k["reset"] = torch.zeros(1, L, dtype=torch.uint8, device=DEV)
+        k["reset"][:, at] = 1
+        zero = dict(k, h0=torch.zeros_like(k["h0"]))
+        bad = dict(k, h0=k["h0"].clone())
+        bad["h0"][:, :, ::3] = float("inf")
+        bad["h0"][:, :, 1::3] = float("nan")
+        o, hf = ssm.gated_delta_fwd(return_final_state=True, **bad)
+        ro, rs = ssm.gated_delta_fwd(return_final_state=True, **zero)
+        assert torch.equal(o[:, at:], ro[:, at:]) and torch.equal(hf, rs)
+
+
+@pytest.mark.parametrize("dtype", **IDS)
 @pytest.mark.parametrize("shape", [(1, 1, 1, 8, 8), (3, 2, 4, 128, 128), (5, 1, 3, 72, 40), (2, 4, 4, 64, 136),
                                    (130, 2, 2, 24, 32)], ids=lambda s: "x".join(map(str, s)))
 def test_step(shape, dtype):
