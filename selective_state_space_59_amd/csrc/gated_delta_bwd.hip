@@ -3,7 +3,7 @@
 // entering a chunk, dS the gradient of the state leaving it:
 //   dU = P^T dO + leave K dS,  dX = N^T diag(beta) dU = dV
 //   gradient of S:  through dS + (scale enter Q)^T dO - (enter K)^T dX
-// which back_chain_kernel carries from the last chunk to the first, each wave 16 value channels as in the
+// which back_chain_kernel carries from the last chunk to the first, a workgroup 16 or 32 value channels as in the
 // forward.  Then, for all chunks at once (grads_kernel), with dP = dO U^T (s <= t), Y = dX E^T (s < t) and
 // dB = -Y diag(beta):
 //   dq = scale enter dO S^T + scale (dP D) K
@@ -41,7 +41,8 @@ struct BackLds {
 };
 
 // The forward's chain (chain_kernel) backwards: wave w has the steps 16 w .. + 15 and the rows KP/4 w .. of
-// the state's gradient.
+// the state's gradient.  8 x 2048 steps of 12 heads of 128, bf16: 261 us, bound as the forward's by the chain of
+// a chunk's products; it writes 302 MB.
 template <typename IO, int KP, int NC>
 __global__ __launch_bounds__(kThreads, 2) void back_chain_kernel(BackArgs p) {
     using O = Op<IO>;
@@ -290,7 +291,9 @@ __device__ __forceinline__ void lower_tile(int i, int &ti, int &tj) {
 }
 
 // One chunk of one key head, over the value heads that share it.  Wave w has the result columns
-// 16 (w % KT) .. + 15 of the products with K channels and, with KP = 64, half of their rows.
+// 16 (w % KT) .. + 15 of the products with K channels and, with KP = 64, half of their rows.  8 x 2048 steps of
+// 12 heads of 128, bf16: 361 us for 0.7 GB, bound by latency: half of the waves' cycles wait, mostly for the
+// value slices' way through LDS (27000 of a chunk's 75000 cycles), at one workgroup a CU (142 KB of LDS).
 template <typename IO, int KP>
 __global__ __launch_bounds__(kGradThreads) void grads_kernel(GradArgs p) {
     using O = Op<IO>;

@@ -268,7 +268,11 @@ template <typename OUT>
 void launch(const ssm_matmul_fp8_args_t &a, hipStream_t stream) {
     const int blocks = (int)((a.k + 127) / 128);
     const bool wide = a.n % 4 == 0 && reinterpret_cast<uintptr_t>(a.y) % (4 * OUT::bytes) == 0;
-    if (a.m <= 64) {
+    // Few rows, where tiles of 64 would be too few as well.  Skinny and tiles, bf16 y (fp32: up to a fifth more on
+    // either side): 10240 x 2560 with 1 row 7.1 us (3.7 TB/s of w) and 12.8, 16 rows 10.3 and 12.9, 32 rows 14.8
+    // and 13.0, 64 rows 23.1 and 13.4; 2560 x 5120 with 1 row 8.4 and 22.1, 32 rows 11.5 and 22.5, 64 rows 18.4
+    // and 23.0.
+    if (a.m <= 16 || (a.m <= 64 && a.n < 8192)) {
         const unsigned grid = (unsigned)((a.n + 15) / 16), threads = 64 * kSkinnyWaves;
         if (a.m <= 16) skinny_kernel<OUT, 1><<<grid, threads, 0, stream>>>(a, blocks, wide);
         else if (a.m <= 32) skinny_kernel<OUT, 2><<<grid, threads, 0, stream>>>(a, blocks, wide);
@@ -276,9 +280,9 @@ void launch(const ssm_matmul_fp8_args_t &a, hipStream_t stream) {
         return;
     }
     const auto tiles = [&](int64_t bm, int64_t bn) { return ((a.m + bm - 1) / bm) * ((a.n + bn - 1) / bn); };
-    // The largest tile that still gives every CU a workgroup.  16384 x 10240 x 2560 in bf16: tiles of 256 490 us,
-    // of 128 624; fp32 results, whose widened operands would not fit the registers beside 256 x 256 of sums,
-    // stay with 128.
+    // The largest tile that still gives every CU a workgroup.  16384 x 10240 x 2560 in bf16: tiles of 256 490 us
+    // (1750 TFLOP/s), of 128 624; 256 x 10240 x 2560: of 64 17 us, of 128 22; fp32 results, whose widened operands
+    // would not fit the registers beside 256 x 256 of sums, stay with 128.
     if (OUT::bytes == 2 && tiles(256, 256) >= 256) {
         if constexpr (OUT::bytes == 2)
             tile_kernel<OUT, 256, 256, 64, 128><<<(unsigned)tiles(256, 256), 512, 0, stream>>>(

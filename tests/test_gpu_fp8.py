@@ -108,7 +108,7 @@ def _operands(M, N_, K, seed):
 # the skinny kernel's and the three tiles' ranges, edges that are no multiple of anything, K within a block
 MATS = [(1, 16, 16), (1, 1, 128), (2, 130, 272), (16, 300, 512), (17, 129, 2560), (33, 100, 144), (64, 257, 400),
         (65, 64, 64), (65, 1000, 1040), (200, 333, 256), (1237, 1331, 2000), (1100, 4100, 128), (4096, 1027, 272),
-        (4200, 4000, 400), (4097, 4097, 160)]
+        (4200, 4000, 400), (4097, 4097, 160), (17, 8200, 144), (64, 8192, 272)]
 
 
 @pytest.mark.parametrize("dtype", **IDS)
