@@ -192,15 +192,14 @@ __device__ __forceinline__ float decay(const Gates &s, int t, int u) {
     return u <= t && s.doc[t] == s.doc[u] ? expf((float)(s.G[t] - s.G[u])) : 0.0f;
 }
 
-// 64 rows of K channels (rows from t0 on of one head) between memory, registers and LDS, 16 bytes a
-// piece: lane = row.  Loads have no condition (a
-// conditional one is waited for where its branch ends, and the next chunk's are to stay in flight).
+// 64 rows of K channels (rows from t0 on of one head) between memory, registers and LDS, 16 bytes a piece:
+// lane = row.  Loads have no condition (a conditional one is waited for where its branch ends, and the next
+// chunk's are to stay in flight).
 template <typename IO, int KP>
 struct HeadRows {
     using E = typename Op<IO>::elem;
     static constexpr int PER = 16 / IO::bytes;           // elements of a piece
     static constexpr int STRIDE = KP + PER;               // LDS row, in elements
-    static constexpr int TSTRIDE = kC + PER;              // row of the transposed copy
     template <int WAVES>
     struct Regs {
         u4 r[KP / PER / WAVES];

@@ -215,7 +215,9 @@ struct ChainArgs {
     float *h_final, *ck;
     float *parts;  // (heads, segments - 1): Z, K x V floats, and T transposed, K x K
     int64_t per;   // chunks of a segment
-    int segments, slices;
+    int segments;
+    bool wide;  // 32 value channels a workgroup in segments
+    int slices;
 };
 
 // Four waves carry 16 NC value channels of one head along the chunks.  Wave w has the steps 16 w .. + 15 of
@@ -230,7 +232,8 @@ struct ChainArgs {
 // A long sequence of few heads runs in segments.  The state that leaves a segment is T S + Z for the state S
 // entering it; first (FIRST) all segments but the last form, without outputs, their Z (from a state of zeros,
 // the first one's from h0) and, as K more columns without values, their T (from the identity); join_kernel
-// turns these into the states entering the segments, and the chains run again from there.
+// turns these into the states entering the segments, and the chains run again from there.  32768 steps of 12
+// heads of 128, bf16, ten segments: 369 us, 31 and 298; in one piece 1272.
 template <typename IO, int KP, int NC, bool FIRST>
 __global__ __launch_bounds__(kThreads, 2) void chain_kernel(ChainArgs p) {
     using O = Op<IO>;
@@ -464,7 +467,7 @@ __global__ __launch_bounds__(kThreads, 2) void chain_kernel(ChainArgs p) {
 // through LDS.  A segment's T is loaded while the one before it is worked on.  What T does not take up, or S
 // does not hold, has no part in T S (T is 0 behind a reset, and S may hold infinities or NaNs): sums that come
 // out as NaN are formed again without the terms that have a zero.  (Rows of T behind K repeat others, where S
-// is put as 0.)
+// is put as 0.)  About 1 us a segment for a few heads: T, 64 KB, comes from memory once a workgroup.
 constexpr int kJoinV = 4;
 
 __global__ __launch_bounds__(kThreads, 2) void join_kernel(ChainArgs p) {
@@ -663,12 +666,13 @@ hipError_t chain_pass(ChainArgs p, hipStream_t stream) {
 template <typename IO, int KP>
 hipError_t chain(const ChainArgs &p, hipStream_t stream) {
     if (p.segments > 1) {
-        hipError_t e = chain_pass<IO, KP, 1, true>(p, stream);
+        hipError_t e = p.wide ? chain_pass<IO, KP, 2, true>(p, stream) : chain_pass<IO, KP, 1, true>(p, stream);
         if (e != hipSuccess) return e;
         if (p.segments > 2)
             join_kernel<<<(unsigned)(p.a.B * p.a.H * (p.a.V / kJoinV)), kThreads, 0, stream>>>(p);
         e = hipGetLastError();
-        return e != hipSuccess ? e : chain_pass<IO, KP, 1, false>(p, stream);
+        if (e != hipSuccess) return e;
+        return p.wide ? chain_pass<IO, KP, 2, false>(p, stream) : chain_pass<IO, KP, 1, false>(p, stream);
     }
     // 32 channels a workgroup where every CU gets one all the same (8 x 2048 x 12 heads: 197 us, 230 with 16;
     // where checkpoints are written as well 259 and 312)
@@ -701,34 +705,46 @@ hipError_t launch_prepare(const Call &a, int io_dtype, bool backward, char *bloc
                      : prepare<io_f32, 128>(a, backward, blocks, stream);
 }
 
+struct Segments {
+    int count;
+    bool wide;
+};
+
 // Segments of a sequence of n chunks: as many as run at once, two workgroups a CU with outputs and three
-// without; of at least eight chunks, as each costs a step of join_kernel and its state once more.  bf16, K = V =
-// 128, whole calls, in segments and in one piece: 32768 steps of 12 heads 992 us in 5 segments and 1407, of 4
-// heads 340 in 13 and 1165, of one head 152 in 32 and 1026; 4096 steps of 4 heads 80 in 8 and 164; 2048 steps of
-// 12 heads 100 in 4 and 98; 1024 steps of 12 heads 73 in 3 and 60, and two segments of them 59.
-static int segments_of(int64_t heads, int64_t n, int64_t K, int64_t V) {
-    const int64_t values = heads * ((V + 15) / 16), matrices = heads * ((K + 15) / 16);
-    const auto fits = [&](int64_t s) {
-        return s <= n / 8 && s * s <= 2 * n && values * s <= 512 && values * (s - 1) + matrices * (s - 2) <= 768;
+// without; of at least eight chunks, as each costs a step of join_kernel and its state once more.  Where that is
+// fewer than eight segments, workgroups take 32 channels, which leaves room for more.  bf16, K = V = 128, whole
+// calls, in segments and in one piece: 32768 steps of one head 152 us (32 segments) and 1026, of 4 heads 334
+// (13) and 1170, of 12 heads 836 (10 of 32 channels; 986 in 5 of 16) and 1408; 16384 steps of 8 heads 272 and
+// 615 (311 in 7 of 16), of 20 heads 644 (852) and 795; 4096 steps of 4 heads 80 and 164, of 16 heads 164 and
+// 179; 2048 steps of 12 heads 98 and 99; 1024 steps of 12 heads 73 in 3 and 60, and two segments of them 59;
+// 4096 steps of 24 heads 226 in 5 and 191.
+static Segments segments_of(int64_t heads, int64_t n, int64_t K, int64_t V) {
+    const auto long_enough = [&](int64_t s) { return s <= n / 8 && s * s <= 2 * n; };
+    const auto fits = [&](int64_t s, int width) {
+        const int64_t values = heads * ((V + width - 1) / width), matrices = heads * ((K + width - 1) / width);
+        return long_enough(s) && values * s <= 512 && values * (s - 1) + matrices * (s - 2) <= 48 * width;
     };
+    if (n < 32 || !fits(3, 16)) return {1, false};
     int64_t s = 3;
-    if (!fits(s) || n < 32) return 1;
-    while (fits(s + 1)) ++s;
+    while (fits(s + 1, 16)) ++s;
+    const bool wide = s < 8 && long_enough(s + 1);
+    if (wide)
+        while (fits(s + 1, 32)) ++s;
     const int64_t per = (n + s - 1) / s;
-    return (int)((n + per - 1) / per);
+    return {(int)((n + per - 1) / per), wide};
 }
 
 size_t chain_bytes(int io_dtype, int64_t heads, int64_t n, int64_t K, int64_t V) {
     return up256((size_t)(heads * n) * block_bytes(io_dtype, K, false)) +
-           up256((size_t)(heads * (segments_of(heads, n, K, V) - 1) * K * (V + K)) * sizeof(float));
+           up256((size_t)(heads * (segments_of(heads, n, K, V).count - 1) * K * (V + K)) * sizeof(float));
 }
 
 hipError_t launch_chain(const Call &a, int io_dtype, char *blocks, const float *h0, void *o, float *h_final, float *ck,
                         hipStream_t stream) {
     const int64_t heads = a.B * a.H;
-    const int segments = segments_of(heads, a.n, a.K, a.V);
+    const Segments split = segments_of(heads, a.n, a.K, a.V);
     float *parts = reinterpret_cast<float *>(blocks + up256((size_t)(heads * a.n) * block_bytes(io_dtype, a.K, false)));
-    const ChainArgs p{a, blocks, h0, o, h_final, ck, parts, (a.n + segments - 1) / segments, segments, 0};
+    const ChainArgs p{a, blocks, h0, o, h_final, ck, parts, (a.n + split.count - 1) / split.count, split.count, split.wide, 0};
     if (io_dtype == SSM_BF16) return a.K <= 64 ? chain<io_bf16, 64>(p, stream) : chain<io_bf16, 128>(p, stream);
     return a.K <= 64 ? chain<io_f32, 64>(p, stream) : chain<io_f32, 128>(p, stream);
 }

@@ -64,10 +64,11 @@ def test_slices_of_32_channels(shape, dtype):
 
 @pytest.mark.parametrize("dtype", **IDS)
 @pytest.mark.parametrize("shape", [(1, 2048, 1, 1, 128, 128), (1, 2100, 2, 2, 72, 24), (2, 2090, 1, 3, 40, 136),
-                                   (1, 4100, 1, 2, 8, 8), (1, 2049, 4, 4, 128, 264)], ids=lambda s: "x".join(map(str, s)))
+                                   (1, 4100, 1, 2, 8, 8), (1, 2049, 4, 4, 128, 264),
+                                   (1, 3100, 2, 16, 72, 104), (1, 3100, 1, 5, 16, 344)], ids=lambda s: "x".join(map(str, s)))
 def test_segments(shape, dtype):
-    """Sequences of 32 to 65 chunks and few heads, which are run in segments; memories of more steps than a
-    segment, resets in all, some and none of the segments."""
+    """Sequences of 32 to 65 chunks and few heads, which are run in segments, in slices of 16 and (the last two)
+    of 32 value channels; memories of more steps than a segment, resets in all, some and none of the segments."""
     for i, (l2norm, doc, h0, beta, ck) in enumerate([(True, 0, True, 2.0, True), (True, 600, True, 1.0, False),
                                                      (False, 40, False, 1.0, True)]):
         k = delta_case(*shape, dtype, seed=i, l2norm=l2norm, doc=doc, h0=h0, beta=beta)
