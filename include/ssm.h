@@ -760,7 +760,9 @@ ssm_status_t ssm_gated_rmsnorm_bwd(const ssm_gated_norm_bwd_args_t *args, void *
  * Arithmetic is fp32: bf16 tensors run on the bf16 matrix cores, with what was
  * computed carried through the products as the sum of three bf16 numbers (two,
  * 16 bits, where only a bf16 output follows); outputs are rounded once.  Results
- * do not change from run to run.  kdim: a multiple of 8 up to SSM_DELTA_MAX_KDIM;
+ * do not change from run to run.  Long sequences of few heads run as parallel
+ * segments, in other places for another length: a sequence in two calls gives
+ * what one call does to rounding.  kdim: a multiple of 8 up to SSM_DELTA_MAX_KDIM;
  * vdim: a multiple of 8 up to SSM_DELTA_MAX_VDIM; kheads divides heads <= 65535;
  * batch <= 65535; seqlen < 2^30; heads * vdim and kheads * kdim < 2^24;
  * (batch * heads + 8) * ceil(vdim / 16) < 2^23.

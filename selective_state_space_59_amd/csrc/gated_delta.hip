@@ -675,7 +675,7 @@ hipError_t chain(const ChainArgs &p, hipStream_t stream) {
         return p.wide ? chain_pass<IO, KP, 2, false>(p, stream) : chain_pass<IO, KP, 1, false>(p, stream);
     }
     // 32 channels a workgroup where every CU gets one all the same (8 x 2048 x 12 heads: 197 us, 230 with 16;
-    // where checkpoints are written as well 259 and 312)
+    // where checkpoints are written as well 251 and 312)
     return wide_slices(p.a) ? chain_pass<IO, KP, 2, false>(p, stream) : chain_pass<IO, KP, 1, false>(p, stream);
 }
 

@@ -168,7 +168,12 @@ def _calls():
     ck = torch.empty(ssm.gated_delta_checkpoint_shape(2, 300, 4, 72, 40), device=DEV)
     x = torch.randn(300, 400, generator=torch.Generator().manual_seed(11)).to(DEV)
     w, ones = ssm.quantize_fp8(x[:130].contiguous(), 128), torch.ones(400, device=DEV)
-    return dict(forward=lambda: ssm.gated_delta_fwd(return_final_state=True, checkpoints=ck, **k),
+    long, wide = delta_case(1, 2100, 1, 2, 40, 24, BF, seed=12, doc=900), delta_case(1, 3100, 1, 5, 16, 344, BF, seed=13)
+    dlong = torch.randn(long["v"].shape, generator=torch.Generator().manual_seed(14)).to(BF).to(DEV)
+    return dict(segments=lambda: ssm.gated_delta_fwd(return_final_state=True, **long),
+                wide_segments=lambda: ssm.gated_delta_fwd(return_final_state=True, **wide),
+                segments_backward=lambda: ssm.gated_delta_bwd(do=dlong, **long),
+                forward=lambda: ssm.gated_delta_fwd(return_final_state=True, checkpoints=ck, **k),
                 backward=lambda: ssm.gated_delta_bwd(do=do, **k),
                 product=lambda: ssm.matmul_fp8(*ssm.quantize_fp8(x), *w),
                 norm=lambda: ssm.add_rmsnorm_fp8(x, ones, x))
@@ -178,7 +183,7 @@ def _equal(a, b):
     return torch.equal(a.view(torch.uint8), b.view(torch.uint8))
 
 
-@pytest.mark.parametrize("name", ["forward", "backward", "product", "norm"])
+@pytest.mark.parametrize("name", ["forward", "backward", "segments", "wide_segments", "segments_backward", "product", "norm"])
 def test_replays_match_eager(name):
     call = _calls()[name]
     want = [t.clone() for t in _flat(call())]
