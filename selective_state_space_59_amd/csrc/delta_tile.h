@@ -347,11 +347,11 @@ __device__ __forceinline__ const char *bytes(const T *p, int64_t elements, int64
     return reinterpret_cast<const char *>(p) + elements * size;
 }
 
-// A lane's value channels in a chain's workgroup: with two of them side by side, so that they are loaded and
-// stored together (V is even: both are there or neither).  Channels past the last repeat it.
+// A lane's first value channel in a chain's workgroup: two of them lie side by side, so that they are loaded and
+// stored together (V is even: both are there or neither).
 template <int NC>
-__device__ __forceinline__ int channel(int slice, int r16, int n) {
-    return NC * (16 * slice + r16) + n;
+__device__ __forceinline__ int channel(int slice, int r16) {
+    return NC * (16 * slice + r16);
 }
 typedef f2 f2_a4 __attribute__((aligned(4)));
 typedef uint32_t u1_a2 __attribute__((aligned(2)));
@@ -395,29 +395,26 @@ __device__ __forceinline__ void store_rows(char *to, uint32_t v_row, int K, int 
 template <typename IO, int NC>
 struct Elements {
     typedef typename IO::storage one;
-    struct Two {
-        one v[NC];
-    };
-    Two e;
+    one v[NC];
     static __device__ __forceinline__ Elements load(const void *row, uint32_t off) {
         Elements r;
         if constexpr (NC == 2 && IO::bytes == 2) {
             const uint32_t w = at<u1_a2>(row, off);
-            __builtin_memcpy(&r.e, &w, 4);
+            __builtin_memcpy(&r.v, &w, 4);
         } else if constexpr (NC == 2) {
             const f2 w = at<f2_a4>(row, off);
-            r.e.v[0] = w[0];
-            r.e.v[1] = w[1];
+            r.v[0] = w[0];
+            r.v[1] = w[1];
         } else {
-            r.e.v[0] = at<one>(row, off);
+            r.v[0] = at<one>(row, off);
         }
         return r;
     }
     __device__ __forceinline__ float get(int n) const {
         if constexpr (IO::bytes == 2)
-            return bf16_bits_to_f32(e.v[n]);
+            return bf16_bits_to_f32(v[n]);
         else
-            return e.v[n];
+            return v[n];
     }
 };
 

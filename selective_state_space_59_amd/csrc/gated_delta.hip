@@ -265,7 +265,7 @@ __global__ __launch_bounds__(kThreads, 2) void chain_kernel(ChainArgs p) {
     const int value_slices = (a.V + 16 * NC - 1) / (16 * NC);
     const bool matrix = FIRST && place.slice >= value_slices;  // columns of T
     if (matrix && segment == 0) return;
-    const int width = matrix ? a.K : a.V, vw = channel<NC>(place.slice - (matrix ? value_slices : 0), r16, 0);
+    const int width = matrix ? a.K : a.V, vw = channel<NC>(place.slice - (matrix ? value_slices : 0), r16);
     const uint32_t v0 = min(vw, width - NC);
     const bool live = vw < width;
     const auto part = [&](int i) { return p.parts + (head * (p.segments - 1) + i) * a.K * (int64_t)(a.V + a.K); };

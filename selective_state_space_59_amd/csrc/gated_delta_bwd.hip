@@ -68,7 +68,7 @@ __global__ __launch_bounds__(kThreads, 2) void back_chain_kernel(BackArgs p) {
     const uint32_t k_step = (uint32_t)a.k_token * IO::bytes, o_step = (uint32_t)(a.H * a.V) * IO::bytes;
     const uint32_t v_row = (uint32_t)a.V * 4;  // a state's row in bytes
     // lanes past the last channels repeat them, store nothing and count for nothing
-    const int vw = channel<NC>(place.slice, r16, 0);
+    const int vw = channel<NC>(place.slice, r16);
     const uint32_t v0 = min(vw, a.V - NC);
     const bool live = vw < a.V;
 
