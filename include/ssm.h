@@ -750,9 +750,13 @@ ssm_status_t ssm_gated_rmsnorm_bwd(const ssm_gated_norm_bwd_args_t *args, void *
  * uses q and k of head h / (heads / kheads).  With l2norm, q and k stand for
  * q / sqrt(sum q^2 + 1e-6) and k / sqrt(sum k^2 + 1e-6) over a head's channels.
  *
- * g is the log of the decay: usually <= 0, any finite value or -infinity; a step
- * with g < SSM_DELTA_FORGET (e^g is 0 in fp32) is a reset, with dg = 0.  The
- * state settles for beta |k|^2 in (0, 2); beyond, it grows as the formulas say.
+ * g is the log of the decay: usually <= 0, or above as long as e^g is finite in
+ * fp32; a step with g < SSM_DELTA_FORGET (e^g is 0 in fp32; -infinity is one) is
+ * a reset, with dg = 0.  The state settles for beta |k|^2 in (0, 2); beyond, it
+ * grows as the formulas say.  Decays that grow: a head in which those of some
+ * steps of a chunk multiply to more than e is computed one step after another
+ * (backwards: all heads of its key head), far slower, as the 64 steps of a chunk
+ * at once would lose what such a product exceeds the state by.
  * A reset drops the state whatever it held, an infinity or a NaN included; the
  * inputs themselves have to be finite, in a row's left padding too (the 64 steps
  * of a chunk are computed together).

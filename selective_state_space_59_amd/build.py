@@ -22,7 +22,7 @@ ARCH = "gfx950"
 
 SOURCES = ["ssm_api.cpp", "scan_fwd.hip", "scan_bwd.hip", "conv1d.hip", "state_update.hip", "block.hip",
            "ssd.hip", "scan_noalloc.hip", "gated_scan.hip", "gated_scan_bwd.hip", "add_norm.hip", "gated_norm.hip",
-           "colsum.hip", "gated_delta.hip", "gated_delta_bwd.hip", "quant_fp8.hip", "matmul_fp8.hip"]
+           "colsum.hip", "gated_delta.hip", "gated_delta_bwd.hip", "gated_delta_grow.hip", "quant_fp8.hip", "matmul_fp8.hip"]
 # hipBLASLt runs the plain GEMMs of the Mamba block.
 LIBS = ["-L/opt/rocm/lib", "-lhipblaslt", "-Wl,-rpath,/opt/rocm/lib"]
 

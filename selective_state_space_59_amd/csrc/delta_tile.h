@@ -21,6 +21,7 @@ constexpr int kC = 64;          // steps of a chunk (SSM_DELTA_CHUNK)
 constexpr int kThreads = 256;
 constexpr float kForget = -104.0f;  // e^g is 0 in fp32 from here on: such a step is a reset
 constexpr float kL2Eps = 1e-6f;
+constexpr float kGrowth = 1.0f;  // a chunk in which decays multiply to more than e^kGrowth is marked (gated_delta_grow.hip)
 
 typedef float f4 __attribute__((ext_vector_type(4)));
 typedef float f2 __attribute__((ext_vector_type(2)));
@@ -155,9 +156,10 @@ struct Gates {
     float beta[kC], enter[kC], leave[kC];
     float rq[kC], rk[kC];
     float through;
+    int grows;      // whether a product of decays in the chunk exceeds e^kGrowth
 };
 
-// Wave 0 fills G, doc, beta, enter, leave and through.  A barrier has to follow.
+// Wave 0 fills G, doc, beta, enter, leave, through and grows.  A barrier has to follow.
 template <typename IO>
 __device__ __forceinline__ void load_gates(const Call &a, int64_t b, int h, int64_t t0, Gates &s) {
     if (threadIdx.x >= 64) return;
@@ -184,7 +186,22 @@ __device__ __forceinline__ void load_gates(const Call &a, int64_t b, int h, int6
     s.beta[t] = in ? load_io<IO>(a.beta, at) : 0.0f;
     s.enter[t] = doc == 0 ? expf((float)G) : 0.0f;
     s.leave[t] = doc == last ? expf((float)(end - G)) : 0.0f;
-    if (t == 0) s.through = last == 0 ? expf((float)end) : 0.0f;
+    // the largest G_t - G_s of a document (its entering state stands at 0)
+    bool grows = false;
+    if (__any(g > 0.0f)) {
+        double low = doc == 0 ? fmin(G, 0.0) : G;
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) {
+            const double up = __shfl_up(low, d, 64);
+            const int ud = __shfl_up(doc, d, 64);
+            if (t >= d && ud == doc) low = fmin(low, up);
+        }
+        grows = __any(G - low > (double)kGrowth);
+    }
+    if (t == 0) {
+        s.through = last == 0 ? expf((float)end) : 0.0f;
+        s.grows = grows;
+    }
 }
 
 // D_ts = product of the decays behind step s up to t, 0 where t does not see s (s <= t).
@@ -418,14 +435,22 @@ struct Elements {
     }
 };
 
-// Enqueue the chunks' kernel (gated_delta.hip); `blocks`: block_bytes a chunk.
-hipError_t launch_prepare(const Call &a, int io_dtype, bool backward, char *blocks, hipStream_t stream);
+// A call's workspace begins with a mark for each chunk of each head (marks_bytes), then the chunks' blocks
+// (block_bytes each).
+inline size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+inline size_t marks_bytes(int64_t chunks) { return up256((size_t)chunks * sizeof(uint32_t)); }
+// Enqueue the chunks' kernel (gated_delta.hip).
+hipError_t launch_prepare(const Call &a, int io_dtype, bool backward, char *workspace, hipStream_t stream);
 size_t block_bytes(int io_dtype, int64_t kdim, bool backward);
-// The forward chain; o, h_final and ck may be NULL.  `blocks`: chain_bytes, the chunks' blocks first.
-hipError_t launch_chain(const Call &a, int io_dtype, char *blocks, const float *h0, void *o, float *h_final, float *ck,
+// The forward chain, and the heads that grow; o, h_final and ck may be NULL.  `workspace`: chain_bytes.
+hipError_t launch_chain(const Call &a, int io_dtype, char *workspace, const float *h0, void *o, float *h_final, float *ck,
                         hipStream_t stream);
 size_t chain_bytes(int io_dtype, int64_t heads, int64_t n, int64_t kdim, int64_t vdim);
-inline size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+// Heads with a marked chunk again, step by step (gated_delta_grow.hip); key heads of one backwards.
+hipError_t launch_grow(const Call &a, int io_dtype, const uint32_t *marks, const float *h0, void *o, float *h_final,
+                       float *ck, hipStream_t stream);
+hipError_t launch_grow_back(const Call &c, const ssm_gated_delta_bwd_args_t &a, const uint32_t *marks, const float *ck,
+                            char *blocks, float *dbeta_sum, hipStream_t stream);
 // The backward of a call (gated_delta_bwd.hip).
 hipError_t launch_backward(const Call &c, const ssm_gated_delta_bwd_args_t &a, hipStream_t stream);
 size_t backward_bytes(const ssm_gated_delta_bwd_args_t &a);

@@ -9,6 +9,7 @@
 //   S <- through S + (leave K)^T diag(beta) E
 // prepare_kernel forms the inverse of I + B diag(beta) and P for every chunk at once; chain_kernel
 // then carries the states from chunk to chunk, each workgroup 16 or 32 value channels apart from the others.
+// Heads whose decays grow are done again step by step (gated_delta_grow.hip).
 #include "delta_tile.h"
 
 #include <algorithm>
@@ -52,7 +53,7 @@ __device__ __forceinline__ void row_norms(const typename Op<IO>::elem *rows, boo
 // powers of B would not, so equal keys in a row cost no digits.  8 x 2048 steps of 12 heads of 128, bf16: 73 us,
 // bound by the substitution's latency (a third of a chunk's 20000 cycles) at three workgroups a CU.
 template <typename IO, int KP, bool BWD>
-__global__ __launch_bounds__(kThreads) void prepare_kernel(Call a, char *blocks) {
+__global__ __launch_bounds__(kThreads) void prepare_kernel(Call a, char *blocks, uint32_t *marks) {
     using O = Op<IO>;
     using E = typename O::elem;
     using Rows = HeadRows<IO, KP>;
@@ -78,6 +79,7 @@ __global__ __launch_bounds__(kThreads) void prepare_kernel(Call a, char *blocks)
     __syncthreads();
 
     char *block = blocks + ((b * a.H + h) * a.n + c) * Block::kBytes;
+    if (threadIdx.x == 0) marks[(b * a.H + h) * a.n + c] = s.gates.grows;
     float *vec = reinterpret_cast<float *>(block);
     E *inv = reinterpret_cast<E *>(block + Block::kInv), *att = reinterpret_cast<E *>(block + Block::kAtt);
     if constexpr (BWD) {
@@ -646,12 +648,14 @@ __global__ __launch_bounds__(kThreads) void step_kernel(StepArgs p) {
 }
 
 template <typename IO, int KP>
-hipError_t prepare(const Call &a, bool backward, char *blocks, hipStream_t stream) {
+hipError_t prepare(const Call &a, bool backward, char *workspace, hipStream_t stream) {
     const dim3 grid((unsigned)a.n, (unsigned)a.H, (unsigned)a.B);
+    uint32_t *marks = reinterpret_cast<uint32_t *>(workspace);
+    char *blocks = workspace + marks_bytes(a.B * a.H * a.n);
     if (backward)
-        prepare_kernel<IO, KP, true><<<grid, kThreads, 0, stream>>>(a, blocks);
+        prepare_kernel<IO, KP, true><<<grid, kThreads, 0, stream>>>(a, blocks, marks);
     else
-        prepare_kernel<IO, KP, false><<<grid, kThreads, 0, stream>>>(a, blocks);
+        prepare_kernel<IO, KP, false><<<grid, kThreads, 0, stream>>>(a, blocks, marks);
     return hipGetLastError();
 }
 
@@ -697,12 +701,12 @@ size_t block_bytes(int io_dtype, int64_t kdim, bool backward) {
     return io_dtype == SSM_BF16 ? of(io_bf16{}) : of(io_f32{});
 }
 
-hipError_t launch_prepare(const Call &a, int io_dtype, bool backward, char *blocks, hipStream_t stream) {
+hipError_t launch_prepare(const Call &a, int io_dtype, bool backward, char *workspace, hipStream_t stream) {
     if (io_dtype == SSM_BF16)
-        return a.K <= 64 ? prepare<io_bf16, 64>(a, backward, blocks, stream)
-                         : prepare<io_bf16, 128>(a, backward, blocks, stream);
-    return a.K <= 64 ? prepare<io_f32, 64>(a, backward, blocks, stream)
-                     : prepare<io_f32, 128>(a, backward, blocks, stream);
+        return a.K <= 64 ? prepare<io_bf16, 64>(a, backward, workspace, stream)
+                         : prepare<io_bf16, 128>(a, backward, workspace, stream);
+    return a.K <= 64 ? prepare<io_f32, 64>(a, backward, workspace, stream)
+                     : prepare<io_f32, 128>(a, backward, workspace, stream);
 }
 
 struct Segments {
@@ -735,18 +739,25 @@ static Segments segments_of(int64_t heads, int64_t n, int64_t K, int64_t V) {
 }
 
 size_t chain_bytes(int io_dtype, int64_t heads, int64_t n, int64_t K, int64_t V) {
-    return up256((size_t)(heads * n) * block_bytes(io_dtype, K, false)) +
+    return marks_bytes(heads * n) + up256((size_t)(heads * n) * block_bytes(io_dtype, K, false)) +
            up256((size_t)(heads * (segments_of(heads, n, K, V).count - 1) * K * (V + K)) * sizeof(float));
 }
 
-hipError_t launch_chain(const Call &a, int io_dtype, char *blocks, const float *h0, void *o, float *h_final, float *ck,
+hipError_t launch_chain(const Call &a, int io_dtype, char *workspace, const float *h0, void *o, float *h_final, float *ck,
                         hipStream_t stream) {
     const int64_t heads = a.B * a.H;
     const Segments split = segments_of(heads, a.n, a.K, a.V);
-    float *parts = reinterpret_cast<float *>(blocks + up256((size_t)(heads * a.n) * block_bytes(io_dtype, a.K, false)));
+    const char *blocks = workspace + marks_bytes(heads * a.n);
+    float *parts = reinterpret_cast<float *>(workspace + marks_bytes(heads * a.n) +
+                                             up256((size_t)(heads * a.n) * block_bytes(io_dtype, a.K, false)));
     const ChainArgs p{a, blocks, h0, o, h_final, ck, parts, (a.n + split.count - 1) / split.count, split.count, split.wide, 0};
-    if (io_dtype == SSM_BF16) return a.K <= 64 ? chain<io_bf16, 64>(p, stream) : chain<io_bf16, 128>(p, stream);
-    return a.K <= 64 ? chain<io_f32, 64>(p, stream) : chain<io_f32, 128>(p, stream);
+    hipError_t e;
+    if (io_dtype == SSM_BF16)
+        e = a.K <= 64 ? chain<io_bf16, 64>(p, stream) : chain<io_bf16, 128>(p, stream);
+    else
+        e = a.K <= 64 ? chain<io_f32, 64>(p, stream) : chain<io_f32, 128>(p, stream);
+    if (e != hipSuccess) return e;
+    return launch_grow(a, io_dtype, reinterpret_cast<const uint32_t *>(workspace), h0, o, h_final, ck, stream);
 }
 
 }  // namespace delta
@@ -789,10 +800,10 @@ size_t gated_delta_workspace_bytes(const ssm_gated_delta_args_t &a) {
 
 hipError_t launch_gated_delta_fwd(const ssm_gated_delta_args_t &a, hipStream_t stream) {
     const delta::Call c = call_of(a);
-    char *blocks = static_cast<char *>(a.workspace);
-    const hipError_t e = delta::launch_prepare(c, a.io_dtype, false, blocks, stream);
+    char *workspace = static_cast<char *>(a.workspace);
+    const hipError_t e = delta::launch_prepare(c, a.io_dtype, false, workspace, stream);
     if (e != hipSuccess) return e;
-    return delta::launch_chain(c, a.io_dtype, blocks, a.h0, a.o, a.h_final, a.checkpoints, stream);
+    return delta::launch_chain(c, a.io_dtype, workspace, a.h0, a.o, a.h_final, a.checkpoints, stream);
 }
 
 size_t gated_delta_bwd_workspace_bytes(const ssm_gated_delta_bwd_args_t &a) { return delta::backward_bytes(a); }

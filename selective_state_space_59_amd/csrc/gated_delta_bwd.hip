@@ -611,8 +611,8 @@ struct BackPlan {
 BackPlan back_plan(const ssm_gated_delta_bwd_args_t &a) {
     const size_t n = (size_t)((a.seqlen + kC - 1) / kC), chunks = n * a.batch * a.heads;
     BackPlan p;
-    p.blocks = 0;
-    p.after = up256(chunks * block_bytes(a.io_dtype, a.kdim, true));
+    p.blocks = marks_bytes((int64_t)chunks);
+    p.after = p.blocks + up256(chunks * block_bytes(a.io_dtype, a.kdim, true));
     if (!a.checkpoints)
         p.after = std::max(p.after, chain_bytes(a.io_dtype, a.batch * a.heads, (int64_t)n, a.kdim, a.vdim));
     p.dx = p.after + up256(chunks * a.kdim * a.vdim * 4);
@@ -640,11 +640,15 @@ hipError_t launch_backward(const Call &c, const ssm_gated_delta_bwd_args_t &a, h
     if (e != hipSuccess) return e;
     float *after = reinterpret_cast<float *>(ws + plan.after), *dx = reinterpret_cast<float *>(ws + plan.dx);
     float *edu = reinterpret_cast<float *>(ws + plan.edu);
-    const BackArgs p{c, ws, ck, a.dh_final, a.dout, a.dv, a.dh0, after, dx, edu, 0};
-    const GradArgs g{c, ws, ck, after, dx, edu, a.dout, a.dq, a.dk, a.dbeta, a.dg, 0};
+    char *blocks = ws + plan.blocks;
+    const BackArgs p{c, blocks, ck, a.dh_final, a.dout, a.dv, a.dh0, after, dx, edu, 0};
+    const GradArgs g{c, blocks, ck, after, dx, edu, a.dout, a.dq, a.dk, a.dbeta, a.dg, 0};
     if (a.io_dtype == SSM_BF16)
-        return a.kdim <= 64 ? backward<io_bf16, 64>(p, g, stream) : backward<io_bf16, 128>(p, g, stream);
-    return a.kdim <= 64 ? backward<io_f32, 64>(p, g, stream) : backward<io_f32, 128>(p, g, stream);
+        e = a.kdim <= 64 ? backward<io_bf16, 64>(p, g, stream) : backward<io_bf16, 128>(p, g, stream);
+    else
+        e = a.kdim <= 64 ? backward<io_f32, 64>(p, g, stream) : backward<io_f32, 128>(p, g, stream);
+    if (e != hipSuccess) return e;
+    return launch_grow_back(c, a, reinterpret_cast<const uint32_t *>(ws), ck, blocks, edu, stream);
 }
 
 size_t backward_bytes(const ssm_gated_delta_bwd_args_t &a) { return back_plan(a).total; }
