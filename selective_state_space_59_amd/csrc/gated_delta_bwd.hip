@@ -10,7 +10,7 @@
 //   dk = leave U dS^T - enter dX S^T + scale (dP D)^T Q + (dB D) K + (dB D)^T K
 //   dbeta_s = E_s . dU_s - sum_t B_ts Y_ts
 //   dG_t = sum_s Z_ts - sum_s Z_st + q.(scale enter dO S^T) - k.(enter dX S^T) - k.(leave U dS^T),
-//   Z = dP P + dB B;   dG_end += sum_t k.(leave U dS^T) + through <dS, S>;   dg = suffix sums of dG
+//   Z = dP P + dB B;   dG_end += sum_t k.(leave U dS^T) + through <dS, S>;   dg = suffix sums of dG within a document
 // dbeta never divides by beta: E is kept in place of U.
 #include "delta_tile.h"
 #include "wide_io.h"
@@ -500,12 +500,14 @@ __global__ __launch_bounds__(kGradThreads) void grads_kernel(GradArgs p) {
                 for (int i = 0; i < kGradThreads / 64; ++i) through += s.dots[i];
                 dG += leaves + (s.gates.through != 0.0f ? s.gates.through * through : 0.0);
             }
+            // (over a document's steps: those behind a reset add up to 0, but for their rounding)
+            const int doc = s.gates.doc[t];
             for (int d = 1; d < 64; d *= 2) {
                 const double down = __shfl_down(dG, d, 64);
-                if (t + d < 64) dG += down;
+                if (t + d < 64 && s.gates.doc[t + d] == doc) dG += down;
             }
             dbeta += s.edu[t];
-            const bool cut = s.gates.doc[t] != (t ? s.gates.doc[t - 1] : 0);
+            const bool cut = doc != (t ? s.gates.doc[t - 1] : 0);
             if (t0 + t < a.L) {
                 const int64_t at = (b * a.L + t0 + t) * a.H + h;
                 p.dg[at] = cut ? 0.0f : (float)dG;
