@@ -1146,10 +1146,10 @@ class _GatedScanFn(torch.autograd.Function):
     backward reads them (ssm_gated_scan_fwd / _bwd)."""
 
     @staticmethod
-    def forward(ctx, x, gate, A, in_gate, gate_bias, in_bias, h0, mode, reset):
+    def forward(ctx, x, gate, A, in_gate, gate_bias, in_bias, h0, mode, reset, recorded):
         _gpu(x, "x", 3, "(B, L, D)")
         ck = None
-        if any(ctx.needs_input_grad):
+        if recorded and any(ctx.needs_input_grad):  # (which holds for a leaf under no_grad too)
             ck = torch.empty(gated_checkpoint_shape(*x.shape), device=x.device, dtype=torch.float32)
         y, hf = gated_scan_fwd(x, gate, mode, A=A, in_gate=in_gate, gate_bias=gate_bias, in_bias=in_bias,
                                reset=reset, h0=h0, return_final_state=True, checkpoints=ck)
@@ -1164,7 +1164,7 @@ class _GatedScanFn(torch.autograd.Function):
         g = gated_scan_bwd(x, gate, dy.contiguous(), ctx.mode, A=A, in_gate=in_gate, gate_bias=gate_bias,
                            in_bias=in_bias, reset=reset, h0=h0, dh_final=dh_final.contiguous(), checkpoints=ck)
         return (g["dx"], g["dgate"], g.get("dA"), g.get("din_gate"), g.get("dgate_bias"), g.get("din_bias"),
-                g.get("dh0"), None, None)
+                g.get("dh0"), None, None, None)
 
 
 def gated_scan(x: torch.Tensor, gate: torch.Tensor, mode: str = "rate", A: Optional[torch.Tensor] = None,
@@ -1176,7 +1176,7 @@ def gated_scan(x: torch.Tensor, gate: torch.Tensor, mode: str = "rate", A: Optio
 
     To capture a backward() into a graph, capture it on leaves that no earlier, still living
     autograd graph has used (torch's own rule for gradient accumulation under capture)."""
-    return _GatedScanFn.apply(x, gate, A, in_gate, gate_bias, in_bias, h0, mode, reset)
+    return _GatedScanFn.apply(x, gate, A, in_gate, gate_bias, in_bias, h0, mode, reset, torch.is_grad_enabled())
 
 
 # ----------------------------------------------------------------------------- fused norms
@@ -1551,10 +1551,10 @@ class _GatedDeltaFn(torch.autograd.Function):
     reads them (ssm_gated_delta_fwd / _bwd)."""
 
     @staticmethod
-    def forward(ctx, q, k, v, g, beta, h0, scale, l2norm, reset):
+    def forward(ctx, q, k, v, g, beta, h0, scale, l2norm, reset, recorded):
         _delta_q(q)
         ck = None
-        if any(ctx.needs_input_grad) and isinstance(v, torch.Tensor) and v.dim() == 4:
+        if recorded and any(ctx.needs_input_grad) and isinstance(v, torch.Tensor) and v.dim() == 4:
             shape = gated_delta_checkpoint_shape(*q.shape[:2], v.shape[2], q.shape[3], v.shape[3])
             ck = torch.empty(shape, device=q.device, dtype=torch.float32)
         o, hf = gated_delta_fwd(q, k, v, g, beta, scale, l2norm, reset=reset, h0=h0, return_final_state=True,
@@ -1569,7 +1569,7 @@ class _GatedDeltaFn(torch.autograd.Function):
         q, k, v, g, beta, h0, reset, ck = ctx.saved_tensors
         d = gated_delta_bwd(q, k, v, g, beta, do.contiguous(), reset=reset, h0=h0, dh_final=dh_final.contiguous(),
                             checkpoints=ck, **ctx.opts)
-        return d["dq"], d["dk"], d["dv"], d["dg"], d["dbeta"], d.get("dh0"), None, None, None
+        return d["dq"], d["dk"], d["dv"], d["dg"], d["dbeta"], d.get("dh0"), None, None, None, None
 
 
 def gated_delta(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor,
@@ -1578,7 +1578,7 @@ def gated_delta(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tens
     """The gated delta rule as a differentiable torch op (arguments as in gated_delta_fwd): returns
     (o, h_final), and backward() runs ssm_gated_delta_bwd from the checkpoints the forward kept.  A
     captured backward(): as with gated_scan."""
-    return _GatedDeltaFn.apply(q, k, v, g, beta, h0, scale, l2norm, reset)
+    return _GatedDeltaFn.apply(q, k, v, g, beta, h0, scale, l2norm, reset, torch.is_grad_enabled())
 
 
 # ------------------------------------------------------------------------ e4m3 with block scales
