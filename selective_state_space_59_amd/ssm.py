@@ -1561,14 +1561,16 @@ class _GatedDeltaFn(torch.autograd.Function):
                                 checkpoints=ck)
         ctx.save_for_backward(q, k, v, g, beta, h0, reset, ck)
         ctx.opts = dict(scale=scale, l2norm=l2norm)
+        ctx.set_materialize_grads(False)  # (a final state that nobody used: no zeros to read)
         return o, hf
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, do, dh_final):
         q, k, v, g, beta, h0, reset, ck = ctx.saved_tensors
-        d = gated_delta_bwd(q, k, v, g, beta, do.contiguous(), reset=reset, h0=h0, dh_final=dh_final.contiguous(),
-                            checkpoints=ck, **ctx.opts)
+        do = torch.zeros(v.shape, device=v.device, dtype=v.dtype) if do is None else do.contiguous()
+        dh_final = None if dh_final is None else dh_final.contiguous()
+        d = gated_delta_bwd(q, k, v, g, beta, do, reset=reset, h0=h0, dh_final=dh_final, checkpoints=ck, **ctx.opts)
         return d["dq"], d["dk"], d["dv"], d["dg"], d["dbeta"], d.get("dh0"), None, None, None, None
 
 

@@ -43,6 +43,27 @@ def test_no_checkpoints_where_no_gradient_is_recorded(monkeypatch):
     assert not learnable[0].requires_grad and recorded[0].requires_grad
 
 
+def test_gradients_of_the_outputs_that_were_used(monkeypatch):
+    """A loss of the outputs alone, of the final state alone, and of both: what is not there is not read as
+    zeros, and counts as zeros all the same."""
+    calls = _spy(monkeypatch, "gated_delta_bwd")
+    k = _args()
+    n = torch.Generator().manual_seed(4)
+    do = torch.randn(k["v"].shape, generator=n).bfloat16().to(DEV)
+    dhf = torch.randn(k["h0"].shape, generator=n).to(DEV)
+    names = ("q", "k", "v", "g", "beta", "h0")
+    for of_o, of_state in ((True, False), (False, True), (True, True)):
+        leaves = {m: k[m].clone().requires_grad_() for m in names}
+        o, hf = ssm.gated_delta(l2norm=True, **leaves)
+        outs = [(t, d) for t, d, used in ((o, do, of_o), (hf, dhf, of_state)) if used]
+        torch.autograd.backward(*zip(*outs))
+        assert (calls[-1]["dh_final"] is None) == (not of_state)
+        want = ssm.gated_delta_bwd(*(k[m] for m in names[:5]), do if of_o else torch.zeros_like(do), l2norm=True,
+                                   h0=k["h0"], dh_final=dhf if of_state else torch.zeros_like(dhf))
+        for m in names:
+            assert torch.equal(leaves[m].grad, want["d" + m]), m
+
+
 def test_none_of_the_gated_scan_either(monkeypatch):
     calls = _spy(monkeypatch, "gated_scan_fwd")
     n = torch.Generator().manual_seed(2)
