@@ -29,14 +29,15 @@ __device__ __forceinline__ uint32_t magnitude16(uint32_t m) {
 __device__ __forceinline__ float scale_of(uint32_t m) { return __uint_as_float(max(m, kLeastBits)) / 448.0f; }
 
 // x / scale as a product with the reciprocal and one correction: the rounded quotient, which bf16 values
-// often put on a border between two e4m3 ones.
+// often put on a border between two e4m3 ones.  (The correction is formed from t scale - x, whose zero has the
+// sign that leaves a t of -0 as it is.)
 __device__ __forceinline__ uint2 quantise8(const float (&x)[8], float scale) {
     const float inv = 1.0f / scale;
     float q[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
         const float t = x[e] * inv;
-        q[e] = __builtin_fmaf(__builtin_fmaf(-t, scale, x[e]), inv, t);
+        q[e] = __builtin_fmaf(-__builtin_fmaf(t, scale, -x[e]), inv, t);
     }
     int lo = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false), hi = __builtin_amdgcn_cvt_pk_fp8_f32(q[4], q[5], 0, false);
     lo = __builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], lo, true);
