@@ -763,7 +763,9 @@ ssm_status_t ssm_gated_rmsnorm_bwd(const ssm_gated_norm_bwd_args_t *args, void *
  *
  * Arithmetic is fp32: bf16 tensors run on the bf16 matrix cores, with what was
  * computed carried through the products as the sum of three bf16 numbers (two,
- * 16 bits, where only a bf16 output follows); outputs are rounded once.  Results
+ * 16 bits, where only bf16 outputs follow: o, and dq and dk, with l2norm ahead of
+ * the norm's gradient, which takes their part along q and k out); outputs are
+ * rounded once.  Results
  * do not change from run to run.  Long sequences of few heads run as parallel
  * segments, in other places for another length: a sequence in two calls gives
  * what one call does to rounding.  kdim: a multiple of 8 up to SSM_DELTA_MAX_KDIM;
@@ -916,10 +918,15 @@ ssm_status_t ssm_add_rmsnorm_fp8(const ssm_add_norm_fp8_args_t *args, void *stre
 /*
  * The product of 8-bit matrices, y = x w^T:
  *   y[m,n] = sum_j x_scales[m,j] w_scales[n/128,j] sum_{k in block j} xq[m,k] wq[n,k]
- * Sums are fp32; y is rounded once.  For a bf16 y a block's 128 terms are summed by
- * the 8-bit matrix instruction, which drops what lies 2^14 below the largest of
- * eight terms (about 1.5e-5 of a result, where the rounding to bf16 is 2e-3); for an
- * fp32 y they are summed in fp32.  x is quantised by rows of 1, w by rows of 128.
+ * Sums are fp32; y is rounded once.  x is quantised by rows of 1, w by rows of 128.
+ * For a bf16 y a block's 128 terms are summed by the 8-bit matrix instruction, which
+ * aligns eight products at a time to the largest and drops what lies 2^14 below it:
+ * beside its rounding y is off by less than 7 * 2^-14 sum |x w|.  For random data
+ * that is 1.5e-5 of y, where the rounding is 2e-3; where large terms cancel, or one
+ * channel stands far above the others, it may be more than the rounding.  For an
+ * fp32 y the terms are summed in fp32 and nothing is dropped.
+ * A block's two scales are multiplied first, in fp32: a product below 2^-126 loses
+ * digits of the block's part, one of 2^128 or more is infinite.
  */
 typedef struct ssm_matmul_fp8_args {
     int64_t m, n, k;        /* M >= 0; 1 <= N < 2^24; K: a multiple of 16 up to 2^20;

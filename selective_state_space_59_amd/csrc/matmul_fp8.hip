@@ -20,9 +20,10 @@ typedef int i8 __attribute__((ext_vector_type(8)));
 constexpr int kOne = 0x7f7f7f7f;  // 1.0 in the exponent bytes of the scaled instruction
 
 // 32 bytes of a row as a block's product takes them.  The 8-bit instruction adds the products of a lane in
-// groups of eight, aligned to the largest of each: what lies 2^14 below it is lost (random data: 1.5e-5 of
-// the result).  That is far below a bf16 result's own rounding; for an fp32 result the values are widened
-// to bf16, exactly, and summed by the bf16 instruction at half the rate.
+// groups of eight, aligned to the largest of each: what lies 2^14 below it is lost, less than 7 * 2^-14 of the
+// sum of all magnitudes.  For random data that is 1.5e-5 of the result, far below a bf16 result's own rounding
+// (2e-3), and more than it only where large terms cancel; for an fp32 result the values are widened to bf16,
+// exactly, and summed by the bf16 instruction at half the rate.
 template <typename OUT>
 struct Operand {
     i8 v;

@@ -1653,8 +1653,8 @@ def matmul_fp8(xq: torch.Tensor, x_scales: torch.Tensor, wq: torch.Tensor, w_sca
                out_dtype: torch.dtype = torch.bfloat16, y: Optional[torch.Tensor] = None) -> torch.Tensor:
     """ssm_matmul_fp8: y (..., N) = x w^T of e4m3 matrices, xq (..., K) with scales (..., ceil(K / 128)), as
     quantize_fp8 or add_rmsnorm_fp8 give them, wq (N, K) with scales (ceil(N / 128), ceil(K / 128)), as
-    quantize_fp8(w, block_rows=128) does; K a multiple of 16; y in bf16 or fp32.  For serving: it has no
-    gradients."""
+    quantize_fp8(w, block_rows=128) does; K a multiple of 16; y in bf16 or fp32 (which keeps small terms
+    beside large ones that cancel, at half the rate).  For serving: it has no gradients."""
     shape = _shape_of(xq)
     dev, K = xq.device, shape[-1]
     if not isinstance(wq, torch.Tensor) or wq.dim() != 2:
