@@ -269,11 +269,17 @@ template <typename OUT>
 void launch(const ssm_matmul_fp8_args_t &a, hipStream_t stream) {
     const int blocks = (int)((a.k + 127) / 128);
     const bool wide = a.n % 4 == 0 && reinterpret_cast<uintptr_t>(a.y) % (4 * OUT::bytes) == 0;
-    // Few rows, where tiles of 64 would be too few as well.  Skinny and tiles, bf16 y (fp32: up to a fifth more on
-    // either side): 10240 x 2560 with 1 row 7.1 us (3.7 TB/s of w) and 12.8, 16 rows 10.3 and 12.9, 32 rows 14.8
-    // and 13.0, 64 rows 23.1 and 13.4; 2560 x 5120 with 1 row 8.4 and 22.1, 32 rows 11.5 and 22.5, 64 rows 18.4
-    // and 23.0.
-    if (a.m <= 16 || (a.m <= 64 && a.n < 8192)) {
+    // Few rows.  The skinny kernel's time goes by the rounds of its workgroups (16 rows of w each) over the CUs and
+    // by its pieces of 16 rows of x, a tile's hardly by either; so it takes over where it has 512 workgroups' work
+    // of 32 rows at most.  us, skinny and tiles, bf16 y (fp32: up to a fifth more on either side), K = 2560 (at
+    // 1280 and 5120 the same side wins, but for 17 rows of N = 10240, 6.4 and 7.1 at 1280):
+    //   N              2560         4096         5120         8192         10240        16384
+    //   17 rows     5.6  11.3    5.7  11.3    7.9  11.4    8.0  11.3   11.6  11.5   14.9  13.4
+    //   32 rows     6.2  11.3    6.3  11.4   10.0  11.5   10.0  11.4   14.6  11.7   18.4  13.6
+    //   33 rows     7.7  11.3    7.7  11.4   12.1  11.5   12.1  11.4   17.6  11.6   22.4  13.5
+    //   64 rows     9.3  11.5    9.3  11.6   15.8  11.6   16.0  11.7   23.1  12.0   29.7  13.9
+    // and with 1 row of 10240 x 2560 7.1 us (3.7 TB/s of w) and 12.8, of 2560 x 5120 8.4 and 22.1.
+    if (a.m <= 16 || (a.m <= 64 && (a.n + 15) / 16 <= (a.m <= 32 ? 512 : 256))) {
         const unsigned grid = (unsigned)((a.n + 15) / 16), threads = 64 * kSkinnyWaves;
         if (a.m <= 16) skinny_kernel<OUT, 1><<<grid, threads, 0, stream>>>(a, blocks, wide);
         else if (a.m <= 32) skinny_kernel<OUT, 2><<<grid, threads, 0, stream>>>(a, blocks, wide);

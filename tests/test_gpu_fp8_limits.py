@@ -1,5 +1,5 @@
-"""The e4m3 product at the limits it states (needs an MI355X): large terms that cancel beside small ones, and
-scales far from 1."""
+"""The e4m3 product at the limits it states (needs an MI355X): large terms that cancel beside small ones,
+scales far from 1, either kernel for few rows."""
 import numpy as np
 import pytest
 import torch
@@ -60,3 +60,16 @@ def test_scales_far_from_1(ex, ew, M, N, K, dtype):
     want, size = R.matmul_blocks(xq, sx, wq, sw)
     assert 1e-30 < np.abs(want).max() < 1e36
     check(y, want, _tolerance(K, size, dtype), "%dx%dx%d" % (M, N, K))
+
+
+@pytest.mark.parametrize("dtype", **IDS)
+@pytest.mark.parametrize("M,N,K", [(32, 8192, 144), (32, 8193, 144), (33, 4096, 272), (33, 4097, 272), (64, 4096, 144),
+                                   (64, 6000, 144)])
+def test_few_rows_of_either_kernel(M, N, K, dtype):
+    """On both sides of where tiles take over from the skinny kernel."""
+    g = np.random.default_rng(N + M)
+    xq, wq = (R.e4m3(np.clip(100 * g.standard_normal(s), -448, 448)) for s in ((M, K), (N, K)))
+    kb = -(-K // 128)
+    sx, sw = (f64(torch.from_numpy(np.exp(g.standard_normal((n, kb)))).float()) for n in (M, -(-N // 128)))
+    want, size = R.matmul_blocks(xq, sx, wq, sw)
+    check(_call(xq, sx, wq, sw, dtype), want, _tolerance(K, size, dtype), "%dx%dx%d" % (M, N, K))
