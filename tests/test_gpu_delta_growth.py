@@ -21,6 +21,7 @@ from selective_state_space_59_amd import ssm as capi
 from tests.delta_helpers import bound, case64, close, delta_case
 from tests.recurrent_helpers import check, f64
 from tests.test_gpu_delta_edges import _call, _same, _take
+from tests.test_gpu_recurrent_block import _capture, _flat
 from tests.test_gpu_recurrent_frames import Frames
 
 pytestmark = pytest.mark.gpu
@@ -224,3 +225,32 @@ def test_stores_stay_inside(shape, dtype):
         _call("ssm_gated_delta_bwd", capi.GatedDeltaBwdArgs(**sizes), fr, "ssm_gated_delta_bwd_workspace_size", **k,
               **out, dout=do, dh_final=hf, checkpoints=given)
         _same(out, want, "backward")
+
+
+def test_a_captured_call_whose_decays_begin_to_grow():
+    """Which heads grow is found anew in each replay."""
+    B, L, Hk, H, K, V = 1, 150, 1, 2, 16, 24
+    k = _case(B, L, Hk, H, K, V, BF, -0.1, 1.0, seed=9)
+    do = torch.randn(B, L, H, V, generator=torch.Generator().manual_seed(1)).to(BF).to(DEV)
+    gates = [k["g"].clone(), torch.where(k["g"] == k["g"][0, 0, 0], 0.4, k["g"])]
+
+    def call():
+        o, hf = ssm.gated_delta_fwd(return_final_state=True, **k)
+        return o, hf, ssm.gated_delta_bwd(do=do, **k)
+
+    want = []
+    for g in gates:
+        k["g"].copy_(g)
+        want.append([t.clone() for t in _flat(call())])
+    k["g"].copy_(gates[0])
+    graph, out = _capture(call)
+    for i in (0, 1, 0, 1, 1, 0):
+        k["g"].copy_(gates[i])
+        call()  # eager work between replays
+        torch.cuda.synchronize()
+        for t in _flat(out):
+            t.view(torch.uint8).fill_(255)
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(_flat(out), want[i]):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
