@@ -228,14 +228,14 @@ struct ChainArgs {
 // into registers, reloaded for the next chunk as soon as it has been used; only states, X and E go round
 // through LDS, split into their planes once, by the wave that owns them.  Three barriers a chunk.
 // What bounds it is a chunk's chain of products, each behind a barrier and a read of LDS: 2.5 us a chunk where
-// a CU has one workgroup, of which 0.35 wait for loads.  8 x 2048 steps of 12 heads of 128, bf16: 197 us, 251
+// a CU has one workgroup, of which 0.35 wait for loads.  8 x 2048 steps of 12 heads of 128, bf16: 175 us, 252
 // with checkpoints (302 MB).
 //
 // A long sequence of few heads runs in segments.  The state that leaves a segment is T S + Z for the state S
 // entering it; first (FIRST) all segments but the last form, without outputs, their Z (from a state of zeros,
 // the first one's from h0) and, as K more columns without values, their T (from the identity); join_kernel
 // turns these into the states entering the segments, and the chains run again from there.  32768 steps of 12
-// heads of 128, bf16, ten segments: 369 us, 31 and 298; in one piece 1272.
+// heads of 128, bf16, ten segments: 337 us, 31 and 278; the whole call 790, in one piece 1410.
 template <typename IO, int KP, int NC, bool FIRST>
 __global__ __launch_bounds__(kThreads, 2) void chain_kernel(ChainArgs p) {
     using O = Op<IO>;
@@ -678,8 +678,8 @@ hipError_t chain(const ChainArgs &p, hipStream_t stream) {
         if (e != hipSuccess) return e;
         return p.wide ? chain_pass<IO, KP, 2, false>(p, stream) : chain_pass<IO, KP, 1, false>(p, stream);
     }
-    // 32 channels a workgroup where every CU gets one all the same (8 x 2048 x 12 heads: 197 us, 230 with 16;
-    // where checkpoints are written as well 251 and 312)
+    // 32 channels a workgroup where every CU gets one all the same (8 x 2048 x 12 heads: 175 us, 215 with 16;
+    // where checkpoints are written as well 257 and 314)
     return wide_slices(p.a) ? chain_pass<IO, KP, 2, false>(p, stream) : chain_pass<IO, KP, 1, false>(p, stream);
 }
 
@@ -714,14 +714,17 @@ struct Segments {
     bool wide;
 };
 
-// Segments of a sequence of n chunks: as many as run at once, two workgroups a CU with outputs and three
-// without; of at least eight chunks, as each costs a step of join_kernel and its state once more.  Where that is
-// fewer than eight segments, workgroups take 32 channels, which leaves room for more.  bf16, K = V = 128, whole
-// calls, in segments and in one piece: 32768 steps of one head 152 us (32 segments) and 1026, of 4 heads 334
-// (13) and 1170, of 12 heads 836 (10 of 32 channels; 986 in 5 of 16) and 1408; 16384 steps of 8 heads 272 and
-// 615 (311 in 7 of 16), of 20 heads 644 (852) and 795; 4096 steps of 4 heads 80 and 164, of 16 heads 164 and
-// 179; 2048 steps of 12 heads 98 and 99; 1024 steps of 12 heads 73 in 3 and 60, and two segments of them 59;
-// 4096 steps of 24 heads 226 in 5 and 191.
+// Segments of a sequence of n chunks: as many as run at once with outputs, two workgroups a CU, of at least eight
+// chunks, as each costs a step of join_kernel and its state once more.  The pass without outputs has up to three
+// workgroups a CU of 16 channels, which run at once, or six of 32, of which two do (held to two, 32768 steps of 12
+// heads take 886 us and not 789, 16384 of 20 heads 715 and 643, 8192 of 12 238 and 225, 4096 of 12 139 and 142).
+// Where there would be fewer than eight segments, workgroups take 32 channels, which leaves room for more.
+// bf16, K = V = 128, whole calls, us, as they run and in one piece (in slices of 16 alone):
+//   32768 steps of one head 160 (32 segments) and 1035, of 4 heads 334 (13) and 1167, of 12 heads 787 (10 of 32
+//   channels) and 1410 (988); 16384 steps of 8 heads 268 and 614 (309), of 20 heads 644 and 794 (852); 4096 steps
+//   of 4 heads 79 and 161, of 12 heads 143 and 172 (137), of 16 heads 163 and 179 (161); 2048 of 12 heads 99 and 96.
+// Not taken: 1024 steps of 12 heads in three segments 73, in two 59, in one piece 60; 4096 steps of 24 heads in five
+// 226, in one piece 191.
 static Segments segments_of(int64_t heads, int64_t n, int64_t K, int64_t V) {
     const auto long_enough = [&](int64_t s) { return s <= n / 8 && s * s <= 2 * n; };
     const auto fits = [&](int64_t s, int width) {

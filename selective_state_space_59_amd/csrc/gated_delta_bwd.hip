@@ -599,7 +599,7 @@ hipError_t back_chain(BackArgs p, GradArgs g, hipStream_t stream) {
 
 template <typename IO, int KP>
 hipError_t backward(const BackArgs &p, const GradArgs &g, hipStream_t stream) {
-    // 32 value channels a workgroup where that leaves one for each CU, as forwards (8 x 2048 x 12 heads: 261 us, 340
+    // 32 value channels a workgroup where that leaves one for each CU, as forwards (8 x 2048 x 12 heads: 253 us, 320
     // with 16); floats keep to 16, as 32 would not fit the registers
     if constexpr (IO::bytes == 2)
         if (wide_slices(p.a)) return back_chain<IO, KP, 2>(p, g, stream);

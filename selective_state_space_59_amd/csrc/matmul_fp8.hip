@@ -278,7 +278,8 @@ void launch(const ssm_matmul_fp8_args_t &a, hipStream_t stream) {
     //   32 rows     6.2  11.3    6.3  11.4   10.0  11.5   10.0  11.4   14.6  11.7   18.4  13.6
     //   33 rows     7.7  11.3    7.7  11.4   12.1  11.5   12.1  11.4   17.6  11.6   22.4  13.5
     //   64 rows     9.3  11.5    9.3  11.6   15.8  11.6   16.0  11.7   23.1  12.0   29.7  13.9
-    // and with 1 row of 10240 x 2560 7.1 us (3.7 TB/s of w) and 12.8, of 2560 x 5120 8.4 and 22.1.
+    // and with 1 row of 10240 x 2560 6.4 and 10.9, of 2560 x 5120 6.2 and 19.5 (20 calls in a graph, which w outlasts
+    // in the last cache; where it comes from memory a row of 10240 x 2560 takes 7.4 us, 3.5 TB/s of w).
     if (a.m <= 16 || (a.m <= 64 && (a.n + 15) / 16 <= (a.m <= 32 ? 512 : 256))) {
         const unsigned grid = (unsigned)((a.n + 15) / 16), threads = 64 * kSkinnyWaves;
         if (a.m <= 16) skinny_kernel<OUT, 1><<<grid, threads, 0, stream>>>(a, blocks, wide);
@@ -287,8 +288,8 @@ void launch(const ssm_matmul_fp8_args_t &a, hipStream_t stream) {
         return;
     }
     const auto tiles = [&](int64_t bm, int64_t bn) { return ((a.m + bm - 1) / bm) * ((a.n + bn - 1) / bn); };
-    // The largest tile that still gives every CU a workgroup.  16384 x 10240 x 2560 in bf16: tiles of 256 490 us
-    // (1750 TFLOP/s), of 128 624; 256 x 10240 x 2560: of 64 17 us, of 128 22; fp32 results, whose widened operands
+    // The largest tile that still gives every CU a workgroup.  16384 x 10240 x 2560 in bf16: tiles of 256 473 us
+    // (1810 TFLOP/s), of 128 575; 256 x 10240 x 2560: of 64 17.2 us, of 128 21.8; fp32 results, whose widened operands
     // would not fit the registers beside 256 x 256 of sums, stay with 128.
     if (OUT::bytes == 2 && tiles(256, 256) >= 256) {
         if constexpr (OUT::bytes == 2)

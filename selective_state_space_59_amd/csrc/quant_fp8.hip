@@ -3,7 +3,8 @@
 //   scale = max(m, 2^-100) / 448,   q = e4m3(x / scale)
 // 16 lanes of 8 elements each hold a row of a block, so m is four steps between lanes and a lane stores
 // 8 bytes.  The magnitude is compared as an integer, which lets a NaN through.  Bound by HBM:
-// the norm of 16384 x 2560 with an fp32 stream, post norm and scale 90 us, 5.1 TB/s, as fast as a plain copy.
+// the norm of 16384 x 2560 with an fp32 stream, post norm and scale 90 us, 5.1 TB/s, as fast as a plain copy; 16384 x
+// 10240 quantised by rows and by 128 rows 107 and 94 us in bf16 (4.7 and 5.4 TB/s), 142 and 148 in fp32.
 #include "norm_rows.h"
 
 namespace ssm {
