@@ -1434,7 +1434,8 @@ def gated_delta_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.
     """ssm_gated_delta_fwd: per value head, S' = exp(g_t) S, e_t = v_t - S'^T k_t,
     S = S' + beta_t k_t e_t^T, o_t = scale S^T q_t.  q, k: (B, L, Hk, K); v: (B, L, H, V), bf16 or fp32,
     dense or parts of a wider tensor (steps and rows any distance apart); Hk divides H; g: (B, L, H) fp32
-    log decays; beta: (B, L, H) in q's dtype; scale: K ** -0.5 unless given; l2norm: q and k are divided by
+    log decays (a head whose decays multiply to more than e within a chunk of 64 steps is computed step by
+    step, far slower); beta: (B, L, H) in q's dtype; scale: K ** -0.5 unless given; l2norm: q and k are divided by
     their norms first; reset: (B, L) uint8 or bool; h0: (B, H, K, V) fp32.
 
     Returns (o, h_final or None).  A float32 tensor `checkpoints` of gated_delta_checkpoint_shape(B, L, H,
